@@ -1,6 +1,8 @@
 /*
  * qkvp.h - C ABI of libqkvp: paged MLA decode attention that reads a quantized latent KV cache
- * (FP8 E4M3 or NVFP4) directly, for NVIDIA GB300 (sm_103a).
+ * (FP8 E4M3 or NVFP4) directly, for NVIDIA GB300 (sm_103a). Next to it: the appends that apply the
+ * rotary position embedding on the way into a cache, and decode attention over a paged 8-bit cache of
+ * K and V heads (gqa_*), whole or through a sliding window with sink tokens.
  *
  * The problem, as the source pages state it:
  *  - Each token stores one 576-wide latent: kv_lora_rank 512 ("nope") + qk_rope_head_dim 64. All
@@ -36,6 +38,11 @@
  *                buffer, 64 tokens per page: "The Precision Frontier: Implementing bf16 Index Keys",
  *                section "The Message: Planning the bf16-K Implementation") carrying the latent.
  *  - BF16 pool : kv_data uint16 [num_pages][64][576] (the cast-then-attend baseline only).
+ *  - head pool (gqa_*): kv_data uint8 [num_pages][2][num_kv_heads][64][head_dim], the K blocks of a
+ *                page and then its V blocks, one code per element (qkvp_cache_dtype), and kv_scale
+ *                float [num_pages][2][num_kv_heads], one scale per (page, K or V, head). An element
+ *                decodes to kv_scale(block) * value(code). 2 * num_kv_heads * (64 * head_dim + 4)
+ *                bytes per page.
  *  - q         : bf16 [batch][num_heads][576], row-major, contiguous.
  *  - out       : bf16 [batch][num_heads][512], 16-byte aligned (the attend kernels store 16-byte
  *                vectors); lse: float [batch][num_heads] (natural log), or NULL.
@@ -109,6 +116,12 @@ typedef enum {
                               236 / 333 against 347 / 361 us). At 16 heads the mma.sync kernel is
                               faster. */
 } qkvp_algo;
+
+/* Code type of a head pool. E4M3: as in the FP8 pools. INT8: two's complement codes in [-127, 127]. */
+typedef enum { QKVP_CACHE_E4M3 = 1, QKVP_CACHE_INT8 = 2 } qkvp_cache_dtype;
+/* Which dims of a head's first r dims the rotary embedding turns as pair i (i < r / 2):
+ * HALVES (x[i], x[i + r/2]), PAIRS (x[2i], x[2i + 1]). */
+typedef enum { QKVP_ROPE_HALVES = 0, QKVP_ROPE_PAIRS = 1 } qkvp_rope_style;
 
 #define QKVP_LATENT_DIM 576
 #define QKVP_V_DIM 512
@@ -342,6 +355,144 @@ int kv_gather_fp8(const void* kv_data, const uint8_t* kv_scale, int32_t kv_dtype
  */
 int kv_gather_pages_bf16(const uint8_t* kv_data, int32_t page_size, int64_t num_pages, const int32_t* page_ids,
                          int64_t n_pages, void* out, qkvp_stream_t stream);
+
+/*
+ * mla_append_rope - one MLA step's append with the rotary position embedding on the way: token t's
+ * latent row [c_kv(t) | R(p) k_pe(t)] goes into the pool as by kv_append_quant, p = positions[t], and the
+ * query's rope parts go, rotated, into the last 64 dims of the q that mla_decode_run reads. The
+ * source pages name the operation (a fused norm, rotation and store for indexer keys: "The Precision
+ * Frontier: Implementing bf16 Index Keys") but give no arithmetic.
+ *   R(p) turns each pair (a, b) of the 64 rope dims (rope_style) into (a c - b s, b c + a s), c =
+ *   cos_sin[p][i], s = cos_sin[p][32 + i], in FP32 with one rounding per operation. The rotated values
+ *   are quantized from FP32 (no rounding to BF16 in between), by the formulas of kv_append_quant.
+ *  c_kv         device bf16, row t at c_kv + t * c_kv_stride (elements), 512 values.
+ *  k_pe         device bf16, row t at k_pe + t * k_pe_stride, 64 values. May be a slice of a wider row.
+ *  n_tokens     rows of c_kv, k_pe, slot_mapping, positions, q_pe and q.
+ *  slot_mapping device int64 [n_tokens], as for kv_append_quant: slots outside the pool skip the row.
+ *  positions    device int64 [n_tokens]. A position outside [0, max_positions) skips the token: neither
+ *               its row nor its q is written.
+ *  cos_sin      device float [max_positions][64]: the 32 cosines of a position, then the 32 sines.
+ *  q_pe         device bf16, head h of token t at q_pe + t * q_pe_token_stride + h * q_pe_head_stride,
+ *               64 values; NULL: no query is rotated (q must be NULL, num_heads 0).
+ *  q            device bf16 [n_tokens][num_heads][576]; dims 512..575 of every head are written, the
+ *               others are left as they are. q_pe may be q + 512 itself (strides num_heads * 576 and
+ *               576): rotation in place. Other overlaps are not supported.
+ *  kv_data, kv_scale, kv_dtype, global_scale, page_size, num_pages: as for kv_append_quant (an FP8,
+ *               NVFP4 or per-token-scaled FP8 pool).
+ * Row strides are multiples of 8 elements, c_kv, k_pe, q_pe, q, kv_data and cos_sin 16-byte aligned.
+ * If two tokens of one call name the same slot, which of them is stored is unspecified.
+ */
+int mla_append_rope(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
+                    int64_t n_tokens, const int64_t* slot_mapping, const int64_t* positions,
+                    const float* cos_sin, int64_t max_positions, int32_t rope_style, const void* q_pe,
+                    int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t num_heads, void* q,
+                    void* kv_data, uint8_t* kv_scale, int32_t kv_dtype, float global_scale,
+                    int32_t page_size, int64_t num_pages, qkvp_stream_t stream);
+
+/*
+ * gqa_append_rope - append new tokens' K and V heads to a paged head pool (layout above), K rotated on
+ * the way, and rotate the query heads in the same launch. Every array below is on the device, so a
+ * captured call replays with new lengths.
+ *   Request r brings the tokens tok_indptr[r] .. tok_indptr[r+1] - 1 and holds kv_len[r] tokens already;
+ *   its j-th new token goes to cache position kv_len[r] + j, i.e. offset (kv_len[r] + j) % 64 of page
+ *   kv_indices[kv_indptr[r] + (kv_len[r] + j) / 64]. Rows behind tok_indptr[batch] are padding: nothing
+ *   of them is read or written.
+ *   Block scale, per (page, K or V, head): need = amax / m, m = 448 (E4M3) or 127 (INT8), amax the
+ *   largest finite |x| of the new elements that the call puts into the block. If the call writes the
+ *   block's offset 0, or its scale is 0, the scale becomes need. Otherwise it becomes scale * 2^j with the
+ *   smallest j >= 0 for which that is at least need, and if j > 0 the codes of the block's older tokens
+ *   (the offsets before the call's first) become round(code * 2^-j): exact for E4M3 but for codes that
+ *   become subnormal, and for INT8 each growth halves the errors before it, so that they stay below one
+ *   step of the final scale. Codes are round(x / scale), or round(x) when scale is 0: E4M3 to nearest
+ *   even, saturating at +-448, NaN gives 0x7F; INT8 to nearest even, held in [-127, 127], NaN gives 0.
+ *   FP32 arithmetic with one rounding per operation; the rotation as for mla_append_rope, over the first
+ *   rot_dim dims of a head, the others unchanged.
+ *  k, v         device bf16, head h of token t at k + t * k_stride + h * head_dim (elements).
+ *  n_tokens     rows of k, v, positions, q and q_out (tok_indptr entries beyond it are cut to it).
+ *  tok_indptr   device int32 [batch + 1], non-decreasing from 0. kv_len device int32 [batch].
+ *  kv_indptr, kv_indices, nnz: page table on the device, as for kv_gather_fp8.
+ *  positions    device int64 [n_tokens], the positions that rotate K and Q; NULL: the cache positions.
+ *  cos_sin      device float [max_positions][rot_dim], cosines then sines; rot_dim a multiple of 16 up to
+ *               head_dim, or 0 (no rotation, cos_sin NULL).
+ *  q, q_out     device bf16 [.][num_heads][head_dim], token t at q + t * q_stride, q_out contiguous; the
+ *               same buffer (q_stride = num_heads * head_dim) rotates in place. NULL, NULL, num_heads 0:
+ *               none.
+ * Skipped on the device: a token whose page lies outside the request's pages, the table or the pool
+ * (its query is still rotated), and a token whose position lies outside [0, max_positions) (so is its
+ * query). A page must not be appended to by two requests of one call.
+ * head_dim 64, 128 or 256; num_kv_heads 1 to 256; row strides multiples of 8; k, v, q, q_out, kv_data and
+ * cos_sin 16-byte aligned.
+ */
+int gqa_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t n_tokens,
+                    const int32_t* tok_indptr, const int32_t* kv_len, int32_t batch,
+                    const int32_t* kv_indptr, const int32_t* kv_indices, int64_t nnz,
+                    const int64_t* positions, const float* cos_sin, int64_t max_positions,
+                    int32_t rot_dim, int32_t rope_style, int32_t num_kv_heads, int32_t head_dim,
+                    void* kv_data, float* kv_scale, int32_t cache_dtype, int32_t page_size,
+                    int64_t num_pages, const void* q, int64_t q_stride, int32_t num_heads, void* q_out,
+                    qkvp_stream_t stream);
+
+/* Host-side plan produced by gqa_decode_plan and consumed by gqa_decode_run; plain data, used as a
+ * qkvp_plan is. */
+typedef struct {
+  int32_t batch, num_heads, num_kv_heads, head_dim, page_size, cache_dtype;
+  int32_t window, sinks;       /* as given; window 0: every token is visible */
+  int32_t num_workers;         /* CTAs of the decode kernel */
+  int32_t num_segments;        /* (request, KV head, page range) pieces */
+  int32_t num_split_groups;    /* (request, KV head) pairs cut into more than one segment */
+  int32_t max_group_segments;  /* most segments of one pair */
+  int32_t num_partials;        /* FP32 split partials held in the workspace */
+  int32_t max_worker_pages, min_worker_pages;
+  int64_t total_pages;         /* visible pages, summed over requests (of one KV head) */
+  int64_t total_tokens;        /* visible tokens, summed over requests */
+  uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;
+  uint64_t status_offset;      /* int32 status word, as in qkvp_plan */
+  uint64_t magic;
+} gqa_plan;
+
+/*
+ * gqa_decode_plan - split the visible pages of a batch into balanced work for gqa_decode_run.
+ *  kv_indptr_host, kv_len_host, batch, page_size, num_sms, min_splits, workspace, workspace_bytes, stream:
+ *               as for mla_decode_plan (also its return values, the size query with workspace NULL, and
+ *               the refusal under stream capture). kv_len counts the token that asks: the query of
+ *               request r sits at position kv_len[r] - 1.
+ *  num_heads    a multiple of num_kv_heads; query heads h * G .. h * G + G - 1, G = num_heads /
+ *               num_kv_heads, read KV head h. Any G: the kernel takes up to 16 of them in one pass over
+ *               the pages and reads the pages again for each further 16.
+ *  num_kv_heads 1 to 256. head_dim 64, 128 or 256. cache_dtype a qkvp_cache_dtype.
+ *  window       tokens that a query sees back from its own, itself included; 0: all of them.
+ *  sinks        with a window, the first tokens that stay visible as well; without one it must be 0.
+ *               Token t of len is visible if t >= len - window or t < sinks. Pages with no visible token
+ *               are never read: their table entries may be anything.
+ * Host memory that runs out is reported as QKVP_E_WORKSPACE, too.
+ */
+int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, int32_t batch,
+                    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                    int32_t cache_dtype, int32_t window, int32_t sinks, int32_t num_sms,
+                    int32_t min_splits, void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream,
+                    gqa_plan* plan);
+
+/*
+ * gqa_decode_run - decode attention of one layer over a head pool. Per request r and query head a with
+ * KV head h = a / G, over the visible tokens t,
+ *   z_t = sm_scale * sum_d q[r,a,d] * sk * kcode_t[d],  out[r,a,d] = sum_t softmax(z)_t * sv * vcode_t[d],
+ *   lse[r,a] = log sum_t exp(z_t),
+ * sk, sv the scales of the token's K and V block. A request with no visible token (kv_len 0, or every
+ * page id out of the pool) gives out 0 and lse -inf. One kernel launch: requests that are split are
+ * joined by the last of their CTAs to finish, in a fixed order, so equal inputs give equal bits.
+ * Codes of tokens that are not visible take no part, whatever they hold (NaN too).
+ *  q            device bf16 [batch][num_heads][head_dim]. Held as FP16 times a power of two per head.
+ *  kv_data, kv_scale, num_pages: the head pool; kv_data 128-byte aligned (TMA reads it), scales finite
+ *               and not negative. Page ids outside [0, num_pages) read as tokens that are not visible.
+ *  kv_indices   device int32 page ids addressed by the plan's kv_indptr.
+ *  out          device bf16 [batch][num_heads][head_dim], 16-byte aligned; lse float [batch][num_heads]
+ *               or NULL.
+ *  workspace    the buffer given to gqa_decode_plan. It holds partials and counters during the run: two
+ *               runs that use one workspace must not overlap (nor two graphs that captured them).
+ */
+int gqa_decode_run(const gqa_plan* plan, const void* q, const void* kv_data, const float* kv_scale,
+                   int64_t num_pages, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
+                   void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream);
 
 /*
  * qkvp_encode_f32 - the device rounding routines of kv_append_quant applied to raw FP32 values:

@@ -21,11 +21,14 @@ KV_FP8_E4M3, KV_NVFP4, KV_BF16, KV_FP8_PER_TOKEN = 1, 2, 3, 4
 PAGE_BYTES_FP8_PER_TOKEN = 64 * (576 + 4)   # 64 rows of E4M3 codes, then 64 FP32 token scales
 SRC_FP8_E4M3, SRC_BF16 = 1, 2
 ALGO_AUTO, ALGO_MMA_SYNC, ALGO_TCGEN05, ALGO_MMA_FP8, ALGO_TCGEN05_TOKENS = 0, 1, 2, 3, 4
+CACHE_E4M3, CACHE_INT8 = 1, 2
+ROPE_HALVES, ROPE_PAIRS = 0, 1
 LATENT_DIM, V_DIM, PAGE_SIZE = 576, 512, 64
 
 EXPORTS = ["kv_append_quant", "mla_decode_plan", "mla_decode_run", "mla_decode_attend",
            "mla_decode_combine", "mla_decode_noalloc", "kv_pool_cast_bf16", "kv_gather_fp8",
-           "kv_gather_pages_bf16", "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
+           "kv_gather_pages_bf16", "mla_append_rope", "gqa_append_rope", "gqa_decode_plan", "gqa_decode_run",
+           "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
 
 
 class qkvp_plan(ctypes.Structure):
@@ -41,6 +44,19 @@ class qkvp_plan(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class gqa_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_heads", "num_kv_heads", "head_dim", "page_size", "cache_dtype", "window", "sinks",
+        "num_workers", "num_segments", "num_split_groups", "max_group_segments", "num_partials",
+        "max_worker_pages", "min_worker_pages")] + [
+        ("total_pages", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64),
+        ("partial_o_offset", ctypes.c_uint64), ("partial_lse_offset", ctypes.c_uint64),
+        ("status_offset", ctypes.c_uint64), ("magic", ctypes.c_uint64)]
+
+    as_dict = qkvp_plan.as_dict
 
 
 class QkvpError(RuntimeError):
@@ -77,12 +93,20 @@ def load(path: str | None = None):
         L.kv_pool_cast_bf16.argtypes = [vp, i64, vp, vp]
         L.kv_gather_fp8.argtypes = [vp, vp, i32, f32, i32, i64, vp, vp, i64, vp, i32, i64, vp, vp]
         L.kv_gather_pages_bf16.argtypes = [vp, i32, i64, vp, i64, vp, vp]
+        L.mla_append_rope.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp, i64, i32, vp, i64, i64, i32, vp,
+                                      vp, vp, i32, f32, i32, i64, vp]
+        L.gqa_append_rope.argtypes = [vp, i64, vp, i64, i64, vp, vp, i32, vp, vp, i64, vp, vp, i64, i32,
+                                      i32, i32, i32, vp, vp, i32, i32, i64, vp, i64, i32, vp, vp]
+        L.gqa_decode_plan.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, u64,
+                                      vp, c.POINTER(gqa_plan)]
+        L.gqa_decode_run.argtypes = [c.POINTER(gqa_plan), vp, vp, vp, i64, vp, f32, vp, vp, vp, u64, vp]
         L.qkvp_encode_f32.argtypes = [vp, i64, i32, vp, vp]
         L.qkvp_status_string.restype = c.c_char_p
         L.qkvp_status_string.argtypes = [c.c_int]
         for fn in ("kv_append_quant", "mla_decode_plan", "mla_decode_run", "mla_decode_attend",
                    "mla_decode_combine", "mla_decode_noalloc", "kv_pool_cast_bf16", "kv_gather_fp8",
-                   "kv_gather_pages_bf16", "qkvp_encode_f32", "qkvp_version"):
+                   "kv_gather_pages_bf16", "mla_append_rope", "gqa_append_rope", "gqa_decode_plan",
+                   "gqa_decode_run", "qkvp_encode_f32", "qkvp_version"):
             getattr(L, fn).restype = c.c_int
         _lib = L
         return L
@@ -229,6 +253,152 @@ def kv_gather_pages_bf16(kv_data, page_ids, out, num_pages: int | None = None, p
     st = load().kv_gather_pages_bf16(_ptr(kv_data), page_size, int(num_pages), _ptr(page_ids),
                                      int(page_ids.numel()), _ptr(out), _stream(stream))
     return _check("kv_gather_pages_bf16", st, raise_on_error)
+
+
+def _need(name: str, t, shape, dtypes, contiguous: bool = True):
+    """Checks a tensor's shape (None: any extent), type (by name) and layout; contiguous False asks only
+    that the last dim is dense."""
+    if tuple(t.shape) != tuple(s if w is None else w for s, w in zip(t.shape, shape)) or t.dim() != len(shape):
+        raise ValueError(f"{name} needs the shape {tuple('*' if w is None else w for w in shape)}, got {tuple(t.shape)}")
+    if str(t.dtype)[6:] not in dtypes:
+        raise ValueError(f"{name} needs one of the types {', '.join(dtypes)}, got {t.dtype}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} needs to be contiguous")
+    elif t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs a dense last dimension")
+
+
+def _on_current(*tensors):
+    """The launch goes to the current device: tensors elsewhere are refused."""
+    import torch
+    at = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (t.device.type != "cuda" or t.device.index != at):
+            raise ValueError(f"tensors need to be on the current CUDA device ({at}), got one on {t.device}")
+
+
+def _heads_rows(name: str, t, heads, dim):
+    """Row stride of [n, heads, dim] whose heads are dense."""
+    _need(name, t, (None, heads, dim), ("bfloat16",), contiguous=False)
+    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != dim:
+        raise ValueError(f"{name} needs dense heads: stride {dim} between heads, got {t.stride(1)}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+
+
+def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: int, kv_data, kv_scale,
+                    kv_dtype: int, q_pe=None, q=None, global_scale: float = 1.0,
+                    num_pages: int | None = None, page_size: int = PAGE_SIZE, stream=None,
+                    raise_on_error: bool = True) -> int:
+    """Append latent rows [c_kv | rotated k_pe] at slot_mapping, quantized, and rotate q_pe [n, H, 64] into
+    the last 64 dims of q [n, H, 576] (see qkvp.h). c_kv [n, 512], k_pe [n, 64] and q_pe may be slices with
+    their own row strides; cos_sin float32 [max_positions, 64]."""
+    n = int(c_kv.shape[0])
+    _need("c_kv", c_kv, (n, 512), ("bfloat16",), contiguous=False)
+    _need("k_pe", k_pe, (n, 64), ("bfloat16",), contiguous=False)
+    _need("slot_mapping", slot_mapping, (n,), ("int64",))
+    _need("positions", positions, (n,), ("int64",))
+    _need("cos_sin", cos_sin, (None, 64), ("float32",))
+    heads = 0
+    if (q_pe is None) != (q is None):
+        raise ValueError("q_pe and q go together")
+    if q is not None:
+        heads = int(q.shape[1])
+        _need("q", q, (n, heads, LATENT_DIM), ("bfloat16",))
+        _need("q_pe", q_pe, (n, heads, 64), ("bfloat16",), contiguous=False)
+        if heads == 0:
+            q = q_pe = None
+    _on_current(c_kv, k_pe, slot_mapping, positions, cos_sin, kv_data, kv_scale, q_pe, q)
+    if num_pages is None:
+        num_pages = int(kv_data.shape[0])
+    # the stride of an extent of one says nothing
+    st = load().mla_append_rope(
+        _ptr(c_kv), c_kv.stride(0) if n > 1 else 512, _ptr(k_pe), k_pe.stride(0) if n > 1 else 64, n,
+        _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), int(cos_sin.shape[0]), rope_style, _ptr(q_pe),
+        (q_pe.stride(0) if n > 1 else 64 * heads) if heads else 0, (q_pe.stride(1) if heads > 1 else 64) if heads else 0,
+        heads, _ptr(q), _ptr(kv_data), _ptr(kv_scale), kv_dtype, float(global_scale), page_size,
+        int(num_pages), _stream(stream))
+    return _check("mla_append_rope", st, raise_on_error)
+
+
+def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, rope_style: int, kv_data,
+                    kv_scale, cache_dtype: int, q=None, q_out=None, positions=None, stream=None,
+                    raise_on_error: bool = True) -> int:
+    """Append K (rotated) and V heads [n, Hkv, D] to the head pool kv_data uint8 [pages, 2, Hkv, 64, D] with
+    kv_scale float32 [pages, 2, Hkv], and rotate q [n, H, D] into q_out (see qkvp.h). k, v and q may be
+    slices of one projection; request r's tokens are tok_indptr[r] .. tok_indptr[r + 1] - 1 and go behind
+    its kv_len[r] cached ones. cos_sin float32 [max_positions, rot_dim], or None: no rotation."""
+    _need("kv_data", kv_data, (None, 2, None, PAGE_SIZE, None), ("uint8", "int8", "float8_e4m3fn"))
+    pages, heads_kv, dim = int(kv_data.shape[0]), int(kv_data.shape[2]), int(kv_data.shape[4])
+    _need("kv_scale", kv_scale, (pages, 2, heads_kv), ("float32",))
+    n, batch = int(k.shape[0]), int(kv_len.shape[0])
+    k_stride, v_stride = _heads_rows("k", k, heads_kv, dim), _heads_rows("v", v, heads_kv, dim)
+    if int(v.shape[0]) != n:
+        raise ValueError(f"v has {int(v.shape[0])} rows, k has {n}")
+    _need("tok_indptr", tok_indptr, (batch + 1,), ("int32",))
+    _need("kv_len", kv_len, (batch,), ("int32",))
+    _need("kv_indptr", kv_indptr, (batch + 1,), ("int32",))
+    _need("kv_indices", kv_indices, (None,), ("int32",))
+    if cos_sin is not None:
+        _need("cos_sin", cos_sin, (None, None), ("float32",))
+    if positions is not None:
+        _need("positions", positions, (n,), ("int64",))
+    heads, q_stride = 0, 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        heads = int(q_out.shape[1])
+        _need("q_out", q_out, (n, heads, dim), ("bfloat16",))
+        q_stride = _heads_rows("q", q, heads, dim)
+        if int(q.shape[0]) != n:
+            raise ValueError(f"q has {int(q.shape[0])} rows, k has {n}")
+        if heads == 0:
+            q = q_out = None
+    _on_current(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, kv_data, kv_scale, q, q_out, positions)
+    st = load().gqa_append_rope(
+        _ptr(k), k_stride, _ptr(v), v_stride, n, _ptr(tok_indptr), _ptr(kv_len), batch, _ptr(kv_indptr),
+        _ptr(kv_indices), int(kv_indices.numel()), _ptr(positions), _ptr(cos_sin),
+        int(cos_sin.shape[0]) if cos_sin is not None else 0, int(cos_sin.shape[1]) if cos_sin is not None else 0,
+        rope_style, heads_kv, dim, _ptr(kv_data), _ptr(kv_scale), cache_dtype, PAGE_SIZE, pages, _ptr(q),
+        q_stride, heads, _ptr(q_out), _stream(stream))
+    return _check("gqa_append_rope", st, raise_on_error)
+
+
+def gqa_decode_plan(kv_indptr, kv_len, num_heads: int, num_kv_heads: int, head_dim: int, cache_dtype: int,
+                    window: int = 0, sinks: int = 0, num_sms: int = 0, min_splits: int = 0, workspace=None,
+                    page_size: int = PAGE_SIZE, stream=None, raise_on_error: bool = True):
+    """Plan a head-pool decode on the host; with workspace=None only sizes are computed. Returns a gqa_plan."""
+    indptr, lens = _table(kv_indptr, kv_len)
+    plan = gqa_plan()
+    ws = _ptr(workspace)
+    nbytes = int(workspace.numel() * workspace.element_size()) if workspace is not None else 0
+    st = load().gqa_decode_plan(indptr.ctypes.data, lens.ctypes.data, int(lens.shape[0]), num_heads,
+                                num_kv_heads, head_dim, page_size, cache_dtype, window, sinks, num_sms,
+                                min_splits, ws, nbytes, _stream(stream) if ws else None, ctypes.byref(plan))
+    _check("gqa_decode_plan", st, raise_on_error)
+    plan.status = st
+    return plan
+
+
+def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: float, out, lse, workspace,
+                   stream=None, raise_on_error: bool = True) -> int:
+    """Decode one layer over a head pool: q, out bf16 [B, H, D], lse float32 [B, H] or None; kv_data and
+    kv_scale as for gqa_append_rope."""
+    batch, heads, dim, heads_kv = plan.batch, plan.num_heads, plan.head_dim, plan.num_kv_heads
+    _need("q", q, (batch, heads, dim), ("bfloat16",))
+    _need("kv_data", kv_data, (None, 2, heads_kv, PAGE_SIZE, dim), ("uint8", "int8", "float8_e4m3fn"))
+    pages = int(kv_data.shape[0])
+    _need("kv_scale", kv_scale, (pages, 2, heads_kv), ("float32",))
+    _need("kv_indices", kv_indices, (None,), ("int32",))
+    _need("out", out, (batch, heads, dim), ("bfloat16",))
+    if lse is not None:
+        _need("lse", lse, (batch, heads), ("float32",))
+    _on_current(q, kv_data, kv_scale, kv_indices, out, lse, workspace)
+    nbytes = int(workspace.numel() * workspace.element_size())
+    st = load().gqa_decode_run(ctypes.byref(plan), _ptr(q), _ptr(kv_data), _ptr(kv_scale), pages,
+                               _ptr(kv_indices), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
+                               _stream(stream))
+    return _check("gqa_decode_run", st, raise_on_error)
 
 
 def qkvp_encode_f32(x, fmt: int, codes, stream=None, raise_on_error: bool = True) -> int:

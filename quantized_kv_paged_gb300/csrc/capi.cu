@@ -25,8 +25,6 @@ constexpr int kTcSegmentCost = 14;  // pages of work one request start costs the
 // and the one-pass softmax, 119 / 163 / 265 us)
 constexpr int kTmSegmentCost = 14;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 // Pinned host staging for work-table uploads, per device: a small ring of buffers, each with an
 // event recorded after its copy. A copy from pageable memory can hold the calling thread until the
 // stream's earlier work has drained, which serialises a host loop of plan + decode with the GPU;
@@ -42,6 +40,10 @@ struct StageSlot {
 std::mutex g_stage_mutex;
 StageSlot g_stage[kStageDevices][kStageSlots];
 int g_stage_next[kStageDevices] = {};
+
+}  // namespace
+
+namespace qkvp {
 
 // Copies n bytes to the device buffer dst in stream order (never called during stream capture).
 // Pinned staging where it can; a pageable copy if pinned memory is refused (the runtime stages a
@@ -83,6 +85,10 @@ int query_sms() {
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
   return sms;
 }
+
+}  // namespace qkvp
+
+namespace {
 
 bool finite_float(float x) { return std::isfinite(x); }
 

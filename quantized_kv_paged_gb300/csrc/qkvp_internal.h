@@ -131,6 +131,102 @@ struct GatherArgs {
   float g;
 };
 
+// Arguments of mla_append_rope.
+struct MlaAppendArgs {
+  const uint16_t* c_kv;       // bf16 [n][512], row stride c_kv_stride
+  const uint16_t* k_pe;       // bf16 [n][64], row stride k_pe_stride
+  const int64_t* slots;
+  const int64_t* positions;
+  const float* cos_sin;       // [max_pos][64]
+  const uint16_t* q_pe;       // bf16 [n][heads][64], strides q_pe_tok, q_pe_head
+  uint16_t* q;                // bf16 [n][heads][576]
+  uint8_t* kv;
+  uint8_t* kv_scale;
+  int64_t c_kv_stride, k_pe_stride, q_pe_tok, q_pe_head, n, max_pos, num_slots;
+  int heads, style, kv_dtype;
+  float g;
+};
+
+// Arguments of gqa_append_rope.
+struct GqaAppendArgs {
+  const uint16_t* k;          // bf16 [n][kv_heads][dim], row stride k_stride
+  const uint16_t* v;
+  const int32_t* tok_indptr;  // [batch + 1]
+  const int32_t* kv_len;      // [batch]
+  const int32_t* kv_indptr;   // [batch + 1]
+  const int32_t* kv_indices;  // [nnz]
+  const int64_t* positions;   // [n] or null
+  const float* cos_sin;       // [max_pos][rot]
+  const uint16_t* q;          // bf16 [n][heads][dim], row stride q_stride
+  uint16_t* q_out;            // bf16 [n][heads][dim]
+  uint8_t* kv;                // [num_pages][2][kv_heads][64][dim]
+  float* kv_scale;            // [num_pages][2][kv_heads]
+  int64_t k_stride, v_stride, q_stride, n, nnz, max_pos, num_pages;
+  int batch, rot, style, kv_heads, dim, heads, cache_dtype;
+  int per_token;              // one job per token instead of per candidate page (set by the launcher)
+  uint32_t kv_ctas;           // CTAs of the K and V blocks; the query's follow (set by the launcher)
+};
+
+// One piece of the visible pages of one (request, KV head, pass of 16 query heads), processed by one CTA
+// of the head-pool decode. Visible page v of a request is page v of its list below sink_pages, and page
+// win_page + (v - sink_pages) from there on.
+struct GqaSegment {
+  int32_t req, kv_head;
+  int32_t head0, heads;        // first query head and how many (1 to 16)
+  int32_t page0;               // index into kv_indices of the request's first page
+  int32_t len;                 // tokens of the request
+  int32_t sink_pages, win_page;
+  int32_t win_begin, sink_end; // token t is visible if t < sink_end or win_begin <= t < len
+  int32_t page_begin, num_pages;  // visible pages [page_begin, page_begin + num_pages)
+  int32_t partial;             // partial slot, or -1 for a direct write
+  int32_t group_first, group_count;  // the partial slots of all segments of this group
+  int32_t counter;             // the group's arrival counter
+};
+static_assert(sizeof(GqaSegment) == 64, "segment layout");
+
+constexpr uint64_t kGqaMagic = 0x716b76702d677161ull;
+constexpr int kGqaPassHeads = 16;   // query heads of one pass over the pages
+
+struct GqaDecodeArgs {
+  const uint16_t* q;          // bf16 [B][H][D]
+  const uint8_t* kv;
+  const float* kv_scale;
+  int64_t num_pages;
+  const int32_t* kv_indices;
+  const GqaSegment* segs;
+  const int32_t* worker_ptr;  // [num_workers + 1]
+  uint32_t* counters;         // one per split group, zero between runs
+  int* status;
+  float* part_o;              // [num_partials][16][D], normalised
+  float* part_lse;            // [num_partials][16], log2 domain
+  uint16_t* out;              // bf16 [B][H][D]
+  float* lse;                 // [B][H] or null
+  int heads, kv_heads, dim, cache_dtype, num_workers;
+  float scale_log2;           // sm_scale * log2(e)
+};
+
+// Work table of a head-pool plan: segments, worker ranges, then the status word and the groups' counters.
+struct GqaTable {
+  uint64_t segs, wptr, status, counters, bytes;
+};
+inline GqaTable gqa_table(int64_t segments, int64_t workers, int64_t groups) {
+  GqaTable t;
+  t.segs = 0;
+  t.wptr = align_up(static_cast<uint64_t>(segments) * sizeof(GqaSegment));
+  t.status = t.wptr + align_up(static_cast<uint64_t>(workers + 1) * 4);
+  t.counters = t.status + kTableAlign;
+  t.bytes = t.counters + align_up(static_cast<uint64_t>(groups) * 4);
+  return t;
+}
+
+// Copies a work table to the device in stream order, through pinned staging where it can (capi.cu).
+cudaError_t upload_table(void* dst, const void* src, size_t n, cudaStream_t st);
+int query_sms();
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s);
+cudaError_t launch_gqa_append_rope(GqaAppendArgs a, cudaStream_t s);
+cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_gather_fp8(const GatherArgs& a, cudaStream_t s);
 cudaError_t launch_gather_pages_bf16(const uint8_t* pool, int64_t num_pages, const int32_t* ids, int64_t n,
                                      void* out, cudaStream_t s);
