@@ -437,7 +437,8 @@ int gqa_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_st
 typedef struct {
   int32_t batch, num_heads, num_kv_heads, head_dim, page_size, cache_dtype;
   int32_t window, sinks;       /* as given; window 0: every token is visible */
-  int32_t num_workers;         /* CTAs of the decode kernel */
+  int32_t num_workers;         /* independent workers of the decode kernel */
+  int32_t warps_per_worker;    /* warps that share a worker's segments: 4 (a CTA) or 1 */
   int32_t num_segments;        /* (request, KV head, page range) pieces */
   int32_t num_split_groups;    /* (request, KV head) pairs cut into more than one segment */
   int32_t max_group_segments;  /* most segments of one pair */

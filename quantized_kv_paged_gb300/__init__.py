@@ -49,7 +49,7 @@ class qkvp_plan(ctypes.Structure):
 class gqa_plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_heads", "num_kv_heads", "head_dim", "page_size", "cache_dtype", "window", "sinks",
-        "num_workers", "num_segments", "num_split_groups", "max_group_segments", "num_partials",
+        "num_workers", "warps_per_worker", "num_segments", "num_split_groups", "max_group_segments", "num_partials",
         "max_worker_pages", "min_worker_pages")] + [
         ("total_pages", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
         ("workspace_bytes", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64),
@@ -255,35 +255,62 @@ def kv_gather_pages_bf16(kv_data, page_ids, out, num_pages: int | None = None, p
     return _check("kv_gather_pages_bf16", st, raise_on_error)
 
 
-def _need(name: str, t, shape, dtypes, contiguous: bool = True):
-    """Checks a tensor's shape (None: any extent), type (by name) and layout; contiguous False asks only
-    that the last dim is dense."""
-    if tuple(t.shape) != tuple(s if w is None else w for s, w in zip(t.shape, shape)) or t.dim() != len(shape):
-        raise ValueError(f"{name} needs the shape {tuple('*' if w is None else w for w in shape)}, got {tuple(t.shape)}")
-    if str(t.dtype)[6:] not in dtypes:
-        raise ValueError(f"{name} needs one of the types {', '.join(dtypes)}, got {t.dtype}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} needs to be contiguous")
-    elif t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} needs a dense last dimension")
+class _Types:
+    """Types of the tensors that the checked entry points take (torch is imported on the first call)."""
+    ready = False
+
+    @classmethod
+    def get(cls):
+        if not cls.ready:
+            import torch
+            cls.torch = torch
+            cls.bf16, cls.f32, cls.i32, cls.i64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+            cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+            cls.ready = True
+        return cls
 
 
-def _on_current(*tensors):
-    """The launch goes to the current device: tensors elsewhere are refused."""
-    import torch
-    at = torch.cuda.current_device() if torch.cuda.is_available() else None
+def _refuse(name: str, t, shape, dtypes, layout: str):
+    raise ValueError(f"{name} needs the shape {tuple(shape)}, the type {' or '.join(map(str, dtypes))} and {layout}; got "
+                     f"{tuple(t.shape)}, {t.dtype}, strides {t.stride()}")
+
+
+def _dense(name: str, t, shape, dtypes):
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        _refuse(name, t, shape, dtypes, "a contiguous layout")
+
+
+def _rows(name: str, t, shape, dtypes):
+    """Row stride of a tensor whose rows (all dims but the first) are dense. The stride of an extent of one
+    says nothing: such a tensor counts as dense."""
+    stride = t.stride()
+    width, ok = 1, t.dtype in dtypes and t.shape == shape
+    for d in range(len(shape) - 1, 0, -1):
+        ok = ok and (shape[d] <= 1 or stride[d] == width)
+        width *= shape[d]
+    if not ok:
+        _refuse(name, t, shape, dtypes, "dense rows")
+    return stride[0] if shape[0] > 1 else width
+
+
+def _launch_on(stream, tensors):
+    """The stream to launch on. The launch goes to the current device: tensors elsewhere are refused."""
+    torch = _Types.torch
+    at = None
     for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != at):
-            raise ValueError(f"tensors need to be on the current CUDA device ({at}), got one on {t.device}")
+        if t is not None:
+            d = t.get_device()
+            if d != at:
+                if at is not None or d < 0 or d != torch.cuda.current_device():
+                    raise ValueError(f"tensors need to be on the current CUDA device, got one on {t.device}")
+                at = d
+    if stream is None:
+        return torch.cuda.current_stream(at).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _heads_rows(name: str, t, heads, dim):
-    """Row stride of [n, heads, dim] whose heads are dense."""
-    _need(name, t, (None, heads, dim), ("bfloat16",), contiguous=False)
-    if t.shape[0] and t.shape[1] > 1 and t.stride(1) != dim:
-        raise ValueError(f"{name} needs dense heads: stride {dim} between heads, got {t.stride(1)}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: int, kv_data, kv_scale,
@@ -293,32 +320,44 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
     """Append latent rows [c_kv | rotated k_pe] at slot_mapping, quantized, and rotate q_pe [n, H, 64] into
     the last 64 dims of q [n, H, 576] (see qkvp.h). c_kv [n, 512], k_pe [n, 64] and q_pe may be slices with
     their own row strides; cos_sin float32 [max_positions, 64]."""
-    n = int(c_kv.shape[0])
-    _need("c_kv", c_kv, (n, 512), ("bfloat16",), contiguous=False)
-    _need("k_pe", k_pe, (n, 64), ("bfloat16",), contiguous=False)
-    _need("slot_mapping", slot_mapping, (n,), ("int64",))
-    _need("positions", positions, (n,), ("int64",))
-    _need("cos_sin", cos_sin, (None, 64), ("float32",))
-    heads = 0
-    if (q_pe is None) != (q is None):
-        raise ValueError("q_pe and q go together")
-    if q is not None:
-        heads = int(q.shape[1])
-        _need("q", q, (n, heads, LATENT_DIM), ("bfloat16",))
-        _need("q_pe", q_pe, (n, heads, 64), ("bfloat16",), contiguous=False)
+    T = _Types.get()
+    n = c_kv.shape[0]
+    c_stride = _rows("c_kv", c_kv, (n, 512), T.bf16)
+    pe_stride = _rows("k_pe", k_pe, (n, 64), T.bf16)
+    _dense("slot_mapping", slot_mapping, (n,), T.i64)
+    _dense("positions", positions, (n,), T.i64)
+    max_positions = cos_sin.shape[0]
+    _dense("cos_sin", cos_sin, (max_positions, 64), T.f32)
+    heads = tok_stride = head_stride = 0
+    if q is not None or q_pe is not None:
+        if q is None or q_pe is None or q.dim() != 3:
+            raise ValueError("q_pe [n, H, 64] and q [n, H, 576] go together")
+        heads = q.shape[1]
+        _dense("q", q, (n, heads, LATENT_DIM), T.bf16)
+        stride = q_pe.stride()
+        if q_pe.shape != (n, heads, 64) or q_pe.dtype not in T.bf16 or stride[2] != 1:
+            _refuse("q_pe", q_pe, (n, heads, 64), T.bf16, "a dense last dimension")
         if heads == 0:
             q = q_pe = None
-    _on_current(c_kv, k_pe, slot_mapping, positions, cos_sin, kv_data, kv_scale, q_pe, q)
-    if num_pages is None:
-        num_pages = int(kv_data.shape[0])
-    # the stride of an extent of one says nothing
+        else:
+            head_stride = stride[1] if heads > 1 else 64
+            tok_stride = stride[0] if n > 1 else 64
+    on = _launch_on(stream, (c_kv, k_pe, slot_mapping, positions, cos_sin, kv_data, kv_scale, q_pe, q))
     st = load().mla_append_rope(
-        _ptr(c_kv), c_kv.stride(0) if n > 1 else 512, _ptr(k_pe), k_pe.stride(0) if n > 1 else 64, n,
-        _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin), int(cos_sin.shape[0]), rope_style, _ptr(q_pe),
-        (q_pe.stride(0) if n > 1 else 64 * heads) if heads else 0, (q_pe.stride(1) if heads > 1 else 64) if heads else 0,
-        heads, _ptr(q), _ptr(kv_data), _ptr(kv_scale), kv_dtype, float(global_scale), page_size,
-        int(num_pages), _stream(stream))
-    return _check("mla_append_rope", st, raise_on_error)
+        c_kv.data_ptr(), c_stride, k_pe.data_ptr(), pe_stride, n, slot_mapping.data_ptr(), positions.data_ptr(),
+        cos_sin.data_ptr(), max_positions, rope_style, _at(q_pe), tok_stride, head_stride, heads, _at(q),
+        kv_data.data_ptr(), _at(kv_scale), kv_dtype, global_scale, page_size,
+        kv_data.shape[0] if num_pages is None else num_pages, on)
+    return st if st == QKVP_OK else _check("mla_append_rope", st, raise_on_error)
+
+
+def _head_pool(kv_data, kv_scale, T):
+    """(pages, KV heads, head dim) of a head pool."""
+    shape = kv_data.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != PAGE_SIZE or kv_data.dtype not in T.codes or not kv_data.is_contiguous():
+        _refuse("kv_data", kv_data, ("pages", 2, "heads", PAGE_SIZE, "dim"), T.codes, "a contiguous layout")
+    _dense("kv_scale", kv_scale, (shape[0], 2, shape[2]), T.f32)
+    return shape[0], shape[2], shape[4]
 
 
 def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, rope_style: int, kv_data,
@@ -328,40 +367,37 @@ def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, ro
     kv_scale float32 [pages, 2, Hkv], and rotate q [n, H, D] into q_out (see qkvp.h). k, v and q may be
     slices of one projection; request r's tokens are tok_indptr[r] .. tok_indptr[r + 1] - 1 and go behind
     its kv_len[r] cached ones. cos_sin float32 [max_positions, rot_dim], or None: no rotation."""
-    _need("kv_data", kv_data, (None, 2, None, PAGE_SIZE, None), ("uint8", "int8", "float8_e4m3fn"))
-    pages, heads_kv, dim = int(kv_data.shape[0]), int(kv_data.shape[2]), int(kv_data.shape[4])
-    _need("kv_scale", kv_scale, (pages, 2, heads_kv), ("float32",))
-    n, batch = int(k.shape[0]), int(kv_len.shape[0])
-    k_stride, v_stride = _heads_rows("k", k, heads_kv, dim), _heads_rows("v", v, heads_kv, dim)
-    if int(v.shape[0]) != n:
-        raise ValueError(f"v has {int(v.shape[0])} rows, k has {n}")
-    _need("tok_indptr", tok_indptr, (batch + 1,), ("int32",))
-    _need("kv_len", kv_len, (batch,), ("int32",))
-    _need("kv_indptr", kv_indptr, (batch + 1,), ("int32",))
-    _need("kv_indices", kv_indices, (None,), ("int32",))
+    T = _Types.get()
+    pages, heads_kv, dim = _head_pool(kv_data, kv_scale, T)
+    n, batch, nnz = k.shape[0], kv_len.shape[0], kv_indices.shape[0]
+    k_stride, v_stride = _rows("k", k, (n, heads_kv, dim), T.bf16), _rows("v", v, (n, heads_kv, dim), T.bf16)
+    _dense("tok_indptr", tok_indptr, (batch + 1,), T.i32)
+    _dense("kv_len", kv_len, (batch,), T.i32)
+    _dense("kv_indptr", kv_indptr, (batch + 1,), T.i32)
+    _dense("kv_indices", kv_indices, (nnz,), T.i32)
+    max_positions = rot = heads = q_stride = 0
     if cos_sin is not None:
-        _need("cos_sin", cos_sin, (None, None), ("float32",))
+        if cos_sin.dim() != 2:
+            _refuse("cos_sin", cos_sin, ("positions", "rot_dim"), T.f32, "a contiguous layout")
+        max_positions, rot = cos_sin.shape
+        _dense("cos_sin", cos_sin, (max_positions, rot), T.f32)
     if positions is not None:
-        _need("positions", positions, (n,), ("int64",))
-    heads, q_stride = 0, 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
-        heads = int(q_out.shape[1])
-        _need("q_out", q_out, (n, heads, dim), ("bfloat16",))
-        q_stride = _heads_rows("q", q, heads, dim)
-        if int(q.shape[0]) != n:
-            raise ValueError(f"q has {int(q.shape[0])} rows, k has {n}")
+        _dense("positions", positions, (n,), T.i64)
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q_out.dim() != 3:
+            raise ValueError("q and q_out [n, H, D] go together")
+        heads = q_out.shape[1]
+        _dense("q_out", q_out, (n, heads, dim), T.bf16)
+        q_stride = _rows("q", q, (n, heads, dim), T.bf16)
         if heads == 0:
             q = q_out = None
-    _on_current(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, kv_data, kv_scale, q, q_out, positions)
+    on = _launch_on(stream, (k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, kv_data, kv_scale, q, q_out, positions))
     st = load().gqa_append_rope(
-        _ptr(k), k_stride, _ptr(v), v_stride, n, _ptr(tok_indptr), _ptr(kv_len), batch, _ptr(kv_indptr),
-        _ptr(kv_indices), int(kv_indices.numel()), _ptr(positions), _ptr(cos_sin),
-        int(cos_sin.shape[0]) if cos_sin is not None else 0, int(cos_sin.shape[1]) if cos_sin is not None else 0,
-        rope_style, heads_kv, dim, _ptr(kv_data), _ptr(kv_scale), cache_dtype, PAGE_SIZE, pages, _ptr(q),
-        q_stride, heads, _ptr(q_out), _stream(stream))
-    return _check("gqa_append_rope", st, raise_on_error)
+        k.data_ptr(), k_stride, v.data_ptr(), v_stride, n, tok_indptr.data_ptr(), kv_len.data_ptr(), batch,
+        kv_indptr.data_ptr(), kv_indices.data_ptr(), nnz, _at(positions), _at(cos_sin), max_positions, rot,
+        rope_style, heads_kv, dim, kv_data.data_ptr(), kv_scale.data_ptr(), cache_dtype, PAGE_SIZE, pages, _at(q),
+        q_stride, heads, _at(q_out), on)
+    return st if st == QKVP_OK else _check("gqa_append_rope", st, raise_on_error)
 
 
 def gqa_decode_plan(kv_indptr, kv_len, num_heads: int, num_kv_heads: int, head_dim: int, cache_dtype: int,
@@ -384,21 +420,21 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
                    stream=None, raise_on_error: bool = True) -> int:
     """Decode one layer over a head pool: q, out bf16 [B, H, D], lse float32 [B, H] or None; kv_data and
     kv_scale as for gqa_append_rope."""
-    batch, heads, dim, heads_kv = plan.batch, plan.num_heads, plan.head_dim, plan.num_kv_heads
-    _need("q", q, (batch, heads, dim), ("bfloat16",))
-    _need("kv_data", kv_data, (None, 2, heads_kv, PAGE_SIZE, dim), ("uint8", "int8", "float8_e4m3fn"))
-    pages = int(kv_data.shape[0])
-    _need("kv_scale", kv_scale, (pages, 2, heads_kv), ("float32",))
-    _need("kv_indices", kv_indices, (None,), ("int32",))
-    _need("out", out, (batch, heads, dim), ("bfloat16",))
+    T = _Types.get()
+    batch, heads, dim = plan.batch, plan.num_heads, plan.head_dim
+    _dense("q", q, (batch, heads, dim), T.bf16)
+    _dense("out", out, (batch, heads, dim), T.bf16)
+    pages, heads_kv, kv_dim = _head_pool(kv_data, kv_scale, T)
+    if heads_kv != plan.num_kv_heads or kv_dim != dim:
+        raise ValueError(f"kv_data has {heads_kv} heads of {kv_dim}, the plan {plan.num_kv_heads} of {dim}")
+    _dense("kv_indices", kv_indices, (kv_indices.shape[0],), T.i32)
     if lse is not None:
-        _need("lse", lse, (batch, heads), ("float32",))
-    _on_current(q, kv_data, kv_scale, kv_indices, out, lse, workspace)
-    nbytes = int(workspace.numel() * workspace.element_size())
-    st = load().gqa_decode_run(ctypes.byref(plan), _ptr(q), _ptr(kv_data), _ptr(kv_scale), pages,
-                               _ptr(kv_indices), float(sm_scale), _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
-                               _stream(stream))
-    return _check("gqa_decode_run", st, raise_on_error)
+        _dense("lse", lse, (batch, heads), T.f32)
+    on = _launch_on(stream, (q, kv_data, kv_scale, kv_indices, out, lse, workspace))
+    st = load().gqa_decode_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
+                               kv_indices.data_ptr(), sm_scale, out.data_ptr(), _at(lse), workspace.data_ptr(),
+                               workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("gqa_decode_run", st, raise_on_error)
 
 
 def qkvp_encode_f32(x, fmt: int, codes, stream=None, raise_on_error: bool = True) -> int:

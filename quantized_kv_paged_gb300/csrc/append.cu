@@ -63,7 +63,10 @@ __global__ void append_fp8_kernel(const void* __restrict__ src, int src_dtype, i
   }
   float x[16];
   load16(src, src_dtype, tok, blk, x);
-  *reinterpret_cast<uint4*>(dst) = dev::encode_e4m3_plain(x);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i / 4] |= dev::encode_e4m3(x[i]) << (8 * (i % 4));
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __global__ void append_nvfp4_kernel(const void* __restrict__ src, int src_dtype, int64_t n,
@@ -77,9 +80,27 @@ __global__ void append_nvfp4_kernel(const void* __restrict__ src, int src_dtype,
   if (slot < 0 || slot >= num_slots) return;
   float x[16];
   load16(src, src_dtype, tok, blk, x);
-  uint32_t s8;
-  const uint2 codes = dev::encode_nvfp4_block(x, g, s8);
-  *reinterpret_cast<uint2*>(data + slot * kPacked + blk * 8) = codes;
+  // amax over the block; any NaN makes it NaN
+  float amax = 0.0f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    nan |= (x[i] != x[i]);
+    amax = fmaxf(amax, fabsf(x[i]));
+  }
+  if (nan) amax = __uint_as_float(0x7FC00000u);
+  const float s = __fdiv_rn(amax, __fmul_rn(6.0f, g));
+  const uint32_t s8 = dev::encode_e4m3(s);
+  const float sd = __fmul_rn(dev::e4m3_to_float(s8), g);
+  uint32_t w[2] = {0, 0};
+  if (sd != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t c = dev::encode_e2m1(__fdiv_rn(x[i], sd));
+      w[i / 8] |= c << (4 * (i % 8));     // element 2k -> low nibble of byte k
+    }
+  }
+  *reinterpret_cast<uint2*>(data + slot * kPacked + blk * 8) = make_uint2(w[0], w[1]);
   scale[slot * kScales + blk] = static_cast<uint8_t>(s8);
 }
 
@@ -113,8 +134,15 @@ __global__ void append_fp8pt_kernel(const void* __restrict__ src, int src_dtype,
   const float sc = any_nan ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
   uint8_t* page = pool + (slot / kPage) * kPtPageBytes;
   uint8_t* row = page + (slot % kPage) * kLatent;
-  *reinterpret_cast<uint4*>(row + lane * 16) = dev::encode_e4m3_scaled(x0, sc);
-  if (lane < kExtra) *reinterpret_cast<uint4*>(row + (32 + lane) * 16) = dev::encode_e4m3_scaled(x1, sc);
+  auto encode16 = [&](const float (&x)[16], int blk) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i / 4] |= dev::encode_e4m3(sc == 0.0f ? x[i] : __fdiv_rn(x[i], sc)) << (8 * (i % 4));
+    *reinterpret_cast<uint4*>(row + blk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  };
+  encode16(x0, lane);
+  if (lane < kExtra) encode16(x1, 32 + lane);
   if (lane == 0) *reinterpret_cast<float*>(page + kPtScaleOff + (slot % kPage) * 4) = sc;
 }
 

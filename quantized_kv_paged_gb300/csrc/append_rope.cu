@@ -5,9 +5,10 @@
 // cost no precision. Every product and sum is one FP32 rounding (no contraction), which makes the codes
 // reproducible bit for bit by any other implementation of the same formula.
 //
-// Both kernels are streams: BF16 in, 8-bit codes (and BF16 queries) out, each byte once. A lane holds 16
-// bytes = 8 dims of a head; where a pair's halves lie r/2 dims apart its partner's 8 dims come from the
-// lane r/16 further on by shuffle, so no element is loaded twice.
+// Both kernels are streams: BF16 in, 8-bit codes (and BF16 queries) out, each byte once. A lane holds 8
+// dims of a head as two quads that rotate together: dims 4 l .. and r/2 + 4 l .. (HALVES), or 8 l .. and
+// 8 l + 4 .. (PAIRS and what is not rotated). Either way it needs 4 cosines and 4 sines and nothing from
+// another lane.
 #include <algorithm>
 #include <cstdint>
 
@@ -18,8 +19,7 @@ namespace qkvp {
 namespace {
 
 constexpr int kRope = kLatent - kDv;    // 64 rope dims of the latent
-constexpr int kBlocks = kLatent / 16;   // 36 blocks of 16 elements per latent row
-constexpr int kFull = 0xffffffff;
+constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ float rot_a(float a, float b, float c, float s) {
   return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
@@ -28,49 +28,63 @@ __device__ __forceinline__ float rot_b(float a, float b, float c, float s) {
   return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-__device__ __forceinline__ uint4 shfl4(uint4 v, int src) {
-  return make_uint4(__shfl_sync(kFull, v.x, src), __shfl_sync(kFull, v.y, src), __shfl_sync(kFull, v.z, src),
-                    __shfl_sync(kFull, v.w, src));
-}
-
-// cos and sin of the pairs that 8 consecutive dims (chunk c8 of a head, dims 8 c8 ..) belong to. PAIRS:
-// four pairs, HALVES: eight.
-struct Turn {
-  float c[8], s[8];
+// Where the two quads of lane l of a head start. `apart`: not next to one another.
+struct Quads {
+  int a, b;
+  bool turned, apart;
+  __device__ Quads(int l, int rot, int style) : turned(8 * l < rot), apart(turned && style == QKVP_ROPE_HALVES) {
+    a = apart ? 4 * l : 8 * l;
+    b = apart ? rot / 2 + 4 * l : 8 * l + 4;
+  }
 };
-__device__ __forceinline__ void load_turn(Turn& t, const float* row, int rot, int c8, int style) {
-  if (style == QKVP_ROPE_PAIRS) {
-    const float4 c = *reinterpret_cast<const float4*>(row + 4 * c8), s = *reinterpret_cast<const float4*>(row + rot / 2 + 4 * c8);
-    t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
-    t.s[0] = s.x; t.s[1] = s.y; t.s[2] = s.z; t.s[3] = s.w;
+
+__device__ __forceinline__ uint4 load_quads(const uint16_t* head, const Quads& q) {
+  if (!q.apart) return *reinterpret_cast<const uint4*>(head + q.a);
+  const uint2 x = *reinterpret_cast<const uint2*>(head + q.a), y = *reinterpret_cast<const uint2*>(head + q.b);
+  return make_uint4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ void store_quads(uint16_t* head, const Quads& q, uint4 v) {
+  if (!q.apart) {
+    *reinterpret_cast<uint4*>(head + q.a) = v;
   } else {
-    const int i = 8 * c8 < rot / 2 ? 8 * c8 : 8 * c8 - rot / 2;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 c = *reinterpret_cast<const float4*>(row + i + 4 * k), s = *reinterpret_cast<const float4*>(row + rot / 2 + i + 4 * k);
-      t.c[4 * k] = c.x; t.c[4 * k + 1] = c.y; t.c[4 * k + 2] = c.z; t.c[4 * k + 3] = c.w;
-      t.s[4 * k] = s.x; t.s[4 * k + 1] = s.y; t.s[4 * k + 2] = s.z; t.s[4 * k + 3] = s.w;
-    }
+    *reinterpret_cast<uint2*>(head + q.a) = make_uint2(v.x, v.y);
+    *reinterpret_cast<uint2*>(head + q.b) = make_uint2(v.z, v.w);
+  }
+}
+// The same two quads as codes, one byte each.
+__device__ __forceinline__ void store_codes(uint8_t* head, const Quads& q, uint2 v) {
+  if (!q.apart) {
+    *reinterpret_cast<uint2*>(head + q.a) = v;
+  } else {
+    *reinterpret_cast<uint32_t*>(head + q.a) = v.x;
+    *reinterpret_cast<uint32_t*>(head + q.b) = v.y;
   }
 }
 
-// Rotates the 8 dims x of chunk c8; `other` holds the partner chunk's 8 dims (HALVES only).
-__device__ __forceinline__ void turn8(float (&x)[8], const float (&other)[8], const Turn& t, int rot, int c8, int style) {
-  if (style == QKVP_ROPE_PAIRS) {
+// Lane l's cosines and sines from the row of a position, and the rotation of its quads.
+struct Turn {
+  float4 c, s;
+  __device__ void load(const float* row, int rot, int l) {
+    c = *reinterpret_cast<const float4*>(row + 4 * l);
+    s = *reinterpret_cast<const float4*>(row + rot / 2 + 4 * l);
+  }
+  __device__ void apply(float (&x)[8], int style) const {
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    const bool halves = style == QKVP_ROPE_HALVES;       // pair i of the lane: (i, 4 + i), or (2 i, 2 i + 1)
+    float ra[4], rb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = rot_a(a, b, t.c[i], t.s[i]);
-      x[2 * i + 1] = rot_b(a, b, t.c[i], t.s[i]);
+      const float p = halves ? x[i] : x[2 * i], q = halves ? x[4 + i] : x[2 * i + 1];
+      ra[i] = rot_a(p, q, cc[i], ss[i]);
+      rb[i] = rot_b(p, q, cc[i], ss[i]);
     }
-  } else if (8 * c8 < rot / 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = rot_a(x[i], other[i], t.c[i], t.s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = rot_b(other[i], x[i], t.c[i], t.s[i]);
+    for (int i = 0; i < 4; ++i) {
+      x[i] = halves ? ra[i] : i % 2 ? rb[i / 2] : ra[i / 2];
+      x[4 + i] = halves ? rb[i] : i % 2 ? rb[2 + i / 2] : ra[2 + i / 2];
+    }
   }
-}
+};
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(dev::pack_bf16x2(x[0], x[1]), dev::pack_bf16x2(x[2], x[3]), dev::pack_bf16x2(x[4], x[5]),
@@ -78,186 +92,20 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Latent rows. One warp per token, or per (token, 16 query heads): a decode step of 44 tokens and 128
-// heads is 44 + 352 warps, enough to reach every SM; with a warp for all 128 heads it was 44 + 44.
+// x / s for many x and one s, correctly rounded, without a division each: Markstein's correction of a
+// quotient by fused multiply-adds (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). r is 1 / s correctly rounded; q0 = x r is off by at most 2 steps, one
+// correction brings it within one, and a correction from there rounds as the division does. The
+// remainders are exact when nothing in them underflows: s in [2^-60, 2^60] and finite x, where a quotient
+// that does not round to the code 0 comes from an x of 2^-72 and more. The signs are arranged so that -0
+// stays -0. Equal to the division on 1.9e10 pairs on GB300, in five operations: with a division per element
+// the chunked append of 15,500 tokens (8 KV heads, 32 query heads of 128) was issue-bound, 95 us.
 // ------------------------------------------------------------------------------------------------
-constexpr int kLatentThreads = 128;
-constexpr int kQHeads = 16;             // query heads per warp
-constexpr int kRopeLanes = kRope / 8;   // 8 lanes hold one head's 64 dims
-
-__global__ void __launch_bounds__(kLatentThreads) mla_append_rope_kernel(const MlaAppendArgs a) {
-  const int64_t job = (static_cast<int64_t>(blockIdx.x) * kLatentThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int head_jobs = (a.heads + kQHeads - 1) / kQHeads;
-  if (job >= a.n * (1 + head_jobs)) return;       // the whole warp
-  if (job >= a.n) {
-    // query heads h0 .. h0 + 15 of one token, four at a time, 8 lanes each
-    const int64_t tok = (job - a.n) / head_jobs;
-    const int h0 = static_cast<int>((job - a.n) % head_jobs) * kQHeads;
-    const int64_t pos = a.positions[tok];
-    if (pos < 0 || pos >= a.max_pos) return;
-    const int c8 = lane % kRopeLanes, hl = lane / kRopeLanes;
-    const uint16_t* src = a.q_pe + tok * a.q_pe_tok + c8 * 8;
-    uint4 raw[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int h = h0 + 4 * k + hl;
-      raw[k] = h < a.heads ? *reinterpret_cast<const uint4*>(src + h * a.q_pe_head) : make_uint4(0, 0, 0, 0);
-    }
-    Turn t;
-    load_turn(t, a.cos_sin + pos * kRope, kRope, c8, a.style);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int h = h0 + 4 * k + hl;
-      const uint4 far = shfl4(raw[k], lane ^ (kRopeLanes / 2));
-      float x[8], o[8];
-      dev::bf16x8_to_float(raw[k], x);
-      dev::bf16x8_to_float(far, o);
-      turn8(x, o, t, kRope, c8, a.style);
-      if (h < a.heads) *reinterpret_cast<uint4*>(a.q + (tok * a.heads + h) * kLatent + kDv + c8 * 8) = pack8(x);
-    }
-    return;
-  }
-  // the latent row: lane l quantizes block l of c_kv, lanes 0..3 also the rotated blocks 32..35
-  const int64_t tok = job;
-  const int64_t slot = a.slots[tok], pos = a.positions[tok];
-  if (slot < 0 || slot >= a.num_slots || pos < 0 || pos >= a.max_pos) return;
-  constexpr int kExtra = kBlocks - 32;
-  float x0[16], x1[16];
-  {
-    const uint4* p = reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + lane * 16);
-    dev::bf16x8_to_float(p[0], x0);
-    dev::bf16x8_to_float(p[1], x0 + 8);
-  }
-  uint4 pe[2] = {};
-  if (lane < kExtra) {
-    const uint4* p = reinterpret_cast<const uint4*>(a.k_pe + tok * a.k_pe_stride + lane * 16);
-    pe[0] = p[0];
-    pe[1] = p[1];
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint4 far = shfl4(pe[k], lane ^ (kExtra / 2));      // 32 dims further
-    if (lane < kExtra) {
-      const int c8 = 2 * lane + k;
-      float x[8], o[8];
-      Turn t;
-      load_turn(t, a.cos_sin + pos * kRope, kRope, c8, a.style);
-      dev::bf16x8_to_float(pe[k], x);
-      dev::bf16x8_to_float(far, o);
-      turn8(x, o, t, kRope, c8, a.style);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x1[8 * k + i] = x[i];
-    }
-  }
-  if (a.kv_dtype == KV_NVFP4) {
-    uint32_t s8;
-    const uint2 w = dev::encode_nvfp4_block(x0, a.g, s8);
-    *reinterpret_cast<uint2*>(a.kv + slot * kPacked + lane * 8) = w;
-    a.kv_scale[slot * kScales + lane] = static_cast<uint8_t>(s8);
-    if (lane < kExtra) {
-      const uint2 w1 = dev::encode_nvfp4_block(x1, a.g, s8);
-      *reinterpret_cast<uint2*>(a.kv + slot * kPacked + (32 + lane) * 8) = w1;
-      a.kv_scale[slot * kScales + 32 + lane] = static_cast<uint8_t>(s8);
-    }
-  } else if (a.kv_dtype == KV_FP8) {
-    uint8_t* row = a.kv + slot * kLatent;
-    *reinterpret_cast<uint4*>(row + lane * 16) = dev::encode_e4m3_plain(x0);
-    if (lane < kExtra) *reinterpret_cast<uint4*>(row + (32 + lane) * 16) = dev::encode_e4m3_plain(x1);
-  } else {
-    float amax = 0.0f;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      nan |= (x0[i] != x0[i]);
-      amax = fmaxf(amax, fabsf(x0[i]));
-      if (lane < kExtra) {
-        nan |= (x1[i] != x1[i]);
-        amax = fmaxf(amax, fabsf(x1[i]));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-    const float sc = __any_sync(kFull, nan) ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
-    uint8_t* page = a.kv + (slot / kPage) * kPtPageBytes;
-    uint8_t* row = page + (slot % kPage) * kLatent;
-    *reinterpret_cast<uint4*>(row + lane * 16) = dev::encode_e4m3_scaled(x0, sc);
-    if (lane < kExtra) *reinterpret_cast<uint4*>(row + (32 + lane) * 16) = dev::encode_e4m3_scaled(x1, sc);
-    if (lane == 0) *reinterpret_cast<float*>(page + kPtScaleOff + (slot % kPage) * 4) = sc;
-  }
-}
-
-// ------------------------------------------------------------------------------------------------
-// K and V heads. One CTA per (page that the call writes, K or V, head): the block's scale needs the
-// amax of all the page's new tokens, and its older codes change with it, so a block has one owner and
-// no atomics. The CTA keeps the new elements in registers between the amax and the codes.
-//
-// Which pages are written is known on the device only. The launch has, for request r, floor(n_r / 64) + 2
-// candidates, the most pages that n_r tokens can touch: job c belongs to the last request with
-// tok_indptr[r] / 64 + 2 r <= c. With few tokens there is a job per token instead, and the first token of
-// each page does the work. Idle jobs leave after the search.
-// ------------------------------------------------------------------------------------------------
-constexpr int kHeadThreads = 256;
-
-// The largest r in [0, batch) with f(r) <= c for a non-decreasing f with f(0) <= c (0 if there is none):
-// 32 probes at a time, so two dependent loads for up to 1,024 requests.
-template <class F>
-__device__ __forceinline__ int last_at_most(int batch, int64_t c, F f) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = batch;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int off = lane * step;
-    const unsigned hit = __ballot_sync(kFull, off < n && f(lo + off) <= c);
-    const int k = max(__popc(hit) - 1, 0) * step;
-    lo += k;
-    n = min(step, n - k);
-  }
-  return lo;
-}
-
-struct Place {
-  int64_t page;        // pool page, -1: none
-  int64_t tok, pos;    // source row and cache position of the token at offset `first`
-  int first, last;     // the page's new tokens are the offsets [first, last)
-};
-
-// The clipped token range of request r.
-__device__ __forceinline__ void request_tokens(const GqaAppendArgs& a, int r, int64_t& t0, int64_t& t1) {
-  t0 = min(max(static_cast<int64_t>(a.tok_indptr[r]), int64_t(0)), a.n);
-  t1 = min(max(static_cast<int64_t>(a.tok_indptr[r + 1]), t0), a.n);
-}
-
-__device__ __forceinline__ Place find_place(const GqaAppendArgs& a, int64_t job) {
-  Place p{-1, 0, 0, 0, 0};
-  const int32_t* tp = a.tok_indptr;
-  const int r = a.per_token ? last_at_most(a.batch, job, [tp](int i) { return static_cast<int64_t>(tp[i]); })
-                            : last_at_most(a.batch, job, [tp](int i) { return static_cast<int64_t>(tp[i] / kPage) + 2ll * i; });
-  int64_t t0, t1;
-  request_tokens(a, r, t0, t1);
-  const int64_t held = a.kv_len[r];
-  const int64_t p0 = a.kv_indptr[r], p1 = a.kv_indptr[r + 1];
-  if (held < 0 || t0 >= t1) return p;
-  int64_t local;                         // page of the request
-  if (a.per_token) {
-    if (job < t0 || job >= t1) return p;
-    const int64_t pos = held + job - t0;
-    if (job != t0 && pos % kPage != 0) return p;
-    local = pos / kPage;
-  } else {
-    local = held / kPage + (job - (static_cast<int64_t>(tp[r] / kPage) + 2ll * r));
-  }
-  const int64_t lo = max(held, local * kPage), hi = min(held + t1 - t0, (local + 1) * kPage);
-  const int64_t e = p0 + local;
-  if (lo >= hi || p0 < 0 || e < p0 || e >= p1 || e >= a.nnz) return p;
-  const int64_t page = a.kv_indices[e];
-  if (page < 0 || page >= a.num_pages) return p;
-  p.page = page;
-  p.tok = t0 + lo - held;
-  p.pos = lo;
-  p.first = static_cast<int>(lo - local * kPage);
-  p.last = static_cast<int>(hi - local * kPage);
-  return p;
+__device__ __forceinline__ bool divides_fast(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q0 = __fmul_rn(x, r);
+  const float q1 = __fmaf_rn(-__fmaf_rn(q0, s, -x), r, q0);
+  return __fmaf_rn(-__fmaf_rn(q1, s, -x), r, q1);
 }
 
 template <bool E4M3>
@@ -272,108 +120,355 @@ __device__ __forceinline__ float decode8(uint32_t c) {
   return static_cast<float>(static_cast<int8_t>(c & 0xFFu));
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kHeadThreads) gqa_append_rope_kernel(const GqaAppendArgs a) {
-  constexpr int kLanes = D / 8;                    // lanes of one token's head
-  constexpr int kTok = kHeadThreads / kLanes;      // tokens of one pass over the CTA
-  constexpr int kPasses = kPage / kTok;
-  const int lane = threadIdx.x & 31, c8 = threadIdx.x % kLanes;
-  const int partner = (lane & ~(kLanes - 1)) | ((c8 + (8 * c8 < a.rot / 2 ? a.rot / 16 : -(a.rot / 16))) & (kLanes - 1));
-  const bool turned = 8 * c8 < a.rot;
-  if (blockIdx.x >= a.kv_ctas) {
-    // query heads: a warp per (token, 4 passes of heads)
-    constexpr int kH = 32 / kLanes;                // heads of one pass over the warp
-    const int64_t job = ((static_cast<int64_t>(blockIdx.x) - a.kv_ctas) * kHeadThreads + threadIdx.x) >> 5;
-    const int head_jobs = (a.heads + 4 * kH - 1) / (4 * kH);
-    if (job >= a.n * head_jobs) return;
-    const int64_t tok = job / head_jobs;
-    const int h0 = static_cast<int>(job % head_jobs) * 4 * kH + lane / kLanes;
-    const int32_t* tp = a.tok_indptr;
-    const int r = last_at_most(a.batch, tok, [tp](int i) { return static_cast<int64_t>(tp[i]); });
-    int64_t t0, t1;
-    request_tokens(a, r, t0, t1);
-    if (tok < t0 || tok >= t1) return;             // padding
-    const int64_t pos = a.positions ? a.positions[tok] : a.kv_len[r] + tok - t0;
-    if (a.rot > 0 && (pos < 0 || pos >= a.max_pos)) return;
-    uint4 raw[4];
+// Four and eight FP32 -> E4M3 two at a time: nearest even, saturating, NaN to 0x7F and the sign of a zero kept, the
+// same byte as encode_e4m3 for every one of the 2^32 inputs (compared on GB300).
+__device__ __forceinline__ uint32_t encode_e4m3x4(const float* y) {
+  return dev::f32x2_to_e4m3x2(y[0], y[1]) | dev::f32x2_to_e4m3x2(y[2], y[3]) << 16;
+}
+__device__ __forceinline__ uint2 encode_e4m3x8(const float (&x)[8]) { return make_uint2(encode_e4m3x4(x), encode_e4m3x4(x + 4)); }
+
+// Codes of 8 values over the scale s: round(x / s), or round(x) where s is 0. fast: every x is finite and
+// divides_fast(s), so |x / s| is at most 448 (127) up to its rounding, and the conversions below need no
+// care for infinities (the corrected quotient of one is NaN). INT8: adding 1.5 * 2^23 leaves the nearest whole number, ties to even, in the
+// low byte.
+template <bool E4M3>
+__device__ __forceinline__ uint2 encode_scaled(const float (&x)[8], float s, float r, bool fast) {
+  uint32_t w[2] = {0, 0};
+  if (fast) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int h = h0 + k * kH;
-      raw[k] = h < a.heads ? *reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + h * D + c8 * 8) : make_uint4(0, 0, 0, 0);
-    }
-    Turn t;
-    if (turned) load_turn(t, a.cos_sin + pos * a.rot, a.rot, c8, a.style);
+    for (int i = 0; i < 2; ++i) {
+      float y[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int h = h0 + k * kH;
-      const uint4 far = shfl4(raw[k], partner);
-      uint4 res = raw[k];
-      if (turned) {
-        float x[8], o[8];
-        dev::bf16x8_to_float(raw[k], x);
-        dev::bf16x8_to_float(far, o);
-        turn8(x, o, t, a.rot, c8, a.style);
-        res = pack8(x);
+      for (int k = 0; k < 4; ++k) y[k] = quotient(x[4 * i + k], s, r);
+      if constexpr (E4M3) {
+        w[i] = encode_e4m3x4(y);
+      } else {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = __float_as_uint(__fadd_rn(y[k], 12582912.0f));
+        w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
       }
-      if (h < a.heads) *reinterpret_cast<uint4*>(a.q_out + (tok * a.heads + h) * D + c8 * 8) = res;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i / 4] |= encode8<E4M3>(s == 0.0f ? x[i] : __fdiv_rn(x[i], s)) << (8 * (i % 4));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Latent rows. One warp per token, or per (token, 16 query heads): a decode step of 44 tokens and 128
+// heads is 44 + 352 warps, enough to reach every SM. Everything that does not depend on the position is
+// loaded before it is known.
+// ------------------------------------------------------------------------------------------------
+constexpr int kLatentThreads = 128;
+constexpr int kQHeads = 16;             // query heads per warp
+constexpr int kRopeLanes = kRope / 8;   // 8 lanes hold one head's 64 dims
+
+// NVFP4 codes of 4 values (two bytes) under a block's E4M3 scale: the formulas of kv_append_quant.
+__device__ __forceinline__ uint32_t nvfp4_scale(float amax, float g) { return dev::encode_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, g))); }
+__device__ __forceinline__ uint32_t nvfp4_quad(const float* x, uint32_t s8, float g) {
+  const float sd = __fmul_rn(dev::e4m3_to_float(s8), g);
+  uint32_t w = 0;
+  if (sd != 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= dev::encode_e2m1(__fdiv_rn(x[i], sd)) << (4 * i);
+  }
+  return w;
+}
+__device__ __forceinline__ float amax4(const float* x) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = dev::max_nan(m, fabsf(x[i]));
+  return m;
+}
+
+// The lane's two quads of the latent row, at dims qa and qb, as NVFP4. Next to one another they are half a block
+// of 16 and lane ^ 1 holds the other half; apart each is a quarter of its block, with lanes ^ 1, ^ 2, ^ 3.
+__device__ __forceinline__ void store_nvfp4(const MlaAppendArgs& a, int64_t slot, const float (&x)[8], int qa, int qb, bool apart, bool writes) {
+  float ma = amax4(x), mb = amax4(x + 4);
+  if (!apart) ma = mb = dev::max_nan(ma, mb);
+  ma = dev::max_nan(ma, __shfl_xor_sync(kFull, ma, 1));
+  mb = dev::max_nan(mb, __shfl_xor_sync(kFull, mb, 1));
+  const float ma2 = dev::max_nan(ma, __shfl_xor_sync(kFull, ma, 2)), mb2 = dev::max_nan(mb, __shfl_xor_sync(kFull, mb, 2));
+  if (!writes) return;
+  const uint32_t sa = nvfp4_scale(apart ? ma2 : ma, a.g), sb = apart ? nvfp4_scale(mb2, a.g) : sa;
+  uint8_t* row = a.kv + slot * kPacked;
+  *reinterpret_cast<uint16_t*>(row + qa / 2) = static_cast<uint16_t>(nvfp4_quad(x, sa, a.g));
+  *reinterpret_cast<uint16_t*>(row + qb / 2) = static_cast<uint16_t>(nvfp4_quad(x + 4, sb, a.g));
+  if (qa % 16 == 0) a.kv_scale[slot * kScales + qa / 16] = static_cast<uint8_t>(sa);
+  if (apart && qb % 16 == 0) a.kv_scale[slot * kScales + qb / 16] = static_cast<uint8_t>(sb);
+}
+
+__global__ void __launch_bounds__(kLatentThreads) mla_append_rope_kernel(const MlaAppendArgs a) {
+  const int64_t job = (static_cast<int64_t>(blockIdx.x) * kLatentThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const int head_jobs = (a.heads + kQHeads - 1) / kQHeads;
+  if (job >= a.n * (1 + head_jobs)) return;       // the whole warp
+  const Quads quads(lane % kRopeLanes, kRope, a.style);
+  if (job >= a.n) {
+    // query heads h0 .. h0 + 15 of one token, four at a time, 8 lanes each
+    const int64_t tok = (job - a.n) / head_jobs;
+    const int h0 = static_cast<int>((job - a.n) % head_jobs) * kQHeads + lane / kRopeLanes;
+    const int64_t pos = a.positions[tok];
+    uint4 raw[kQHeads / 4];
+#pragma unroll
+    for (int k = 0; k < kQHeads / 4; ++k)
+      raw[k] = h0 + 4 * k < a.heads ? load_quads(a.q_pe + tok * a.q_pe_tok + (h0 + 4 * k) * a.q_pe_head, quads) : make_uint4(0, 0, 0, 0);
+    if (pos < 0 || pos >= a.max_pos) return;
+    Turn t;
+    t.load(a.cos_sin + pos * kRope, kRope, lane % kRopeLanes);
+#pragma unroll
+    for (int k = 0; k < kQHeads / 4; ++k) {
+      if (h0 + 4 * k >= a.heads) continue;
+      float x[8];
+      dev::bf16x8_to_float(raw[k], x);
+      t.apply(x, a.style);
+      store_quads(a.q + (tok * a.heads + h0 + 4 * k) * kLatent + kDv, quads, pack8(x));
     }
     return;
   }
+  // the latent row: lane l holds dims 8 l .. and 256 + 8 l .. of c_kv, and lanes 0..7 the rope dims
+  const int64_t tok = job;
+  const int64_t slot = a.slots[tok], pos = a.positions[tok];
+  const bool rope = lane < kRopeLanes;
+  const uint4 raw0 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 8 * lane);
+  const uint4 raw1 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 256 + 8 * lane);
+  const uint4 raw2 = rope ? load_quads(a.k_pe + tok * a.k_pe_stride, quads) : make_uint4(0, 0, 0, 0);
+  if (slot < 0 || slot >= a.num_slots || pos < 0 || pos >= a.max_pos) return;
+  float x[3][8];
+  dev::bf16x8_to_float(raw0, x[0]);
+  dev::bf16x8_to_float(raw1, x[1]);
+  dev::bf16x8_to_float(raw2, x[2]);
+  if (rope) {
+    Turn t;
+    t.load(a.cos_sin + pos * kRope, kRope, lane);
+    t.apply(x[2], a.style);
+  }
+  if (a.kv_dtype == KV_NVFP4) {
+    store_nvfp4(a, slot, x[0], 8 * lane, 8 * lane + 4, false, true);
+    store_nvfp4(a, slot, x[1], 256 + 8 * lane, 256 + 8 * lane + 4, false, true);
+    store_nvfp4(a, slot, x[2], kDv + quads.a, kDv + quads.b, quads.apart, rope);
+    return;
+  }
+  if (a.kv_dtype == KV_FP8) {
+    uint8_t* row = a.kv + slot * kLatent;
+    *reinterpret_cast<uint2*>(row + 8 * lane) = encode_e4m3x8(x[0]);
+    *reinterpret_cast<uint2*>(row + 256 + 8 * lane) = encode_e4m3x8(x[1]);
+    if (rope) store_codes(row + kDv, quads, encode_e4m3x8(x[2]));
+    return;
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = dev::max_nan(amax, fabsf(x[k][i]));
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) amax = dev::max_nan(amax, __shfl_xor_sync(kFull, amax, o));
+  uint8_t* page = a.kv + (slot / kPage) * kPtPageBytes;
+  uint8_t* row = page + (slot % kPage) * kLatent;
+  // a token holding a NaN gets the scale 0x7FC00000 (one fixed NaN pattern for the stored bytes)
+  const float sc = amax != amax ? __uint_as_float(0x7FC00000u) : __fdiv_rn(amax, 448.0f);
+  const bool fast = divides_fast(sc) && amax <= 3.402823466e38f;
+  const float inv = __frcp_rn(sc);
+  if (lane == 0) *reinterpret_cast<float*>(page + kPtScaleOff + (slot % kPage) * 4) = sc;
+  *reinterpret_cast<uint2*>(row + 8 * lane) = encode_scaled<true>(x[0], sc, inv, fast);
+  *reinterpret_cast<uint2*>(row + 256 + 8 * lane) = encode_scaled<true>(x[1], sc, inv, fast);
+  if (rope) store_codes(row + kDv, quads, encode_scaled<true>(x[2], sc, inv, fast));
+}
+
+// ------------------------------------------------------------------------------------------------
+// K and V heads. One CTA per (page that the call writes, K or V, head): the block's scale needs the
+// amax of all the page's new tokens, and its older codes change with it, so a block has one owner and
+// no atomics. The CTA keeps the new elements in registers between the amax and the codes.
+//
+// Which pages are written is known on the device only. The launch has, for request r, floor(n_r / 64) + 2
+// candidates, the most pages that n_r tokens can touch: job c belongs to the last request with
+// tok_indptr[r] / 64 + 2 r <= c. With few tokens there is a job per token instead (and smaller CTAs), and
+// the first token of each page does the work. Idle jobs leave after the search.
+// ------------------------------------------------------------------------------------------------
+
+// The largest r in [0, batch) with f(r) <= c for a non-decreasing f with f(0) <= c (0 if there is none):
+// 256 probes at a time, one round of loads for up to 256 requests.
+template <class F>
+__device__ __forceinline__ int last_at_most(int batch, int64_t c, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 255) / 256;
+    int hits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int off = (lane + 32 * j) * step;
+      if (32 * j * step < n) hits += __popc(__ballot_sync(kFull, off < n && f(lo + off) <= c));
+    }
+    const int k = max(hits - 1, 0) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  return lo;
+}
+
+// The new tokens of one page: offsets [first, last) of it, from source row tok, cache position pos on.
+// entry: of the page table, -1: nothing to do.
+struct Place {
+  int64_t entry, tok, pos;
+  int first, last;
+};
+
+// The token range of request r, cut to the rows that there are.
+__device__ __forceinline__ void request_tokens(const GqaAppendArgs& a, int r, int64_t& t0, int64_t& t1) {
+  t0 = min(max(static_cast<int64_t>(a.tok_indptr[r]), int64_t(0)), a.n);
+  t1 = min(max(static_cast<int64_t>(a.tok_indptr[r + 1]), t0), a.n);
+}
+
+template <bool PER_TOKEN>
+__device__ __forceinline__ Place find_place(const GqaAppendArgs& a, int64_t job) {
+  Place p{-1, 0, 0, 0, 0};
+  const int32_t* tp = a.tok_indptr;
+  const int r = PER_TOKEN ? last_at_most(a.batch, job, [tp](int i) { return static_cast<int64_t>(tp[i]); })
+                          : last_at_most(a.batch, job, [tp](int i) { return static_cast<int64_t>(tp[i] / kPage) + 2ll * i; });
+  int64_t t0, t1;
+  request_tokens(a, r, t0, t1);
+  const int64_t held = a.kv_len[r];
+  const int64_t p0 = a.kv_indptr[r], p1 = a.kv_indptr[r + 1];
+  if (held < 0 || t0 >= t1) return p;
+  int64_t local;                         // page of the request
+  if (PER_TOKEN) {
+    if (job < t0 || job >= t1) return p;
+    const int64_t pos = held + job - t0;
+    if (job != t0 && pos % kPage != 0) return p;
+    local = pos / kPage;
+  } else {
+    local = held / kPage + (job - (static_cast<int64_t>(tp[r] / kPage) + 2ll * r));
+  }
+  const int64_t lo = max(held, local * kPage), hi = min(held + t1 - t0, (local + 1) * kPage);
+  const int64_t e = p0 + local;
+  if (lo >= hi || p0 < 0 || e < p0 || e >= p1 || e >= a.nnz) return p;
+  p.entry = e;
+  p.tok = t0 + lo - held;
+  p.pos = lo;
+  p.first = static_cast<int>(lo - local * kPage);
+  p.last = static_cast<int>(hi - local * kPage);
+  return p;
+}
+
+// A warp's query heads: 4 passes over 32 / (D / 8) heads of one token.
+template <int D>
+__device__ __forceinline__ void rotate_queries(const GqaAppendArgs& a, int64_t job) {
+  constexpr int kLanes = D / 8, kH = 32 / kLanes, kPasses = 4;
+  const int lane = threadIdx.x & 31;
+  const int head_jobs = (a.heads + kPasses * kH - 1) / (kPasses * kH);
+  if (job >= a.n * head_jobs) return;
+  const int64_t tok = job / head_jobs;
+  const int h0 = static_cast<int>(job % head_jobs) * kPasses * kH + lane / kLanes;
+  const Quads quads(lane % kLanes, a.rot, a.style);
+  uint4 raw[kPasses];
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k)
+    raw[k] = h0 + k * kH < a.heads ? load_quads(a.q + tok * a.q_stride + (h0 + k * kH) * D, quads) : make_uint4(0, 0, 0, 0);
+  const int32_t* tp = a.tok_indptr;
+  const int r = last_at_most(a.batch, tok, [tp](int i) { return static_cast<int64_t>(tp[i]); });
+  int64_t t0, t1;
+  request_tokens(a, r, t0, t1);
+  const int64_t pos = a.positions ? a.positions[tok] : a.kv_len[r] + tok - t0;
+  if (tok < t0 || tok >= t1) return;             // padding
+  if (a.rot > 0 && (pos < 0 || pos >= a.max_pos)) return;
+  Turn t;
+  if (quads.turned) t.load(a.cos_sin + pos * a.rot, a.rot, lane % kLanes);
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    if (h0 + k * kH >= a.heads) continue;
+    uint4 res = raw[k];
+    if (quads.turned) {
+      float x[8];
+      dev::bf16x8_to_float(raw[k], x);
+      t.apply(x, a.style);
+      res = pack8(x);
+    }
+    store_quads(a.q_out + (tok * a.heads + h0 + k * kH) * D, quads, res);
+  }
+}
+
+template <int D, bool E4M3, bool PER_TOKEN, int THREADS>
+__global__ void __launch_bounds__(THREADS) gqa_append_rope_kernel(const GqaAppendArgs a) {
+  constexpr int kLanes = D / 8;                    // lanes of one token's head
+  constexpr int kTok = THREADS / kLanes;           // tokens of one pass over the CTA
+  constexpr int kPasses = kPage / kTok;
+  if (blockIdx.x >= a.kv_ctas) {
+    rotate_queries<D>(a, ((static_cast<int64_t>(blockIdx.x) - a.kv_ctas) * THREADS + threadIdx.x) >> 5);
+    return;
+  }
+  const int lane = threadIdx.x & 31;
   const int blocks = 2 * a.kv_heads;
   const int blk = static_cast<int>(blockIdx.x % blocks);       // K heads, then V heads
   const bool is_k = blk < a.kv_heads;
   const int h = is_k ? blk : blk - a.kv_heads;
-  const Place p = find_place(a, blockIdx.x / blocks);
-  if (p.page < 0) return;                                      // the whole CTA
-  const uint16_t* src = (is_k ? a.k + p.tok * a.k_stride : a.v + p.tok * a.v_stride) + h * D + c8 * 8;
+  const Place p = find_place<PER_TOKEN>(a, blockIdx.x / blocks);
+  if (p.entry < 0) return;                                     // the whole CTA
+  const int64_t page = a.kv_indices[p.entry];
+  const int count = p.last - p.first, mine0 = threadIdx.x / kLanes;
+  const Quads quads(threadIdx.x % kLanes, is_k ? a.rot : 0, a.style);
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
-  const bool rotate = is_k && a.rot > 0;
+  const uint16_t* src = (is_k ? a.k : a.v) + p.tok * stride + h * D;
   uint4 raw[kPasses];
-  bool mine[kPasses];
   int64_t pos[kPasses];
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    const int o = k * kTok + threadIdx.x / kLanes;
-    mine[k] = o >= p.first && o < p.last;
-    raw[k] = mine[k] ? *reinterpret_cast<const uint4*>(src + (o - p.first) * stride) : make_uint4(0, 0, 0, 0);
-    pos[k] = 0;
-    if (a.rot > 0 && mine[k]) {
-      pos[k] = a.positions ? a.positions[p.tok + o - p.first] : p.pos + o - p.first;
-      mine[k] = pos[k] >= 0 && pos[k] < a.max_pos;
+    const int i = k * kTok + mine0;                            // the page's i-th new token
+    raw[k] = make_uint4(0, 0, 0, 0);
+    pos[k] = -1;
+    if (i < count) {
+      raw[k] = load_quads(src + i * stride, quads);
+      pos[k] = a.rot == 0 ? 0 : a.positions ? a.positions[p.tok + i] : p.pos + i;
+      if (a.rot > 0 && pos[k] >= a.max_pos) pos[k] = -1;       // skipped, as a negative one
     }
   }
+  if (page < 0 || page >= a.num_pages) return;
+  const int64_t block = page * blocks + blk;
+  const float old = a.kv_scale[block];
   float x[kPasses][8];
   float amax = 0.0f;
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
+    if (k * kTok >= count) break;                              // the same for the whole CTA
     dev::bf16x8_to_float(raw[k], x[k]);
-    if (rotate) {
-      const uint4 far = shfl4(raw[k], partner);
-      if (turned && mine[k]) {
-        float o[8];
-        Turn t;
-        dev::bf16x8_to_float(far, o);
-        load_turn(t, a.cos_sin + pos[k] * a.rot, a.rot, c8, a.style);
-        turn8(x[k], o, t, a.rot, c8, a.style);
-      }
+    if (pos[k] < 0) continue;
+    if (quads.turned) {
+      Turn t;
+      t.load(a.cos_sin + pos[k] * a.rot, a.rot, threadIdx.x % kLanes);
+      t.apply(x[k], a.style);
     }
-    if (mine[k]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(x[k][i]);
-        if (m <= 3.402823466e38f) amax = fmaxf(amax, m);       // finite: not NaN, not inf
-      }
-    }
+    for (int i = 0; i < 8; ++i) amax = dev::max_nan(amax, fabsf(x[k][i]));
   }
+  __shared__ float part[THREADS / 32];
+  auto over_cta = [&](float v) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
-  __shared__ float part[kHeadThreads / 32];
-  if (lane == 0) part[threadIdx.x / 32] = amax;
-  const int64_t block = p.page * blocks + blk;
-  const float old = a.kv_scale[block];
-  __syncthreads();
+    for (int o = 16; o >= 1; o >>= 1) v = dev::max_nan(v, __shfl_xor_sync(kFull, v, o));
+    if (lane == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = part[0];
 #pragma unroll
-  for (int i = 0; i < kHeadThreads / 32; ++i) amax = fmaxf(amax, part[i]);
+    for (int i = 1; i < THREADS / 32; ++i) v = dev::max_nan(v, part[i]);
+    return v;
+  };
+  amax = over_cta(amax);
+  const bool finite = amax <= 3.402823466e38f;
+  if (!finite) {
+    // a NaN or an infinity among the new elements: the largest of the others
+    amax = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      if (k * kTok >= count) break;
+      if (pos[k] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (fabsf(x[k][i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[k][i]));
+    }
+    __syncthreads();
+    amax = over_cta(amax);
+  }
   const float need = __fdiv_rn(amax, E4M3 ? 448.0f : 127.0f);
   float scale = old, shrink = 1.0f;
   if (p.first == 0 || !(old > 0.0f)) {
@@ -388,7 +483,7 @@ __global__ void __launch_bounds__(kHeadThreads) gqa_append_rope_kernel(const Gqa
   if (shrink != 1.0f) {
     // older codes, 4 at a time
     uint32_t* w = reinterpret_cast<uint32_t*>(dst);
-    for (int i = threadIdx.x; i < p.first * D / 4; i += kHeadThreads) {
+    for (int i = threadIdx.x; i < p.first * D / 4; i += THREADS) {
       const uint32_t c = w[i];
       uint32_t n = 0;
 #pragma unroll
@@ -397,21 +492,29 @@ __global__ void __launch_bounds__(kHeadThreads) gqa_append_rope_kernel(const Gqa
     }
   }
   if (threadIdx.x == 0 && scale != old) a.kv_scale[block] = scale;
+  const bool fast = finite && divides_fast(scale);
+  const float inv = __frcp_rn(scale);
 #pragma unroll
   for (int k = 0; k < kPasses; ++k) {
-    if (!mine[k]) continue;
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i / 4] |= encode8<E4M3>(scale == 0.0f ? x[k][i] : __fdiv_rn(x[k][i], scale)) << (8 * (i % 4));
-    *reinterpret_cast<uint2*>(dst + (k * kTok + threadIdx.x / kLanes) * D + c8 * 8) = make_uint2(w[0], w[1]);
+    if (k * kTok >= count) break;
+    if (pos[k] >= 0) store_codes(dst + (p.first + k * kTok + mine0) * D, quads, encode_scaled<E4M3>(x[k], scale, inv, fast));
   }
 }
 
-template <int D>
-cudaError_t launch_heads(const GqaAppendArgs& a, int64_t ctas, cudaStream_t s) {
-  if (a.cache_dtype == QKVP_CACHE_E4M3) gqa_append_rope_kernel<D, true><<<static_cast<unsigned>(ctas), kHeadThreads, 0, s>>>(a);
-  else gqa_append_rope_kernel<D, false><<<static_cast<unsigned>(ctas), kHeadThreads, 0, s>>>(a);
+template <int D, bool E4M3>
+cudaError_t launch_heads(GqaAppendArgs a, cudaStream_t s) {
+  constexpr int kPageThreads = 256, kTokenThreads = D == 256 ? 128 : 64;
+  const int64_t by_page = a.n / kPage + 2ll * a.batch;
+  const bool per_token = a.n <= by_page;
+  const int threads = per_token ? kTokenThreads : kPageThreads;
+  const int64_t kv_ctas = std::min(a.n, by_page) * 2 * a.kv_heads;
+  constexpr int kHeadsPerWarp = 4 * 32 / (D / 8);
+  const int64_t q_jobs = a.heads > 0 ? a.n * ((a.heads + kHeadsPerWarp - 1) / kHeadsPerWarp) : 0;
+  const int64_t ctas = kv_ctas + (q_jobs * 32 + threads - 1) / threads;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  a.kv_ctas = static_cast<uint32_t>(kv_ctas);
+  if (per_token) gqa_append_rope_kernel<D, E4M3, true, kTokenThreads><<<static_cast<unsigned>(ctas), threads, 0, s>>>(a);
+  else gqa_append_rope_kernel<D, E4M3, false, kPageThreads><<<static_cast<unsigned>(ctas), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -425,21 +528,12 @@ cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_gqa_append_rope(GqaAppendArgs a, cudaStream_t s) {
-  const int64_t by_page = a.n / kPage + 2ll * a.batch;
-  a.per_token = a.n <= by_page ? 1 : 0;
-  const int64_t jobs = std::min(a.n, by_page);
-  const int64_t kv_ctas = jobs * 2 * a.kv_heads;
-  const int heads_per_warp = 4 * 32 / (a.dim / 8);
-  const int64_t q_jobs = a.heads > 0 ? a.n * ((a.heads + heads_per_warp - 1) / heads_per_warp) : 0;
-  const int64_t ctas = kv_ctas + (q_jobs * 32 + kHeadThreads - 1) / kHeadThreads;
-  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  if (ctas == 0) return cudaSuccess;
-  a.kv_ctas = static_cast<uint32_t>(kv_ctas);
+cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s) {
+  const bool e4m3 = a.cache_dtype == QKVP_CACHE_E4M3;
   switch (a.dim) {
-    case 64: return launch_heads<64>(a, ctas, s);
-    case 128: return launch_heads<128>(a, ctas, s);
-    default: return launch_heads<256>(a, ctas, s);
+    case 64: return e4m3 ? launch_heads<64, true>(a, s) : launch_heads<64, false>(a, s);
+    case 128: return e4m3 ? launch_heads<128, true>(a, s) : launch_heads<128, false>(a, s);
+    default: return e4m3 ? launch_heads<256, true>(a, s) : launch_heads<256, false>(a, s);
   }
 }
 

@@ -3,6 +3,7 @@
 // The plan reuses the split-KV planner: each (request, KV head, pass of up to 16 query heads) is a row of
 // pages to it, the visible ones only, so the workers share out exactly the pages that are read.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -18,9 +19,18 @@ namespace {
 
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxHeads = 4096;
-// Workers (CTAs) per SM of the decode kernel, and the pages of work that starting a segment costs.
-constexpr int kCtasPerSm = 2;
-constexpr int kSegmentCost = 2;
+// The split, from decode times on one GB300 over 256 to 4,096 rows (a row: the visible pages of one request and
+// KV head, or of 16 of its query heads) of 128 to 2,048 tokens, D 64 to 256, 4 to 16 query heads per KV head:
+// - Rows per SM from which a worker is a warp: 512 rows of 512 tokens (D 64) 8.9 us against 11.4 with CTAs, 1,024 of
+//   2,048 (D 128) 81 against 87; below it CTAs: 352 of 32,768 428 against 436, 256 ragged ones (16 heads, INT8) 80
+//   against 88. From one row per SM already where a row has no more than 8 units: 256 of 128 tokens (D 256) 10.0 / 12.0.
+// - Pages below which a CTA is not worth its start: 8 rows of 4 pages 4.5 us whole, 6.4 as pairs of pages, 7.4 when
+//   workers span two rows.
+// - Pages of work that starting a row counts as: 4, 8, 16 within 3 % of one another at most sizes, 8 against 4 for
+//   CTAs 5.7 / 9.8 us at 256 rows of 128 tokens, 4 against 8 for warps 25.9 / 29.0 us at 1,024 rows of 512 (D 128).
+constexpr double kWarpRowsPerSm = 2.5;
+constexpr int kMinCtaPages = 4, kCtaRowCost = 8, kWarpRowCost = 4;
+constexpr int kJoinFan = 40;
 
 // Row strides in elements: multiples of 8 (16-byte vectors), at least one row wide.
 bool stride_ok(int64_t s, int64_t width) { return s >= width && s % 8 == 0; }
@@ -47,6 +57,53 @@ Visible visible_pages(int32_t len, int32_t window, int32_t sinks) {
   v.pages = v.sink_pages + pages - v.win_page;
   v.tokens = static_cast<int64_t>(window) + v.sink_end;
   return v;
+}
+
+// Subgroups that the join of m segments is cut into (1: none). A CTA joins a slot in about 0.1 us, a second level
+// costs about 2 us: one request of 65,536 tokens and one KV head (D 128, 256 segments) took 21.8 us with one
+// level and 11.8 with two; 8 x 8,192 tokens (32 segments each) 9.9 with one and 11.0 with two.
+int join_subgroups(int m) {
+  if (m <= kJoinFan) return 1;
+  int size = 1;
+  while (size * size < m) ++size;
+  return (m + size - 1) / size;
+}
+
+// What a worker's time is made of, in microseconds (rough, from timelines of the kernel): its pages, each started
+// segment, and each partial that it writes or joins.
+struct Times {
+  double page, segment, partial;
+};
+Times worker_times(int dim, int group, int team) {
+  const double unit = (dim == 256 ? 1.2 : 0.9) * (group > 8 ? 1.3 : 1.0);      // 8 KB by one warp
+  return {unit * (2.0 * kPage * dim / 8192) / team, team == 1 ? 1.0 : 2.5, team == 1 ? 2.5 : 3.0};
+}
+
+// Rows kept whole, consecutive rows to a worker: the least makespan for `workers`, by bisection, and its ranges.
+double whole_rows(const std::vector<int32_t>& pages, int workers, const Times& t, std::vector<int32_t>& wptr) {
+  auto fill = [&](double budget, int32_t* ptr) {
+    size_t i = 0;
+    for (int w = 0; w < workers; ++w) {
+      if (ptr) ptr[w] = static_cast<int32_t>(i);
+      double sum = 0.0;
+      while (i < pages.size() && (sum += pages[i] * t.page + t.segment) <= budget) ++i;
+    }
+    if (ptr) ptr[workers] = static_cast<int32_t>(i);
+    return i == pages.size();
+  };
+  double lo = 0.0, hi = 0.0;
+  for (int32_t p : pages) {
+    lo = std::max(lo, p * t.page + t.segment);
+    hi += p * t.page + t.segment;
+  }
+  hi = hi * 1.001 + 1.0;
+  for (int i = 0; i < 30 && hi > lo * 1.005; ++i) {
+    const double mid = 0.5 * (lo + hi);
+    if (fill(mid, nullptr)) hi = mid; else lo = mid;
+  }
+  wptr.resize(workers + 1);
+  fill(hi, wptr.data());
+  return hi;
 }
 
 bool dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
@@ -189,7 +246,6 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
     if (num_sms <= 0) return QKVP_E_CUDA;
   }
   if (num_sms > 65536) return QKVP_E_INVALID;
-  const int workers = num_sms * kCtasPerSm;
 
   // one row of visible pages per (request, KV head, pass)
   std::vector<Visible> vis(batch);
@@ -210,17 +266,84 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   }
   indptr[rows] = static_cast<int32_t>(row_pages);
 
+  // Workers are CTAs where there are few rows: their four warps share a row and join at its end. With many rows, or
+  // as many as SMs but short ones, they are single warps, which need no barrier.
+  const int64_t units = row_pages * (kPage * head_dim / 4096);
+  const int team = rows >= static_cast<int64_t>(kWarpRowsPerSm * num_sms) || (rows >= num_sms && units <= 8 * rows) ? 1 : 4;
+  const int per_cta = 4 / team, min_pages = team == 1 ? 1 : kMinCtaPages;
+  const int64_t useful = std::max<int64_t>(1, (row_pages + min_pages - 1) / min_pages);
+  int workers = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms) * gqa_ctas_per_sm(head_dim, group) * per_cta, useful));
+  workers = (workers + per_cta - 1) / per_cta * per_cta;
+  const int cost = team == 1 ? kWarpRowCost : kCtaRowCost;
   SplitInfo info;
-  split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, kSegmentCost);
+  split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, cost);
   std::vector<Segment> cut(static_cast<size_t>(std::max<int64_t>(1, info.num_segments)));
   std::vector<int32_t> wptr(workers + 1), rptr(rows + 1), wide(std::max<int64_t>(1, rows));
-  const SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
-  if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, kSegmentCost))
+  SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
+  if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, cost))
     return QKVP_E_INVALID;
+  // Whole rows instead, where that does not take longer: the bandwidth is shared, so a worker with less than the
+  // others costs nothing while the others keep the memory busy, and partials do cost. (128 x 2,048 tokens of 8 KV
+  // heads, D 128: 81 us whole, 89 split evenly.)
+  if (min_splits == 0 && info.partials > 0) {
+    const Times times = worker_times(head_dim, group, team);
+    double split_us = 0.0;
+    for (int w = 0; w < workers; ++w) {
+      double sum = 0.0;
+      for (int32_t i = wptr[w]; i < wptr[w + 1]; ++i)
+        sum += cut[i].num_pages * times.page + times.segment + (cut[i].partial >= 0 ? times.partial : 0.0);
+      split_us = std::max(split_us, sum);
+    }
+    const double memory_us = static_cast<double>(row_pages) * 2 * kPage * head_dim / 6.7e6;
+    std::vector<int32_t> whole;
+    std::vector<int32_t> row_len(rows);
+    for (int64_t i = 0; i < rows; ++i) row_len[i] = len[i] / kPage;
+    if (whole_rows(row_len, workers, times, whole) <= std::max(split_us, 0.8 * memory_us)) {
+      cut.clear();
+      info.num_segments = info.partials = info.split_reqs = info.max_req_segs = 0;
+      info.max_pages = 0;
+      info.min_pages = INT32_MAX;
+      for (int w = 0; w < workers; ++w) {
+        wptr[w] = static_cast<int32_t>(cut.size());
+        int32_t held = 0;
+        for (int32_t i = whole[w]; i < whole[w + 1]; ++i) {
+          if (len[i] == 0) continue;
+          Segment g{};
+          g.req = i;
+          g.page_begin = indptr[i];
+          g.num_pages = row_len[i];
+          g.partial = -1;
+          held += row_len[i];
+          cut.push_back(g);
+        }
+        info.max_pages = std::max(info.max_pages, held);
+        info.min_pages = std::min(info.min_pages, held);
+      }
+      info.num_segments = static_cast<int64_t>(cut.size());
+      info.max_req_segs = 1;
+      wptr[workers] = static_cast<int32_t>(cut.size());
+      int32_t at = 0;
+      for (int64_t i = 0; i < rows; ++i) {
+        rptr[i] = at;
+        at += len[i] > 0;
+      }
+      rptr[rows] = at;
+    }
+  }
   // rows without a visible page get a segment of no pages, which writes zeros: appended to the workers in turn
   const int64_t empty = info.empty_reqs;
   const int64_t total = info.num_segments + empty;
-  const GqaTable t = gqa_table(total, workers, info.split_reqs);
+  // the joins: their counters, and the slots of the subgroups behind those of the segments
+  int64_t counters = 0, slots = info.partials;
+  for (int64_t i = 0; i < rows; ++i) {
+    const int m = rptr[i + 1] - rptr[i];
+    if (m < 2) continue;
+    const int subs = join_subgroups(m);
+    counters += subs > 1 ? subs + 1 : 1;
+    if (subs > 1) slots += subs;
+  }
+  if (slots > INT32_MAX || total > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  const GqaTable t = gqa_table(total, workers, counters);
 
   plan->batch = batch;
   plan->num_heads = num_heads;
@@ -231,10 +354,11 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   plan->window = window;
   plan->sinks = sinks;
   plan->num_workers = workers;
+  plan->warps_per_worker = team;
   plan->num_segments = static_cast<int32_t>(total);
   plan->num_split_groups = info.split_reqs;
   plan->max_group_segments = info.max_req_segs;
-  plan->num_partials = info.partials;
+  plan->num_partials = static_cast<int32_t>(slots);
   plan->max_worker_pages = info.max_pages;
   plan->min_worker_pages = info.min_pages;
   plan->total_pages = pages;
@@ -242,8 +366,8 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   plan->table_bytes = t.bytes;
   plan->status_offset = t.status;
   plan->partial_o_offset = t.bytes;
-  plan->partial_lse_offset = t.bytes + align_up(static_cast<uint64_t>(info.partials) * kGqaPassHeads * head_dim * 4);
-  plan->workspace_bytes = plan->partial_lse_offset + align_up(static_cast<uint64_t>(info.partials) * kGqaPassHeads * 4);
+  plan->partial_lse_offset = t.bytes + align_up(static_cast<uint64_t>(slots) * kGqaPassHeads * head_dim * 4);
+  plan->workspace_bytes = plan->partial_lse_offset + align_up(static_cast<uint64_t>(slots) * kGqaPassHeads * 4);
   if (workspace == nullptr) return QKVP_OK;
   if (workspace_bytes < plan->workspace_bytes || !aligned(workspace, kTableAlign)) {
     const uint64_t need = plan->workspace_bytes;
@@ -260,10 +384,18 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
 
   std::vector<uint8_t> blob(t.bytes);
   GqaSegment* segs = reinterpret_cast<GqaSegment*>(blob.data() + t.segs);
-  int32_t* ptr = reinterpret_cast<int32_t*>(blob.data() + t.wptr);
-  std::vector<int32_t> counter(rows, 0);
-  for (int64_t i = 0, c = 0; i < rows; ++i)
-    if (rptr[i + 1] - rptr[i] > 1) counter[i] = static_cast<int32_t>(c++);
+  GqaWorker* work = reinterpret_cast<GqaWorker*>(blob.data() + t.workers);
+  std::vector<int32_t> counter(rows, 0), sub_slot(rows, 0);
+  int32_t next_counter = 0, next_slot = info.partials;
+  for (int64_t i = 0; i < rows; ++i) {
+    const int m = rptr[i + 1] - rptr[i];
+    if (m < 2) continue;
+    const int subs = join_subgroups(m);
+    counter[i] = next_counter;
+    sub_slot[i] = next_slot;
+    next_counter += subs > 1 ? subs + 1 : 1;
+    if (subs > 1) next_slot += subs;
+  }
   auto fill = [&](GqaSegment& g, int64_t row) {
     const int r = static_cast<int>(row / (num_kv_heads * passes));
     const int h = static_cast<int>(row / passes % num_kv_heads), pass = static_cast<int>(row % passes);
@@ -279,10 +411,11 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
     g.win_begin = v.win_begin;
     g.sink_end = v.sink_end;
     g.partial = -1;
+    g.top_counter = -1;
   };
   int64_t n = 0, next_empty = 0, given = 0;
   for (int w = 0; w < workers; ++w) {
-    ptr[w] = static_cast<int32_t>(n);
+    work[w].begin = static_cast<int32_t>(n);
     for (int32_t i = wptr[w]; i < wptr[w + 1]; ++i) {
       const Segment& s = cut[i];
       GqaSegment& g = segs[n++];
@@ -291,17 +424,27 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
       g.num_pages = s.num_pages;
       g.partial = s.partial;
       if (s.partial >= 0) {
-        g.group_first = cut[rptr[s.req]].partial;
-        g.group_count = rptr[s.req + 1] - rptr[s.req];
-        g.counter = counter[s.req];
+        // segment `at` of the row's m; subgroups of `size` consecutive segments where there are many
+        const int m = rptr[s.req + 1] - rptr[s.req], at = i - rptr[s.req], subs = join_subgroups(m);
+        const int size = (m + subs - 1) / subs, sub = at / size, first = cut[rptr[s.req]].partial;
+        g.group_first = first + sub * size;
+        g.group_count = std::min(size, m - sub * size);
+        g.counter = counter[s.req] + sub;
+        if (subs > 1) {
+          g.top_first = sub_slot[s.req];
+          g.top_count = subs;
+          g.top_counter = counter[s.req] + subs;
+          g.sub_slot = sub_slot[s.req] + sub;
+        }
       }
     }
     for (const int64_t share = empty * (w + 1) / workers; given < share; ++given) {
       while (len[next_empty] > 0) ++next_empty;
       fill(segs[n++], next_empty++);
     }
+    work[w].end = static_cast<int32_t>(n);
+    if (work[w].begin < work[w].end) work[w].first = segs[work[w].begin];
   }
-  ptr[workers] = static_cast<int32_t>(n);
   if (upload_table(workspace, blob.data(), blob.size(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return QKVP_E_CUDA;
   plan->magic = kGqaMagic;
@@ -326,7 +469,7 @@ int gqa_decode_run(const gqa_plan* plan, const void* q, const void* kv_data, con
   }
   const int64_t page_bytes = 2ll * plan->num_kv_heads * kPage * plan->head_dim;
   if (num_pages > (int64_t(1) << 31) * 128 / page_bytes) return QKVP_E_UNSUPPORTED;   // 256 GiB: TMA row coordinates
-  const GqaTable t = gqa_table(plan->num_segments, plan->num_workers, plan->num_split_groups);
+  const GqaTable t = gqa_table(plan->num_segments, plan->num_workers, 0);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   GqaDecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
@@ -335,7 +478,7 @@ int gqa_decode_run(const gqa_plan* plan, const void* q, const void* kv_data, con
   a.num_pages = num_pages;
   a.kv_indices = kv_indices;
   a.segs = reinterpret_cast<const GqaSegment*>(ws + t.segs);
-  a.worker_ptr = reinterpret_cast<const int32_t*>(ws + t.wptr);
+  a.workers = reinterpret_cast<const GqaWorker*>(ws + t.workers);
   a.counters = reinterpret_cast<uint32_t*>(ws + t.counters);
   a.status = reinterpret_cast<int*>(ws + t.status);
   a.part_o = reinterpret_cast<float*>(ws + plan->partial_o_offset);
@@ -347,6 +490,7 @@ int gqa_decode_run(const gqa_plan* plan, const void* q, const void* kv_data, con
   a.dim = plan->head_dim;
   a.cache_dtype = plan->cache_dtype;
   a.num_workers = plan->num_workers;
+  a.team = plan->warps_per_worker;
   a.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   return launch_gqa_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QKVP_OK : QKVP_E_CUDA;
 }

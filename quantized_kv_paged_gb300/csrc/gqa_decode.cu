@@ -5,12 +5,14 @@
 // Reading the pages once is the floor (2 G operations per byte, G query heads per KV head: far below the
 // tensor rate), so the kernel is a stream with the arithmetic kept out of its way.
 //
-// Work. A CTA of four warps walks the segments of its worker; each warp takes every fourth unit of 4 KB of
-// K and 4 KB of V (64 / 32 / 16 tokens at D = 64 / 128 / 256) and runs a pipeline of its own: a ring of
-// units that its lane 0 fills by TMA, one mbarrier per unit, no barrier with other warps until the segment
-// ends. Two CTAs per SM keep up to 192 KB of loads in flight, several times what the latency asks for. The
-// four warps join their sums at a segment's end; a group (request, KV head) cut into segments leaves
-// normalised FP32 partials, joined by the last of its CTAs to arrive, in segment order.
+// Work. A worker, a CTA's four warps (TEAM 4) or one warp (TEAM 1), walks its segments in units of 4 KB of K and
+// 4 KB of V (64 / 32 / 16 tokens at D = 64 / 128 / 256). Each warp takes its units through a pipeline of its
+// own: a ring of two that its lane 0 fills by TMA, one mbarrier per unit, no barrier with other warps until
+// the segment ends. Two units, not three: 8 warps with 128 KB in flight per SM ran 44 x 32,768 tokens (8 KV
+// heads of 128) in 428 us, 192 KB in 446, and 12 warps with 192 KB in 455; D = 64 takes 12 warps all the
+// same, its units take more time each (128 x 1,024 tokens 24 against 26 us). The warps of a CTA join their
+// sums at a segment's end; a group (request, KV head) cut into segments leaves normalised FP32 partials,
+// joined by the last to arrive, in segment order, in two levels where there are many.
 //
 // Products. Heads are the columns (N = 8) of both products, so that G <= 8 wastes no rows:
 //   S^T [tokens x heads] = K Q^T,  O^T [dims x heads] += V^T P^T,  mma m16n8k16, FP16 in, FP32 sums.
@@ -50,16 +52,22 @@ constexpr float kSlack = 8.0f;           // how far (log2) a logit may pass the 
 constexpr float kLift = 6.0f;            // P is held as 2^(z - m + kLift)
 constexpr float kNone = -3e38f;          // reference before the first unit
 
-template <int D, int NT>
+// At D = 256 and 16 heads Q^T would take 64 of the 255 registers next to 128 of O^T: it is kept in shared memory.
+constexpr bool query_in_smem(int dim, int nt) { return dim == 256 && nt == 2; }
+
+template <int D, int NT, int TEAM>
 struct Shape {
   static constexpr int kTokens = kHalf / D;            // tokens of a unit
   static constexpr int kUnits = kPage / kTokens;       // units of a page
-  static constexpr int kStages = D == 256 && NT == 2 ? 2 : 3;
+  static constexpr int kCtas = gqa_ctas_per_sm(D, 8 * NT);
+  static constexpr int kStages = 2;                    // units of a warp's ring
   static constexpr int kTiles = D / 16;                // 16-dim row tiles of O^T
   static constexpr int kPart = kTiles * NT * 32 * 16;  // bytes of one warp's O^T
-  // shared memory: rings, the join's buffer, the units' scales, barriers, per-warp lse, flags
+  // shared memory: rings, the join's buffer, Q^T where it is kept there, the units' scales, barriers, per-warp lse, flags
   static constexpr int kJoin = kWarps * kStages * kUnit;
-  static constexpr int kScale = kJoin + 2 * kPart;
+  static constexpr int kQ = kJoin + (TEAM > 1 ? 2 * kPart : 0);
+  static constexpr int kQBytes = query_in_smem(D, NT) ? D / 16 * 32 * 8 * NT : 0;   // of one worker
+  static constexpr int kScale = kQ + kWarps / TEAM * kQBytes;
   static constexpr int kBars = kScale + kWarps * kStages * 8;
   static constexpr int kLse = kBars + kWarps * kStages * 8;
   static constexpr int kFlags = kLse + kWarps * kH * 4;
@@ -88,34 +96,35 @@ struct Range {
   __device__ bool all(int n) const { return lim >= n && (win <= 0 || sink >= n); }
 };
 
-__device__ __forceinline__ GqaSegment load_segment(const GqaSegment* p) {
-  GqaSegment s;
+template <class T>
+__device__ __forceinline__ T load_record(const T* p) {
+  static_assert(sizeof(T) % 16 == 0, "records are read 16 bytes at a time");
+  T s;
   const int4* src = reinterpret_cast<const int4*>(p);
   int4* dst = reinterpret_cast<int4*>(&s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dst[i] = __ldg(src + i);
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 16); ++i) dst[i] = __ldg(src + i);
   return s;
 }
 
 // Walks the units that one warp will take, ahead of their use; the page id of the unit it stands on is
 // loaded when it gets there, one unit before it is needed.
-template <int U>
+template <int U, int TEAM>
 struct Feed {
   const GqaDecodeArgs& a;
   int si, se, u, t0, sub;
   int32_t page;
   GqaSegment s;
-  __device__ Feed(const GqaDecodeArgs& args, int s0, int s1, int warp) : a(args), si(s0), se(s1), u(warp - kWarps), t0(0), sub(0), page(-1) {
-    if (si < se) s = load_segment(a.segs + si);
-    next(warp);
+  __device__ Feed(const GqaDecodeArgs& args, const GqaWorker& w, int member) : a(args), si(w.begin), se(w.end), u(member - TEAM), t0(0), sub(0), page(-1), s(w.first) {
+    next(member);
   }
-  __device__ void next(int warp) {
+  __device__ void next(int member) {
     if (si >= se) return;
-    u += kWarps;
+    u += TEAM;
     while (u >= s.num_pages * U) {
       if (++si >= se) return;
-      s = load_segment(a.segs + si);
-      u = warp;
+      s = load_record(a.segs + si);
+      u = member;
     }
     const int local = page_of(s, s.page_begin + u / U);
     sub = u % U;
@@ -148,6 +157,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
   const uint2 v = lds64(addr);
   return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -196,30 +211,44 @@ struct State {
 // Q^T as the B operand of K Q^T: [64-dim group][k-step][register][head tile].
 template <int D, int NT>
 struct Query {
-  uint32_t q[D / 64][4][2][NT];
+  static constexpr bool kShared = query_in_smem(D, NT);
+  uint32_t q[kShared ? 1 : D / 64][4][2][NT];
+  uint32_t addr;            // of the worker's copy in shared memory: 16 bytes per lane and k-step
   float scale[NT][2];       // logit factor of the lane's columns: sm_scale log2(e) / (the head's power of two)
 };
 
+// The lane's share of a segment's queries as stored: 16 dims of each 64-dim group of heads g, 8 + g.
 template <int D, int NT>
-__device__ __forceinline__ void load_query(Query<D, NT>& Q, const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
-  const int g = lane >> 2, t = lane & 3;
+struct RawQuery {
+  uint4 v[NT][D / 64][2];
+  __device__ void load(const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + g;
+      const uint16_t* row = a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0 + h) * D + 16 * t;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          v[n][c][k] = h < s.heads ? __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 8 * k)) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+
+// `only` >= 0: of a Q^T in shared memory, this 64-dim group alone (the others are the team's other warps').
+template <int D, int NT>
+__device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D, NT>& raw, float scale_log2, int only, int lane) {
+  const int t = lane & 3;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int h = 8 * n + g;
-    uint4 raw[D / 64][2];
-    const uint16_t* row = a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0 + h) * D + 16 * t;
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        raw[c][k] = h < s.heads ? __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 8 * k)) : make_uint4(0, 0, 0, 0);
     float amax = 0.0f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[8];
-        dev::bf16x8_to_float(raw[c][k], x);
+        dev::bf16x8_to_float(raw.v[n][c][k], x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
       }
@@ -230,14 +259,20 @@ __device__ __forceinline__ void load_query(Query<D, NT>& Q, const GqaDecodeArgs&
     const int e = amax == 0.0f ? 0 : min(126, 14 + 127 - ex);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c)
+    for (int c = 0; c < D / 64; ++c) {
+      if (Query<D, NT>::kShared && only >= 0 && c != only) continue;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t w[4] = {raw[c][k].x, raw[c][k].y, raw[c][k].z, raw[c][k].w};
+        const uint32_t w[4] = {raw.v[n][c][k].x, raw.v[n][c][k].y, raw.v[n][c][k].z, raw.v[n][c][k].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) Q.q[c][2 * k + i / 2][i % 2][n] = dev::bf16x2_to_f16x2(w[i], up);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = dev::bf16x2_to_f16x2(w[i], up);
+          if constexpr (Query<D, NT>::kShared) tc::sts_u32(Q.addr + ((c * 4 + 2 * k + i / 2) * 32 + lane) * 16 + (i % 2) * 8 + n * 4, x);
+          else Q.q[c][2 * k + i / 2][i % 2][n] = x;
+        }
       }
-    const float f = a.scale_log2 * down;
+    }
+    const float f = scale_log2 * down;
 #pragma unroll
     for (int e2 = 0; e2 < 2; ++e2) Q.scale[n][e2] = __shfl_sync(kFull, f, 4 * (2 * t + e2));
   }
@@ -251,13 +286,17 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t vbase = kbase + kHalf;
   const float2 sc = lds_f2(scale_addr);
-  float s[MT][NT][4];
+  // two sums, of the even and of the odd 64-dim groups, halve the chain of dependent products
+  constexpr int kChains = D == 64 ? 1 : 2;
+  float s[MT][NT][4], part[kChains][MT][NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int c = 0; c < kChains; ++c)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[m][n][k] = 0.0f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) part[c][m][n][k] = 0.0f;
   const int tg = tok8<D>(g);
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
@@ -274,11 +313,72 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         uint32_t a0, a1, a2, a3;
         codes_to_f16<E4M3>(xw[j], a0, a2);
         codes_to_f16<E4M3>(yw[j], a1, a3);
+        uint32_t b[2][NT];
+        if constexpr (Query<D, NT>::kShared) {
+          const uint4 x = lds128(Q.addr + ((c * 4 + j) * 32 + lane) * 16);
+          b[0][0] = x.x;
+          b[0][NT - 1] = x.y;
+          b[1][0] = x.z;
+          b[1][NT - 1] = x.w;
+        } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dev::mma_f16(s[m][n], a0, a1, a2, a3, Q.q[c][j][0][n], Q.q[c][j][1][n]);
+          for (int n = 0; n < NT; ++n) {
+            b[0][n] = Q.q[c][j][0][n];
+            b[1][n] = Q.q[c][j][1][n];
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) dev::mma_f16(part[c % kChains][m][n], a0, a1, a2, a3, b[0][n], b[1][n]);
       }
     }
   }
+
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s[m][n][k] = part[0][m][n][k];
+#pragma unroll
+        for (int c = 1; c < kChains; ++c) s[m][n][k] += part[c][m][n][k];
+      }
+
+  // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them
+  const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
+  constexpr int kSides = (D + 127) / 128;              // 128-dim halves of a token
+  constexpr int W = D == 64 ? 2 : 4;                   // words of a lane's piece of a token
+  uint32_t v[kSides][MT][4][W];                        // tokens ta, tb, ta + 8, tb + 8 of each tile
+  auto load_v = [&](int h, int m) {
+    const uint32_t oa = ta * D + h * 128 + g * 4 * W, ob = tb * D + h * 128 + g * 4 * W;
+    const uint32_t va = vbase + (oa ^ (((oa >> 7) & 7) << 4)), vb = vbase + (ob ^ (((ob >> 7) & 7) << 4));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      uint32_t at = r & 1 ? vb : va;
+      if (D == 64 && r >= 2) at ^= 64;
+      at += (16 * m + (r >= 2 ? 8 : 0)) * D;
+      if constexpr (D == 64) {
+        const uint2 x = lds64(at);
+        v[h][m][r][0] = x.x;
+        v[h][m][r][1] = x.y;
+      } else {
+        const uint4 x = lds128(at);
+        v[h][m][r][0] = x.x;
+        v[h][m][r][1] = x.y;
+        v[h][m][r][2] = x.z;
+        v[h][m][r][3] = x.w;
+      }
+      // what stands behind a token that is not visible may be NaN, and 0 * NaN is not 0
+      if (PARTIAL && !range.sees(16 * m + (r >= 2 ? 8 : 0) + (r & 1 ? tb : ta))) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[h][m][r][i] = 0;
+      }
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < kSides; ++h)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) load_v(h, m);
 
   // V's scale f 2^k, k relative to the warp's first page of the segment
   const uint32_t vs = __float_as_uint(sc.y);
@@ -355,45 +455,17 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
     for (int e = 0; e < 2; ++e) st.l[n][e] += sum[e] * back;
   }
 
-  const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
 #pragma unroll
-  for (int h = 0; h < (D + 127) / 128; ++h) {
-    const int width = D == 64 ? 8 : 16;                // bytes of a lane's piece of a token
-    const uint32_t oa = ta * D + h * 128 + g * width, ob = tb * D + h * 128 + g * width;
-    const uint32_t va = vbase + (oa ^ (((oa >> 7) & 7) << 4)), vb = vbase + (ob ^ (((ob >> 7) & 7) << 4));
+  for (int h = 0; h < kSides; ++h) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      constexpr int W = D == 64 ? 2 : 4;
-      uint32_t w[4][W];                                // tokens ta, tb, ta + 8, tb + 8 of the tile
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        uint32_t at = r & 1 ? vb : va;
-        if (D == 64 && r >= 2) at ^= 64;
-        at += (16 * m + (r >= 2 ? 8 : 0)) * D;
-        if constexpr (D == 64) {
-          const uint2 v = lds64(at);
-          w[r][0] = v.x;
-          w[r][1] = v.y;
-        } else {
-          const uint4 v = lds128(at);
-          w[r][0] = v.x;
-          w[r][1] = v.y;
-          w[r][2] = v.z;
-          w[r][3] = v.w;
-        }
-        // what stands behind a token that is not visible may be NaN, and 0 * NaN is not 0
-        if (PARTIAL && !range.sees(16 * m + (r >= 2 ? 8 : 0) + (r & 1 ? tb : ta))) {
-#pragma unroll
-          for (int i = 0; i < W; ++i) w[r][i] = 0;
-        }
-      }
 #pragma unroll
       for (int i = 0; i < W; ++i) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {                  // dims 4 i + 2 q (row g) and 4 i + 2 q + 1 (row g + 8)
           uint32_t a0, a1, a2, a3;
-          codes_to_f16<E4M3>(__byte_perm(w[0][i], w[1][i], q ? 0x7362 : 0x5140), a0, a1);
-          codes_to_f16<E4M3>(__byte_perm(w[2][i], w[3][i], q ? 0x7362 : 0x5140), a2, a3);
+          codes_to_f16<E4M3>(__byte_perm(v[h][m][0][i], v[h][m][1][i], q ? 0x7362 : 0x5140), a0, a1);
+          codes_to_f16<E4M3>(__byte_perm(v[h][m][2][i], v[h][m][3][i], q ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
           for (int n = 0; n < NT; ++n) dev::mma_f16(st.o[8 * h + 2 * i + q][n], a0, a1, a2, a3, p[m][n][0], p[m][n][1]);
         }
@@ -432,6 +504,26 @@ __device__ __forceinline__ void sum_warps(float (&o)[D / 16][NT][4], float4* buf
   }
 }
 
+// 2^(top - M) / sum_w 2^(lse_w - M) over the four warps' lse at stride kH, M their maximum: what a sum that
+// a warp holds relative to 2^top counts in the whole. `joined` becomes the whole's lse.
+__device__ __forceinline__ float weigh(const float* lse, float top, float& joined) {
+  float x[kWarps], M = -INFINITY, W = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    x[w] = lse[w * kH];
+    M = dev::max_nan(M, x[w]);
+  }
+  if (M == -INFINITY) {
+    joined = -INFINITY;
+    return 0.0f;
+  }
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) W += dev::fast_exp2(x[w] - M);
+  const float mine = __fdividef(dev::fast_exp2(top - M), W);
+  joined = M + lg2(W);
+  return mine;
+}
+
 // Warp 0's finished O^T (normalised) and base-2 lse of a segment's heads to out and lse.
 template <int D, int NT>
 __device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegment& s, const float (&o)[D / 16][NT][4],
@@ -460,12 +552,14 @@ __device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegme
     }
 }
 
-template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kThreads, 2) gqa_decode_kernel(const GqaDecodeArgs a, const __grid_constant__ CUtensorMap map) {
-  using P = Shape<D, NT>;
+// TEAM warps share a worker's segments: 4 (the CTA) or 1 (each warp a worker of its own, no barrier at all).
+template <int D, bool E4M3, int NT, int TEAM>
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decode_kernel(const GqaDecodeArgs a, const __grid_constant__ CUtensorMap map) {
+  using P = Shape<D, NT, TEAM>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = dev::smem_u32(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int member = TEAM == 1 ? 0 : warp;
   const uint32_t ring = base + warp * P::kStages * kUnit;
   const uint32_t scales = base + P::kScale + warp * P::kStages * 8;
   const uint32_t bars = base + P::kBars + warp * P::kStages * 8;
@@ -476,10 +570,14 @@ __global__ void __launch_bounds__(kThreads, 2) gqa_decode_kernel(const GqaDecode
   tc::fence_mbar_init();
   __syncwarp();
 
-  const int s0 = a.worker_ptr[blockIdx.x], s1 = a.worker_ptr[blockIdx.x + 1];
+  const GqaWorker w = load_record(a.workers + (TEAM == 1 ? blockIdx.x * kWarps + warp : blockIdx.x));
   bool dead = (base & 1023) != 0;          // the swizzle needs the ring aligned; never expected
   if (dead && threadIdx.x == 0) atomicOr(a.status, 2);
-  Feed<P::kUnits> feed(a, s0, s1, warp);
+  // a segment's queries are loaded before what precedes its first unit: the first fills, the join of the last segment
+  RawQuery<D, NT> raw;
+  GqaSegment s = w.first;
+  if (w.begin < w.end) raw.load(a, s, lane);
+  Feed<P::kUnits, TEAM> feed(a, w, member);
   uint32_t loaded = 0, parity = 0;         // bit i: stage i holds a unit to take / parity of its barrier
   auto fill = [&](int stage) {
     const bool ok = feed.si < feed.se && !dead && feed.page >= 0 && feed.page < a.num_pages && Range(feed.s, feed.t0).any(P::kTokens);
@@ -494,23 +592,30 @@ __global__ void __launch_bounds__(kThreads, 2) gqa_decode_kernel(const GqaDecode
       tma_load_2d(dst, &map, 0, static_cast<int>(kb * (kPage * D / 128) + feed.sub * (kHalf / 128)), bar);
       tma_load_2d(dst + kHalf, &map, 0, static_cast<int>(vb * (kPage * D / 128) + feed.sub * (kHalf / 128)), bar);
     }
-    feed.next(warp);
+    feed.next(member);
   };
 #pragma unroll 1
   for (int i = 0; i < P::kStages; ++i) fill(i);
 
   State<D, NT> st;
   Query<D, NT> Q;
+  Q.addr = base + P::kQ + (TEAM == 1 ? warp : 0) * P::kQBytes;
   int stage = 0;
   const int t = lane & 3, g = lane >> 2;
 #pragma unroll 1
-  for (int si = s0; si < s1; ++si) {
-    const GqaSegment s = load_segment(a.segs + si);
-    load_query<D, NT>(Q, a, s, lane);
+  for (int si = w.begin; si < w.end;) {
+    // of a Q^T in shared memory each warp of a team writes its part; none still reads the last segment's, which
+    // ended at a barrier
+    static_assert(!Query<D, NT>::kShared || D / 64 == kWarps, "a 64-dim group per warp");
+    convert_query<D, NT>(Q, raw, a.scale_log2, TEAM > 1 ? warp : -1, lane);
+    if constexpr (Query<D, NT>::kShared) {
+      if constexpr (TEAM > 1) __syncthreads();
+      else __syncwarp();
+    }
     st.clear();
     int kref = INT32_MIN;
 #pragma unroll 1
-    for (int u = warp; u < s.num_pages * P::kUnits; u += kWarps) {
+    for (int u = member; u < s.num_pages * P::kUnits; u += TEAM) {
       if (loaded >> stage & 1) {
         if (!dead && !tc::mbar_wait(bars + 8 * stage, parity >> stage & 1)) {
           dead = true;
@@ -526,9 +631,14 @@ __global__ void __launch_bounds__(kThreads, 2) gqa_decode_kernel(const GqaDecode
       fill(stage);
       stage = stage + 1 == P::kStages ? 0 : stage + 1;
     }
-    // this warp's l over its lanes, its lse, and the four warps' weights
+    GqaSegment next = s;
+    if (++si < w.end) {
+      next = load_record(a.segs + si);
+      raw.load(a, next, lane);
+    }
+    // this warp's l over its lanes, and its lse
     const float vref = kref == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(max(127 + kref, 1)) << 23);
-    float L[NT][2];
+    float L[NT][2], weight[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -538,114 +648,161 @@ __global__ void __launch_bounds__(kThreads, 2) gqa_decode_kernel(const GqaDecode
         l += __shfl_xor_sync(kFull, l, 8);
         l += __shfl_xor_sync(kFull, l, 16);
         st.l[n][e] = l;
-        if (g == 0) wl[warp * kH + 8 * n + 2 * t + e] = l == 0.0f ? -INFINITY : st.m[n][e] - kLift + log2f(l);
+        L[n][e] = l == 0.0f ? -INFINITY : st.m[n][e] - kLift + lg2(l);
+        weight[n][e] = 1.0f;
+        if (TEAM > 1 && g == 0) wl[warp * kH + 8 * n + 2 * t + e] = L[n][e];
       }
-    __syncthreads();
+    if constexpr (TEAM > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) weight[n][e] = weigh(wl + 8 * n + 2 * t + e, L[n][e], L[n][e]);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float lw[kWarps], M = -INFINITY, W = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          lw[w] = wl[w * kH + 8 * n + 2 * t + e];
-          M = dev::max_nan(M, lw[w]);
-        }
-        float mine = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float c = M == -INFINITY ? 0.0f : exp2f(lw[w] - M);
-          W += c;
-          if (w == warp) mine = c;
-        }
-        L[n][e] = M == -INFINITY ? -INFINITY : M + log2f(W);
-        const float c = mine == 0.0f ? 0.0f : mine / W * vref / st.l[n][e];
+        const float c = st.l[n][e] == 0.0f || weight[n][e] == 0.0f ? 0.0f : __fdividef(weight[n][e], st.l[n][e]) * vref;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           st.o[i][n][e] *= c;
           st.o[i][n][2 + e] *= c;
         }
       }
-    sum_warps<D, NT>(st.o, join, warp, lane);
+    if constexpr (TEAM > 1) sum_warps<D, NT>(st.o, join, warp, lane);
     if (s.partial < 0) {
-      if (warp == 0) write_out<D, NT>(a, s, st.o, L, lane);
+      if (member == 0) write_out<D, NT>(a, s, st.o, L, lane);
+      s = next;
       continue;
     }
-    if (warp == 0) {
-      float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(s.partial) * kH * D);
+    int slot = s.partial, first = s.group_first, count = s.group_count, counter = s.counter;
+    bool top = s.top_counter < 0;
+#pragma unroll 1
+    while (true) {
+      int last = 0;
+      if (member == 0) {
+        float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kH * D);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32 + lane, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
-      if (g == 0) {
+          for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32 + lane, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
+        if (g == 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(slot) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) last = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
+        if (TEAM > 1 && lane == 0) *flag = last;
+      }
+      if constexpr (TEAM > 1) {
+        __syncthreads();
+        last = *flag;
+      } else {
+        last = __shfl_sync(kFull, last, 0);
+      }
+      if (last == 0) break;
+      // The last arrival: every slot is written. The team's warps take the slots in turn, a few at a
+      // time with their lse, under a running maximum.
+      __threadfence();
+      if (member == 0 && lane == 0) a.counters[counter] = 0;        // ready for the next run
+      const float* gl = a.part_lse + static_cast<int64_t>(first) * kH + 2 * t;
+      const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(first) * kH * D) + lane;
+      float M[NT][2], W[NT][2];
+      st.clear();
+#pragma unroll
+      for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = -INFINITY, W[n][0] = W[n][1] = 0.0f;
+      constexpr int kVecs = P::kCtas == 3 ? 16 : 32;
+      constexpr int kBatch = D / 16 * NT >= kVecs ? 1 : kVecs / (D / 16 * NT);
+#pragma unroll 1
+      for (int k0 = member; k0 < count; k0 += TEAM * kBatch) {
+        float4 v[kBatch][D / 16][NT];
+        float2 x[kBatch][NT];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int k = k0 + j * TEAM;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            x[j][n] = k < count ? __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n)) : make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+              v[j][i][n] = k < count ? __ldcg(go + static_cast<int64_t>(k) * (kH * D / 4) + (i * NT + n) * 32) : make_float4(0, 0, 0, 0);
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(s.partial) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = M[n][e];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) top = dev::max_nan(top, e ? x[j][n].y : x[j][n].x);
+            const float c = top == -INFINITY ? 1.0f : dev::fast_exp2(M[n][e] - top);
+            W[n][e] *= c;
+            M[n][e] = top;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              st.o[i][n][e] *= c;
+              st.o[i][n][2 + e] *= c;
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const float z = top == -INFINITY ? 0.0f : dev::fast_exp2((e ? x[j][n].y : x[j][n].x) - top);
+              W[n][e] += z;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                st.o[i][n][e] += z * (e ? v[j][i][n].y : v[j][i][n].x);
+                st.o[i][n][2 + e] += z * (e ? v[j][i][n].w : v[j][i][n].z);
+              }
+            }
+          }
       }
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) *flag = atomicAdd(a.counters + s.counter, 1u) == static_cast<unsigned>(s.group_count - 1);
+      if constexpr (TEAM > 1) {
+        // the warps' maxima and sums, as at a segment's end
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (g == 0) wl[warp * kH + 8 * n + 2 * t + e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mine = weigh(wl + 8 * n + 2 * t + e, M[n][e], L[n][e]);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              st.o[i][n][e] *= mine;
+              st.o[i][n][2 + e] *= mine;
+            }
+          }
+        sum_warps<D, NT>(st.o, join, warp, lane);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float mine = W[n][e] == 0.0f ? 0.0f : 1.0f / W[n][e];
+            L[n][e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              st.o[i][n][e] *= mine;
+              st.o[i][n][2 + e] *= mine;
+            }
+          }
+      }
+      if (top) {
+        if (member == 0) write_out<D, NT>(a, s, st.o, L, lane);
+        break;
+      }
+      slot = s.sub_slot;
+      first = s.top_first;
+      count = s.top_count;
+      counter = s.top_counter;
+      top = true;
     }
-    __syncthreads();
-    if (*flag == 0) continue;
-    // the group's last CTA: every partial is written. Warp w takes slots w, w + 4, ...
-    __threadfence();
-    if (threadIdx.x == 0) a.counters[s.counter] = 0;      // ready for the next run
-    const float* gl = a.part_lse + static_cast<int64_t>(s.group_first) * kH;
-    const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(s.group_first) * kH * D);
-    float M[NT][2], W[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float m0 = -INFINITY, m1 = -INFINITY;
-      for (int k = g; k < s.group_count; k += 8) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n + 2 * t));
-        m0 = dev::max_nan(m0, x.x);
-        m1 = dev::max_nan(m1, x.y);
-      }
-#pragma unroll
-      for (int d = 4; d <= 16; d *= 2) {
-        m0 = dev::max_nan(m0, __shfl_xor_sync(kFull, m0, d));
-        m1 = dev::max_nan(m1, __shfl_xor_sync(kFull, m1, d));
-      }
-      float w0 = 0.0f, w1 = 0.0f;
-      for (int k = g; k < s.group_count; k += 8) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n + 2 * t));
-        w0 += m0 == -INFINITY ? 0.0f : exp2f(x.x - m0);
-        w1 += m1 == -INFINITY ? 0.0f : exp2f(x.y - m1);
-      }
-#pragma unroll
-      for (int d = 4; d <= 16; d *= 2) {
-        w0 += __shfl_xor_sync(kFull, w0, d);
-        w1 += __shfl_xor_sync(kFull, w1, d);
-      }
-      M[n][0] = m0;
-      M[n][1] = m1;
-      W[n][0] = w0;
-      W[n][1] = w1;
-    }
-    st.clear();
-    for (int k = warp; k < s.group_count; k += kWarps) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n + 2 * t));
-        const float c0 = M[n][0] == -INFINITY ? 0.0f : exp2f(x.x - M[n][0]) / W[n][0];
-        const float c1 = M[n][1] == -INFINITY ? 0.0f : exp2f(x.y - M[n][1]) / W[n][1];
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const float4 v = __ldcg(go + static_cast<int64_t>(k) * (kH * D / 4) + (i * NT + n) * 32 + lane);
-          st.o[i][n][0] += c0 * v.x;
-          st.o[i][n][1] += c1 * v.y;
-          st.o[i][n][2] += c0 * v.z;
-          st.o[i][n][3] += c1 * v.w;
-        }
-      }
-    }
-    sum_warps<D, NT>(st.o, join, warp, lane);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) L[n][e] = M[n][e] == -INFINITY ? -INFINITY : M[n][e] + log2f(W[n][e]);
-    if (warp == 0) write_out<D, NT>(a, s, st.o, L, lane);
+    s = next;
   }
   if (dead) {
     // copies may still be on their way into this CTA's shared memory: let them land before it is given up
@@ -684,28 +841,29 @@ cudaError_t pool_map(const GqaDecodeArgs& a, CUtensorMap* map) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, int TEAM>
 cudaError_t launch(const GqaDecodeArgs& a, const CUtensorMap& map, cudaStream_t st) {
+  constexpr int bytes = Shape<D, NT, TEAM>::kBytes;
+  auto kernel = gqa_decode_kernel<D, E4M3, NT, TEAM>;
   // once per device: the attribute belongs to the device's copy of the kernel
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(done.load(std::memory_order_relaxed) & bit) || bit == 0) {
-    e = cudaFuncSetAttribute(gqa_decode_kernel<D, E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, NT>::kBytes);
+  if (!(done.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  gqa_decode_kernel<D, E4M3, NT><<<a.num_workers, kThreads, Shape<D, NT>::kBytes, st>>>(a, map);
+  kernel<<<a.num_workers * TEAM / kWarps, kThreads, bytes, st>>>(a, map);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool E4M3>
 cudaError_t launch_dim(const GqaDecodeArgs& a, const CUtensorMap& map, cudaStream_t st) {
-  const bool wide = a.heads / a.kv_heads > 8;
-  if (a.cache_dtype == QKVP_CACHE_E4M3) return wide ? launch<D, true, 2>(a, map, st) : launch<D, true, 1>(a, map, st);
-  return wide ? launch<D, false, 2>(a, map, st) : launch<D, false, 1>(a, map, st);
+  if (a.heads / a.kv_heads > 8) return a.team == 1 ? launch<D, E4M3, 2, 1>(a, map, st) : launch<D, E4M3, 2, 4>(a, map, st);
+  return a.team == 1 ? launch<D, E4M3, 1, 1>(a, map, st) : launch<D, E4M3, 1, 4>(a, map, st);
 }
 
 }  // namespace
@@ -717,10 +875,11 @@ cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t st) {
     const cudaError_t e = pool_map(a, &map);
     if (e != cudaSuccess) return e;
   }
+  const bool e4m3 = a.cache_dtype == QKVP_CACHE_E4M3;
   switch (a.dim) {
-    case 64: return launch_dim<64>(a, map, st);
-    case 128: return launch_dim<128>(a, map, st);
-    default: return launch_dim<256>(a, map, st);
+    case 64: return e4m3 ? launch_dim<64, true>(a, map, st) : launch_dim<64, false>(a, map, st);
+    case 128: return e4m3 ? launch_dim<128, true>(a, map, st) : launch_dim<128, false>(a, map, st);
+    default: return e4m3 ? launch_dim<256, true>(a, map, st) : launch_dim<256, false>(a, map, st);
   }
 }
 

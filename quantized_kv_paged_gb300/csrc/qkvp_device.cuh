@@ -113,6 +113,16 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t two, float scale = 
   return pack_f16x2(__uint_as_float(two << 16) * scale, __uint_as_float(two & 0xFFFF0000u) * scale);
 }
 
+// Eight BF16 of a 16-byte load -> FP32, exact.
+__device__ __forceinline__ void bf16x8_to_float(const uint4 v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
 // One packed NVFP4 byte (low nibble = first element) times a block scale held as F16x2 (both
 // halves equal) -> F16x2, exact.
 __device__ __forceinline__ uint32_t nvfp4x2_to_f16x2(uint32_t byte, uint32_t scale_h2) {
@@ -132,60 +142,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
-}
-
-// ---------------------------------------------------------------------------------------------
-// Quantize-on-append of 16 values, shared by the appends with and without rotation.
-// ---------------------------------------------------------------------------------------------
-
-// NVFP4: one block of 16 values -> 8 bytes of E2M1 pairs and the E4M3 block scale amax / (6 g).
-__device__ __forceinline__ uint2 encode_nvfp4_block(const float (&x)[16], float g, uint32_t& s8) {
-  // amax over the block; any NaN makes it NaN
-  float amax = 0.0f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    nan |= (x[i] != x[i]);
-    amax = fmaxf(amax, fabsf(x[i]));
-  }
-  if (nan) amax = __uint_as_float(0x7FC00000u);
-  const float s = __fdiv_rn(amax, __fmul_rn(6.0f, g));
-  s8 = encode_e4m3(s);
-  const float sd = __fmul_rn(e4m3_to_float(s8), g);
-  uint32_t w[2] = {0, 0};
-  if (sd != 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t c = encode_e2m1(__fdiv_rn(x[i], sd));
-      w[i / 8] |= c << (4 * (i % 8));     // element 2k -> low nibble of byte k
-    }
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-// E4M3(x / sc), or E4M3(x) where sc is 0.
-__device__ __forceinline__ uint4 encode_e4m3_scaled(const float (&x)[16], float sc) {
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i / 4] |= encode_e4m3(sc == 0.0f ? x[i] : __fdiv_rn(x[i], sc)) << (8 * (i % 4));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ uint4 encode_e4m3_plain(const float (&x)[16]) {
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) w[i / 4] |= encode_e4m3(x[i]) << (8 * (i % 4));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Eight BF16 of a 16-byte load -> FP32, exact.
-__device__ __forceinline__ void bf16x8_to_float(const uint4 v, float* x) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -163,7 +163,6 @@ struct GqaAppendArgs {
   float* kv_scale;            // [num_pages][2][kv_heads]
   int64_t k_stride, v_stride, q_stride, n, nnz, max_pos, num_pages;
   int batch, rot, style, kv_heads, dim, heads, cache_dtype;
-  int per_token;              // one job per token instead of per candidate page (set by the launcher)
   uint32_t kv_ctas;           // CTAs of the K and V blocks; the query's follow (set by the launcher)
 };
 
@@ -179,13 +178,26 @@ struct GqaSegment {
   int32_t win_begin, sink_end; // token t is visible if t < sink_end or win_begin <= t < len
   int32_t page_begin, num_pages;  // visible pages [page_begin, page_begin + num_pages)
   int32_t partial;             // partial slot, or -1 for a direct write
-  int32_t group_first, group_count;  // the partial slots of all segments of this group
-  int32_t counter;             // the group's arrival counter
+  // Arrivals at `counter` are joined by the last of `group_count`, from the slots group_first ... A group of
+  // many segments joins in two levels: subgroups first, each into sub_slot, and the last subgroup joins the
+  // top_count slots from top_first. top_counter -1: one level.
+  int32_t group_first, group_count, counter;
+  int32_t top_first, top_count, top_counter, sub_slot;
 };
-static_assert(sizeof(GqaSegment) == 64, "segment layout");
+static_assert(sizeof(GqaSegment) == 80, "segment layout");
+
+// What a worker starts from, in one read: the range of its segments and the first of them.
+struct GqaWorker {
+  GqaSegment first;
+  int32_t begin, end;
+  int32_t pad[2];
+};
+static_assert(sizeof(GqaWorker) == 96, "worker layout");
 
 constexpr uint64_t kGqaMagic = 0x716b76702d677161ull;
 constexpr int kGqaPassHeads = 16;   // query heads of one pass over the pages
+// CTAs of the head-pool decode that one SM holds.
+constexpr int gqa_ctas_per_sm(int dim, int group) { return dim == 64 && group <= 8 ? 3 : 2; }
 
 struct GqaDecodeArgs {
   const uint16_t* q;          // bf16 [B][H][D]
@@ -194,28 +206,29 @@ struct GqaDecodeArgs {
   int64_t num_pages;
   const int32_t* kv_indices;
   const GqaSegment* segs;
-  const int32_t* worker_ptr;  // [num_workers + 1]
-  uint32_t* counters;         // one per split group, zero between runs
+  const GqaWorker* workers;   // [num_workers]
+  uint32_t* counters;         // arrival counters of the joins, zero between runs
   int* status;
   float* part_o;              // [num_partials][16][D], normalised
   float* part_lse;            // [num_partials][16], log2 domain
   uint16_t* out;              // bf16 [B][H][D]
   float* lse;                 // [B][H] or null
   int heads, kv_heads, dim, cache_dtype, num_workers;
+  int team;                   // warps of a worker: 4 (a CTA) or 1
   float scale_log2;           // sm_scale * log2(e)
 };
 
-// Work table of a head-pool plan: segments, worker ranges, then the status word and the groups' counters.
+// Work table of a head-pool plan: segments, workers, then the status word and the joins' counters.
 struct GqaTable {
-  uint64_t segs, wptr, status, counters, bytes;
+  uint64_t segs, workers, status, counters, bytes;
 };
-inline GqaTable gqa_table(int64_t segments, int64_t workers, int64_t groups) {
+inline GqaTable gqa_table(int64_t segments, int64_t workers, int64_t counters) {
   GqaTable t;
   t.segs = 0;
-  t.wptr = align_up(static_cast<uint64_t>(segments) * sizeof(GqaSegment));
-  t.status = t.wptr + align_up(static_cast<uint64_t>(workers + 1) * 4);
+  t.workers = align_up(static_cast<uint64_t>(segments) * sizeof(GqaSegment));
+  t.status = t.workers + align_up(static_cast<uint64_t>(workers) * sizeof(GqaWorker));
   t.counters = t.status + kTableAlign;
-  t.bytes = t.counters + align_up(static_cast<uint64_t>(groups) * 4);
+  t.bytes = t.counters + align_up(static_cast<uint64_t>(counters) * 4);
   return t;
 }
 
@@ -225,7 +238,7 @@ int query_sms();
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s);
-cudaError_t launch_gqa_append_rope(GqaAppendArgs a, cudaStream_t s);
+cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_gather_fp8(const GatherArgs& a, cudaStream_t s);
 cudaError_t launch_gather_pages_bf16(const uint8_t* pool, int64_t num_pages, const int32_t* ids, int64_t n,
