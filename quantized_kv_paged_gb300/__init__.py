@@ -280,32 +280,30 @@ def _dense(name: str, t, shape, dtypes):
         _refuse(name, t, shape, dtypes, "a contiguous layout")
 
 
-def _rows(name: str, t, shape, dtypes):
-    """Row stride of a tensor whose rows (all dims but the first) are dense. The stride of an extent of one
-    says nothing: such a tensor counts as dense."""
+def _rows(name: str, t, n: int, heads: int, dim: int, dtypes):
+    """Row stride of a [n, heads, dim] tensor (heads 0: [n, dim]) whose rows are dense. The stride of an extent
+    of one says nothing: such a tensor counts as dense."""
     stride = t.stride()
-    width, ok = 1, t.dtype in dtypes and t.shape == shape
-    for d in range(len(shape) - 1, 0, -1):
-        ok = ok and (shape[d] <= 1 or stride[d] == width)
-        width *= shape[d]
-    if not ok:
-        _refuse(name, t, shape, dtypes, "dense rows")
-    return stride[0] if shape[0] > 1 else width
+    if heads == 0:
+        if t.shape != (n, dim) or t.dtype not in dtypes or stride[1] != 1:
+            _refuse(name, t, (n, dim), dtypes, "dense rows")
+        return stride[0] if n > 1 else dim
+    if t.shape != (n, heads, dim) or t.dtype not in dtypes or stride[2] != 1 or (stride[1] != dim and heads > 1):
+        _refuse(name, t, (n, heads, dim), dtypes, "dense rows")
+    return stride[0] if n > 1 else heads * dim
 
 
 def _launch_on(stream, tensors):
     """The stream to launch on. The launch goes to the current device: tensors elsewhere are refused."""
-    torch = _Types.torch
-    at = None
+    cuda = _Types.torch.cuda
+    here = tensors[0].get_device()
+    if here < 0 or here != cuda.current_device():
+        raise ValueError(f"tensors need to be on the current CUDA device, got one on {tensors[0].device}")
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d != at:
-                if at is not None or d < 0 or d != torch.cuda.current_device():
-                    raise ValueError(f"tensors need to be on the current CUDA device, got one on {t.device}")
-                at = d
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors need to be on the current CUDA device, got one on {t.device}")
     if stream is None:
-        return torch.cuda.current_stream(at).cuda_stream
+        return cuda.current_stream(here).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -322,8 +320,8 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
     their own row strides; cos_sin float32 [max_positions, 64]."""
     T = _Types.get()
     n = c_kv.shape[0]
-    c_stride = _rows("c_kv", c_kv, (n, 512), T.bf16)
-    pe_stride = _rows("k_pe", k_pe, (n, 64), T.bf16)
+    c_stride = _rows("c_kv", c_kv, n, 0, V_DIM, T.bf16)
+    pe_stride = _rows("k_pe", k_pe, n, 0, 64, T.bf16)
     _dense("slot_mapping", slot_mapping, (n,), T.i64)
     _dense("positions", positions, (n,), T.i64)
     max_positions = cos_sin.shape[0]
@@ -343,7 +341,7 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
             head_stride = stride[1] if heads > 1 else 64
             tok_stride = stride[0] if n > 1 else 64
     on = _launch_on(stream, (c_kv, k_pe, slot_mapping, positions, cos_sin, kv_data, kv_scale, q_pe, q))
-    st = load().mla_append_rope(
+    st = (_lib or load()).mla_append_rope(
         c_kv.data_ptr(), c_stride, k_pe.data_ptr(), pe_stride, n, slot_mapping.data_ptr(), positions.data_ptr(),
         cos_sin.data_ptr(), max_positions, rope_style, _at(q_pe), tok_stride, head_stride, heads, _at(q),
         kv_data.data_ptr(), _at(kv_scale), kv_dtype, global_scale, page_size,
@@ -370,7 +368,7 @@ def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, ro
     T = _Types.get()
     pages, heads_kv, dim = _head_pool(kv_data, kv_scale, T)
     n, batch, nnz = k.shape[0], kv_len.shape[0], kv_indices.shape[0]
-    k_stride, v_stride = _rows("k", k, (n, heads_kv, dim), T.bf16), _rows("v", v, (n, heads_kv, dim), T.bf16)
+    k_stride, v_stride = _rows("k", k, n, heads_kv, dim, T.bf16), _rows("v", v, n, heads_kv, dim, T.bf16)
     _dense("tok_indptr", tok_indptr, (batch + 1,), T.i32)
     _dense("kv_len", kv_len, (batch,), T.i32)
     _dense("kv_indptr", kv_indptr, (batch + 1,), T.i32)
@@ -388,11 +386,12 @@ def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, ro
             raise ValueError("q and q_out [n, H, D] go together")
         heads = q_out.shape[1]
         _dense("q_out", q_out, (n, heads, dim), T.bf16)
-        q_stride = _rows("q", q, (n, heads, dim), T.bf16)
         if heads == 0:
             q = q_out = None
+        else:
+            q_stride = _rows("q", q, n, heads, dim, T.bf16)
     on = _launch_on(stream, (k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, kv_data, kv_scale, q, q_out, positions))
-    st = load().gqa_append_rope(
+    st = (_lib or load()).gqa_append_rope(
         k.data_ptr(), k_stride, v.data_ptr(), v_stride, n, tok_indptr.data_ptr(), kv_len.data_ptr(), batch,
         kv_indptr.data_ptr(), kv_indices.data_ptr(), nnz, _at(positions), _at(cos_sin), max_positions, rot,
         rope_style, heads_kv, dim, kv_data.data_ptr(), kv_scale.data_ptr(), cache_dtype, PAGE_SIZE, pages, _at(q),
@@ -431,7 +430,7 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
     if lse is not None:
         _dense("lse", lse, (batch, heads), T.f32)
     on = _launch_on(stream, (q, kv_data, kv_scale, kv_indices, out, lse, workspace))
-    st = load().gqa_decode_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
+    st = (_lib or load()).gqa_decode_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
                                kv_indices.data_ptr(), sm_scale, out.data_ptr(), _at(lse), workspace.data_ptr(),
                                workspace.nbytes, on)
     return st if st == QKVP_OK else _check("gqa_decode_run", st, raise_on_error)

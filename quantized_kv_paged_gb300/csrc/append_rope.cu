@@ -163,6 +163,7 @@ __device__ __forceinline__ uint2 encode_scaled(const float (&x)[8], float s, flo
 // ------------------------------------------------------------------------------------------------
 constexpr int kLatentThreads = 128;
 constexpr int kQHeads = 16;             // query heads per warp
+constexpr int kFusedTokens = 1024;
 constexpr int kRopeLanes = kRope / 8;   // 8 lanes hold one head's 64 dims
 
 // NVFP4 codes of 4 values (two bytes) under a block's E4M3 scale: the formulas of kv_append_quant.
@@ -200,51 +201,56 @@ __device__ __forceinline__ void store_nvfp4(const MlaAppendArgs& a, int64_t slot
   if (apart && qb % 16 == 0) a.kv_scale[slot * kScales + qb / 16] = static_cast<uint8_t>(sb);
 }
 
+// FUSED: the warp of a token takes the row and the token's first 16 query heads, with all loads in flight
+// together and one look at the position and its table row: for many tokens. Apart, a decode step of few tokens
+// reaches twice as many SMs.
+template <bool FUSED>
 __global__ void __launch_bounds__(kLatentThreads) mla_append_rope_kernel(const MlaAppendArgs a) {
   const int64_t job = (static_cast<int64_t>(blockIdx.x) * kLatentThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int head_jobs = (a.heads + kQHeads - 1) / kQHeads;
-  if (job >= a.n * (1 + head_jobs)) return;       // the whole warp
+  if (job >= a.n * (FUSED ? head_jobs : 1 + head_jobs)) return;       // the whole warp
   const Quads quads(lane % kRopeLanes, kRope, a.style);
-  if (job >= a.n) {
-    // query heads h0 .. h0 + 15 of one token, four at a time, 8 lanes each
-    const int64_t tok = (job - a.n) / head_jobs;
-    const int h0 = static_cast<int>((job - a.n) % head_jobs) * kQHeads + lane / kRopeLanes;
-    const int64_t pos = a.positions[tok];
-    uint4 raw[kQHeads / 4];
+  const bool has_row = job < a.n, has_heads = FUSED || !has_row;
+  // job n + i (FUSED: the jobs from n on, and the first n for their own token's first heads)
+  const int more = FUSED ? head_jobs - 1 : head_jobs;
+  const int64_t tok = has_row ? job : (job - a.n) / more;
+  const int chunk = has_row ? 0 : static_cast<int>((job - a.n) % more) + (FUSED ? 1 : 0);
+  const int h0 = chunk * kQHeads + lane / kRopeLanes;
+  const int64_t pos = a.positions[tok], slot = has_row ? a.slots[tok] : 0;
+  // query heads: four at a time, 8 lanes each
+  uint4 raw[kQHeads / 4];
 #pragma unroll
-    for (int k = 0; k < kQHeads / 4; ++k)
-      raw[k] = h0 + 4 * k < a.heads ? load_quads(a.q_pe + tok * a.q_pe_tok + (h0 + 4 * k) * a.q_pe_head, quads) : make_uint4(0, 0, 0, 0);
-    if (pos < 0 || pos >= a.max_pos) return;
-    Turn t;
-    t.load(a.cos_sin + pos * kRope, kRope, lane % kRopeLanes);
+  for (int k = 0; k < kQHeads / 4; ++k)
+    raw[k] = has_heads && h0 + 4 * k < a.heads ? load_quads(a.q_pe + tok * a.q_pe_tok + (h0 + 4 * k) * a.q_pe_head, quads)
+                                               : make_uint4(0, 0, 0, 0);
+  // the latent row: lane l holds dims 8 l .. and 256 + 8 l .. of c_kv, and lanes 0..7 the rope dims
+  const bool rope = lane < kRopeLanes;
+  uint4 raw0{}, raw1{}, raw2{};
+  if (has_row) {
+    raw0 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 8 * lane);
+    raw1 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 256 + 8 * lane);
+    if (rope) raw2 = load_quads(a.k_pe + tok * a.k_pe_stride, quads);
+  }
+  if (pos < 0 || pos >= a.max_pos) return;
+  Turn t;
+  t.load(a.cos_sin + pos * kRope, kRope, lane % kRopeLanes);
+  if (has_heads) {
 #pragma unroll
     for (int k = 0; k < kQHeads / 4; ++k) {
       if (h0 + 4 * k >= a.heads) continue;
-      float x[8];
-      dev::bf16x8_to_float(raw[k], x);
-      t.apply(x, a.style);
-      store_quads(a.q + (tok * a.heads + h0 + 4 * k) * kLatent + kDv, quads, pack8(x));
+      float y[8];
+      dev::bf16x8_to_float(raw[k], y);
+      t.apply(y, a.style);
+      store_quads(a.q + (tok * a.heads + h0 + 4 * k) * kLatent + kDv, quads, pack8(y));
     }
-    return;
   }
-  // the latent row: lane l holds dims 8 l .. and 256 + 8 l .. of c_kv, and lanes 0..7 the rope dims
-  const int64_t tok = job;
-  const int64_t slot = a.slots[tok], pos = a.positions[tok];
-  const bool rope = lane < kRopeLanes;
-  const uint4 raw0 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 8 * lane);
-  const uint4 raw1 = *reinterpret_cast<const uint4*>(a.c_kv + tok * a.c_kv_stride + 256 + 8 * lane);
-  const uint4 raw2 = rope ? load_quads(a.k_pe + tok * a.k_pe_stride, quads) : make_uint4(0, 0, 0, 0);
-  if (slot < 0 || slot >= a.num_slots || pos < 0 || pos >= a.max_pos) return;
+  if (!has_row || slot < 0 || slot >= a.num_slots) return;
   float x[3][8];
   dev::bf16x8_to_float(raw0, x[0]);
   dev::bf16x8_to_float(raw1, x[1]);
   dev::bf16x8_to_float(raw2, x[2]);
-  if (rope) {
-    Turn t;
-    t.load(a.cos_sin + pos * kRope, kRope, lane);
-    t.apply(x[2], a.style);
-  }
+  if (rope) t.apply(x[2], a.style);
   if (a.kv_dtype == KV_NVFP4) {
     store_nvfp4(a, slot, x[0], 8 * lane, 8 * lane + 4, false, true);
     store_nvfp4(a, slot, x[1], 256 + 8 * lane, 256 + 8 * lane + 4, false, true);
@@ -521,10 +527,13 @@ cudaError_t launch_heads(GqaAppendArgs a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s) {
-  const int64_t jobs = a.n * (1 + (a.heads + kQHeads - 1) / kQHeads);
+  const int head_jobs = (a.heads + kQHeads - 1) / kQHeads;
+  const bool fused = a.n >= kFusedTokens && head_jobs > 0;
+  const int64_t jobs = a.n * (fused ? head_jobs : 1 + head_jobs);
   const int64_t ctas = (jobs * 32 + kLatentThreads - 1) / kLatentThreads;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  mla_append_rope_kernel<<<static_cast<unsigned>(ctas), kLatentThreads, 0, s>>>(a);
+  if (fused) mla_append_rope_kernel<true><<<static_cast<unsigned>(ctas), kLatentThreads, 0, s>>>(a);
+  else mla_append_rope_kernel<false><<<static_cast<unsigned>(ctas), kLatentThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
