@@ -221,6 +221,11 @@ struct Query {
 template <int D, int NT>
 struct RawQuery {
   uint4 v[NT][D / 64][2];
+  // Towards L2 only: 128 bytes per lane and step.
+  __device__ static void fetch(const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
+    const char* p = reinterpret_cast<const char*>(a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0) * D);
+    for (int i = lane * 128; i < s.heads * D * 2; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+  }
   __device__ void load(const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -474,34 +479,60 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   }
 }
 
-// Sums the O^T of the four warps into warp 0's, in a fixed order, through two warps' worth of buffer.
+// Sums the four warps' O^T so that warp w is left with the sum of its quarter of the tiles, w D / 64 .., in the
+// first elements of o: halves first (with warp ^ 2), then quarters (with warp ^ 1), (o0 + o2) + (o1 + o3) for
+// every tile. Between the two exchanges a warp writes where only it has read.
 template <int D, int NT>
-__device__ __forceinline__ void sum_warps(float (&o)[D / 16][NT][4], float4* buf, int warp, int lane) {
-  constexpr int kVec = D / 16 * NT * 32;
+__device__ __forceinline__ void scatter_sum(float (&o)[D / 16][NT][4], float4* buf, int warp, int lane) {
+  constexpr int kHalfTiles = D / 32, kQuarter = D / 64, kVec = kHalfTiles * NT * 32;
 #pragma unroll
-  for (int step = kWarps / 2; step >= 1; step /= 2) {
-    if (warp >= step && warp < 2 * step) {
+  for (int i = 0; i < kHalfTiles; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+    for (int n = 0; n < NT; ++n) {
+      float4 out;
+      float* v = &out.x;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          buf[(warp - step) * kVec + (i * NT + n) * 32 + lane] = make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+      for (int k = 0; k < 4; ++k) {
+        v[k] = warp & 2 ? o[i][n][k] : o[kHalfTiles + i][n][k];
+        o[i][n][k] = warp & 2 ? o[kHalfTiles + i][n][k] : o[i][n][k];
+      }
+      buf[warp * kVec + (i * NT + n) * 32 + lane] = out;
     }
-    __syncthreads();
-    if (warp < step) {
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
+  for (int i = 0; i < kHalfTiles; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float4 v = buf[warp * kVec + (i * NT + n) * 32 + lane];
-          o[i][n][0] += v.x;
-          o[i][n][1] += v.y;
-          o[i][n][2] += v.z;
-          o[i][n][3] += v.w;
-        }
+    for (int n = 0; n < NT; ++n) {
+      const float4 v = buf[(warp ^ 2) * kVec + (i * NT + n) * 32 + lane];
+      o[i][n][0] += v.x;
+      o[i][n][1] += v.y;
+      o[i][n][2] += v.z;
+      o[i][n][3] += v.w;
     }
-    if (step > 1) __syncthreads();
-  }
+#pragma unroll
+  for (int i = 0; i < kQuarter; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float4 out;
+      float* v = &out.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = warp & 1 ? o[i][n][k] : o[kQuarter + i][n][k];
+        o[i][n][k] = warp & 1 ? o[kQuarter + i][n][k] : o[i][n][k];
+      }
+      buf[(warp ^ 2) * kVec + (i * NT + n) * 32 + lane] = out;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuarter; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float4 v = buf[(warp ^ 3) * kVec + (i * NT + n) * 32 + lane];
+      o[i][n][0] += v.x;
+      o[i][n][1] += v.y;
+      o[i][n][2] += v.z;
+      o[i][n][3] += v.w;
+    }
 }
 
 // 2^(top - M) / sum_w 2^(lse_w - M) over the four warps' lse at stride kH, M their maximum: what a sum that
@@ -524,31 +555,35 @@ __device__ __forceinline__ float weigh(const float* lse, float top, float& joine
   return mine;
 }
 
-// Warp 0's finished O^T (normalised) and base-2 lse of a segment's heads to out and lse.
-template <int D, int NT>
-__device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegment& s, const float (&o)[D / 16][NT][4],
+// The first TILES tiles of o (normalised), which are O^T's tiles tile0 .., and the base-2 lse of a segment's heads, to
+// out and lse. A lane holds 2 TILES consecutive dims of each of its heads.
+template <int D, int NT, int TILES>
+__device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegment& s, const float (&o)[D / 16][NT][4], int tile0,
                                           const float (&L)[NT][2], int lane) {
   const int g = lane >> 2, t = lane & 3;
   const int64_t row0 = static_cast<int64_t>(s.req) * a.heads + s.head0;
+  // tile i of a 128-dim half: dims 16 g + 2 i, 16 g + 2 i + 1 of it (D = 64: 8 g + ...)
+  const int dim0 = D == 64 ? 8 * g + 2 * tile0 : 128 * (tile0 / 8) + 16 * g + 2 * (tile0 % 8);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int h = 8 * n + 2 * t + e;
       if (h >= s.heads) continue;
-      uint16_t* dst = a.out + (row0 + h) * D;
-      if constexpr (D == 64) {
-        *reinterpret_cast<uint4*>(dst + 8 * g) =
-            make_uint4(dev::pack_bf16x2(o[0][n][e], o[0][n][2 + e]), dev::pack_bf16x2(o[1][n][e], o[1][n][2 + e]),
-                       dev::pack_bf16x2(o[2][n][e], o[2][n][2 + e]), dev::pack_bf16x2(o[3][n][e], o[3][n][2 + e]));
+      uint16_t* dst = a.out + (row0 + h) * D + dim0;
+      uint32_t w[TILES];
+#pragma unroll
+      for (int i = 0; i < TILES; ++i) w[i] = dev::pack_bf16x2(o[i][n][e], o[i][n][2 + e]);
+      if constexpr (TILES == 1) {
+        *reinterpret_cast<uint32_t*>(dst) = w[0];
+      } else if constexpr (TILES == 2) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
       } else {
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 4)
-          *reinterpret_cast<uint4*>(dst + 128 * (i / 8) + 16 * g + 2 * (i % 8)) =
-              make_uint4(dev::pack_bf16x2(o[i][n][e], o[i][n][2 + e]), dev::pack_bf16x2(o[i + 1][n][e], o[i + 1][n][2 + e]),
-                         dev::pack_bf16x2(o[i + 2][n][e], o[i + 2][n][2 + e]), dev::pack_bf16x2(o[i + 3][n][e], o[i + 3][n][2 + e]));
+        for (int i = 0; i < TILES; i += 4)
+          *reinterpret_cast<uint4*>(dst + 128 * (i / 8) + 2 * (i % 8)) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
       }
-      if (a.lse && g == 0) a.lse[row0 + h] = L[n][e] * 0.69314718055994531f;
+      if (a.lse && g == 0 && tile0 == 0) a.lse[row0 + h] = L[n][e] * 0.69314718055994531f;
     }
 }
 
@@ -604,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   const int t = lane & 3, g = lane >> 2;
 #pragma unroll 1
   for (int si = w.begin; si < w.end;) {
+    if (Query<D, NT>::kShared && si != w.begin) raw.load(a, s, lane);
     // of a Q^T in shared memory each warp of a team writes its part; none still reads the last segment's, which
     // ended at a barrier
     static_assert(!Query<D, NT>::kShared || D / 64 == kWarps, "a 64-dim group per warp");
@@ -634,7 +670,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
     GqaSegment next = s;
     if (++si < w.end) {
       next = load_record(a.segs + si);
-      raw.load(a, next, lane);
+      if constexpr (!Query<D, NT>::kShared) raw.load(a, next, lane);
+      else RawQuery<D, NT>::fetch(a, next, lane);
     }
     // this warp's l over its lanes, and its lse
     const float vref = kref == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(max(127 + kref, 1)) << 23);
@@ -670,9 +707,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
           st.o[i][n][2 + e] *= c;
         }
       }
-    if constexpr (TEAM > 1) sum_warps<D, NT>(st.o, join, warp, lane);
+    // from here on a warp of a team owns a quarter of the tiles, the first kOwn of st.o
+    constexpr int kOwn = D / 16 / TEAM;
+    const int tile0 = member * kOwn;
+    if constexpr (TEAM > 1) scatter_sum<D, NT>(st.o, join, warp, lane);
     if (s.partial < 0) {
-      if (member == 0) write_out<D, NT>(a, s, st.o, L, lane);
+      write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
       s = next;
       continue;
     }
@@ -680,54 +720,54 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
     bool top = s.top_counter < 0;
 #pragma unroll 1
     while (true) {
-      int last = 0;
-      if (member == 0) {
-        float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kH * D);
+      float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kH * D) + tile0 * NT * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+      for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32 + lane, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
-        if (g == 0) {
+        for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
+      if (member == 0 && g == 0) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(slot) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) last = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
-        if (TEAM > 1 && lane == 0) *flag = last;
+        for (int n = 0; n < NT; ++n)
+          __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(slot) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
       }
+      // arrive once all of the slot is written
+      __threadfence();
+      int last = 0;
       if constexpr (TEAM > 1) {
+        __syncthreads();
+        if (threadIdx.x == 0) *flag = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
         __syncthreads();
         last = *flag;
       } else {
+        __syncwarp();
+        if (lane == 0) last = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
         last = __shfl_sync(kFull, last, 0);
       }
       if (last == 0) break;
-      // The last arrival: every slot is written. The team's warps take the slots in turn, a few at a
-      // time with their lse, under a running maximum.
+      // The last arrival: every slot is written. Each warp joins its tiles of all slots, in their order, a few
+      // slots at a time with their lse, under a running maximum.
       __threadfence();
       if (member == 0 && lane == 0) a.counters[counter] = 0;        // ready for the next run
       const float* gl = a.part_lse + static_cast<int64_t>(first) * kH + 2 * t;
-      const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(first) * kH * D) + lane;
+      const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(first) * kH * D) + tile0 * NT * 32 + lane;
       float M[NT][2], W[NT][2];
       st.clear();
 #pragma unroll
       for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = -INFINITY, W[n][0] = W[n][1] = 0.0f;
-      constexpr int kVecs = P::kCtas == 3 ? 16 : 32;
-      constexpr int kBatch = D / 16 * NT >= kVecs ? 1 : kVecs / (D / 16 * NT);
+      constexpr int kVecs = P::kCtas == 3 ? 16 : 32;                // 16-byte loads in flight of a lane
+      constexpr int kBatch = kOwn * NT >= kVecs ? 1 : kVecs / (kOwn * NT) > 8 ? 8 : kVecs / (kOwn * NT);
 #pragma unroll 1
-      for (int k0 = member; k0 < count; k0 += TEAM * kBatch) {
-        float4 v[kBatch][D / 16][NT];
+      for (int k0 = 0; k0 < count; k0 += kBatch) {
+        float4 v[kBatch][kOwn][NT];
         float2 x[kBatch][NT];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-          const int k = k0 + j * TEAM;
+          const int k = k0 + j;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             x[j][n] = k < count ? __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n)) : make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int i = 0; i < kOwn; ++i)
               v[j][i][n] = k < count ? __ldcg(go + static_cast<int64_t>(k) * (kH * D / 4) + (i * NT + n) * 32) : make_float4(0, 0, 0, 0);
           }
         }
@@ -735,65 +775,43 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = M[n][e];
+            float m = M[n][e];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) top = dev::max_nan(top, e ? x[j][n].y : x[j][n].x);
-            const float c = top == -INFINITY ? 1.0f : dev::fast_exp2(M[n][e] - top);
+            for (int j = 0; j < kBatch; ++j) m = dev::max_nan(m, e ? x[j][n].y : x[j][n].x);
+            const float c = m == -INFINITY ? 1.0f : dev::fast_exp2(M[n][e] - m);
             W[n][e] *= c;
-            M[n][e] = top;
+            M[n][e] = m;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            for (int i = 0; i < kOwn; ++i) {
               st.o[i][n][e] *= c;
               st.o[i][n][2 + e] *= c;
             }
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-              const float z = top == -INFINITY ? 0.0f : dev::fast_exp2((e ? x[j][n].y : x[j][n].x) - top);
+              const float z = m == -INFINITY ? 0.0f : dev::fast_exp2((e ? x[j][n].y : x[j][n].x) - m);
               W[n][e] += z;
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
+              for (int i = 0; i < kOwn; ++i) {
                 st.o[i][n][e] += z * (e ? v[j][i][n].y : v[j][i][n].x);
                 st.o[i][n][2 + e] += z * (e ? v[j][i][n].w : v[j][i][n].z);
               }
             }
           }
       }
-      if constexpr (TEAM > 1) {
-        // the warps' maxima and sums, as at a segment's end
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (g == 0) wl[warp * kH + 8 * n + 2 * t + e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
-        __syncthreads();
+        for (int e = 0; e < 2; ++e) {
+          const float c = W[n][e] == 0.0f ? 0.0f : __fdividef(1.0f, W[n][e]);
+          L[n][e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mine = weigh(wl + 8 * n + 2 * t + e, M[n][e], L[n][e]);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              st.o[i][n][e] *= mine;
-              st.o[i][n][2 + e] *= mine;
-            }
+          for (int i = 0; i < kOwn; ++i) {
+            st.o[i][n][e] *= c;
+            st.o[i][n][2 + e] *= c;
           }
-        sum_warps<D, NT>(st.o, join, warp, lane);
-      } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mine = W[n][e] == 0.0f ? 0.0f : 1.0f / W[n][e];
-            L[n][e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              st.o[i][n][e] *= mine;
-              st.o[i][n][2 + e] *= mine;
-            }
-          }
-      }
+        }
       if (top) {
-        if (member == 0) write_out<D, NT>(a, s, st.o, L, lane);
+        write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
         break;
       }
       slot = s.sub_slot;
