@@ -444,10 +444,13 @@ typedef struct {
   int32_t max_group_segments;  /* most segments of one pair */
   int32_t num_partials;        /* FP32 split partials held in the workspace */
   int32_t max_worker_pages, min_worker_pages;
+  int32_t table_entries;       /* entries of kv_indices that the plan may address: kv_indptr[batch] */
+  int32_t reserved;
   int64_t total_pages;         /* visible pages, summed over requests (of one KV head) */
   int64_t total_tokens;        /* visible tokens, summed over requests */
   uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;
-  uint64_t status_offset;      /* int32 status word, as in qkvp_plan */
+  uint64_t status_offset;      /* int32 status word, as in qkvp_plan; after a run that left it non-zero,
+                                  plan again before the next */
   uint64_t magic;
 } gqa_plan;
 

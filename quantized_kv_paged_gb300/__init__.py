@@ -50,7 +50,7 @@ class gqa_plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_heads", "num_kv_heads", "head_dim", "page_size", "cache_dtype", "window", "sinks",
         "num_workers", "warps_per_worker", "num_segments", "num_split_groups", "max_group_segments", "num_partials",
-        "max_worker_pages", "min_worker_pages")] + [
+        "max_worker_pages", "min_worker_pages", "table_entries", "reserved")] + [
         ("total_pages", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
         ("workspace_bytes", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64),
         ("partial_o_offset", ctypes.c_uint64), ("partial_lse_offset", ctypes.c_uint64),
@@ -426,7 +426,10 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
     pages, heads_kv, kv_dim = _head_pool(kv_data, kv_scale, T)
     if heads_kv != plan.num_kv_heads or kv_dim != dim:
         raise ValueError(f"kv_data has {heads_kv} heads of {kv_dim}, the plan {plan.num_kv_heads} of {dim}")
-    _dense("kv_indices", kv_indices, (kv_indices.shape[0],), T.i32)
+    entries = kv_indices.shape[0]
+    _dense("kv_indices", kv_indices, (entries,), T.i32)
+    if entries < plan.table_entries:
+        raise ValueError(f"kv_indices has {entries} entries, the plan's page table {plan.table_entries}")
     if lse is not None:
         _dense("lse", lse, (batch, heads), T.f32)
     on = _launch_on(stream, (q, kv_data, kv_scale, kv_indices, out, lse, workspace))

@@ -361,6 +361,7 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   plan->num_partials = static_cast<int32_t>(slots);
   plan->max_worker_pages = info.max_pages;
   plan->min_worker_pages = info.min_pages;
+  plan->table_entries = batch > 0 ? kv_indptr_host[batch] : 0;
   plan->total_pages = pages;
   plan->total_tokens = tokens;
   plan->table_bytes = t.bytes;

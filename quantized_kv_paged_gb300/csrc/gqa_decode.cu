@@ -92,7 +92,8 @@ struct Range {
   int lim, win, sink;
   __device__ Range(const GqaSegment& s, int t0) : lim(s.len - t0), win(s.win_begin - t0), sink(s.sink_end - t0) {}
   __device__ bool sees(int i) const { return i < lim && (i >= win || i < sink); }
-  __device__ bool any(int n) const { return lim > 0 && (sink > 0 || win < min(lim, n)); }
+  // any of the tokens [i, i + n) / all of the tokens [0, n)
+  __device__ bool any(int i, int n) const { return i < min(sink, lim) || max(win, i) < min(lim, i + n); }
   __device__ bool all(int n) const { return lim >= n && (win <= 0 || sink >= n); }
 };
 
@@ -186,6 +187,11 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
   }
 }
 
+// The pool to the TMA: boxes of a unit's K or V, and of a quarter of it.
+struct PoolMaps {
+  CUtensorMap unit, piece;
+};
+
 // O^T and softmax state of one warp; column e of tile nt is head 8 nt + 2 (lane % 4) + e.
 template <int D, int NT>
 struct State {
@@ -217,23 +223,22 @@ struct Query {
   float scale[NT][2];       // logit factor of the lane's columns: sm_scale log2(e) / (the head's power of two)
 };
 
-// The lane's share of a segment's queries as stored: 16 dims of each 64-dim group of heads g, 8 + g.
-template <int D, int NT>
+// The lane's share of a segment's queries as stored: 16 dims of GROUPS 64-dim groups, from group c0 on, of heads g
+// and 8 + g. A team that keeps Q^T in shared memory splits the groups among its warps.
+template <int D, int NT, int TEAM>
 struct RawQuery {
-  uint4 v[NT][D / 64][2];
-  // Towards L2 only: 128 bytes per lane and step.
-  __device__ static void fetch(const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
-    const char* p = reinterpret_cast<const char*>(a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0) * D);
-    for (int i = lane * 128; i < s.heads * D * 2; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
-  }
-  __device__ void load(const GqaDecodeArgs& a, const GqaSegment& s, int lane) {
+  static constexpr bool kSplit = Query<D, NT>::kShared && TEAM > 1;
+  static constexpr int kGroups = kSplit ? 1 : D / 64;
+  static_assert(!kSplit || D / 64 == TEAM, "a 64-dim group per warp");
+  uint4 v[NT][kGroups][2];
+  __device__ void load(const GqaDecodeArgs& a, const GqaSegment& s, int member, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int h = 8 * n + g;
-      const uint16_t* row = a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0 + h) * D + 16 * t;
+      const uint16_t* row = a.q + (static_cast<int64_t>(s.req) * a.heads + s.head0 + h) * D + (kSplit ? 64 * member : 0) + 16 * t;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
+      for (int c = 0; c < kGroups; ++c)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           v[n][c][k] = h < s.heads ? __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 8 * k)) : make_uint4(0, 0, 0, 0);
@@ -241,46 +246,59 @@ struct RawQuery {
   }
 };
 
-// `only` >= 0: of a Q^T in shared memory, this 64-dim group alone (the others are the team's other warps').
-template <int D, int NT>
-__device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D, NT>& raw, float scale_log2, int only, int lane) {
-  const int t = lane & 3;
+// `top`: shared memory [kWarps][kH] for the largest |q| of each warp's groups, where the groups are split.
+template <int D, int NT, int TEAM>
+__device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D, NT, TEAM>& raw, float scale_log2, float* top, int member, int lane) {
+  using R = RawQuery<D, NT, TEAM>;
+  const int g = lane >> 2, t = lane & 3;
+  float amax[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float amax = 0.0f;
+    amax[n] = 0.0f;
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c)
+    for (int c = 0; c < R::kGroups; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[8];
         dev::bf16x8_to_float(raw.v[n][c][k], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+        for (int i = 0; i < 8; ++i) amax[n] = fmaxf(amax[n], fabsf(x[i]));
       }
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+    amax[n] = fmaxf(amax[n], __shfl_xor_sync(kFull, amax[n], 1));
+    amax[n] = fmaxf(amax[n], __shfl_xor_sync(kFull, amax[n], 2));
+    if (R::kSplit && t == 0) top[member * kH + 8 * n + g] = amax[n];
+  }
+  if constexpr (R::kSplit) {
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) amax[n] = fmaxf(amax[n], top[w * kH + 8 * n + g]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
     // 2^e that brings the largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it
-    const int ex = static_cast<int>(__float_as_uint(amax) >> 23);
-    const int e = amax == 0.0f ? 0 : min(126, 14 + 127 - ex);
+    const int ex = static_cast<int>(__float_as_uint(amax[n]) >> 23);
+    const int e = amax[n] == 0.0f ? 0 : min(126, 14 + 127 - ex);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      if (Query<D, NT>::kShared && only >= 0 && c != only) continue;
+    for (int c = 0; c < R::kGroups; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t w[4] = {raw.v[n][c][k].x, raw.v[n][c][k].y, raw.v[n][c][k].z, raw.v[n][c][k].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t x = dev::bf16x2_to_f16x2(w[i], up);
-          if constexpr (Query<D, NT>::kShared) tc::sts_u32(Q.addr + ((c * 4 + 2 * k + i / 2) * 32 + lane) * 16 + (i % 2) * 8 + n * 4, x);
+          if constexpr (Query<D, NT>::kShared) tc::sts_u32(Q.addr + (((R::kSplit ? member : c) * 4 + 2 * k + i / 2) * 32 + lane) * 16 + (i % 2) * 8 + n * 4, x);
           else Q.q[c][2 * k + i / 2][i % 2][n] = x;
         }
       }
-    }
     const float f = scale_log2 * down;
 #pragma unroll
     for (int e2 = 0; e2 < 2; ++e2) Q.scale[n][e2] = __shfl_sync(kFull, f, 4 * (2 * t + e2));
   }
+  if constexpr (R::kSplit) __syncthreads();
+  else if constexpr (Query<D, NT>::kShared) __syncwarp();
 }
 
 // One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens are not visible.
@@ -589,7 +607,7 @@ __device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegme
 
 // TEAM warps share a worker's segments: 4 (the CTA) or 1 (each warp a worker of its own, no barrier at all).
 template <int D, bool E4M3, int NT, int TEAM>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decode_kernel(const GqaDecodeArgs a, const __grid_constant__ CUtensorMap map) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decode_kernel(const GqaDecodeArgs a, const __grid_constant__ PoolMaps maps) {
   using P = Shape<D, NT, TEAM>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = dev::smem_u32(smem);
@@ -609,13 +627,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   bool dead = (base & 1023) != 0;          // the swizzle needs the ring aligned; never expected
   if (dead && threadIdx.x == 0) atomicOr(a.status, 2);
   // a segment's queries are loaded before what precedes its first unit: the first fills, the join of the last segment
-  RawQuery<D, NT> raw;
+  RawQuery<D, NT, TEAM> raw;
   GqaSegment s = w.first;
-  if (w.begin < w.end) raw.load(a, s, lane);
+  if (w.begin < w.end) raw.load(a, s, member, lane);
   Feed<P::kUnits, TEAM> feed(a, w, member);
   uint32_t loaded = 0, parity = 0;         // bit i: stage i holds a unit to take / parity of its barrier
   auto fill = [&](int stage) {
-    const bool ok = feed.si < feed.se && !dead && feed.page >= 0 && feed.page < a.num_pages && Range(feed.s, feed.t0).any(P::kTokens);
+    const bool ok = feed.si < feed.se && !dead && feed.page >= 0 && feed.page < a.num_pages && Range(feed.s, feed.t0).any(0, P::kTokens);
     loaded = (loaded & ~(1u << stage)) | (ok ? 1u << stage : 0u);
     if (ok && lane == 0) {
       const int64_t kb = static_cast<int64_t>(feed.page) * 2 * a.kv_heads + feed.s.kv_head, vb = kb + a.kv_heads;
@@ -623,9 +641,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
       cp_async4(scales + 8 * stage, a.kv_scale + kb);
       cp_async4(scales + 8 * stage + 4, a.kv_scale + vb);
       cp_async_arrive(bar);
-      tc::mbar_arrive_expect_tx(bar, kUnit);
-      tma_load_2d(dst, &map, 0, static_cast<int>(kb * (kPage * D / 128) + feed.sub * (kHalf / 128)), bar);
-      tma_load_2d(dst + kHalf, &map, 0, static_cast<int>(vb * (kPage * D / 128) + feed.sub * (kHalf / 128)), bar);
+      const int krow = static_cast<int>(kb * (kPage * D / 128)) + feed.sub * (kHalf / 128);
+      const int vrow = static_cast<int>(vb * (kPage * D / 128)) + feed.sub * (kHalf / 128);
+      const Range range(feed.s, feed.t0);
+      if (range.all(P::kTokens)) {
+        tc::mbar_arrive_expect_tx(bar, kUnit);
+        tma_load_2d(dst, &maps.unit, 0, krow, bar);
+        tma_load_2d(dst + kHalf, &maps.unit, 0, vrow, bar);
+      } else {
+        // of a unit at an edge only the quarters that hold a visible token; what is left in the others is masked
+        constexpr int kPiece = P::kTokens / 4;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bytes += range.any(i * kPiece, kPiece) ? 2 * kHalf / 4 : 0;
+        tc::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!range.any(i * kPiece, kPiece)) continue;
+          tma_load_2d(dst + i * (kHalf / 4), &maps.piece, 0, krow + i * (kHalf / 4 / 128), bar);
+          tma_load_2d(dst + kHalf + i * (kHalf / 4), &maps.piece, 0, vrow + i * (kHalf / 4 / 128), bar);
+        }
+      }
     }
     feed.next(member);
   };
@@ -639,15 +675,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   const int t = lane & 3, g = lane >> 2;
 #pragma unroll 1
   for (int si = w.begin; si < w.end;) {
-    if (Query<D, NT>::kShared && si != w.begin) raw.load(a, s, lane);
-    // of a Q^T in shared memory each warp of a team writes its part; none still reads the last segment's, which
-    // ended at a barrier
-    static_assert(!Query<D, NT>::kShared || D / 64 == kWarps, "a 64-dim group per warp");
-    convert_query<D, NT>(Q, raw, a.scale_log2, TEAM > 1 ? warp : -1, lane);
-    if constexpr (Query<D, NT>::kShared) {
-      if constexpr (TEAM > 1) __syncthreads();
-      else __syncwarp();
-    }
+    // no warp still reads the last segment's Q^T in shared memory: that segment ended at a barrier
+    convert_query<D, NT, TEAM>(Q, raw, a.scale_log2, wl, member, lane);
     st.clear();
     int kref = INT32_MIN;
 #pragma unroll 1
@@ -670,8 +699,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
     GqaSegment next = s;
     if (++si < w.end) {
       next = load_record(a.segs + si);
-      if constexpr (!Query<D, NT>::kShared) raw.load(a, next, lane);
-      else RawQuery<D, NT>::fetch(a, next, lane);
+      raw.load(a, next, member, lane);
     }
     // this warp's l over its lanes, and its lse
     const float vref = kref == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(max(127 + kref, 1)) << 23);
@@ -847,12 +875,12 @@ EncodeTiledFn encode_tiled() {
 
 // The pool as rows of 128 bytes: a unit's K or V is 32 consecutive rows whatever the head size, and the
 // 128-byte swizzle is a function of the linear offset in it alone.
-cudaError_t pool_map(const GqaDecodeArgs& a, CUtensorMap* map) {
+cudaError_t pool_map(const GqaDecodeArgs& a, cuuint32_t box_rows, CUtensorMap* map) {
   const EncodeTiledFn fn = encode_tiled();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t rows = static_cast<cuuint64_t>(a.num_pages) * 2 * a.kv_heads * kPage * a.dim / 128;
   const cuuint64_t dims[2] = {128, rows}, strides[1] = {128};
-  const cuuint32_t box[2] = {128, kHalf / 128}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.kv), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -860,7 +888,7 @@ cudaError_t pool_map(const GqaDecodeArgs& a, CUtensorMap* map) {
 }
 
 template <int D, bool E4M3, int NT, int TEAM>
-cudaError_t launch(const GqaDecodeArgs& a, const CUtensorMap& map, cudaStream_t st) {
+cudaError_t launch(const GqaDecodeArgs& a, const PoolMaps& maps, cudaStream_t st) {
   constexpr int bytes = Shape<D, NT, TEAM>::kBytes;
   auto kernel = gqa_decode_kernel<D, E4M3, NT, TEAM>;
   // once per device: the attribute belongs to the device's copy of the kernel
@@ -874,30 +902,31 @@ cudaError_t launch(const GqaDecodeArgs& a, const CUtensorMap& map, cudaStream_t 
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  kernel<<<a.num_workers * TEAM / kWarps, kThreads, bytes, st>>>(a, map);
+  kernel<<<a.num_workers * TEAM / kWarps, kThreads, bytes, st>>>(a, maps);
   return cudaGetLastError();
 }
 
 template <int D, bool E4M3>
-cudaError_t launch_dim(const GqaDecodeArgs& a, const CUtensorMap& map, cudaStream_t st) {
-  if (a.heads / a.kv_heads > 8) return a.team == 1 ? launch<D, E4M3, 2, 1>(a, map, st) : launch<D, E4M3, 2, 4>(a, map, st);
-  return a.team == 1 ? launch<D, E4M3, 1, 1>(a, map, st) : launch<D, E4M3, 1, 4>(a, map, st);
+cudaError_t launch_dim(const GqaDecodeArgs& a, const PoolMaps& maps, cudaStream_t st) {
+  if (a.heads / a.kv_heads > 8) return a.team == 1 ? launch<D, E4M3, 2, 1>(a, maps, st) : launch<D, E4M3, 2, 4>(a, maps, st);
+  return a.team == 1 ? launch<D, E4M3, 1, 1>(a, maps, st) : launch<D, E4M3, 1, 4>(a, maps, st);
 }
 
 }  // namespace
 
 cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t st) {
-  CUtensorMap map;
-  std::memset(&map, 0, sizeof(map));
+  PoolMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
   if (a.kv != nullptr && a.num_pages > 0) {
-    const cudaError_t e = pool_map(a, &map);
+    cudaError_t e = pool_map(a, kHalf / 128, &maps.unit);
+    if (e == cudaSuccess) e = pool_map(a, kHalf / 4 / 128, &maps.piece);
     if (e != cudaSuccess) return e;
   }
   const bool e4m3 = a.cache_dtype == QKVP_CACHE_E4M3;
   switch (a.dim) {
-    case 64: return e4m3 ? launch_dim<64, true>(a, map, st) : launch_dim<64, false>(a, map, st);
-    case 128: return e4m3 ? launch_dim<128, true>(a, map, st) : launch_dim<128, false>(a, map, st);
-    default: return e4m3 ? launch_dim<256, true>(a, map, st) : launch_dim<256, false>(a, map, st);
+    case 64: return e4m3 ? launch_dim<64, true>(a, maps, st) : launch_dim<64, false>(a, maps, st);
+    case 128: return e4m3 ? launch_dim<128, true>(a, maps, st) : launch_dim<128, false>(a, maps, st);
+    default: return e4m3 ? launch_dim<256, true>(a, maps, st) : launch_dim<256, false>(a, maps, st);
   }
 }
 

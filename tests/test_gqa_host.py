@@ -179,7 +179,8 @@ def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(ValueError, match="current CUDA device"):
         q.gqa_decode_run(**run)
     for kw in (dict(q=bf(2, 4, 128)), dict(q=bf(1, 4, 256)[..., ::2]), dict(kv_data=pool[..., :64]), dict(kv_scale=torch.zeros((4, 4))),
-               dict(out=torch.zeros((1, 4, 128))), dict(lse=torch.zeros((1, 2))), dict(kv_indices=torch.zeros(2, dtype=torch.int64))):
+               dict(out=torch.zeros((1, 4, 128))), dict(lse=torch.zeros((1, 2))), dict(kv_indices=torch.zeros(2, dtype=torch.int64)),
+               dict(kv_indices=i32(1))):
         with pytest.raises(ValueError) as e:
             q.gqa_decode_run(**dict(run, **kw))
         assert "current CUDA device" not in str(e.value), kw
