@@ -76,7 +76,7 @@ class Batch:
 
 @pytest.mark.parametrize("cache", [R.E4M3, R.INT8])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 1), (10, 2), (32, 2), (7, 7), (37, 1), (24, 8)])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 1), (10, 2), (32, 2), (7, 7), (37, 1), (40, 8)])
 def test_ragged_batch(qkvp, cache, dim, heads, kv_heads):
     Batch(RAGGED, heads, kv_heads, dim, cache, seed=heads + dim).check()
 
@@ -171,6 +171,84 @@ def test_repeats_bit_for_bit_and_in_graphs(qkvp):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_two_streams_at_once(qkvp):
+    """Two batches with plans and workspaces of their own, run many times on two streams side by side."""
+    bs = [Batch([3000, 700, 65], 16, 2, 128, R.E4M3, seed=50), Batch([900] * 30, 16, 8, 64, R.INT8, 200, 5, seed=51)]
+    want = [b.run()[:2] for b in bs]
+    plans = [b.plan() for b in bs]
+    outs = [(torch.empty_like(w[0]), torch.empty_like(w[1])) for w in want]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for b, (p, ws), (o, l), st in zip(bs, plans, outs, streams):
+            q.gqa_decode_run(p, b.dev["q"], b.dev["codes"], b.dev["scale"], b.dev["ids"], b.sm_scale, o, l, ws, stream=st)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl)
+
+
+def test_offsets_past_32_bits(qkvp):
+    """Pages at the end of a 6 GiB pool: appended to and attended, at offsets past 2^32."""
+    kv_heads, dim, heads, n = 8, 256, 16, 300
+    pages = (6 << 30) // (2 * kv_heads * 64 * dim)
+    codes = torch.empty((pages, 2, kv_heads, 64, dim), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((pages, 2, kv_heads), device="cuda")
+    ids = np.array([pages - 1, pages - 7, 0, pages - 2, pages // 2, pages - 3], np.int32)
+    rng = np.random.default_rng(60)
+    k, v = (R.to_bf16(rng.standard_normal((n, kv_heads, dim)).astype(np.float32)) for _ in range(2))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")          # noqa: E731
+    dids = torch.from_numpy(ids).cuda()
+    q.gqa_append_rope(k.cuda(), v.cuda(), i32(0, n), i32(0), i32(0, len(ids)), dids, None, R.HALVES, codes, scale, R.E4M3)
+    used = ids[:(n + 63) // 64].astype(np.int64)
+    small_codes, small_scale = np.zeros((6, 2, kv_heads, 64, dim), np.uint8), np.zeros((6, 2, kv_heads), np.float32)
+    R.append_heads(R.bf16_to_f32(k), R.bf16_to_f32(v), [0, n], [0], [0, 6], np.arange(6), None, R.HALVES, small_codes, small_scale, R.E4M3)
+    for i, page in enumerate(used):
+        c = min(64, n - 64 * i)
+        assert np.array_equal(codes[page, :, :, :c].cpu().numpy(), small_codes[i, :, :, :c])
+        assert np.array_equal(scale[page].cpu().numpy(), small_scale[i])
+    query = R.to_bf16(rng.standard_normal((1, heads, dim)).astype(np.float32))
+    args = ([0, 6], [n], heads, kv_heads, dim, R.E4M3)
+    ws = torch.empty(q.gqa_decode_plan(*args).workspace_bytes, dtype=torch.uint8, device="cuda")
+    p = q.gqa_decode_plan(*args, workspace=ws)
+    out, lse = torch.empty((1, heads, dim), dtype=torch.bfloat16, device="cuda"), torch.empty((1, heads), device="cuda")
+    q.gqa_decode_run(p, query.cuda(), codes, scale, dids, 0.1, out, lse, ws)
+    torch.cuda.synchronize()
+    ref = R.attend(R.bf16_to_f32(query), small_codes, small_scale, R.E4M3, [0, 6], np.arange(6), [n], 0.1)
+    R.check_attend(out, lse, ref, n, dim)
+
+
+def test_first_call_of_a_process_is_captured(qkvp):
+    """No eager call goes before: kernel set-up inside a capture, append and decode in one graph."""
+    code = """
+import torch, quantized_kv_paged_gb300 as q
+dev = "cuda"
+codes, scale = torch.zeros((4, 2, 1, 64, 64), dtype=torch.uint8, device=dev), torch.zeros((4, 2, 1), device=dev)
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+k = torch.randn((100, 1, 64), device=dev).bfloat16()
+query, out = torch.randn((1, 2, 64), device=dev).bfloat16(), torch.zeros((1, 2, 64), device=dev).bfloat16()
+tok, held, ptr, ids = i32(0, 100), i32(0), i32(0, 2), i32(3, 1)
+args = ([0, 2], [100], 2, 1, 64, q.CACHE_E4M3)
+ws = torch.empty(q.gqa_decode_plan(*args).workspace_bytes, dtype=torch.uint8, device=dev)
+plan = q.gqa_decode_plan(*args, workspace=ws)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+    q.gqa_append_rope(k, k, tok, held, ptr, ids, None, q.ROPE_HALVES, codes, scale, q.CACHE_E4M3)
+    q.gqa_decode_run(plan, query, codes, scale, ids, 0.125, out, None, ws)
+g.replay()
+torch.cuda.synchronize()
+kv = (codes.view(torch.float8_e4m3fn).float() * scale[..., None, None])[[3, 1], 0, 0].reshape(-1, 64)[:100]
+want = torch.softmax(query[0].float() @ kv.T * 0.125, 1) @ kv
+assert (out[0].float() - want).abs().max() < 0.02, (out, want)
+print("captured first: ok")
+"""
+    import subprocess
+    import sys
+    from tests.conftest import ROOT
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first: ok" in r.stdout, r.stdout + r.stderr
 
 
 def test_nan_in_a_visible_key_reaches_its_head_only(qkvp):

@@ -142,6 +142,8 @@ CASES = [
     # new tokens per request, cached before
     ([1], [0]), ([1, 1, 1, 1, 1], [63, 64, 0, 130, 1]), ([5, 0, 3, 1], [62, 9, 64, 127]), ([64, 65, 63], [0, 63, 1]),
     ([200, 1, 0, 333], [100, 5, 7, 0]), ([0, 0, 2], [0, 4, 30]), ([700], [0]),
+    # few tokens for many requests, one of them with most of two pages
+    ([1] * 20 + [70] + [0, 1] * 10 + [2] * 12, list(range(53))),
 ]
 
 
@@ -152,7 +154,7 @@ def test_gqa_append_rope_bit_exact(qkvp, dim, rot, cache, style):
     rng = np.random.default_rng(dim + rot + 7 * cache + style)
     cs = R.table(1200, rot) if rot else None
     dev_cs = torch.from_numpy(cs).cuda() if rot else None
-    for kv_heads, heads, (new, held) in zip((1, 2, 3, 4, 2, 1, 8), (1, 14, 6, 0, 32, 5, 8), CASES):
+    for kv_heads, heads, (new, held) in zip((1, 2, 3, 4, 2, 1, 8, 2), (1, 14, 7, 0, 32, 5, 16, 4), CASES):
         n = sum(new)
         counts = [(a + b + 63) // 64 + 1 for a, b in zip(new, held)]
         pages = sum(counts) + 2
