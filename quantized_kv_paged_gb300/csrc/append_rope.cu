@@ -206,6 +206,8 @@ __device__ __forceinline__ void store_nvfp4(const MlaAppendArgs& a, int64_t slot
 // reaches twice as many SMs.
 template <bool FUSED>
 __global__ void __launch_bounds__(kLatentThreads) mla_append_rope_kernel(const MlaAppendArgs a) {
+  dev::allow_dependents();
+  dev::wait_for_previous();
   const int64_t job = (static_cast<int64_t>(blockIdx.x) * kLatentThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   const int head_jobs = (a.heads + kQHeads - 1) / kQHeads;
@@ -401,6 +403,8 @@ __global__ void __launch_bounds__(THREADS) gqa_append_rope_kernel(const GqaAppen
   constexpr int kLanes = D / 8;                    // lanes of one token's head
   constexpr int kTok = THREADS / kLanes;           // tokens of one pass over the CTA
   constexpr int kPasses = kPage / kTok;
+  dev::allow_dependents();
+  dev::wait_for_previous();
   if (blockIdx.x >= a.kv_ctas) {
     rotate_queries<D>(a, ((static_cast<int64_t>(blockIdx.x) - a.kv_ctas) * THREADS + threadIdx.x) >> 5);
     return;
@@ -519,9 +523,8 @@ cudaError_t launch_heads(GqaAppendArgs a, cudaStream_t s) {
   const int64_t ctas = kv_ctas + (q_jobs * 32 + threads - 1) / threads;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
   a.kv_ctas = static_cast<uint32_t>(kv_ctas);
-  if (per_token) gqa_append_rope_kernel<D, E4M3, true, kTokenThreads><<<static_cast<unsigned>(ctas), threads, 0, s>>>(a);
-  else gqa_append_rope_kernel<D, E4M3, false, kPageThreads><<<static_cast<unsigned>(ctas), threads, 0, s>>>(a);
-  return cudaGetLastError();
+  auto kernel = per_token ? gqa_append_rope_kernel<D, E4M3, true, kTokenThreads> : gqa_append_rope_kernel<D, E4M3, false, kPageThreads>;
+  return launch_overlapped(kernel, static_cast<unsigned>(ctas), threads, 0, s, a);
 }
 
 }  // namespace
@@ -532,9 +535,7 @@ cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s) {
   const int64_t jobs = a.n * (fused ? head_jobs : 1 + head_jobs);
   const int64_t ctas = (jobs * 32 + kLatentThreads - 1) / kLatentThreads;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  if (fused) mla_append_rope_kernel<true><<<static_cast<unsigned>(ctas), kLatentThreads, 0, s>>>(a);
-  else mla_append_rope_kernel<false><<<static_cast<unsigned>(ctas), kLatentThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(fused ? mla_append_rope_kernel<true> : mla_append_rope_kernel<false>, static_cast<unsigned>(ctas), kLatentThreads, 0, s, a);
 }
 
 cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s) {

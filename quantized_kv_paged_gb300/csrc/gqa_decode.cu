@@ -623,6 +623,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   tc::fence_mbar_init();
   __syncwarp();
 
+  // the launch may overlap the end of the kernel before it in the stream (launch_overlapped)
+  dev::allow_dependents();
+  dev::wait_for_previous();
   const GqaWorker w = load_record(a.workers + (TEAM == 1 ? blockIdx.x * kWarps + warp : blockIdx.x));
   bool dead = (base & 1023) != 0;          // the swizzle needs the ring aligned; never expected
   if (dead && threadIdx.x == 0) atomicOr(a.status, 2);
@@ -902,8 +905,7 @@ cudaError_t launch(const GqaDecodeArgs& a, const PoolMaps& maps, cudaStream_t st
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  kernel<<<a.num_workers * TEAM / kWarps, kThreads, bytes, st>>>(a, maps);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, a.num_workers * TEAM / kWarps, kThreads, bytes, st, a, maps);
 }
 
 template <int D, bool E4M3>

@@ -200,6 +200,12 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return r;
 }
 
+// Programmatic dependent launch. wait_for_previous: everything that the kernels before this one in the stream did is
+// done and visible afterwards. allow_dependents: a following kernel that was launched to overlap may start once all
+// CTAs of this one have said so or ended; it waits for this one's end in its turn.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(nthreads) : "memory");
 }

@@ -237,6 +237,23 @@ cudaError_t upload_table(void* dst, const void* src, size_t n, cudaStream_t st);
 int query_sms();
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Launches a kernel that calls dev::wait_for_previous() before it touches anything that the kernel before it in the
+// stream may have written, so that it may start while that one ends.
+template <class... Params, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t s);
