@@ -286,15 +286,22 @@ __global__ void __launch_bounds__(kLatentThreads) mla_append_rope_kernel(const M
 }
 
 // ------------------------------------------------------------------------------------------------
-// K and V heads. One CTA per (page that the call writes, K or V, head): the block's scale needs the
-// amax of all the page's new tokens, and its older codes change with it, so a block has one owner and
-// no atomics. The CTA keeps the new elements in registers between the amax and the codes.
+// K and V heads. A CTA has one page that the call writes, of K or of V, and walks some of its heads: the
+// block's scale needs the amax of all the page's new tokens, and its older codes change with it, so a
+// block has one owner and no atomics. The new elements stay in registers between the amax and the codes.
+// To find the page takes four dependent reads (request, its length, page table, page id), some 4 us cold:
+// a CTA of many heads pays that once and loads each head's elements while it works on the one before.
 //
 // Which pages are written is known on the device only. The launch has, for request r, floor(n_r / 64) + 2
 // candidates, the most pages that n_r tokens can touch: job c belongs to the last request with
-// tok_indptr[r] / 64 + 2 r <= c. With few tokens there is a job per token instead (and smaller CTAs), and
-// the first token of each page does the work. Idle jobs leave after the search.
+// tok_indptr[r] / 64 + 2 r <= c. With few tokens there is a job per token instead, and the first token of
+// each page does the work, in smaller CTAs of one head that keep the first few tokens only (the others are
+// read again for their codes): 128 single tokens of 8 KV heads took 11 us at the 205 registers that 64 tokens ask
+// for. Idle jobs leave after the search.
 // ------------------------------------------------------------------------------------------------
+
+constexpr int kQueryPasses = 8;
+constexpr int kFillCtas = 300;
 
 // The largest r in [0, batch) with f(r) <= c for a non-decreasing f with f(0) <= c (0 if there is none):
 // 256 probes at a time, one round of loads for up to 256 requests.
@@ -361,10 +368,10 @@ __device__ __forceinline__ Place find_place(const GqaAppendArgs& a, int64_t job)
   return p;
 }
 
-// A warp's query heads: 4 passes over 32 / (D / 8) heads of one token.
+// A warp's query heads: some passes over 32 / (D / 8) heads of one token.
 template <int D>
 __device__ __forceinline__ void rotate_queries(const GqaAppendArgs& a, int64_t job) {
-  constexpr int kLanes = D / 8, kH = 32 / kLanes, kPasses = 4;
+  constexpr int kLanes = D / 8, kH = 32 / kLanes, kPasses = kQueryPasses;
   const int lane = threadIdx.x & 31;
   const int head_jobs = (a.heads + kPasses * kH - 1) / (kPasses * kH);
   if (job >= a.n * head_jobs) return;
@@ -403,111 +410,134 @@ __global__ void __launch_bounds__(THREADS) gqa_append_rope_kernel(const GqaAppen
   constexpr int kLanes = D / 8;                    // lanes of one token's head
   constexpr int kTok = THREADS / kLanes;           // tokens of one pass over the CTA
   constexpr int kPasses = kPage / kTok;
+  constexpr int kHold = PER_TOKEN ? 1 : kPasses;   // passes whose elements stay in registers
   dev::allow_dependents();
   dev::wait_for_previous();
   if (blockIdx.x >= a.kv_ctas) {
     rotate_queries<D>(a, ((static_cast<int64_t>(blockIdx.x) - a.kv_ctas) * THREADS + threadIdx.x) >> 5);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int blocks = 2 * a.kv_heads;
-  const int blk = static_cast<int>(blockIdx.x % blocks);       // K heads, then V heads
-  const bool is_k = blk < a.kv_heads;
-  const int h = is_k ? blk : blk - a.kv_heads;
-  const Place p = find_place<PER_TOKEN>(a, blockIdx.x / blocks);
-  if (p.entry < 0) return;                                     // the whole CTA
+  const int lane = threadIdx.x & 31, l = threadIdx.x % kLanes, mine0 = threadIdx.x / kLanes;
+  const int parts = 2 * a.head_parts;              // of a page: K's heads in head_parts parts, then V's
+  const int part = static_cast<int>(blockIdx.x % parts);
+  const bool is_k = part < a.head_parts;
+  const int per_part = (a.kv_heads + a.head_parts - 1) / a.head_parts;
+  const int h0 = (is_k ? part : part - a.head_parts) * per_part, h1 = min(h0 + per_part, a.kv_heads);
+  const Place p = find_place<PER_TOKEN>(a, blockIdx.x / parts);
+  if (p.entry < 0 || h0 >= h1) return;                         // the whole CTA
   const int64_t page = a.kv_indices[p.entry];
-  const int count = p.last - p.first, mine0 = threadIdx.x / kLanes;
-  const Quads quads(threadIdx.x % kLanes, is_k ? a.rot : 0, a.style);
+  const int count = p.last - p.first;
+  const Quads quads(l, is_k ? a.rot : 0, a.style);
   const int64_t stride = is_k ? a.k_stride : a.v_stride;
-  const uint16_t* src = (is_k ? a.k : a.v) + p.tok * stride + h * D;
-  uint4 raw[kPasses];
-  int64_t pos[kPasses];
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    const int i = k * kTok + mine0;                            // the page's i-th new token
-    raw[k] = make_uint4(0, 0, 0, 0);
-    pos[k] = -1;
-    if (i < count) {
-      raw[k] = load_quads(src + i * stride, quads);
-      pos[k] = a.rot == 0 ? 0 : a.positions ? a.positions[p.tok + i] : p.pos + i;
-      if (a.rot > 0 && pos[k] >= a.max_pos) pos[k] = -1;       // skipped, as a negative one
-    }
-  }
-  if (page < 0 || page >= a.num_pages) return;
-  const int64_t block = page * blocks + blk;
-  const float old = a.kv_scale[block];
-  float x[kPasses][8];
-  float amax = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    if (k * kTok >= count) break;                              // the same for the whole CTA
-    dev::bf16x8_to_float(raw[k], x[k]);
-    if (pos[k] < 0) continue;
-    if (quads.turned) {
+  const uint16_t* src = (is_k ? a.k : a.v) + p.tok * stride;
+  // the page's i-th new token: its elements of head h as stored, and its position (-1: skipped, or none)
+  auto stored = [&](int i, int h) { return i < count ? load_quads(src + i * stride + h * D, quads) : make_uint4(0, 0, 0, 0); };
+  auto position = [&](int i) -> int64_t {
+    if (i >= count) return -1;
+    if (a.rot == 0) return 0;
+    const int64_t at = a.positions ? a.positions[p.tok + i] : p.pos + i;
+    return at < a.max_pos ? max(at, int64_t(-1)) : -1;
+  };
+  auto turned = [&](float (&x)[8], uint4 raw, int64_t at) {
+    dev::bf16x8_to_float(raw, x);
+    if (quads.turned && at >= 0) {
       Turn t;
-      t.load(a.cos_sin + pos[k] * a.rot, a.rot, threadIdx.x % kLanes);
-      t.apply(x[k], a.style);
+      t.load(a.cos_sin + at * a.rot, a.rot, l);
+      t.apply(x, a.style);
     }
+  };
+  uint4 raw[kHold];
+  int at[kHold];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = dev::max_nan(amax, fabsf(x[k][i]));
-  }
-  __shared__ float part[THREADS / 32];
-  auto over_cta = [&](float v) {
+  for (int k = 0; k < kHold; ++k) raw[k] = stored(k * kTok + mine0, h0);
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) at[k] = static_cast<int>(position(k * kTok + mine0));
+  if (page < 0 || page >= a.num_pages) return;
+  const int64_t block0 = page * 2 * a.kv_heads + (is_k ? 0 : a.kv_heads);
+  float old = a.kv_scale[block0 + h0];
+  __shared__ float shared_max[3][THREADS / 32];
+  auto over_cta = [&](float v, int buf) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = dev::max_nan(v, __shfl_xor_sync(kFull, v, o));
-    if (lane == 0) part[threadIdx.x / 32] = v;
+    if (lane == 0) shared_max[buf][threadIdx.x / 32] = v;
     __syncthreads();
-    v = part[0];
+    v = shared_max[buf][0];
 #pragma unroll
-    for (int i = 1; i < THREADS / 32; ++i) v = dev::max_nan(v, part[i]);
+    for (int i = 1; i < THREADS / 32; ++i) v = dev::max_nan(v, shared_max[buf][i]);
     return v;
   };
-  amax = over_cta(amax);
-  const bool finite = amax <= 3.402823466e38f;
-  if (!finite) {
-    // a NaN or an infinity among the new elements: the largest of the others
-    amax = 0.0f;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    float x[kHold][8];
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      if (k * kTok >= count) break;
-      if (pos[k] < 0) continue;
+    for (int k = 0; k < kHold; ++k) turned(x[k], raw[k], at[k]);
+    float next_old = 0.0f;
+    if (h + 1 < h1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (fabsf(x[k][i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[k][i]));
+      for (int k = 0; k < kHold; ++k) raw[k] = stored(k * kTok + mine0, h + 1);
+      next_old = a.kv_scale[block0 + h + 1];
     }
-    __syncthreads();
-    amax = over_cta(amax);
-  }
-  const float need = __fdiv_rn(amax, E4M3 ? 448.0f : 127.0f);
-  float scale = old, shrink = 1.0f;
-  if (p.first == 0 || !(old > 0.0f)) {
-    scale = need;
-  } else {
-    while (scale < need) {             // doubling is exact; ends at the latest when scale is infinite
-      scale *= 2.0f;
-      shrink *= 0.5f;
-    }
-  }
-  uint8_t* dst = a.kv + block * (kPage * D);
-  if (shrink != 1.0f) {
-    // older codes, 4 at a time
-    uint32_t* w = reinterpret_cast<uint32_t*>(dst);
-    for (int i = threadIdx.x; i < p.first * D / 4; i += THREADS) {
-      const uint32_t c = w[i];
-      uint32_t n = 0;
+    // calls f(x, offset of the page) for every new token that is not skipped
+    auto each = [&](auto f) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) n |= encode8<E4M3>(__fmul_rn(decode8<E4M3>(c >> (8 * b)), shrink)) << (8 * b);
-      w[i] = n;
-    }
-  }
-  if (threadIdx.x == 0 && scale != old) a.kv_scale[block] = scale;
-  const bool fast = finite && divides_fast(scale);
-  const float inv = __frcp_rn(scale);
+      for (int k = 0; k < kHold; ++k)
+        if (at[k] >= 0) f(x[k], k * kTok + mine0);
+      if constexpr (kHold < kPasses) {
+#pragma unroll 1
+        for (int i = kTok + mine0; i < count; i += kTok) {
+          const int64_t pos = position(i);
+          if (pos < 0) continue;
+          float y[8];
+          turned(y, stored(i, h), pos);
+          f(y, i);
+        }
+      }
+    };
+    float amax = 0.0f;
+    each([&](const float (&v)[8], int) {
 #pragma unroll
-  for (int k = 0; k < kPasses; ++k) {
-    if (k * kTok >= count) break;
-    if (pos[k] >= 0) store_codes(dst + (p.first + k * kTok + mine0) * D, quads, encode_scaled<E4M3>(x[k], scale, inv, fast));
+      for (int i = 0; i < 8; ++i) amax = dev::max_nan(amax, fabsf(v[i]));
+    });
+    amax = over_cta(amax, (h - h0) & 1);
+    const bool finite = amax <= 3.402823466e38f;
+    if (!finite) {
+      // a NaN or an infinity among the new elements: the largest of the others
+      amax = 0.0f;
+      each([&](const float (&v)[8], int) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (fabsf(v[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(v[i]));
+      });
+      amax = over_cta(amax, 2);
+    }
+    const float need = __fdiv_rn(amax, E4M3 ? 448.0f : 127.0f);
+    float scale = old, shrink = 1.0f;
+    if (p.first == 0 || !(old > 0.0f)) {
+      scale = need;
+    } else {
+      while (scale < need) {             // doubling is exact; ends at the latest when scale is infinite
+        scale *= 2.0f;
+        shrink *= 0.5f;
+      }
+    }
+    const int64_t block = block0 + h;
+    uint8_t* dst = a.kv + block * (kPage * D);
+    if (shrink != 1.0f) {
+      // older codes, 4 at a time
+      uint32_t* w = reinterpret_cast<uint32_t*>(dst);
+      for (int i = threadIdx.x; i < p.first * D / 4; i += THREADS) {
+        const uint32_t c = w[i];
+        uint32_t n = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) n |= encode8<E4M3>(__fmul_rn(decode8<E4M3>(c >> (8 * b)), shrink)) << (8 * b);
+        w[i] = n;
+      }
+    }
+    if (threadIdx.x == 0 && scale != old) a.kv_scale[block] = scale;
+    const bool fast = finite && divides_fast(scale);
+    const float inv = __frcp_rn(scale);
+    each([&](const float (&v)[8], int i) { store_codes(dst + (p.first + i) * D, quads, encode_scaled<E4M3>(v, scale, inv, fast)); });
+    old = next_old;
   }
 }
 
@@ -515,10 +545,15 @@ template <int D, bool E4M3>
 cudaError_t launch_heads(GqaAppendArgs a, cudaStream_t s) {
   constexpr int kPageThreads = 256, kTokenThreads = D == 256 ? 128 : 64;
   const int64_t by_page = a.n / kPage + 2ll * a.batch;
-  const bool per_token = a.n <= by_page;
+  const bool per_token = a.n <= std::max<int64_t>(by_page, 4ll * a.batch);
   const int threads = per_token ? kTokenThreads : kPageThreads;
-  const int64_t kv_ctas = std::min(a.n, by_page) * 2 * a.kv_heads;
-  constexpr int kHeadsPerWarp = 4 * 32 / (D / 8);
+  const int64_t jobs = per_token ? a.n : by_page;
+  // heads to a CTA: as many as leave kFillCtas CTAs that have work (a request's pages and one more on average)
+  const int64_t busy = per_token ? a.n : a.n / kPage + a.batch;
+  int64_t per_cta = per_token ? 1 : std::max<int64_t>(1, std::min<int64_t>(a.kv_heads, busy * 2 * a.kv_heads / kFillCtas));
+  a.head_parts = static_cast<int>((a.kv_heads + per_cta - 1) / per_cta);
+  const int64_t kv_ctas = jobs * 2 * a.head_parts;
+  constexpr int kHeadsPerWarp = kQueryPasses * 32 / (D / 8);
   const int64_t q_jobs = a.heads > 0 ? a.n * ((a.heads + kHeadsPerWarp - 1) / kHeadsPerWarp) : 0;
   const int64_t ctas = kv_ctas + (q_jobs * 32 + threads - 1) / threads;
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;

@@ -180,7 +180,7 @@ int gqa_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_st
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16) return QKVP_E_UNSUPPORTED;
   if ((rot_dim > 0) != (cos_sin != nullptr)) return QKVP_E_INVALID;
   if ((q != nullptr) != (q_out != nullptr) || (q != nullptr) != (num_heads > 0)) return QKVP_E_INVALID;
-  if (n_tokens > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  if (n_tokens > INT32_MAX || max_positions > INT32_MAX) return QKVP_E_UNSUPPORTED;
   if (n_tokens == 0 || batch == 0) return QKVP_OK;
   if (!k || !v || !tok_indptr || !kv_len || !kv_indptr || !kv_indices || !kv_data || !kv_scale) return QKVP_E_INVALID;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_data, 16) || !aligned(tok_indptr, 4) || !aligned(kv_len, 4) ||

@@ -163,6 +163,7 @@ struct GqaAppendArgs {
   float* kv_scale;            // [num_pages][2][kv_heads]
   int64_t k_stride, v_stride, q_stride, n, nnz, max_pos, num_pages;
   int batch, rot, style, kv_heads, dim, heads, cache_dtype;
+  int head_parts;             // CTAs that share a page's K (or V) heads (set by the launcher)
   uint32_t kv_ctas;           // CTAs of the K and V blocks; the query's follow (set by the launcher)
 };
 

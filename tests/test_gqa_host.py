@@ -110,7 +110,7 @@ GQA = dict(k=16, ks=256, v=16, vs=256, n=4, tok=4, klen=4, batch=1, ptr=4, idx=4
     (dict(k=None), "I"), (dict(k=8), "I"), (dict(ks=248), "I"), (dict(ks=260), "I"), (dict(v=None), "I"), (dict(vs=255), "I"),
     (dict(tok=None), "I"), (dict(klen=None), "I"), (dict(ptr=None), "I"), (dict(idx=None), "I"), (dict(kv=None), "I"), (dict(kv=8), "I"),
     (dict(sc=None), "I"), (dict(pos=4), "I"), (dict(q=None), "I"), (dict(qo=None), "I"), (dict(h=0), "I"), (dict(q=8), "I"),
-    (dict(qs=504), "I"), (dict(q=32, qs=1024), "I"), (dict(n=1 << 40), "U"), (dict(pages=1 << 60), "I")])
+    (dict(qs=504), "I"), (dict(q=32, qs=1024), "I"), (dict(n=1 << 40), "U"), (dict(mp=1 << 40), "U"), (dict(pages=1 << 60), "I")])
 def test_gqa_append_refusals(lib, kw, want):
     a = dict(GQA, **kw)
     st = lib.gqa_append_rope(a["k"], a["ks"], a["v"], a["vs"], a["n"], a["tok"], a["klen"], a["batch"], a["ptr"], a["idx"], a["nnz"],
