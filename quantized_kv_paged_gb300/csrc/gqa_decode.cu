@@ -29,6 +29,12 @@
 // largest weight. l is summed from the unrounded FP32 values. The V scale sv = f 2^k of a page multiplies
 // P: f (in [1, 2)) on the value, k in the exponent, less the first page's k; l takes 2^-k back. So pages
 // with scales far apart keep their precision, whichever comes first.
+//
+// Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 428 us, 2.96 GB at
+// 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 87 %, issue 33 %, tensor pipe 18 %); 1 x 1,048,576 (4
+// heads) 162 us; 64 ragged requests (4 KV heads, 16 query heads each, INT8) 79 us. What is short is bound by its
+// start and end: 2.5 to 3 us from the launch to the first unit (the worker's record, its page id and the page
+// are three reads in line, cold), 1 us a unit, 1 us for a partial to be written and counted, 1 to 3 us to join.
 #include <atomic>
 #include <cstdint>
 #include <cstring>

@@ -197,7 +197,7 @@ static_assert(sizeof(GqaWorker) == 96, "worker layout");
 
 constexpr uint64_t kGqaMagic = 0x716b76702d677161ull;
 constexpr int kGqaPassHeads = 16;   // query heads of one pass over the pages
-// CTAs of the head-pool decode that one SM holds.
+// CTAs of the head-pool decode that one SM holds: what registers allow, and at D = 128 no more than two (its comment).
 constexpr int gqa_ctas_per_sm(int dim, int group) { return dim == 64 && group <= 8 ? 3 : 2; }
 
 struct GqaDecodeArgs {
