@@ -266,6 +266,8 @@ class _Types:
             cls.torch = torch
             cls.bf16, cls.f32, cls.i32, cls.i64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
             cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+            # the current stream's handle without a Stream object around it, where this torch has the call
+            cls.handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
             cls.ready = True
         return cls
 
@@ -303,7 +305,7 @@ def _launch_on(stream, tensors):
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensors need to be on the current CUDA device, got one on {t.device}")
     if stream is None:
-        return cuda.current_stream(here).cuda_stream
+        return _Types.handle(here)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
