@@ -11,9 +11,8 @@
 // (PAIRS and what is not rotated). Either way it needs 4 cosines and 4 sines and nothing from another lane.
 // Measured on GB300, kernel time: 20,011 latent rows with 16 query heads into the per-token pool 23.7 us (122
 // MB, 5.1 TB/s; issue slots 48 %, the reads of position, table row and data in line), 4,096 rows with 128
-// heads 24.4 us (142 MB, 5.8 TB/s), 44 rows with 128 heads 1.9 us; 15,500 tokens of 8 KV and 32 query heads of
-// 128 in eight chunks 46 us (358 MB counted, 7.8 TB/s: the queries' output partly stays in L2), 64 single tokens
-// of the same heads 4.0 us.
+// heads 24.4 us (142 MB, 5.8 TB/s), 44 rows with 128 heads 1.9 us; 12,086 tokens of 8 KV and 32 query heads of
+// 128 in eight chunks 46 us (278 MB, 6.1 TB/s), 64 single tokens of the same heads 4.0 us.
 #include <algorithm>
 #include <cstdint>
 
@@ -104,7 +103,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // remainders are exact when nothing in them underflows: s in [2^-60, 2^60] and finite x, where a quotient
 // that does not round to the code 0 comes from an x of 2^-72 and more. The signs are arranged so that -0
 // stays -0. Equal to the division on 1.9e10 pairs on GB300, in five operations: with a division per element
-// the chunked append of 15,500 tokens (8 KV heads, 32 query heads of 128) was issue-bound, 95 us.
+// the chunked append of 12,086 tokens (8 KV heads, 32 query heads of 128) was issue-bound, 95 us.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ bool divides_fast(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
 __device__ __forceinline__ float quotient(float x, float s, float r) {
