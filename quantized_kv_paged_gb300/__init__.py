@@ -255,8 +255,10 @@ def kv_gather_pages_bf16(kv_data, page_ids, out, num_pages: int | None = None, p
     return _check("kv_gather_pages_bf16", st, raise_on_error)
 
 
-class _Types:
-    """Types of the tensors that the checked entry points take (torch is imported on the first call)."""
+class _Torch:
+    """What the checked entry points take from torch, which is imported on the first of their calls. Their
+    checks run on every call of a decode step, so they are written for few attribute reads: one look at
+    each tensor's type, shape, layout and device, all against the first tensor's device."""
     ready = False
 
     @classmethod
@@ -264,7 +266,7 @@ class _Types:
         if not cls.ready:
             import torch
             cls.torch = torch
-            cls.bf16, cls.f32, cls.i32, cls.i64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+            cls.bf16, cls.f32, cls.i32, cls.i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
             cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
             # the current stream's handle without a Stream object around it, where this torch has the call
             cls.handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -272,45 +274,38 @@ class _Types:
         return cls
 
 
-def _refuse(name: str, t, shape, dtypes, layout: str):
-    raise ValueError(f"{name} needs the shape {tuple(shape)}, the type {' or '.join(map(str, dtypes))} and {layout}; got "
-                     f"{tuple(t.shape)}, {t.dtype}, strides {t.stride()}")
+def _refuse(name: str, t, shape, dtype, layout: str, here: int):
+    if t.get_device() != here:
+        raise ValueError(f"tensors need to be on one device, the current CUDA device: {name} is on {t.device}")
+    raise ValueError(f"{name} needs the shape {tuple(shape)}, the type {dtype} and {layout}; got {tuple(t.shape)}, {t.dtype}, "
+                     f"strides {t.stride()}")
 
 
-def _dense(name: str, t, shape, dtypes):
-    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
-        _refuse(name, t, shape, dtypes, "a contiguous layout")
+def _dense(name: str, t, shape, dtype, here: int):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != here:
+        _refuse(name, t, shape, dtype, "a contiguous layout", here)
 
 
-def _rows(name: str, t, n: int, heads: int, dim: int, dtypes):
+def _rows(name: str, t, n: int, heads: int, dim: int, dtype, here: int):
     """Row stride of a [n, heads, dim] tensor (heads 0: [n, dim]) whose rows are dense. The stride of an extent
     of one says nothing: such a tensor counts as dense."""
     stride = t.stride()
     if heads == 0:
-        if t.shape != (n, dim) or t.dtype not in dtypes or stride[1] != 1:
-            _refuse(name, t, (n, dim), dtypes, "dense rows")
+        if t.shape != (n, dim) or t.dtype is not dtype or stride[1] != 1 or t.get_device() != here:
+            _refuse(name, t, (n, dim), dtype, "dense rows", here)
         return stride[0] if n > 1 else dim
-    if t.shape != (n, heads, dim) or t.dtype not in dtypes or stride[2] != 1 or (stride[1] != dim and heads > 1):
-        _refuse(name, t, (n, heads, dim), dtypes, "dense rows")
+    if t.shape != (n, heads, dim) or t.dtype is not dtype or stride[2] != 1 or (stride[1] != dim and heads > 1) or t.get_device() != here:
+        _refuse(name, t, (n, heads, dim), dtype, "dense rows", here)
     return stride[0] if n > 1 else heads * dim
 
 
-def _launch_on(stream, tensors):
-    """The stream to launch on. The launch goes to the current device: tensors elsewhere are refused."""
-    cuda = _Types.torch.cuda
-    here = tensors[0].get_device()
-    if here < 0 or here != cuda.current_device():
-        raise ValueError(f"tensors need to be on the current CUDA device, got one on {tensors[0].device}")
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"tensors need to be on the current CUDA device, got one on {t.device}")
+def _launch_on(stream, here: int):
+    """The stream to launch on. The launch goes to the current device, so the tensors have to be there."""
+    if here < 0 or here != _Torch.torch.cuda.current_device():
+        raise ValueError(f"tensors need to be on the current CUDA device, got device index {here}")
     if stream is None:
-        return _Types.handle(here)
+        return _Torch.handle(here)
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
 
 
 def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: int, kv_data, kv_scale,
@@ -320,44 +315,47 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
     """Append latent rows [c_kv | rotated k_pe] at slot_mapping, quantized, and rotate q_pe [n, H, 64] into
     the last 64 dims of q [n, H, 576] (see qkvp.h). c_kv [n, 512], k_pe [n, 64] and q_pe may be slices with
     their own row strides; cos_sin float32 [max_positions, 64]."""
-    T = _Types.get()
-    n = c_kv.shape[0]
-    c_stride = _rows("c_kv", c_kv, n, 0, V_DIM, T.bf16)
-    pe_stride = _rows("k_pe", k_pe, n, 0, 64, T.bf16)
-    _dense("slot_mapping", slot_mapping, (n,), T.i64)
-    _dense("positions", positions, (n,), T.i64)
+    T = _Torch.get()
+    n, here = c_kv.shape[0], c_kv.get_device()
+    c_stride = _rows("c_kv", c_kv, n, 0, V_DIM, T.bf16, here)
+    pe_stride = _rows("k_pe", k_pe, n, 0, 64, T.bf16, here)
+    _dense("slot_mapping", slot_mapping, (n,), T.i64, here)
+    _dense("positions", positions, (n,), T.i64, here)
     max_positions = cos_sin.shape[0]
-    _dense("cos_sin", cos_sin, (max_positions, 64), T.f32)
+    _dense("cos_sin", cos_sin, (max_positions, 64), T.f32, here)
+    if kv_data.get_device() != here or (kv_scale is not None and kv_scale.get_device() != here):
+        raise ValueError("tensors need to be on one device, the current CUDA device: the pool is on another")
     heads = tok_stride = head_stride = 0
+    q_at = pe_at = None
     if q is not None or q_pe is not None:
         if q is None or q_pe is None or q.dim() != 3:
             raise ValueError("q_pe [n, H, 64] and q [n, H, 576] go together")
         heads = q.shape[1]
-        _dense("q", q, (n, heads, LATENT_DIM), T.bf16)
+        _dense("q", q, (n, heads, LATENT_DIM), T.bf16, here)
         stride = q_pe.stride()
-        if q_pe.shape != (n, heads, 64) or q_pe.dtype not in T.bf16 or stride[2] != 1:
-            _refuse("q_pe", q_pe, (n, heads, 64), T.bf16, "a dense last dimension")
-        if heads == 0:
-            q = q_pe = None
-        else:
+        if q_pe.shape != (n, heads, 64) or q_pe.dtype is not T.bf16 or stride[2] != 1 or q_pe.get_device() != here:
+            _refuse("q_pe", q_pe, (n, heads, 64), T.bf16, "a dense last dimension", here)
+        if heads:
             head_stride = stride[1] if heads > 1 else 64
             tok_stride = stride[0] if n > 1 else 64
-    on = _launch_on(stream, (c_kv, k_pe, slot_mapping, positions, cos_sin, kv_data, kv_scale, q_pe, q))
+            q_at, pe_at = q.data_ptr(), q_pe.data_ptr()
+    on = _launch_on(stream, here)
     st = (_lib or load()).mla_append_rope(
         c_kv.data_ptr(), c_stride, k_pe.data_ptr(), pe_stride, n, slot_mapping.data_ptr(), positions.data_ptr(),
-        cos_sin.data_ptr(), max_positions, rope_style, _at(q_pe), tok_stride, head_stride, heads, _at(q),
-        kv_data.data_ptr(), _at(kv_scale), kv_dtype, global_scale, page_size,
+        cos_sin.data_ptr(), max_positions, rope_style, pe_at, tok_stride, head_stride, heads, q_at,
+        kv_data.data_ptr(), kv_scale if kv_scale is None else kv_scale.data_ptr(), kv_dtype, global_scale, page_size,
         kv_data.shape[0] if num_pages is None else num_pages, on)
     return st if st == QKVP_OK else _check("mla_append_rope", st, raise_on_error)
 
 
-def _head_pool(kv_data, kv_scale, T):
+def _head_pool(kv_data, kv_scale, T, here: int):
     """(pages, KV heads, head dim) of a head pool."""
     shape = kv_data.shape
-    if len(shape) != 5 or shape[1] != 2 or shape[3] != PAGE_SIZE or kv_data.dtype not in T.codes or not kv_data.is_contiguous():
-        _refuse("kv_data", kv_data, ("pages", 2, "heads", PAGE_SIZE, "dim"), T.codes, "a contiguous layout")
-    _dense("kv_scale", kv_scale, (shape[0], 2, shape[2]), T.f32)
-    return shape[0], shape[2], shape[4]
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != PAGE_SIZE or kv_data.dtype not in T.codes or not kv_data.is_contiguous() or kv_data.get_device() != here:
+        _refuse("kv_data", kv_data, ("pages", 2, "heads", PAGE_SIZE, "dim"), T.codes, "a contiguous layout", here)
+    pages, _, heads, _, dim = shape
+    _dense("kv_scale", kv_scale, (pages, 2, heads), T.f32, here)
+    return pages, heads, dim
 
 
 def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, rope_style: int, kv_data,
@@ -367,37 +365,40 @@ def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, ro
     kv_scale float32 [pages, 2, Hkv], and rotate q [n, H, D] into q_out (see qkvp.h). k, v and q may be
     slices of one projection; request r's tokens are tok_indptr[r] .. tok_indptr[r + 1] - 1 and go behind
     its kv_len[r] cached ones. cos_sin float32 [max_positions, rot_dim], or None: no rotation."""
-    T = _Types.get()
-    pages, heads_kv, dim = _head_pool(kv_data, kv_scale, T)
-    n, batch, nnz = k.shape[0], kv_len.shape[0], kv_indices.shape[0]
-    k_stride, v_stride = _rows("k", k, n, heads_kv, dim, T.bf16), _rows("v", v, n, heads_kv, dim, T.bf16)
-    _dense("tok_indptr", tok_indptr, (batch + 1,), T.i32)
-    _dense("kv_len", kv_len, (batch,), T.i32)
-    _dense("kv_indptr", kv_indptr, (batch + 1,), T.i32)
-    _dense("kv_indices", kv_indices, (nnz,), T.i32)
+    T = _Torch.get()
+    n, here = k.shape[0], k.get_device()
+    pages, heads_kv, dim = _head_pool(kv_data, kv_scale, T, here)
+    batch, nnz = kv_len.shape[0], kv_indices.shape[0]
+    bf16, i32 = T.bf16, T.i32
+    k_stride, v_stride = _rows("k", k, n, heads_kv, dim, bf16, here), _rows("v", v, n, heads_kv, dim, bf16, here)
+    _dense("tok_indptr", tok_indptr, (batch + 1,), i32, here)
+    _dense("kv_len", kv_len, (batch,), i32, here)
+    _dense("kv_indptr", kv_indptr, (batch + 1,), i32, here)
+    _dense("kv_indices", kv_indices, (nnz,), i32, here)
     max_positions = rot = heads = q_stride = 0
+    cs_at = pos_at = q_at = out_at = None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
-            _refuse("cos_sin", cos_sin, ("positions", "rot_dim"), T.f32, "a contiguous layout")
-        max_positions, rot = cos_sin.shape
-        _dense("cos_sin", cos_sin, (max_positions, rot), T.f32)
+            _refuse("cos_sin", cos_sin, ("positions", "rot_dim"), T.f32, "a contiguous layout", here)
+        max_positions, rot = shape = cos_sin.shape
+        _dense("cos_sin", cos_sin, shape, T.f32, here)
+        cs_at = cos_sin.data_ptr()
     if positions is not None:
-        _dense("positions", positions, (n,), T.i64)
+        _dense("positions", positions, (n,), T.i64, here)
+        pos_at = positions.data_ptr()
     if q is not None or q_out is not None:
         if q is None or q_out is None or q_out.dim() != 3:
             raise ValueError("q and q_out [n, H, D] go together")
         heads = q_out.shape[1]
-        _dense("q_out", q_out, (n, heads, dim), T.bf16)
-        if heads == 0:
-            q = q_out = None
-        else:
-            q_stride = _rows("q", q, n, heads, dim, T.bf16)
-    on = _launch_on(stream, (k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, kv_data, kv_scale, q, q_out, positions))
+        _dense("q_out", q_out, (n, heads, dim), bf16, here)
+        if heads:
+            q_stride = _rows("q", q, n, heads, dim, bf16, here)
+            q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    on = _launch_on(stream, here)
     st = (_lib or load()).gqa_append_rope(
         k.data_ptr(), k_stride, v.data_ptr(), v_stride, n, tok_indptr.data_ptr(), kv_len.data_ptr(), batch,
-        kv_indptr.data_ptr(), kv_indices.data_ptr(), nnz, _at(positions), _at(cos_sin), max_positions, rot,
-        rope_style, heads_kv, dim, kv_data.data_ptr(), kv_scale.data_ptr(), cache_dtype, PAGE_SIZE, pages, _at(q),
-        q_stride, heads, _at(q_out), on)
+        kv_indptr.data_ptr(), kv_indices.data_ptr(), nnz, pos_at, cs_at, max_positions, rot, rope_style, heads_kv, dim,
+        kv_data.data_ptr(), kv_scale.data_ptr(), cache_dtype, PAGE_SIZE, pages, q_at, q_stride, heads, out_at, on)
     return st if st == QKVP_OK else _check("gqa_append_rope", st, raise_on_error)
 
 
@@ -421,23 +422,28 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
                    stream=None, raise_on_error: bool = True) -> int:
     """Decode one layer over a head pool: q, out bf16 [B, H, D], lse float32 [B, H] or None; kv_data and
     kv_scale as for gqa_append_rope."""
-    T = _Types.get()
+    T = _Torch.get()
     batch, heads, dim = plan.batch, plan.num_heads, plan.head_dim
-    _dense("q", q, (batch, heads, dim), T.bf16)
-    _dense("out", out, (batch, heads, dim), T.bf16)
-    pages, heads_kv, kv_dim = _head_pool(kv_data, kv_scale, T)
+    here = q.get_device()
+    _dense("q", q, (batch, heads, dim), T.bf16, here)
+    _dense("out", out, (batch, heads, dim), T.bf16, here)
+    pages, heads_kv, kv_dim = _head_pool(kv_data, kv_scale, T, here)
     if heads_kv != plan.num_kv_heads or kv_dim != dim:
         raise ValueError(f"kv_data has {heads_kv} heads of {kv_dim}, the plan {plan.num_kv_heads} of {dim}")
     entries = kv_indices.shape[0]
-    _dense("kv_indices", kv_indices, (entries,), T.i32)
+    _dense("kv_indices", kv_indices, (entries,), T.i32, here)
     if entries < plan.table_entries:
         raise ValueError(f"kv_indices has {entries} entries, the plan's page table {plan.table_entries}")
+    lse_at = None
     if lse is not None:
-        _dense("lse", lse, (batch, heads), T.f32)
-    on = _launch_on(stream, (q, kv_data, kv_scale, kv_indices, out, lse, workspace))
+        _dense("lse", lse, (batch, heads), T.f32, here)
+        lse_at = lse.data_ptr()
+    if workspace.get_device() != here:
+        raise ValueError("tensors need to be on one device, the current CUDA device: the workspace is on another")
+    on = _launch_on(stream, here)
     st = (_lib or load()).gqa_decode_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
-                               kv_indices.data_ptr(), sm_scale, out.data_ptr(), _at(lse), workspace.data_ptr(),
-                               workspace.nbytes, on)
+                                         kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse_at, workspace.data_ptr(),
+                                         workspace.nbytes, on)
     return st if st == QKVP_OK else _check("gqa_decode_run", st, raise_on_error)
 
 

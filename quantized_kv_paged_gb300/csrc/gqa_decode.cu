@@ -22,7 +22,9 @@
 // byte moves between lanes. V^T needs two tokens of one dim in a register: two byte permutes of two
 // tokens' words, then the conversion. The tokens of an 8-token block are taken in the order `tok8`, which
 // makes every 16-byte (D = 64: 8-byte) shared-memory read free of bank conflicts under the TMA's 128-byte
-// swizzle. P^T is S^T's accumulator layout transposed: one 8x8 transpose per 8 tokens.
+// swizzle. P^T is S^T's accumulator layout transposed: one 8x8 transpose per 8 tokens. Computing S^T of the
+// next unit along with the softmax of this one (rings of three) was 1 to 5 % slower: two warps per scheduler are
+// short of issue slots, not of independent work (INT8, 16 heads: 874 instructions a unit, 350 of them conversions).
 //
 // Softmax. One running reference m per head. It moves only when a logit passes it by 2^8 (a vote instead
 // of a reduction per unit); P = 2^(z - m + 6) <= 2^14 is in FP16's normal range down to 2^-28 of the
