@@ -26,10 +26,13 @@ constexpr int kMaxHeads = 4096;
 //   against 88. From one row per SM already where a row has no more than 8 units: 256 of 128 tokens (D 256) 10.0 / 12.0.
 // - Pages below which a CTA is not worth its start: 8 rows of 4 pages 4.5 us whole, 6.4 as pairs of pages, 7.4 when
 //   workers span two rows.
-// - Pages of work that starting a row counts as: 4, 8, 16 within 3 % of one another at most sizes, 8 against 4 for
-//   CTAs 5.7 / 9.8 us at 256 rows of 128 tokens, 4 against 8 for warps 25.9 / 29.0 us at 1,024 rows of 512 (D 128).
+// - Pages of work that starting a row counts as, some 128 KB for a CTA and 32 to 48 KB for a warp. Warps, 2 against 4
+//   against 8 pages: 24.7 / 23.0 / 22.3 us in the window case of D 64 (128 requests), 28.5 / 30.0 / 34.4 at 1,280 rows of
+//   512 tokens of D 128, 53.7 / 58.1 / 66.5 of D 256. CTAs, 4 against 8: 14.0 / 13.7 at 256 rows of 2,048 tokens of D 64,
+//   23.7 / 23.0 at 32 requests of 512 to 4,096 tokens of D 128, 24.6 / 27.7 at 40 of 100 to 1,000 of D 256.
 constexpr double kWarpRowsPerSm = 2.5;
-constexpr int kMinCtaPages = 4, kCtaRowCost = 8, kWarpRowCost = 4;
+constexpr int kMinCtaPages = 4;
+int row_cost(int dim, int team) { return team > 1 ? 1024 / dim : dim == 64 ? 6 : 256 / dim; }
 constexpr int kJoinFan = 40;
 
 // Row strides in elements: multiples of 8 (16-byte vectors), at least one row wide.
@@ -274,7 +277,7 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   const int64_t useful = std::max<int64_t>(1, (row_pages + min_pages - 1) / min_pages);
   int workers = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms) * gqa_ctas_per_sm(head_dim, group) * per_cta, useful));
   workers = (workers + per_cta - 1) / per_cta * per_cta;
-  const int cost = team == 1 ? kWarpRowCost : kCtaRowCost;
+  const int cost = row_cost(head_dim, team);
   SplitInfo info;
   split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, cost);
   std::vector<Segment> cut(static_cast<size_t>(std::max<int64_t>(1, info.num_segments)));
