@@ -94,13 +94,15 @@ double whole_rows(const std::vector<int32_t>& pages, int workers, const Times& t
     if (ptr) ptr[workers] = static_cast<int32_t>(i);
     return i == pages.size();
   };
-  double lo = 0.0, hi = 0.0;
+  double longest = 0.0, mean = 0.0;
   for (int32_t p : pages) {
-    lo = std::max(lo, p * t.page + t.segment);
-    hi += p * t.page + t.segment;
+    longest = std::max(longest, p * t.page + t.segment);
+    mean += p * t.page + t.segment;
   }
-  hi = hi * 1.001 + 1.0;
-  for (int i = 0; i < 30 && hi > lo * 1.005; ++i) {
+  mean /= workers;
+  // filled up to the mean and the longest row, a worker holds more than the mean, so every row finds a place
+  double lo = std::max(longest, mean), hi = (mean + longest) * 1.000001;
+  for (int i = 0; i < 12 && hi > lo * 1.01; ++i) {
     const double mid = 0.5 * (lo + hi);
     if (fill(mid, nullptr)) hi = mid; else lo = mid;
   }
@@ -279,7 +281,8 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
   workers = (workers + per_cta - 1) / per_cta * per_cta;
   const int cost = row_cost(head_dim, team);
   SplitInfo info;
-  split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, cost);
+  info.num_segments = rows + workers;      // each worker's end cuts one row at most; asked-for splits are counted first
+  if (min_splits > 0) split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, cost);
   std::vector<Segment> cut(static_cast<size_t>(std::max<int64_t>(1, info.num_segments)));
   std::vector<int32_t> wptr(workers + 1), rptr(rows + 1), wide(std::max<int64_t>(1, rows));
   SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
