@@ -320,7 +320,8 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const uint32_t vbase = kbase + kHalf;
   const float2 sc = lds_f2(scale_addr);
   // At D = 256 with one tile of tokens and one of heads all 16 products are one chain: two sums, of the even and of
-  // the odd 64-dim groups, halve it (4,096 rows of 128 tokens 51.6 us, 53.4 with one sum). Elsewhere one is 1 % faster.
+  // the odd 64-dim groups, halve it (4,096 rows of 128 tokens 51.6 us, 53.4 with one sum). With 16 heads of 256 one
+  // sum is faster (16 x 4,096 tokens 33.4 us, 34.0 with two); D 128 does not tell the two apart.
   constexpr int kChains = D == 256 && NT == 1 ? 2 : 1;
   float s[MT][NT][4], part[kChains][MT][NT][4];
 #pragma unroll
@@ -378,8 +379,10 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         for (int c = 1; c < kChains; ++c) s[m][n][k] += part[c][m][n][k];
       }
 
-  // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them (16 windows of 4,095 at D 256
-  // 2.5 % faster, elsewhere the same)
+  // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 1,024 rows of 2,048 tokens
+  // at D 256 with 16 heads take 165.5 us, and 170.4 with the loads behind it. At D 128 with 16 heads they come behind
+  // it (4,096 rows of 512 tokens 96.1 us, 100.4 ahead of it); the other shapes do not tell the two apart.
+  constexpr bool kEarlyV = D != 128 || NT == 1;
   const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
   constexpr int kSides = (D + 127) / 128;              // 128-dim halves of a token
   constexpr int W = D == 64 ? 2 : 4;                   // words of a lane's piece of a token
@@ -410,10 +413,12 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
     }
   };
+  if constexpr (kEarlyV) {
 #pragma unroll
-  for (int h = 0; h < kSides; ++h)
+    for (int h = 0; h < kSides; ++h)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) load_v(h, m);
+      for (int m = 0; m < MT; ++m) load_v(h, m);
+  }
 
   // V's scale f 2^k, k relative to the warp's first page of the segment
   const uint32_t vs = __float_as_uint(sc.y);
@@ -494,6 +499,7 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   for (int h = 0; h < kSides; ++h) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      if constexpr (!kEarlyV) load_v(h, m);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
 #pragma unroll
