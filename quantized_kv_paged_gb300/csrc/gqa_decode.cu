@@ -29,8 +29,9 @@
 // Softmax. One running reference m per head. It moves only when a logit passes it by 2^8 (a vote instead
 // of a reduction per unit); P = 2^(z - m + 6) <= 2^14 is in FP16's normal range down to 2^-28 of the
 // largest weight. l is summed from the unrounded FP32 values. The V scale sv = f 2^k of a page multiplies
-// P: f (in [1, 2)) on the value, k in the exponent, less the first page's k; l takes 2^-k back. So pages
-// with scales far apart keep their precision, whichever comes first.
+// P: f (in [1, 2)) on the value, k in the exponent, less that of a reference: the first page's, until a
+// scale is 2^24 above it; l takes 2^-k back. So pages with scales far apart keep their precision, whichever comes
+// first, and any finite scale is taken.
 //
 // Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 428 us, 2.96 GB at
 // 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 87 %, issue 33 %, tensor pipe 18 %); 1 x 1,048,576 (4
@@ -60,6 +61,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;
 constexpr float kLift = 6.0f;            // P is held as 2^(z - m + kLift)
 constexpr float kNone = -3e38f;          // reference before the first unit
+// How far (log2) V's scale may be above and below the one that O^T is relative to. Above it the reference moves, below
+// it V counts as zero. A weight may come in relative to a reference that is both apart from its own, 2^-84: FP32
+// leaves it 2^-48 more before it is flushed.
+constexpr int kReachUp = 24, kReachDown = 60;
 
 // At D = 256 and 16 heads Q^T would take 64 of the 255 registers next to 128 of O^T: it is kept in shared memory (16 x
 // 4,096 tokens, 4 KV heads, 10 query heads each: 34 us, and 50 with it in registers, which spill).
@@ -311,6 +316,34 @@ __device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D,
   else if constexpr (Query<D, NT>::kShared) __syncwarp();
 }
 
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Makes O^T relative to a V scale that is 2^rise as large, up to 2^253: m, the reference of z + k, falls by `rise`, so
+// that O^T stays as it is and l grows. Where l would pass 2^64 (tokens whose V is nothing to the new scale hold
+// nearly all of the weight), m falls by less and O^T shrinks: what that costs it is 2^-88 of the new scale's values.
+template <int D, int NT>
+__device__ __forceinline__ void raise_reference(State<D, NT>& st, int rise) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[n][e];              // the column's largest, over the lanes that hold it
+      l = fmaxf(l, __shfl_xor_sync(kFull, l, 4));
+      l = fmaxf(l, __shfl_xor_sync(kFull, l, 8));
+      l = fmaxf(l, __shfl_xor_sync(kFull, l, 16));
+      const int less = static_cast<int>(fminf(fmaxf(ceilf(lg2(l)) + static_cast<float>(rise - 64), 0.0f), 400.0f));
+      const int by = max(rise - less, -250);
+      st.m[n][e] -= static_cast<float>(by);
+      st.l[n][e] = st.l[n][e] * pow2(by / 2) * pow2(by - by / 2);
+      const float c = less > 126 ? 0.0f : pow2(-less);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        st.o[i][n][e] *= c;
+        st.o[i][n][2 + e] *= c;
+      }
+    }
+}
+
 // One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens are not visible.
 template <int D, bool E4M3, int NT, bool PARTIAL>
 __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& Q, uint32_t kbase, uint32_t scale_addr,
@@ -424,9 +457,13 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const uint32_t vs = __float_as_uint(sc.y);
   const bool zero = sc.y == 0.0f;
   const int vk = min(max(static_cast<int>((vs >> 23) & 0xFF), 1) - 127, 126);
-  if (kref == INT32_MIN && !zero) kref = vk;
-  const int k = zero ? 0 : max(-90, min(90, vk - kref));       // the bound keeps l finite
-  const float f = zero ? 0.0f : sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
+  if (!zero && kref == INT32_MIN) kref = vk;
+  if (!zero && vk - kref > kReachUp) {
+    raise_reference(st, vk - kref);
+    kref = vk;
+  }
+  const int k = zero ? 0 : max(vk - kref, -kReachDown);
+  const float f = zero || vk - kref < -kReachDown ? 0.0f : sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
   const float back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 
   float top[NT][2];

@@ -118,6 +118,29 @@ def test_value_scales_far_apart(qkvp, cache):
         b.check(num_sms=2 if seed else 0)
 
 
+@pytest.mark.parametrize("cache", [R.E4M3, R.INT8])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 2), (32, 2)])
+@pytest.mark.parametrize("steps,heavy", [([-110, 0], 0), ([0, -110], 0), ([-115, -20, 75], 0), ([60, -60, 0], 0), ([-110, 0], -110),
+                                         ([-115, -20, 75], -115), ([75, -20, -115], -115)])
+def test_value_scales_over_all_exponents(qkvp, cache, dim, heads, kv_heads, steps, heavy):
+    """V block scales more than 2^90 apart, in every order; `heavy`: the pages of these scales take nearly all
+    of the weight (keys 64 times as large). The reference's exponents, up to 2^7, are held to 2^-18, which the bound's e,
+    at least 2 * 72 * 2^-24 * dot with a dot above 2, exceeds."""
+    b = Batch([900, 200, 70], heads, kv_heads, dim, cache, seed=dim + heads)
+    for r, n in enumerate(b.lens):
+        for i in range((int(n) + 63) // 64):
+            e = steps[i % len(steps)]
+            b.scale[b.ids[b.indptr[r] + i], 1] *= np.float32(2.0 ** e)
+            if heavy and e == heavy:
+                b.scale[b.ids[b.indptr[r] + i], 0] *= np.float32(64)
+    ref = b.ref()
+    assert np.isfinite(ref[0]).all() and (ref[3] > 2).all()
+    for num_sms in (0, 1):
+        out, lse, _ = b.run(num_sms=num_sms)
+        R.check_attend(out, lse, ref, 900, dim)
+
+
 def test_zero_scale_keys_and_equal_logits(qkvp):
     b = Batch([900], 8, 1, 64, R.INT8, seed=5)
     b.scale[:, 0][~np.isnan(b.scale[:, 0])] = 0.0
