@@ -316,36 +316,8 @@ __device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D,
   else if constexpr (Query<D, NT>::kShared) __syncwarp();
 }
 
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
-
-// Makes O^T relative to a V scale that is 2^rise as large, up to 2^253: m, the reference of z + k, falls by `rise`, so
-// that O^T stays as it is and l grows. Where l would pass 2^64 (tokens whose V is nothing to the new scale hold
-// nearly all of the weight), m falls by less and O^T shrinks: what that costs it is 2^-88 of the new scale's values.
-template <int D, int NT>
-__device__ __forceinline__ void raise_reference(State<D, NT>& st, int rise) {
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = st.l[n][e];              // the column's largest, over the lanes that hold it
-      l = fmaxf(l, __shfl_xor_sync(kFull, l, 4));
-      l = fmaxf(l, __shfl_xor_sync(kFull, l, 8));
-      l = fmaxf(l, __shfl_xor_sync(kFull, l, 16));
-      const int less = static_cast<int>(fminf(fmaxf(ceilf(lg2(l)) + static_cast<float>(rise - 64), 0.0f), 400.0f));
-      const int by = max(rise - less, -250);
-      st.m[n][e] -= static_cast<float>(by);
-      st.l[n][e] = st.l[n][e] * pow2(by / 2) * pow2(by - by / 2);
-      const float c = less > 126 ? 0.0f : pow2(-less);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        st.o[i][n][e] *= c;
-        st.o[i][n][2 + e] *= c;
-      }
-    }
-}
-
 // One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens are not visible.
-template <int D, bool E4M3, int NT, bool PARTIAL>
+template <int D, bool E4M3, int NT, int TEAM, bool PARTIAL>
 __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& Q, uint32_t kbase, uint32_t scale_addr,
                                           const Range& range, int& kref, int lane) {
   constexpr int MT = kHalf / D / 16;
@@ -412,10 +384,11 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         for (int c = 1; c < kChains; ++c) s[m][n][k] += part[c][m][n][k];
       }
 
-  // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 1,024 rows of 2,048 tokens
-  // at D 256 with 16 heads take 165.5 us, and 170.4 with the loads behind it. At D 128 with 16 heads they come behind
-  // it (4,096 rows of 512 tokens 96.1 us, 100.4 ahead of it); the other shapes do not tell the two apart.
-  constexpr bool kEarlyV = D != 128 || NT == 1;
+  // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 4,096 rows of 512 tokens of
+  // D 256 with 16 heads take 195 us, and 207 with the loads behind it. With fewer registers left, at D 128 with 16
+  // heads and at D 256 in a team, they come behind it: 4,096 rows of 512 tokens of D 128 96.1 us, 100.4 ahead of it;
+  // 16 x 4,096 tokens of D 256 33.6 us, 34.3. D 64 and up to 8 heads do not tell the two apart.
+  constexpr bool kEarlyV = NT == 1 || D == 64 || (D == 256 && TEAM == 1);
   const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
   constexpr int kSides = (D + 127) / 128;              // 128-dim halves of a token
   constexpr int W = D == 64 ? 2 : 4;                   // words of a lane's piece of a token
@@ -458,10 +431,8 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const bool zero = sc.y == 0.0f;
   const int vk = min(max(static_cast<int>((vs >> 23) & 0xFF), 1) - 127, 126);
   if (!zero && kref == INT32_MIN) kref = vk;
-  if (!zero && vk - kref > kReachUp) {
-    raise_reference(st, vk - kref);
-    kref = vk;
-  }
+  const float rise = !zero && vk - kref > kReachUp ? static_cast<float>(vk - kref) : 0.0f;
+  if (rise > 0.0f) kref = vk;
   const int k = zero ? 0 : max(vk - kref, -kReachDown);
   const float f = zero || vk - kref < -kReachDown ? 0.0f : sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
   const float back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
@@ -485,7 +456,10 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
     }
   }
-  bool move = false;
+  // A reference V scale that is 2^rise as large lowers m, which bounds z + k, by rise: O^T stays as it is and l grows,
+  // by 2^28 at most (it is below 2^96 for 2^22 tokens). What m is not lowered by, O^T shrinks by; l is 2^10 or more
+  // then, so what FP16 flushes of a token's product is below 2^-35 of a V of the new scale.
+  bool move = rise > 0.0f;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -500,10 +474,10 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-        x = fmaxf(fminf(x, 3e38f), st.m[n][e]);
-        c[e] = dev::fast_exp2(st.m[n][e] - x);
+        x = fmaxf(fminf(x, 3e38f), st.m[n][e] - fminf(rise, 28.0f));
+        c[e] = dev::fast_exp2(st.m[n][e] - rise - x);
+        st.l[n][e] *= dev::fast_exp2(st.m[n][e] - x);
         st.m[n][e] = x;
-        st.l[n][e] *= c[e];
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -747,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         dead = __any_sync(kFull, dead);
         parity ^= 1u << stage;
         const Range range(s, page_of(s, s.page_begin + u / P::kUnits) * kPage + u % P::kUnits * P::kTokens);
-        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
-        else take_unit<D, E4M3, NT, true>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
+        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
+        else take_unit<D, E4M3, NT, TEAM, true>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
         __syncwarp();
       }
       fill(stage);
