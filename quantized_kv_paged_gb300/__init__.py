@@ -299,6 +299,23 @@ def _rows(name: str, t, n: int, heads: int, dim: int, dtype, here: int):
     return stride[0] if n > 1 else heads * dim
 
 
+# bytes of a latent pool's page and of its scales, by kv_dtype
+_LATENT_PAGE = {KV_FP8_E4M3: (PAGE_SIZE * LATENT_DIM, 0), KV_NVFP4: (PAGE_SIZE * LATENT_DIM // 2, PAGE_SIZE * LATENT_DIM // 16),
+                KV_FP8_PER_TOKEN: (PAGE_BYTES_FP8_PER_TOKEN, 0)}
+
+
+def _latent_pool(kv_data, kv_scale, kv_dtype: int, num_pages: int, here: int):
+    page, scales = _LATENT_PAGE.get(kv_dtype, (0, 0))
+    for name, t, need in (("kv_data", kv_data, page), ("kv_scale", kv_scale, scales)):
+        if t is None:
+            continue
+        if t.get_device() != here:
+            raise ValueError("tensors need to be on one device, the current CUDA device: the pool is on another")
+        if not t.is_contiguous() or t.nbytes < num_pages * need:
+            raise ValueError(f"{name} needs a contiguous layout and the bytes of {num_pages} pages, {need} each; got {tuple(t.shape)}, "
+                             f"{t.dtype}, strides {t.stride()}")
+
+
 def _launch_on(stream, here: int):
     """The stream to launch on. The launch goes to the current device, so the tensors have to be there."""
     if here < 0 or here != _Torch.torch.cuda.current_device():
@@ -323,8 +340,9 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
     _dense("positions", positions, (n,), T.i64, here)
     max_positions = cos_sin.shape[0]
     _dense("cos_sin", cos_sin, (max_positions, 64), T.f32, here)
-    if kv_data.get_device() != here or (kv_scale is not None and kv_scale.get_device() != here):
-        raise ValueError("tensors need to be on one device, the current CUDA device: the pool is on another")
+    if num_pages is None:
+        num_pages = kv_data.shape[0]
+    _latent_pool(kv_data, kv_scale, kv_dtype, num_pages, here)
     heads = tok_stride = head_stride = 0
     q_at = pe_at = None
     if q is not None or q_pe is not None:
@@ -344,7 +362,7 @@ def mla_append_rope(c_kv, k_pe, slot_mapping, positions, cos_sin, rope_style: in
         c_kv.data_ptr(), c_stride, k_pe.data_ptr(), pe_stride, n, slot_mapping.data_ptr(), positions.data_ptr(),
         cos_sin.data_ptr(), max_positions, rope_style, pe_at, tok_stride, head_stride, heads, q_at,
         kv_data.data_ptr(), kv_scale if kv_scale is None else kv_scale.data_ptr(), kv_dtype, global_scale, page_size,
-        kv_data.shape[0] if num_pages is None else num_pages, on)
+        num_pages, on)
     return st if st == QKVP_OK else _check("mla_append_rope", st, raise_on_error)
 
 

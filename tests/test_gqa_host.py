@@ -184,3 +184,24 @@ def test_binding_refuses_wrong_tensors(lib):
         with pytest.raises(ValueError) as e:
             q.gqa_decode_run(**dict(run, **kw))
         assert "current CUDA device" not in str(e.value), kw
+
+
+@pytest.mark.parametrize("kv,row,scales", [(q.KV_FP8_E4M3, 576, 0), (q.KV_NVFP4, 288, 36), (q.KV_FP8_PER_TOKEN, 580, 0)])
+def test_binding_refuses_latent_pools_that_do_not_hold_the_pages(lib, kv, row, scales):
+    """Slots are checked against the page count on the device, so the pool's bytes have to be there: strided,
+    short and missing ones are refused. A pool of the right size is refused for not being on the GPU."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)          # noqa: E731
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)             # noqa: E731
+    i64 = torch.zeros(2, dtype=torch.int64)
+    good = dict(c_kv=bf(2, 512), k_pe=bf(2, 64), slot_mapping=i64, positions=i64, cos_sin=torch.zeros((10, 64)), rope_style=q.ROPE_PAIRS,
+                kv_data=u8(3, 64, row), kv_scale=u8(3, 64, scales) if scales else None, kv_dtype=kv)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        q.mla_append_rope(**good)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        q.mla_append_rope(**dict(good, num_pages=2))
+    bad = [dict(num_pages=4), dict(kv_data=u8(3, 64, row + 8)[..., :row]), dict(kv_data=u8(3, 32, row)), dict(kv_data=u8(6, 64, row)[::2])]
+    if scales:
+        bad += [dict(kv_scale=u8(2, 64, scales)), dict(kv_scale=u8(3, 64, scales + 4)[..., :scales])]
+    for kw in bad:
+        with pytest.raises(ValueError, match="pages"):
+            q.mla_append_rope(**dict(good, **kw))
