@@ -29,9 +29,12 @@
 // Softmax. One running reference m per head. It moves only when a logit passes it by 2^8 (a vote instead
 // of a reduction per unit); P = 2^(z - m + 6) <= 2^14 is in FP16's normal range down to 2^-28 of the
 // largest weight. l is summed from the unrounded FP32 values. The V scale sv = f 2^k of a page multiplies
-// P: f (in [1, 2)) on the value, k in the exponent, less that of a reference: the first page's, until a
-// scale is 2^24 above it; l takes 2^-k back. So pages with scales far apart keep their precision, whichever comes
-// first, and any finite scale is taken.
+// P: f (in [1, 2)) on the value, k in the exponent, less that of the warp's first page of the segment; l takes 2^-k
+// back. That serves scales within 2^24 of the first. From a page on whose scale is further away, or 0, the warp sums
+// l from exponentials of its own, relative to the largest logit, while m goes on bounding logit + k: what a page adds
+// to l and what it adds to O^T may then be any powers of two apart, in any order. Every finite scale is taken. (That
+// the rare form is there costs 1 x 1,024 tokens 6.2 to 6.5 us and 16 x 4,096 tokens of D 256 with 10 heads 33.5 to 34.7;
+// 44 x 32,768 and the ragged INT8 batch stay.)
 //
 // Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 428 us, 2.96 GB at
 // 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 87 %, issue 33 %, tensor pipe 18 %); 1 x 1,048,576 (4
@@ -61,10 +64,12 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kSlack = 8.0f;
 constexpr float kLift = 6.0f;            // P is held as 2^(z - m + kLift)
 constexpr float kNone = -3e38f;          // reference before the first unit
-// How far (log2) V's scale may be above and below the one that O^T is relative to. Above it the reference moves, below
-// it V counts as zero. A weight may come in relative to a reference that is both apart from its own, 2^-84: FP32
-// leaves it 2^-48 more before it is flushed.
-constexpr int kReachUp = 24, kReachDown = 60;
+// How far (log2) V's scale may be from the first page's for l to be summed from P: the token of the largest logit has a P
+// of at least 2^(kLift - 2 kReach) then, far from where FP32 flushes.
+constexpr int kReach = 24;
+// Factors of O^T at a segment's end from which on they are one product; smaller ones, that may be near where FP32
+// flushes, are two.
+constexpr float kSmall = 0x1p-100f;
 
 // At D = 256 and 16 heads Q^T would take 64 of the 255 registers next to 128 of O^T: it is kept in shared memory (16 x
 // 4,096 tokens, 4 KV heads, 10 query heads each: 34 us, and 50 with it in registers, which spill).
@@ -78,14 +83,16 @@ struct Shape {
   static constexpr int kStages = 2;                    // units of a warp's ring
   static constexpr int kTiles = D / 16;                // 16-dim row tiles of O^T
   static constexpr int kPart = kTiles * NT * 32 * 16;  // bytes of one warp's O^T
-  // shared memory: rings, the join's buffer, Q^T where it is kept there, the units' scales, barriers, per-warp lse, flags
+  // shared memory: rings, the join's buffer, Q^T where it is kept there, the units' scales, barriers, per-warp lse,
+  // per-warp references of l, flags
   static constexpr int kJoin = kWarps * kStages * kUnit;
   static constexpr int kQ = kJoin + (TEAM > 1 ? 2 * kPart : 0);
   static constexpr int kQBytes = query_in_smem(D, NT) ? D / 16 * 32 * 8 * NT : 0;   // of one worker
   static constexpr int kScale = kQ + kWarps / TEAM * kQBytes;
   static constexpr int kBars = kScale + kWarps * kStages * 8;
   static constexpr int kLse = kBars + kWarps * kStages * 8;
-  static constexpr int kFlags = kLse + kWarps * kH * 4;
+  static constexpr int kRefs = kLse + kWarps * kH * 4;
+  static constexpr int kFlags = kRefs + kWarps * kH * 4;
   static constexpr int kBytes = kFlags + 16;
 };
 
@@ -168,6 +175,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float lds_f1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float2 lds_f2(uint32_t addr) {
@@ -316,10 +328,23 @@ __device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D,
   else if constexpr (Query<D, NT>::kShared) __syncwarp();
 }
 
+// The exponent of a scale, at most 126 and at least that of FP32's smallest normal number.
+__device__ __forceinline__ int exponent_of(float scale) {
+  return min(max(static_cast<int>(__float_as_uint(scale) >> 23 & 0xFF), 1), 253) - 127;
+}
+
+// The V scales that a warp has met in its segment: the exponent of the first one that is not 0 (INT32_MIN: none yet),
+// and whether one was so far from it that l has references of its own, in shared memory at `ref` for the lane's columns.
+struct Scales {
+  int first;
+  bool apart;
+  uint32_t ref;
+};
+
 // One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens are not visible.
 template <int D, bool E4M3, int NT, int TEAM, bool PARTIAL>
 __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& Q, uint32_t kbase, uint32_t scale_addr,
-                                          const Range& range, int& kref, int lane) {
+                                          const Range& range, Scales& vs, int lane) {
   constexpr int MT = kHalf / D / 16;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t vbase = kbase + kHalf;
@@ -426,16 +451,22 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       for (int m = 0; m < MT; ++m) load_v(h, m);
   }
 
-  // V's scale f 2^k, k relative to the warp's first page of the segment
-  const uint32_t vs = __float_as_uint(sc.y);
+  // V's scale f 2^vk, k relative to the warp's first page of the segment
   const bool zero = sc.y == 0.0f;
-  const int vk = min(max(static_cast<int>((vs >> 23) & 0xFF), 1) - 127, 126);
-  if (!zero && kref == INT32_MIN) kref = vk;
-  const float rise = !zero && vk - kref > kReachUp ? static_cast<float>(vk - kref) : 0.0f;
-  if (rise > 0.0f) kref = vk;
-  const int k = zero ? 0 : max(vk - kref, -kReachDown);
-  const float f = zero || vk - kref < -kReachDown ? 0.0f : sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
-  const float back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  const int vk = exponent_of(sc.y);
+  if (!zero && vs.first == INT32_MIN) vs.first = vk;
+  const int k = zero ? 0 : vk - vs.first;
+  const float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
+  if (__builtin_expect(zero || abs(k) > kReach, 0) && !vs.apart) {
+    vs.apart = true;                      // so far l is relative to m
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) tc::sts_u32(vs.ref + 32 * n + 4 * e, __float_as_uint(st.m[n][e]));
+  }
+  // what a logit's exponent gets before P; a page of zeros adds to l alone
+  const float kz = vs.apart && zero ? -INFINITY : static_cast<float>(k);
+  const float back = vs.apart ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 
   float top[NT][2];
 #pragma unroll
@@ -456,28 +487,38 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
     }
   }
-  // A reference V scale that is 2^rise as large lowers m, which bounds z + k, by rise: O^T stays as it is and l grows,
-  // by 2^28 at most (it is below 2^96 for 2^22 tokens). What m is not lowered by, O^T shrinks by; l is 2^10 or more
-  // then, so what FP16 flushes of a token's product is below 2^-35 of a V of the new scale.
-  bool move = rise > 0.0f;
+  bool move = vs.apart;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) move |= top[n][e] + k > st.m[n][e] + kSlack;
+    for (int e = 0; e < 2; ++e) move |= top[n][e] + kz > st.m[n][e] + kSlack;
   if (__any_sync(kFull, move)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float c[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = top[n][e] + k;
+        float x = top[n][e];
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-        x = fmaxf(fminf(x, 3e38f), st.m[n][e] - fminf(rise, 28.0f));
-        c[e] = dev::fast_exp2(st.m[n][e] - rise - x);
-        st.l[n][e] *= dev::fast_exp2(st.m[n][e] - x);
+        if (vs.apart) {
+          // the lanes of a column write one value, once all have read the last
+          const uint32_t ref = vs.ref + 32 * n + 4 * e;
+          const float was = lds_f1(ref), y = fmaxf(fminf(x, 3e38f), was);
+          __syncwarp();
+          tc::sts_u32(ref, __float_as_uint(y));
+          float l = st.l[n][e] * dev::fast_exp2(was - y);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) l += dev::fast_exp2(s[m][n][2 * r + e] - y + kLift);
+          st.l[n][e] = l;
+        }
+        x = fmaxf(fminf(x + kz, 3e38f), st.m[n][e]);
+        c[e] = dev::fast_exp2(st.m[n][e] - x);
         st.m[n][e] = x;
+        if (!vs.apart) st.l[n][e] *= c[e];
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -492,7 +533,7 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float sum[2] = {0.0f, 0.0f};
-    const float b0 = static_cast<float>(k) - st.m[n][0] + kLift, b1 = static_cast<float>(k) - st.m[n][1] + kLift;
+    const float b0 = kz - st.m[n][0] + kLift, b1 = kz - st.m[n][1] + kLift;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -710,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
     // no warp still reads the last segment's Q^T in shared memory: that segment ended at a barrier
     convert_query<D, NT, TEAM>(Q, raw, a.scale_log2, wl, member, lane);
     st.clear();
-    int kref = INT32_MIN;
+    Scales vs{INT32_MIN, false, base + P::kRefs + warp * kH * 4 + 8 * t};
 #pragma unroll 1
     for (int u = member; u < s.num_pages * P::kUnits; u += TEAM) {
       if (loaded >> stage & 1) {
@@ -721,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         dead = __any_sync(kFull, dead);
         parity ^= 1u << stage;
         const Range range(s, page_of(s, s.page_begin + u / P::kUnits) * kPage + u % P::kUnits * P::kTokens);
-        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
-        else take_unit<D, E4M3, NT, TEAM, true>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, kref, lane);
+        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vs, lane);
+        else take_unit<D, E4M3, NT, TEAM, true>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vs, lane);
         __syncwarp();
       }
       fill(stage);
@@ -734,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
       raw.load(a, next, member, lane);
     }
     // this warp's l over its lanes, and its lse
-    const float vref = kref == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(max(127 + kref, 1)) << 23);
+    const float vref = __uint_as_float(static_cast<uint32_t>(127 + max(vs.first, -126)) << 23);
     float L[NT][2], weight[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -745,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         l += __shfl_xor_sync(kFull, l, 8);
         l += __shfl_xor_sync(kFull, l, 16);
         st.l[n][e] = l;
-        L[n][e] = l == 0.0f ? -INFINITY : st.m[n][e] - kLift + lg2(l);
+        L[n][e] = l == 0.0f ? -INFINITY : (__builtin_expect(vs.apart, 0) ? lds_f1(vs.ref + 32 * n + 4 * e) : st.m[n][e]) - kLift + lg2(l);
         weight[n][e] = 1.0f;
         if (TEAM > 1 && g == 0) wl[warp * kH + 8 * n + 2 * t + e] = L[n][e];
       }
@@ -756,17 +797,41 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
 #pragma unroll
         for (int e = 0; e < 2; ++e) weight[n][e] = weigh(wl + 8 * n + 2 * t + e, L[n][e], L[n][e]);
     }
+    float c[NT][2];                        // what O^T is multiplied by; any number where it is 0
+    bool small = vs.apart;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float c = st.l[n][e] == 0.0f || weight[n][e] == 0.0f ? 0.0f : __fdividef(weight[n][e], st.l[n][e]) * vref;
+        c[n][e] = st.l[n][e] == 0.0f ? 1.0f : __fdividef(weight[n][e], st.l[n][e]) * vref;
+        small |= c[n][e] < kSmall;
+      }
+    if (__builtin_expect(small, 0)) {
+      // sum 2^z V = O^T 2^(first + m - kLift), of a whole of 2^L: in two factors, neither of which is flushed
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const bool none = vs.first == INT32_MIN || L[n][e] == -INFINITY;
+          const float x = none ? -600.0f : static_cast<float>(vs.first) + (st.m[n][e] - L[n][e]) - kLift;
+          const float half = floorf(0.5f * x), by = dev::fast_exp2(half);
+          c[n][e] = dev::fast_exp2(x - half);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            st.o[i][n][e] *= by;
+            st.o[i][n][2 + e] *= by;
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          st.o[i][n][e] *= c;
-          st.o[i][n][2 + e] *= c;
+          st.o[i][n][e] *= c[n][e];
+          st.o[i][n][2 + e] *= c[n][e];
         }
-      }
     // from here on a warp of a team owns a quarter of the tiles, the first kOwn of st.o
     constexpr int kOwn = D / 16 / TEAM;
     const int tile0 = member * kOwn;
