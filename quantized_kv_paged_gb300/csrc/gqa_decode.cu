@@ -328,9 +328,9 @@ __device__ __forceinline__ void convert_query(Query<D, NT>& Q, const RawQuery<D,
   else if constexpr (Query<D, NT>::kShared) __syncwarp();
 }
 
-// The exponent of a scale, at most 126 and at least that of FP32's smallest normal number.
+// The exponent of a scale, at most 127; that of FP32's smallest normal number where it is below that.
 __device__ __forceinline__ int exponent_of(float scale) {
-  return min(max(static_cast<int>(__float_as_uint(scale) >> 23 & 0xFF), 1), 253) - 127;
+  return min(max(static_cast<int>(__float_as_uint(scale) >> 23 & 0xFF), 1), 254) - 127;
 }
 
 // The V scales that a warp has met in its segment: the exponent of the first one that is not 0 (INT32_MIN: none yet),
@@ -456,8 +456,8 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const int vk = exponent_of(sc.y);
   if (!zero && vs.first == INT32_MIN) vs.first = vk;
   const int k = zero ? 0 : vk - vs.first;
-  const float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - vk) << 23);
-  if (__builtin_expect(zero || abs(k) > kReach, 0) && !vs.apart) {
+  float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - min(vk, 126)) << 23);
+  if (__builtin_expect(zero || vk == 127 || abs(k) > kReach, 0) && !vs.apart) {
     vs.apart = true;                      // so far l is relative to m
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -467,6 +467,7 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   // what a logit's exponent gets before P; a page of zeros adds to l alone
   const float kz = vs.apart && zero ? -INFINITY : static_cast<float>(k);
   const float back = vs.apart ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+  if (vs.apart && vk == 127) f *= 0.5f;   // an f of 4 times a P of 2^14 would be past FP16's largest
 
   float top[NT][2];
 #pragma unroll

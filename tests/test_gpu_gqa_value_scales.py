@@ -104,3 +104,15 @@ class Requests:
 def test_scales_and_logits_that_go_apart(qkvp, cache, dim, heads, rows, num_sms, repeat, copies, team):
     p = Requests(rows, heads, dim, cache, repeat, copies, seed=dim + heads).check(num_sms)
     assert p.warps_per_worker == team
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_scales_at_the_top_of_the_range(qkvp, dim):
+    """V scales next to 2^128 behind a logit that just does not move the softmax's reference."""
+    top = float(np.log2(np.float64(np.finfo(np.float32).max)))
+    b = Requests([[(top, 0), (top, z)] for z in (7.875, 7.9375, 8, 8.0625)], 8, dim, R.E4M3, v_codes=0.25)
+    b.codes[:, 0, :, :, 1] = 0                        # equal logits within a page
+    b.scale[:, 0][b.scale[:, 0] == 2.0 ** -10] = 0.0  # the first page's are 0, the second's up to 8 for head 0
+    b.scale[:, 1] = np.finfo(np.float32).max
+    b.check(1)
+    b.check(152)
