@@ -56,7 +56,7 @@ Visible visible_pages(int32_t len, int32_t window, int32_t sinks) {
   v.sink_end = std::min(sinks, v.win_begin);
   v.win_page = v.win_begin / kPage;
   // a page that holds both sinks and window is counted once
-  v.sink_pages = std::min((v.sink_end + kPage - 1) / kPage, v.win_page);
+  v.sink_pages = std::min(static_cast<int32_t>((static_cast<int64_t>(v.sink_end) + kPage - 1) / kPage), v.win_page);
   v.pages = v.sink_pages + pages - v.win_page;
   v.tokens = static_cast<int64_t>(window) + v.sink_end;
   return v;

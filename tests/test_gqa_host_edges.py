@@ -1,0 +1,28 @@
+"""Edges of the head-pool plan and of the appends' host checks, without a GPU."""
+import numpy as np
+import pytest
+
+import quantized_kv_paged_gb300 as q
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from quantized_kv_paged_gb300 import build
+    build.build()
+    return q.load()
+
+
+LONGEST = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("window,sinks,status,pages,tokens", [
+    (0, 0, q.QKVP_E_UNSUPPORTED, 0, 0),                       # every page of it is visible: more than the plan addresses
+    (1, LONGEST, q.QKVP_E_UNSUPPORTED, 0, 0), (62, LONGEST - 62, q.QKVP_E_UNSUPPORTED, 0, 0),
+    (63, LONGEST, q.QKVP_E_UNSUPPORTED, 0, 0), (LONGEST, 0, q.QKVP_E_UNSUPPORTED, 0, 0),
+    (1, 0, q.QKVP_OK, 1, 1), (62, 65, q.QKVP_OK, 3, 127), (64, 0, q.QKVP_OK, 2, 64)])
+def test_longest_request(lib, window, sinks, status, pages, tokens):
+    p = q.gqa_decode_plan(np.array([0, 1 << 25], np.int32), np.array([LONGEST], np.int32), 4, 1, 64, q.CACHE_E4M3, window=window, sinks=sinks,
+                          num_sms=4, raise_on_error=False)
+    assert p.status == status
+    if status == q.QKVP_OK:
+        assert (p.total_pages, p.total_tokens) == (pages, tokens)
