@@ -134,8 +134,8 @@ int mla_append_rope(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int
     if (kv_scale == nullptr || !std::isfinite(global_scale) || !(global_scale > 0.0f)) return QKVP_E_INVALID;
     if (!aligned(kv_scale, 16)) return QKVP_E_INVALID;
   }
+  if (n_tokens == 0) return QKVP_OK;       // of empty arrays, which may have no addresses
   if ((q_pe != nullptr) != (q != nullptr) || (q_pe != nullptr) != (num_heads > 0)) return QKVP_E_INVALID;
-  if (n_tokens == 0) return QKVP_OK;
   if (!c_kv || !k_pe || !slot_mapping || !positions || !cos_sin || !kv_data) return QKVP_E_INVALID;
   if (!aligned(c_kv, 16) || !aligned(k_pe, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||
       !aligned(cos_sin, 16) || !aligned(kv_data, 16))
@@ -184,9 +184,10 @@ int gqa_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_st
   if (rope_style != QKVP_ROPE_HALVES && rope_style != QKVP_ROPE_PAIRS) return QKVP_E_UNSUPPORTED;
   if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16) return QKVP_E_UNSUPPORTED;
   if ((rot_dim > 0) != (cos_sin != nullptr)) return QKVP_E_INVALID;
-  if ((q != nullptr) != (q_out != nullptr) || (q != nullptr) != (num_heads > 0)) return QKVP_E_INVALID;
   if (n_tokens > INT32_MAX || max_positions > INT32_MAX) return QKVP_E_UNSUPPORTED;
-  if (n_tokens == 0 || batch == 0) return QKVP_OK;
+  if (n_tokens == 0) return QKVP_OK;       // of empty arrays, which may have no addresses
+  if ((q != nullptr) != (q_out != nullptr) || (q != nullptr) != (num_heads > 0)) return QKVP_E_INVALID;
+  if (batch == 0) return QKVP_OK;
   if (!k || !v || !tok_indptr || !kv_len || !kv_indptr || !kv_indices || !kv_data || !kv_scale) return QKVP_E_INVALID;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_data, 16) || !aligned(tok_indptr, 4) || !aligned(kv_len, 4) ||
       !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(kv_scale, 4) || !aligned(positions, 8) ||

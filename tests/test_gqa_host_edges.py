@@ -26,3 +26,10 @@ def test_longest_request(lib, window, sinks, status, pages, tokens):
     assert p.status == status
     if status == q.QKVP_OK:
         assert (p.total_pages, p.total_tokens) == (pages, tokens)
+
+
+def test_a_step_without_tokens_may_have_queries(lib):
+    """An empty tensor has no address: no tokens, a head count and NULL queries are nothing to do, not a misfit."""
+    assert lib.mla_append_rope(None, 512, None, 64, 0, None, None, 16, 9, 1, None, 1024, 64, 16, None, 16, None, 1, 1.0, 64, 4, None) == q.QKVP_OK
+    assert lib.gqa_append_rope(None, 256, None, 256, 0, 4, 4, 1, 4, 4, 9, None, 16, 100, 64, 0, 2, 128, 16, 4, 1, 64, 9, None, 512, 4, None,
+                               None) == q.QKVP_OK
