@@ -410,7 +410,7 @@ int mla_append_rope(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int
  *  k, v         device bf16, head h of token t at k + t * k_stride + h * head_dim (elements).
  *  n_tokens     rows of k, v, positions, q and q_out (tok_indptr entries beyond it are cut to it).
  *  tok_indptr   device int32 [batch + 1], non-decreasing from 0. kv_len device int32 [batch].
- *  kv_indptr, kv_indices, nnz: page table on the device, as for kv_gather_fp8.
+ *  kv_indptr, kv_indices, nnz: page table on the device, as for kv_gather_fp8 (kv_indices may be NULL if nnz is 0).
  *  positions    device int64 [n_tokens], the positions that rotate K and Q; NULL: the cache positions.
  *  cos_sin      device float [max_positions][rot_dim], cosines then sines; rot_dim a multiple of 16 up to
  *               head_dim, or 0 (no rotation, cos_sin NULL).

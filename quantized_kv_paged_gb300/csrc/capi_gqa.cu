@@ -188,7 +188,7 @@ int gqa_append_rope(const void* k, int64_t k_stride, const void* v, int64_t v_st
   if (n_tokens == 0) return QKVP_OK;       // of empty arrays, which may have no addresses
   if ((q != nullptr) != (q_out != nullptr) || (q != nullptr) != (num_heads > 0)) return QKVP_E_INVALID;
   if (batch == 0) return QKVP_OK;
-  if (!k || !v || !tok_indptr || !kv_len || !kv_indptr || !kv_indices || !kv_data || !kv_scale) return QKVP_E_INVALID;
+  if (!k || !v || !tok_indptr || !kv_len || !kv_indptr || (!kv_indices && nnz > 0) || !kv_data || !kv_scale) return QKVP_E_INVALID;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_data, 16) || !aligned(tok_indptr, 4) || !aligned(kv_len, 4) ||
       !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(kv_scale, 4) || !aligned(positions, 8) ||
       !aligned(cos_sin, 16) || !aligned(q, 16) || !aligned(q_out, 16))

@@ -25,3 +25,18 @@ def test_steps_without_tokens(qkvp):
                       q=bf(0, 4, 64), q_out=bf(0, 4, 64))
     torch.cuda.synchronize()
     assert (pool == 0x5A).all() and (codes == 0x5A).all() and (scale == 3).all()
+
+
+def test_tokens_without_any_page(qkvp):
+    """An empty page table: no token has a page, so nothing is stored, and the queries are rotated all the same."""
+    rng = np.random.default_rng(2)
+    k, query = (R.to_bf16(rng.standard_normal((5, h, 64)).astype(np.float32)) for h in (1, 4))
+    cs = R.table(100, 64)
+    codes, scale = torch.full((2, 2, 1, 64, 64), 0x5A, dtype=torch.uint8, device="cuda"), torch.full((2, 2, 1), 3.0, device="cuda")
+    q_out = torch.empty((5, 4, 64), dtype=torch.bfloat16, device="cuda")
+    q.gqa_append_rope(k.cuda(), k.cuda(), _i32(0, 2, 5), _i32(7, 0), _i32(0, 0, 0), _i32(), torch.from_numpy(cs).cuda(), q.ROPE_HALVES, codes, scale,
+                      q.CACHE_E4M3, q=query.cuda(), q_out=q_out)
+    torch.cuda.synchronize()
+    assert (codes == 0x5A).all() and (scale == 3).all()
+    want = np.stack([R.rotate(x, cs[p], R.HALVES) for x, p in zip(R.bf16_to_f32(query), (7, 8, 0, 1, 2))])
+    assert torch.equal(q_out.cpu().view(torch.int16), R.to_bf16(want).view(torch.int16))
