@@ -119,6 +119,8 @@ struct Range {
   __device__ bool all(int n) const { return lim >= n && (win <= 0 || sink >= n); }
 };
 
+// What the kernel before this one may have written while this one was already there is read by ordinary loads: the
+// read-only path is for memory that does not change during a kernel's life.
 template <class T>
 __device__ __forceinline__ T load_record(const T* p) {
   static_assert(sizeof(T) % 16 == 0, "records are read 16 bytes at a time");
@@ -126,7 +128,7 @@ __device__ __forceinline__ T load_record(const T* p) {
   const int4* src = reinterpret_cast<const int4*>(p);
   int4* dst = reinterpret_cast<int4*>(&s);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 16); ++i) dst[i] = __ldg(src + i);
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 16); ++i) dst[i] = src[i];
   return s;
 }
 
@@ -151,7 +153,7 @@ struct Feed {
     }
     const int local = page_of(s, s.page_begin + u / U);
     sub = u % U;
-    page = __ldg(a.kv_indices + s.page0 + local);
+    page = a.kv_indices[s.page0 + local];
     t0 = local * kPage + sub * (kPage / U);
   }
 };
@@ -268,7 +270,7 @@ struct RawQuery {
       for (int c = 0; c < kGroups; ++c)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          v[n][c][k] = h < s.heads ? __ldg(reinterpret_cast<const uint4*>(row + 64 * c + 8 * k)) : make_uint4(0, 0, 0, 0);
+          v[n][c][k] = h < s.heads ? *reinterpret_cast<const uint4*>(row + 64 * c + 8 * k) : make_uint4(0, 0, 0, 0);
     }
   }
 };

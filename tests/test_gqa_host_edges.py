@@ -33,3 +33,15 @@ def test_a_step_without_tokens_may_have_queries(lib):
     assert lib.mla_append_rope(None, 512, None, 64, 0, None, None, 16, 9, 1, None, 1024, 64, 16, None, 16, None, 1, 1.0, 64, 4, None) == q.QKVP_OK
     assert lib.gqa_append_rope(None, 256, None, 256, 0, 4, 4, 1, 4, 4, 9, None, 16, 100, 64, 0, 2, 128, 16, 4, 1, 64, 9, None, 512, 4, None,
                                None) == q.QKVP_OK
+
+
+@pytest.mark.parametrize("name", ["gqa_decode.cu", "append_rope.cu"])
+def test_overlapped_kernels_read_by_ordinary_loads(name):
+    """Kernels that are resident while the one before them still writes their inputs may not read these through the
+    read-only path, whose loads nothing orders behind the wait. No run shows a wrong order reliably; the source does."""
+    import os
+    from tests.conftest import ROOT
+    with open(os.path.join(ROOT, "quantized_kv_paged_gb300", "csrc", name)) as f:
+        text = f.read()
+    assert "launch_overlapped(" in text and "wait_for_previous()" in text
+    assert not [w for w in ("__ldg(", "ldg_nc", "ld.global.nc", "__restrict__") if w in text]
