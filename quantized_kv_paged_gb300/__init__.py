@@ -420,17 +420,29 @@ def gqa_append_rope(k, v, tok_indptr, kv_len, kv_indptr, kv_indices, cos_sin, ro
     return st if st == QKVP_OK else _check("gqa_append_rope", st, raise_on_error)
 
 
+def _workspace(t, here: int):
+    if t.get_device() != here:
+        raise ValueError("tensors need to be on one device, the current CUDA device: the workspace is on another")
+    if not t.is_contiguous():
+        raise ValueError(f"workspace needs a contiguous layout, got strides {t.stride()}")
+
+
 def gqa_decode_plan(kv_indptr, kv_len, num_heads: int, num_kv_heads: int, head_dim: int, cache_dtype: int,
                     window: int = 0, sinks: int = 0, num_sms: int = 0, min_splits: int = 0, workspace=None,
                     page_size: int = PAGE_SIZE, stream=None, raise_on_error: bool = True):
     """Plan a head-pool decode on the host; with workspace=None only sizes are computed. Returns a gqa_plan."""
     indptr, lens = _table(kv_indptr, kv_len)
     plan = gqa_plan()
-    ws = _ptr(workspace)
-    nbytes = int(workspace.numel() * workspace.element_size()) if workspace is not None else 0
+    ws, nbytes, on = None, 0, None
+    if workspace is not None:
+        _Torch.get()
+        here = workspace.get_device()
+        _workspace(workspace, here)
+        on = _launch_on(stream, here)
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
     st = load().gqa_decode_plan(indptr.ctypes.data, lens.ctypes.data, int(lens.shape[0]), num_heads,
                                 num_kv_heads, head_dim, page_size, cache_dtype, window, sinks, num_sms,
-                                min_splits, ws, nbytes, _stream(stream) if ws else None, ctypes.byref(plan))
+                                min_splits, ws, nbytes, on, ctypes.byref(plan))
     _check("gqa_decode_plan", st, raise_on_error)
     plan.status = st
     return plan
@@ -456,8 +468,7 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
     if lse is not None:
         _dense("lse", lse, (batch, heads), T.f32, here)
         lse_at = lse.data_ptr()
-    if workspace.get_device() != here:
-        raise ValueError("tensors need to be on one device, the current CUDA device: the workspace is on another")
+    _workspace(workspace, here)
     on = _launch_on(stream, here)
     st = (_lib or load()).gqa_decode_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
                                          kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse_at, workspace.data_ptr(),

@@ -45,3 +45,23 @@ def test_overlapped_kernels_read_by_ordinary_loads(name):
         text = f.read()
     assert "launch_overlapped(" in text and "wait_for_previous()" in text
     assert not [w for w in ("__ldg(", "ldg_nc", "ld.global.nc", "__restrict__") if w in text]
+
+
+def test_binding_refuses_workspaces_that_are_strided_or_elsewhere(lib):
+    """The plan's table is copied on the current device's stream, and the whole byte range from the workspace's start is
+    written: a workspace on another device would not be ordered before the run, a strided one would lose its gaps."""
+    import torch
+    ptr, lens = np.array([0, 2], np.int32), np.array([100], np.int32)
+    args = (ptr, lens, 4, 2, 128, q.CACHE_E4M3)
+    need = q.gqa_decode_plan(*args, num_sms=4).workspace_bytes
+    with pytest.raises(ValueError, match="current CUDA device"):
+        q.gqa_decode_plan(*args, num_sms=4, workspace=torch.zeros(need, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="contiguous"):
+        q.gqa_decode_plan(*args, num_sms=4, workspace=torch.zeros(2 * need, dtype=torch.uint8)[::2])
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)          # noqa: E731
+    run = dict(plan=q.gqa_decode_plan(*args, num_sms=4), q=bf(1, 4, 128), kv_data=torch.zeros((4, 2, 2, 64, 128), dtype=torch.uint8),
+               kv_scale=torch.zeros((4, 2, 2)), kv_indices=torch.zeros(2, dtype=torch.int32), sm_scale=0.1, out=bf(1, 4, 128), lse=None)
+    with pytest.raises(ValueError, match="contiguous"):
+        q.gqa_decode_run(workspace=torch.zeros(2 * need, dtype=torch.uint8)[::2], **run)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        q.gqa_decode_run(workspace=torch.zeros(need, dtype=torch.uint8), **run)
