@@ -181,7 +181,7 @@ typedef struct {
  * arithmetic, one rounding per operation): amax = max|x|; scale = amax / 448, or the NaN 0x7FC00000
  * if any x is NaN; codes = E4M3(x / scale) rounded to nearest even and saturated (NaN gives 0x7F),
  * or E4M3(x) (a signed zero) when scale == 0. The stored bytes are bit-identical to the CPU oracle.
- * If two tokens of one call name the same slot, which of them is stored is unspecified.
+ * If two tokens of one call name the same slot, that row is unspecified: it may mix what they bring.
  */
 int kv_append_quant(const void* src, int32_t src_dtype, int64_t n_tokens,
                     const int64_t* slot_mapping, void* kv_data, uint8_t* kv_scale,
@@ -380,7 +380,7 @@ int kv_gather_pages_bf16(const uint8_t* kv_data, int32_t page_size, int64_t num_
  *  kv_data, kv_scale, kv_dtype, global_scale, page_size, num_pages: as for kv_append_quant (an FP8,
  *               NVFP4 or per-token-scaled FP8 pool).
  * Row strides are multiples of 8 elements, c_kv, k_pe, q_pe, q, kv_data and cos_sin 16-byte aligned.
- * If two tokens of one call name the same slot, which of them is stored is unspecified.
+ * If two tokens of one call name the same slot, that row is unspecified: it may mix what they bring.
  */
 int mla_append_rope(const void* c_kv, int64_t c_kv_stride, const void* k_pe, int64_t k_pe_stride,
                     int64_t n_tokens, const int64_t* slot_mapping, const int64_t* positions,

@@ -40,3 +40,29 @@ def test_tokens_without_any_page(qkvp):
     assert (codes == 0x5A).all() and (scale == 3).all()
     want = np.stack([R.rotate(x, cs[p], R.HALVES) for x, p in zip(R.bf16_to_f32(query), (7, 8, 0, 1, 2))])
     assert torch.equal(q_out.cpu().view(torch.int16), R.to_bf16(want).view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [40, 1100])
+def test_slots_named_twice_leave_the_other_rows_right(qkvp, n):
+    """Every third token goes to slot 7: that row may hold anything, every other row and all queries are as they should be."""
+    rng = np.random.default_rng(n)
+    c_kv, k_pe, q_pe = (R.to_bf16(rng.standard_normal(s).astype(np.float32)) for s in ((n, 512), (n, 64), (n, 2, 64)))
+    cs = torch.from_numpy(R.table(n, 64)).cuda()
+    slots = 64 + np.arange(n)
+    twice = slots.copy()
+    twice[::3] = 7
+    got = []
+    for s in (slots, twice):
+        pool = torch.full((2 + n // 64 + 1, q.PAGE_BYTES_FP8_PER_TOKEN), 0x5A, dtype=torch.uint8, device="cuda")
+        query = torch.zeros((n, 2, 576), dtype=torch.bfloat16, device="cuda")
+        q.mla_append_rope(c_kv.cuda(), k_pe.cuda(), torch.from_numpy(s).cuda(), torch.arange(n, device="cuda"), cs, q.ROPE_HALVES, pool, None,
+                          q.KV_FP8_PER_TOKEN, q_pe=q_pe.cuda(), q=query)
+        torch.cuda.synchronize()
+        rows = torch.cat([pool[:, :64 * 576].reshape(-1, 576), pool[:, 64 * 576:].reshape(-1, 4)], 1).cpu()
+        got.append((rows, query.cpu()))
+    assert torch.equal(got[0][1].view(torch.int16), got[1][1].view(torch.int16))
+    once, again = got[0][0], got[1][0]
+    single = np.arange(n) % 3 != 0
+    assert torch.equal(once[slots[single]], again[slots[single]])
+    untouched = np.setdiff1d(np.arange(len(again)), np.concatenate([slots[single], [7]]))
+    assert (again[untouched] == 0x5A).all()
