@@ -488,7 +488,7 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
  *  q            device bf16 [batch][num_heads][head_dim]. Held as FP16 times a power of two per head.
  *  kv_data, kv_scale, num_pages: the head pool; kv_data 128-byte aligned (TMA reads it), scales finite
  *               and not negative. Page ids outside [0, num_pages) read as tokens that are not visible.
- *               V scales and logits may be any powers of two apart, in any order; a token's weight below 2^-100
+ *               V scales and logits may be any powers of two apart, in any order; a token's weight below 2^-70
  *               of the request's largest may count as zero.
  *  kv_indices   device int32 page ids addressed by the plan's kv_indptr.
  *  out          device bf16 [batch][num_heads][head_dim], 16-byte aligned; lse float [batch][num_heads]

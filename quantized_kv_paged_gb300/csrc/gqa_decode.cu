@@ -30,15 +30,15 @@
 // of a reduction per unit); P = 2^(z - m + 6) <= 2^14 is in FP16's normal range down to 2^-28 of the
 // largest weight. l is summed from the unrounded FP32 values. The V scale sv = f 2^k of a page multiplies
 // P: f (in [1, 2)) on the value, k in the exponent, less that of the warp's first page of the segment; l takes 2^-k
-// back. That serves scales within 2^24 of the first. From a page on whose scale is further away, or 0, the warp sums
-// l from exponentials of its own, relative to the largest logit, while m goes on bounding logit + k: what a page adds
-// to l and what it adds to O^T may then be any powers of two apart, in any order. Every finite scale is taken. (That
-// the rare form is there costs 1 x 1,024 tokens 6.2 to 6.5 us and 16 x 4,096 tokens of D 256 with 10 heads 33.5 to 34.7;
-// 44 x 32,768 and the ragged INT8 batch stay.)
+// back. That serves scales within 2^24 of the first. A segment with one further away is left for the worker's end, where
+// it is taken in a second form, in which l has exponentials of its own, relative to the largest logit, while m bounds
+// logit + k: what a page adds to l and what it adds to O^T may then be any powers of two apart, in any order. Every
+// finite scale is taken. (The second form in the usual loop took 47.7 us instead of 42.6 for 4,096 rows of 128 tokens of
+// D 128 with 16 heads; without it they take 42.0, and 4,096 rows of 512 tokens of D 256 201 instead of 210.)
 //
-// Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 428 us, 2.96 GB at
-// 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 87 %, issue 33 %, tensor pipe 18 %); 1 x 1,048,576 (4
-// heads) 162 us; 64 ragged requests (4 KV heads, 16 query heads each, INT8) 79 us. What is short is bound by its
+// Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 429 us, 2.96 GB at
+// 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 88 %, issue 33 %, tensor pipe 19 %); 1 x 1,048,576 (4
+// heads) 163 us; 64 ragged requests (4 KV heads, 16 query heads each, INT8) 79 us. What is short is bound by its
 // start and end: 2.5 to 3 us from the launch to the first unit (the worker's record, its page id and the page
 // are three reads in line, cold), 1 us a unit, 1 us for a partial to be written and counted, 1 to 3 us to join.
 #include <atomic>
@@ -60,19 +60,18 @@ constexpr int kH = kGqaPassHeads;
 constexpr int kHalf = 4096;              // bytes of K (and of V) in a unit
 constexpr int kUnit = 2 * kHalf;
 constexpr unsigned kFull = 0xffffffffu;
-// how far (log2) a logit may pass the reference; with 0 the 64 ragged INT8 requests take 81.9 us instead of 79.0
+// how far (log2) a logit may pass the reference; with 0 the 64 ragged INT8 requests take 83.2 us instead of 79.4
 constexpr float kSlack = 8.0f;
 constexpr float kLift = 6.0f;            // P is held as 2^(z - m + kLift)
 constexpr float kNone = -3e38f;          // reference before the first unit
 // How far (log2) V's scale may be from the first page's for l to be summed from P: the token of the largest logit has a P
-// of at least 2^(kLift - 2 kReach) then, far from where FP32 flushes.
-constexpr int kReach = 24;
-// Factors of O^T at a segment's end from which on they are one product; smaller ones, that may be near where FP32
-// flushes, are two.
-constexpr float kSmall = 0x1p-100f;
+// of at least 2^(kLift - 2 kReach) then, far from where FP32 flushes. The scale that a page of zeros counts as, below the
+// first: beside such a page weights down to 2^-80 of its own are normal numbers in FP16. And the least first scale: O^T's
+// last factor, weight / l 2^first, is not flushed for weights of a warp in its team of 2^-70 and more.
+constexpr int kReach = 24, kZeros = 60, kLowest = -30;
 
 // At D = 256 and 16 heads Q^T would take 64 of the 255 registers next to 128 of O^T: it is kept in shared memory (16 x
-// 4,096 tokens, 4 KV heads, 10 query heads each: 34 us, and 50 with it in registers, which spill).
+// 4,096 tokens, 4 KV heads, 10 query heads each: 34 us, and 44 with it in registers, which spill).
 constexpr bool query_in_smem(int dim, int nt) { return dim == 256 && nt == 2; }
 
 template <int D, int NT, int TEAM>
@@ -84,7 +83,7 @@ struct Shape {
   static constexpr int kTiles = D / 16;                // 16-dim row tiles of O^T
   static constexpr int kPart = kTiles * NT * 32 * 16;  // bytes of one warp's O^T
   // shared memory: rings, the join's buffer, Q^T where it is kept there, the units' scales, barriers, per-warp lse,
-  // per-warp references of l, flags
+  // per-warp references of l, the warps' flags of scales far apart, the join's flag
   static constexpr int kJoin = kWarps * kStages * kUnit;
   static constexpr int kQ = kJoin + (TEAM > 1 ? 2 * kPart : 0);
   static constexpr int kQBytes = query_in_smem(D, NT) ? D / 16 * 32 * 8 * NT : 0;   // of one worker
@@ -92,7 +91,8 @@ struct Shape {
   static constexpr int kBars = kScale + kWarps * kStages * 8;
   static constexpr int kLse = kBars + kWarps * kStages * 8;
   static constexpr int kRefs = kLse + kWarps * kH * 4;
-  static constexpr int kFlags = kRefs + kWarps * kH * 4;
+  static constexpr int kFar = kRefs + kWarps * kH * 4;
+  static constexpr int kFlags = kFar + kWarps * 4;
   static constexpr int kBytes = kFlags + 16;
 };
 
@@ -201,6 +201,49 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
+// The pool to the TMA: boxes of a unit's K or V, and of a quarter of it.
+struct PoolMaps {
+  CUtensorMap unit, piece;
+};
+
+// Whether a unit, from token t0 of the request on, is in the pool and has visible tokens.
+template <int D>
+__device__ __forceinline__ bool seen(const GqaDecodeArgs& a, const GqaSegment& s, int32_t page, int t0) {
+  return page >= 0 && page < a.num_pages && Range(s, t0).any(0, kHalf / D);
+}
+
+// One lane: the copies of a unit's K, V and scales, which complete a phase of the barrier.
+template <int D>
+__device__ __forceinline__ void load_unit(const GqaDecodeArgs& a, const PoolMaps& maps, const GqaSegment& s, int32_t page, int t0, int sub,
+                                          uint32_t dst, uint32_t scale, uint32_t bar) {
+  constexpr int kTokens = kHalf / D;
+  const int64_t kb = static_cast<int64_t>(page) * 2 * a.kv_heads + s.kv_head, vb = kb + a.kv_heads;
+  cp_async4(scale, a.kv_scale + kb);
+  cp_async4(scale + 4, a.kv_scale + vb);
+  cp_async_arrive(bar);
+  const int krow = static_cast<int>(kb * (kPage * D / 128)) + sub * (kHalf / 128);
+  const int vrow = static_cast<int>(vb * (kPage * D / 128)) + sub * (kHalf / 128);
+  const Range range(s, t0);
+  if (range.all(kTokens)) {
+    tc::mbar_arrive_expect_tx(bar, kUnit);
+    tma_load_2d(dst, &maps.unit, 0, krow, bar);
+    tma_load_2d(dst + kHalf, &maps.unit, 0, vrow, bar);
+  } else {
+    // of a unit at an edge only the quarters that hold a visible token; what is left in the others is masked
+    constexpr int kPiece = kTokens / 4;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bytes += range.any(i * kPiece, kPiece) ? 2 * kHalf / 4 : 0;
+    tc::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!range.any(i * kPiece, kPiece)) continue;
+      tma_load_2d(dst + i * (kHalf / 4), &maps.piece, 0, krow + i * (kHalf / 4 / 128), bar);
+      tma_load_2d(dst + kHalf + i * (kHalf / 4), &maps.piece, 0, vrow + i * (kHalf / 4 / 128), bar);
+    }
+  }
+}
+
 // The four codes of a word -> FP16 pairs (bytes 0, 1) and (bytes 2, 3), exact. INT8: the biased byte
 // under the exponent of 1024 is 1024 + 128 + c; the subtraction is exact.
 template <bool E4M3>
@@ -215,11 +258,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t&
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(h), "r"(0x64806480u));
   }
 }
-
-// The pool to the TMA: boxes of a unit's K or V, and of a quarter of it.
-struct PoolMaps {
-  CUtensorMap unit, piece;
-};
 
 // O^T and softmax state of one warp; column e of tile nt is head 8 nt + 2 (lane % 4) + e.
 template <int D, int NT>
@@ -335,18 +373,22 @@ __device__ __forceinline__ int exponent_of(float scale) {
   return min(max(static_cast<int>(__float_as_uint(scale) >> 23 & 0xFF), 1), 254) - 127;
 }
 
-// The V scales that a warp has met in its segment: the exponent of the first one that is not 0 (INT32_MIN: none yet),
-// and whether one was so far from it that l has references of its own, in shared memory at `ref` for the lane's columns.
-struct Scales {
-  int first;
-  bool apart;
-  uint32_t ref;
-};
+// Whether a V scale is out of reach of the warp's first one of the segment that is not 0, whose exponent is `first`
+// (INT32_MIN: none yet, then it is this one).
+__device__ __forceinline__ bool out_of_reach(float scale, int& first) {
+  const int vk = exponent_of(scale);
+  if (scale == 0.0f) return false;
+  if (first == INT32_MIN) first = vk;
+  return abs(vk - first) > kReach || first < kLowest || vk == 127;
+}
 
-// One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens are not visible.
-template <int D, bool E4M3, int NT, int TEAM, bool PARTIAL>
+// One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens may be not visible. first: the exponent of the
+// warp's first V scale of the segment that is not 0 (INT32_MIN: none yet). A unit whose scale is out of reach of it sets the
+// flag at `at` in shared memory; the state is worth nothing then. APART: no scale is; l is relative to the references at
+// `at` (for the lane's columns), and both references are renewed at every unit.
+template <int D, bool E4M3, int NT, int TEAM, bool PARTIAL, bool APART>
 __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& Q, uint32_t kbase, uint32_t scale_addr,
-                                          const Range& range, Scales& vs, int lane) {
+                                          const Range& range, int& first, uint32_t at, int lane) {
   constexpr int MT = kHalf / D / 16;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t vbase = kbase + kHalf;
@@ -412,9 +454,9 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
 
   // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 4,096 rows of 512 tokens of
-  // D 256 with 16 heads take 195 us, and 207 with the loads behind it. With fewer registers left, at D 128 with 16
-  // heads and at D 256 in a team, they come behind it: 4,096 rows of 512 tokens of D 128 96.1 us, 100.4 ahead of it;
-  // 16 x 4,096 tokens of D 256 33.6 us, 34.3. D 64 and up to 8 heads do not tell the two apart.
+  // D 256 with 16 heads take 210 us, and 218 with the loads behind it. With fewer registers left, at D 128 with 16
+  // heads and at D 256 in a team, they come behind it: 4,096 rows of 512 tokens of D 128 99 us, 105 ahead of it;
+  // 16 x 4,096 tokens of D 256 34.0 us, 34.7. D 64 and up to 8 heads do not tell the two apart.
   constexpr bool kEarlyV = NT == 1 || D == 64 || (D == 256 && TEAM == 1);
   const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
   constexpr int kSides = (D + 127) / 128;              // 128-dim halves of a token
@@ -453,23 +495,13 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       for (int m = 0; m < MT; ++m) load_v(h, m);
   }
 
-  // V's scale f 2^vk, k relative to the warp's first page of the segment
-  const bool zero = sc.y == 0.0f;
-  const int vk = exponent_of(sc.y);
-  if (!zero && vs.first == INT32_MIN) vs.first = vk;
-  const int k = zero ? 0 : vk - vs.first;
-  float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - min(vk, 126)) << 23);
-  if (__builtin_expect(zero || vk == 127 || abs(k) > kReach, 0) && !vs.apart) {
-    vs.apart = true;                      // so far l is relative to m
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) tc::sts_u32(vs.ref + 32 * n + 4 * e, __float_as_uint(st.m[n][e]));
-  }
-  // what a logit's exponent gets before P; a page of zeros adds to l alone
-  const float kz = vs.apart && zero ? -INFINITY : static_cast<float>(k);
-  const float back = vs.apart ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-  if (vs.apart && vk == 127) f *= 0.5f;   // an f of 4 times a P of 2^14 would be past FP16's largest
+  // V's scale f 2^vk, k relative to the first. A page of zeros adds to l alone.
+  const bool out = out_of_reach(sc.y, first), zero = sc.y == 0.0f;
+  if (!APART && out) tc::sts_u32(at, 1);
+  const int vk = exponent_of(sc.y), k = zero ? -kZeros : vk - first;
+  // (an f of 4 times a P of 2^14 would be past FP16's largest number)
+  const float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - (APART ? min(vk, 126) : vk)) << 23) * (APART && vk == 127 ? 0.5f : 1.0f);
+  const float kz = APART && zero ? -INFINITY : static_cast<float>(k);
 
   float top[NT][2];
 #pragma unroll
@@ -490,7 +522,7 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
     }
   }
-  bool move = vs.apart;
+  bool move = APART;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -505,9 +537,9 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-        if (vs.apart) {
+        if constexpr (APART) {
           // the lanes of a column write one value, once all have read the last
-          const uint32_t ref = vs.ref + 32 * n + 4 * e;
+          const uint32_t ref = at + 32 * n + 4 * e;
           const float was = lds_f1(ref), y = fmaxf(fminf(x, 3e38f), was);
           __syncwarp();
           tc::sts_u32(ref, __float_as_uint(y));
@@ -520,8 +552,8 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         }
         x = fmaxf(fminf(x + kz, 3e38f), st.m[n][e]);
         c[e] = dev::fast_exp2(st.m[n][e] - x);
+        if constexpr (!APART) st.l[n][e] *= c[e];
         st.m[n][e] = x;
-        if (!vs.apart) st.l[n][e] *= c[e];
       }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
@@ -532,6 +564,7 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
       }
     }
   }
+  const float back = __uint_as_float(static_cast<uint32_t>(APART ? 0 : 127 - k) << 23);
   uint32_t p[MT][NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -547,7 +580,9 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         p[m][n][r] = transpose8(dev::pack_f16x2(p0 * f, p1 * f));
       }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) st.l[n][e] += sum[e] * back;
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (!APART) st.l[n][e] += sum[e] * back;
+    }
   }
 
 #pragma unroll
@@ -678,9 +713,275 @@ __device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegme
     }
 }
 
+// The end of a segment: the warp's sums become outputs, or a partial that the last of its group joins. first: the exponent
+// that O^T is relative to. Where one of the warps met scales far apart its flag is cleared, nothing done, and false returned.
+template <int D, int NT, int TEAM>
+__device__ __forceinline__ bool finish_segment(const GqaDecodeArgs& a, const GqaSegment& s, State<D, NT>& st, int first, uint8_t* smem, int warp,
+                                               int lane) {
+  using P = Shape<D, NT, TEAM>;
+  const int member = TEAM == 1 ? 0 : warp, t = lane & 3, g = lane >> 2;
+  float4* join = reinterpret_cast<float4*>(smem + P::kJoin);
+  float* wl = reinterpret_cast<float*>(smem + P::kLse);          // [kWarps][kH] lse of each warp
+  int* flag = reinterpret_cast<int*>(smem + P::kFlags);
+  volatile int* far = reinterpret_cast<volatile int*>(smem + P::kFar);
+  if (TEAM == 1 && __builtin_expect(far[warp] != 0, 0)) {
+    __syncwarp();
+    if (lane == 0) far[warp] = 0;
+    __syncwarp();
+    return false;
+  }
+  // this warp's l over its lanes, and its lse
+  const float vref = first == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + first) << 23);
+  float L[NT][2], weight[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[n][e];
+      l += __shfl_xor_sync(kFull, l, 4);
+      l += __shfl_xor_sync(kFull, l, 8);
+      l += __shfl_xor_sync(kFull, l, 16);
+      st.l[n][e] = l;
+      L[n][e] = l == 0.0f ? -INFINITY : st.m[n][e] - kLift + lg2(l);
+      weight[n][e] = 1.0f;
+      if (TEAM > 1 && g == 0) wl[warp * kH + 8 * n + 2 * t + e] = L[n][e];
+    }
+  if constexpr (TEAM > 1) {
+    __syncthreads();
+    const int4 x = *reinterpret_cast<const int4*>(smem + P::kFar);
+    if (__builtin_expect((x.x | x.y | x.z | x.w) != 0, 0)) {
+      __syncthreads();                     // all have read the flags before they change
+      if (lane == 0) far[warp] = 0;
+      __syncwarp();
+      return false;
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) weight[n][e] = weigh(wl + 8 * n + 2 * t + e, L[n][e], L[n][e]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float c = st.l[n][e] == 0.0f || weight[n][e] == 0.0f ? 0.0f : __fdividef(weight[n][e], st.l[n][e]) * vref;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        st.o[i][n][e] *= c;
+        st.o[i][n][2 + e] *= c;
+      }
+    }
+  // from here on a warp of a team owns a quarter of the tiles, the first kOwn of st.o
+  constexpr int kOwn = D / 16 / TEAM;
+  const int tile0 = member * kOwn;
+  if constexpr (TEAM > 1) scatter_sum<D, NT>(st.o, join, warp, lane);
+  if (s.partial < 0) {
+    write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
+    return true;
+  }
+  int slot = s.partial, from = s.group_first, count = s.group_count, counter = s.counter;
+  bool top = s.top_counter < 0;
+#pragma unroll 1
+  while (true) {
+    float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kH * D) + tile0 * NT * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
+    if (member == 0 && g == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(slot) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
+    }
+    // arrive once all of the slot is written
+    __threadfence();
+    int last = 0;
+    if constexpr (TEAM > 1) {
+      __syncthreads();
+      if (threadIdx.x == 0) *flag = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
+      __syncthreads();
+      last = *flag;
+    } else {
+      __syncwarp();
+      if (lane == 0) last = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
+      last = __shfl_sync(kFull, last, 0);
+    }
+    if (last == 0) break;
+    // The last arrival: every slot is written. Each warp joins its tiles of all slots, in their order, a few
+    // slots at a time with their lse, under a running maximum.
+    __threadfence();
+    if (member == 0 && lane == 0) a.counters[counter] = 0;        // ready for the next run
+    const float* gl = a.part_lse + static_cast<int64_t>(from) * kH + 2 * t;
+    const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(from) * kH * D) + tile0 * NT * 32 + lane;
+    float M[NT][2], W[NT][2];
+    st.clear();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = -INFINITY, W[n][0] = W[n][1] = 0.0f;
+    constexpr int kVecs = P::kCtas == 3 ? 16 : 32;                // 16-byte loads in flight of a lane
+    constexpr int kBatch = kOwn * NT >= kVecs ? 1 : kVecs / (kOwn * NT) > 8 ? 8 : kVecs / (kOwn * NT);
+#pragma unroll 1
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      float4 v[kBatch][kOwn][NT];
+      float2 x[kBatch][NT];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int k = k0 + j;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          x[j][n] = k < count ? __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n)) : make_float2(-INFINITY, -INFINITY);
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i)
+            v[j][i][n] = k < count ? __ldcg(go + static_cast<int64_t>(k) * (kH * D / 4) + (i * NT + n) * 32) : make_float4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = M[n][e];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) m = dev::max_nan(m, e ? x[j][n].y : x[j][n].x);
+          const float c = m == -INFINITY ? 1.0f : dev::fast_exp2(M[n][e] - m);
+          W[n][e] *= c;
+          M[n][e] = m;
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) {
+            st.o[i][n][e] *= c;
+            st.o[i][n][2 + e] *= c;
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const float z = m == -INFINITY ? 0.0f : dev::fast_exp2((e ? x[j][n].y : x[j][n].x) - m);
+            W[n][e] += z;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+              st.o[i][n][e] += z * (e ? v[j][i][n].y : v[j][i][n].x);
+              st.o[i][n][2 + e] += z * (e ? v[j][i][n].w : v[j][i][n].z);
+            }
+          }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float c = W[n][e] == 0.0f ? 0.0f : __fdividef(1.0f, W[n][e]);
+        L[n][e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+          st.o[i][n][e] *= c;
+          st.o[i][n][2 + e] *= c;
+        }
+      }
+    if (top) {
+      write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
+      break;
+    }
+    slot = s.sub_slot;
+    from = s.top_first;
+    count = s.top_count;
+    counter = s.top_counter;
+    top = true;
+  }
+  return true;
+}
+
+// Whether a warp's part of a segment was left: the units in their order, by their V scales alone.
+template <int D, int TEAM>
+__device__ bool was_left(const GqaDecodeArgs& a, const GqaSegment& s, int member) {
+  constexpr int kTokens = kHalf / D, kUnits = kPage / kTokens;
+  int first = INT32_MIN;
+#pragma unroll 1
+  for (int u = member; u < s.num_pages * kUnits; u += TEAM) {
+    const int local = page_of(s, s.page_begin + u / kUnits);
+    const int32_t page = a.kv_indices[s.page0 + local];
+    if (!seen<D>(a, s, page, local * kPage + u % kUnits * kTokens)) continue;
+    if (out_of_reach(a.kv_scale[(static_cast<int64_t>(page) * 2 + 1) * a.kv_heads + s.kv_head], first)) return true;
+  }
+  return false;
+}
+
+// A worker's segments whose V scales are far apart, after all others, with nothing else alive: the usual form loses
+// registers to this one in its own loop. The units come one after the other through the first stage of the warp's ring,
+// whose barrier's parity is given. O^T is normalised here, so that the segment's end finds an l of 1 and values relative
+// to 2^0. Returns whether a wait ran out.
+template <int D, bool E4M3, int NT, int TEAM>
+__device__ __forceinline__ bool take_apart(const GqaDecodeArgs& a, const PoolMaps& maps, int begin, int end, unsigned parity, bool dead) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  using P = Shape<D, NT, TEAM>;
+  const int member = TEAM == 1 ? 0 : warp;
+  volatile int* far = reinterpret_cast<volatile int*>(smem + P::kFar);
+  float* wl = reinterpret_cast<float*>(smem + P::kLse);
+  const uint32_t base = dev::smem_u32(smem), ref = base + P::kRefs + warp * kH * 4 + 8 * (lane & 3);
+  const uint32_t ring = base + warp * P::kStages * kUnit, scale = base + P::kScale + warp * P::kStages * 8, bar = base + P::kBars + warp * P::kStages * 8;
+  Query<D, NT> Q;
+  Q.addr = base + P::kQ + (TEAM == 1 ? warp : 0) * P::kQBytes;
+#pragma unroll 1
+  for (int si = begin; si < end; ++si) {
+    const GqaSegment s = load_record(a.segs + si);
+    bool mine = was_left<D, TEAM>(a, s, member);
+    if constexpr (TEAM > 1) {
+      if (lane == 0) far[warp] = mine;
+      __syncthreads();
+      mine = (far[0] | far[1] | far[2] | far[3]) != 0;
+      __syncthreads();
+      if (lane == 0) far[warp] = 0;
+    }
+    if (!mine) continue;
+    RawQuery<D, NT, TEAM> raw;
+    raw.load(a, s, member, lane);
+    convert_query<D, NT, TEAM>(Q, raw, a.scale_log2, wl, member, lane);
+    State<D, NT> st;
+    st.clear();
+    int first = INT32_MIN;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) tc::sts_u32(ref + 32 * n + 4 * e, __float_as_uint(kNone));
+#pragma unroll 1
+    for (int u = member; u < s.num_pages * P::kUnits; u += TEAM) {
+      const int local = page_of(s, s.page_begin + u / P::kUnits), t0 = local * kPage + u % P::kUnits * P::kTokens;
+      const int32_t page = a.kv_indices[s.page0 + local];
+      if (dead || !seen<D>(a, s, page, t0)) continue;
+      if (lane == 0) load_unit<D>(a, maps, s, page, t0, u % P::kUnits, ring, scale, bar);
+      if (!tc::mbar_wait(bar, parity)) {
+        dead = true;
+        if (lane == 0) atomicOr(a.status, 1);
+      }
+      dead = __any_sync(kFull, dead);
+      parity ^= 1u;
+      take_unit<D, E4M3, NT, TEAM, true, true>(st, Q, ring, scale, Range(s, t0), first, ref, lane);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = st.l[n][e];
+        l += __shfl_xor_sync(kFull, l, 4);
+        l += __shfl_xor_sync(kFull, l, 8);
+        l += __shfl_xor_sync(kFull, l, 16);
+        // sum 2^z V = O^T 2^(first + m - kLift), of a whole of 2^lse: in two factors, neither of which is flushed
+        const float lse = lds_f1(ref + 32 * n + 4 * e) - kLift + lg2(l);
+        const float x = first == INT32_MIN || l == 0.0f ? -600.0f : static_cast<float>(first) + (st.m[n][e] - lse) - kLift;
+        const float half = floorf(0.5f * x), c0 = dev::fast_exp2(half), c1 = dev::fast_exp2(x - half);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          st.o[i][n][e] = st.o[i][n][e] * c0 * c1;
+          st.o[i][n][2 + e] = st.o[i][n][2 + e] * c0 * c1;
+        }
+        st.l[n][e] = l != 0.0f && lane < 4 ? 1.0f : 0.0f;          // one lane of the eight that share a column
+        st.m[n][e] = lse + kLift;
+      }
+    finish_segment<D, NT, TEAM>(a, s, st, 0, smem, warp, lane);
+  }
+  return dead;
+}
+
 // TEAM warps share a worker's segments: 4 (the CTA) or 1 (each warp a worker of its own, no barrier at all).
 template <int D, bool E4M3, int NT, int TEAM>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decode_kernel(const GqaDecodeArgs a, const __grid_constant__ PoolMaps maps) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decode_kernel(const __grid_constant__ GqaDecodeArgs a, const __grid_constant__ PoolMaps maps) {
   using P = Shape<D, NT, TEAM>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = dev::smem_u32(smem);
@@ -689,10 +990,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   const uint32_t ring = base + warp * P::kStages * kUnit;
   const uint32_t scales = base + P::kScale + warp * P::kStages * 8;
   const uint32_t bars = base + P::kBars + warp * P::kStages * 8;
-  float4* join = reinterpret_cast<float4*>(smem + P::kJoin);
-  float* wl = reinterpret_cast<float*>(smem + P::kLse);          // [kWarps][kH] lse of each warp
-  int* flag = reinterpret_cast<int*>(smem + P::kFlags);
+  const uint32_t far = base + P::kFar + warp * 4;
+  float* wl = reinterpret_cast<float*>(smem + P::kLse);
   if (lane < P::kStages) tc::mbar_init(bars + 8 * lane, 2);
+  if (lane == 0) tc::sts_u32(far, 0);
   tc::fence_mbar_init();
   __syncwarp();
 
@@ -709,36 +1010,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   Feed<P::kUnits, TEAM> feed(a, w, member);
   uint32_t loaded = 0, parity = 0;         // bit i: stage i holds a unit to take / parity of its barrier
   auto fill = [&](int stage) {
-    const bool ok = feed.si < feed.se && !dead && feed.page >= 0 && feed.page < a.num_pages && Range(feed.s, feed.t0).any(0, P::kTokens);
+    const bool ok = feed.si < feed.se && !dead && seen<D>(a, feed.s, feed.page, feed.t0);
     loaded = (loaded & ~(1u << stage)) | (ok ? 1u << stage : 0u);
-    if (ok && lane == 0) {
-      const int64_t kb = static_cast<int64_t>(feed.page) * 2 * a.kv_heads + feed.s.kv_head, vb = kb + a.kv_heads;
-      const uint32_t bar = bars + 8 * stage, dst = ring + stage * kUnit;
-      cp_async4(scales + 8 * stage, a.kv_scale + kb);
-      cp_async4(scales + 8 * stage + 4, a.kv_scale + vb);
-      cp_async_arrive(bar);
-      const int krow = static_cast<int>(kb * (kPage * D / 128)) + feed.sub * (kHalf / 128);
-      const int vrow = static_cast<int>(vb * (kPage * D / 128)) + feed.sub * (kHalf / 128);
-      const Range range(feed.s, feed.t0);
-      if (range.all(P::kTokens)) {
-        tc::mbar_arrive_expect_tx(bar, kUnit);
-        tma_load_2d(dst, &maps.unit, 0, krow, bar);
-        tma_load_2d(dst + kHalf, &maps.unit, 0, vrow, bar);
-      } else {
-        // of a unit at an edge only the quarters that hold a visible token; what is left in the others is masked
-        constexpr int kPiece = P::kTokens / 4;
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bytes += range.any(i * kPiece, kPiece) ? 2 * kHalf / 4 : 0;
-        tc::mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!range.any(i * kPiece, kPiece)) continue;
-          tma_load_2d(dst + i * (kHalf / 4), &maps.piece, 0, krow + i * (kHalf / 4 / 128), bar);
-          tma_load_2d(dst + kHalf + i * (kHalf / 4), &maps.piece, 0, vrow + i * (kHalf / 4 / 128), bar);
-        }
-      }
-    }
+    if (ok && lane == 0) load_unit<D>(a, maps, feed.s, feed.page, feed.t0, feed.sub, ring + stage * kUnit, scales + 8 * stage, bars + 8 * stage);
     feed.next(member);
   };
 #pragma unroll 1
@@ -748,13 +1022,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   Query<D, NT> Q;
   Q.addr = base + P::kQ + (TEAM == 1 ? warp : 0) * P::kQBytes;
   int stage = 0;
-  const int t = lane & 3, g = lane >> 2;
+  bool left = false;                       // segments whose V scales are far apart are left for later
 #pragma unroll 1
   for (int si = w.begin; si < w.end;) {
     // no warp still reads the last segment's Q^T in shared memory: that segment ended at a barrier
     convert_query<D, NT, TEAM>(Q, raw, a.scale_log2, wl, member, lane);
     st.clear();
-    Scales vs{INT32_MIN, false, base + P::kRefs + warp * kH * 4 + 8 * t};
+    int vfirst = INT32_MIN;
 #pragma unroll 1
     for (int u = member; u < s.num_pages * P::kUnits; u += TEAM) {
       if (loaded >> stage & 1) {
@@ -765,8 +1039,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         dead = __any_sync(kFull, dead);
         parity ^= 1u << stage;
         const Range range(s, page_of(s, s.page_begin + u / P::kUnits) * kPage + u % P::kUnits * P::kTokens);
-        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vs, lane);
-        else take_unit<D, E4M3, NT, TEAM, true>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vs, lane);
+        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, far, lane);
+        else take_unit<D, E4M3, NT, TEAM, true, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, far, lane);
         __syncwarp();
       }
       fill(stage);
@@ -777,179 +1051,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
       next = load_record(a.segs + si);
       raw.load(a, next, member, lane);
     }
-    // this warp's l over its lanes, and its lse
-    const float vref = __uint_as_float(static_cast<uint32_t>(127 + max(vs.first, -126)) << 23);
-    float L[NT][2], weight[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = st.l[n][e];
-        l += __shfl_xor_sync(kFull, l, 4);
-        l += __shfl_xor_sync(kFull, l, 8);
-        l += __shfl_xor_sync(kFull, l, 16);
-        st.l[n][e] = l;
-        L[n][e] = l == 0.0f ? -INFINITY : (__builtin_expect(vs.apart, 0) ? lds_f1(vs.ref + 32 * n + 4 * e) : st.m[n][e]) - kLift + lg2(l);
-        weight[n][e] = 1.0f;
-        if (TEAM > 1 && g == 0) wl[warp * kH + 8 * n + 2 * t + e] = L[n][e];
-      }
-    if constexpr (TEAM > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) weight[n][e] = weigh(wl + 8 * n + 2 * t + e, L[n][e], L[n][e]);
-    }
-    float c[NT][2];                        // what O^T is multiplied by; any number where it is 0
-    bool small = vs.apart;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        c[n][e] = st.l[n][e] == 0.0f ? 1.0f : __fdividef(weight[n][e], st.l[n][e]) * vref;
-        small |= c[n][e] < kSmall;
-      }
-    if (__builtin_expect(small, 0)) {
-      // sum 2^z V = O^T 2^(first + m - kLift), of a whole of 2^L: in two factors, neither of which is flushed
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool none = vs.first == INT32_MIN || L[n][e] == -INFINITY;
-          const float x = none ? -600.0f : static_cast<float>(vs.first) + (st.m[n][e] - L[n][e]) - kLift;
-          const float half = floorf(0.5f * x), by = dev::fast_exp2(half);
-          c[n][e] = dev::fast_exp2(x - half);
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            st.o[i][n][e] *= by;
-            st.o[i][n][2 + e] *= by;
-          }
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          st.o[i][n][e] *= c[n][e];
-          st.o[i][n][2 + e] *= c[n][e];
-        }
-    // from here on a warp of a team owns a quarter of the tiles, the first kOwn of st.o
-    constexpr int kOwn = D / 16 / TEAM;
-    const int tile0 = member * kOwn;
-    if constexpr (TEAM > 1) scatter_sum<D, NT>(st.o, join, warp, lane);
-    if (s.partial < 0) {
-      write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
-      s = next;
-      continue;
-    }
-    int slot = s.partial, first = s.group_first, count = s.group_count, counter = s.counter;
-    bool top = s.top_counter < 0;
-#pragma unroll 1
-    while (true) {
-      float4* po = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kH * D) + tile0 * NT * 32 + lane;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) __stcg(po + (i * NT + n) * 32, make_float4(st.o[i][n][0], st.o[i][n][1], st.o[i][n][2], st.o[i][n][3]));
-      if (member == 0 && g == 0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          __stcg(reinterpret_cast<float2*>(a.part_lse + static_cast<int64_t>(slot) * kH + 8 * n + 2 * t), make_float2(L[n][0], L[n][1]));
-      }
-      // arrive once all of the slot is written
-      __threadfence();
-      int last = 0;
-      if constexpr (TEAM > 1) {
-        __syncthreads();
-        if (threadIdx.x == 0) *flag = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
-        __syncthreads();
-        last = *flag;
-      } else {
-        __syncwarp();
-        if (lane == 0) last = atomicAdd(a.counters + counter, 1u) == static_cast<unsigned>(count - 1);
-        last = __shfl_sync(kFull, last, 0);
-      }
-      if (last == 0) break;
-      // The last arrival: every slot is written. Each warp joins its tiles of all slots, in their order, a few
-      // slots at a time with their lse, under a running maximum.
-      __threadfence();
-      if (member == 0 && lane == 0) a.counters[counter] = 0;        // ready for the next run
-      const float* gl = a.part_lse + static_cast<int64_t>(first) * kH + 2 * t;
-      const float4* go = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(first) * kH * D) + tile0 * NT * 32 + lane;
-      float M[NT][2], W[NT][2];
-      st.clear();
-#pragma unroll
-      for (int n = 0; n < NT; ++n) M[n][0] = M[n][1] = -INFINITY, W[n][0] = W[n][1] = 0.0f;
-      constexpr int kVecs = P::kCtas == 3 ? 16 : 32;                // 16-byte loads in flight of a lane
-      constexpr int kBatch = kOwn * NT >= kVecs ? 1 : kVecs / (kOwn * NT) > 8 ? 8 : kVecs / (kOwn * NT);
-#pragma unroll 1
-      for (int k0 = 0; k0 < count; k0 += kBatch) {
-        float4 v[kBatch][kOwn][NT];
-        float2 x[kBatch][NT];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int k = k0 + j;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            x[j][n] = k < count ? __ldcg(reinterpret_cast<const float2*>(gl + k * kH + 8 * n)) : make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i)
-              v[j][i][n] = k < count ? __ldcg(go + static_cast<int64_t>(k) * (kH * D / 4) + (i * NT + n) * 32) : make_float4(0, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float m = M[n][e];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) m = dev::max_nan(m, e ? x[j][n].y : x[j][n].x);
-            const float c = m == -INFINITY ? 1.0f : dev::fast_exp2(M[n][e] - m);
-            W[n][e] *= c;
-            M[n][e] = m;
-#pragma unroll
-            for (int i = 0; i < kOwn; ++i) {
-              st.o[i][n][e] *= c;
-              st.o[i][n][2 + e] *= c;
-            }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-              const float z = m == -INFINITY ? 0.0f : dev::fast_exp2((e ? x[j][n].y : x[j][n].x) - m);
-              W[n][e] += z;
-#pragma unroll
-              for (int i = 0; i < kOwn; ++i) {
-                st.o[i][n][e] += z * (e ? v[j][i][n].y : v[j][i][n].x);
-                st.o[i][n][2 + e] += z * (e ? v[j][i][n].w : v[j][i][n].z);
-              }
-            }
-          }
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float c = W[n][e] == 0.0f ? 0.0f : __fdividef(1.0f, W[n][e]);
-          L[n][e] = W[n][e] == 0.0f ? -INFINITY : M[n][e] + lg2(W[n][e]);
-#pragma unroll
-          for (int i = 0; i < kOwn; ++i) {
-            st.o[i][n][e] *= c;
-            st.o[i][n][2 + e] *= c;
-          }
-        }
-      if (top) {
-        write_out<D, NT, kOwn>(a, s, st.o, tile0, L, lane);
-        break;
-      }
-      slot = s.sub_slot;
-      first = s.top_first;
-      count = s.top_count;
-      counter = s.top_counter;
-      top = true;
-    }
+    if (!finish_segment<D, NT, TEAM>(a, s, st, vfirst, smem, warp, lane)) left = true;
     s = next;
   }
+  if (__builtin_expect(left, 0)) dead = take_apart<D, E4M3, NT, TEAM>(a, maps, w.begin, w.end, parity & 1u, dead);
   if (dead) {
     // copies may still be on their way into this CTA's shared memory: let them land before it is given up
     const long long c0 = clock64();

@@ -167,8 +167,8 @@ struct GqaAppendArgs {
   uint32_t kv_ctas;           // CTAs of the K and V blocks; the query's follow (set by the launcher)
 };
 
-// One piece of the visible pages of one (request, KV head, pass of 16 query heads), processed by one CTA
-// of the head-pool decode. Visible page v of a request is page v of its list below sink_pages, and page
+// One piece of the visible pages of one (request, KV head, pass of 16 query heads), processed by one worker
+// of the head-pool decode, a CTA or a warp. Visible page v of a request is page v of its list below sink_pages, and page
 // win_page + (v - sink_pages) from there on.
 struct GqaSegment {
   int32_t req, kv_head;
