@@ -393,19 +393,15 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t vbase = kbase + kHalf;
   const float2 sc = lds_f2(scale_addr);
-  // At D = 256 with one tile of tokens and one of heads all 16 products are one chain: two sums, of the even and of
-  // the odd 64-dim groups, halve it (4,096 rows of 128 tokens 51.6 us, 53.4 with one sum). With 16 heads of 256 one
-  // sum is faster (16 x 4,096 tokens 33.4 us, 34.0 with two); D 128 does not tell the two apart.
-  constexpr int kChains = D == 256 && NT == 1 ? 2 : 1;
-  float s[MT][NT][4], part[kChains][MT][NT][4];
+  // one sum of products: two, of the even and of the odd 64-dim groups, are as fast (9 shapes of D
+  // 256, where one is a chain of 16: within 1 %, 4,096 rows of 32 to 256 tokens 53.9 us, 54.5 with two)
+  float s[MT][NT][4];
 #pragma unroll
-  for (int c = 0; c < kChains; ++c)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) part[c][m][n][k] = 0.0f;
+      for (int k = 0; k < 4; ++k) s[m][n][k] = 0.0f;
   const int tg = tok8<D>(g);
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
@@ -437,21 +433,10 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
           }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dev::mma_f16(part[c % kChains][m][n], a0, a1, a2, a3, b[0][n], b[1][n]);
+        for (int n = 0; n < NT; ++n) dev::mma_f16(s[m][n], a0, a1, a2, a3, b[0][n], b[1][n]);
       }
     }
   }
-
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s[m][n][k] = part[0][m][n][k];
-#pragma unroll
-        for (int c = 1; c < kChains; ++c) s[m][n][k] += part[c][m][n][k];
-      }
 
   // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 4,096 rows of 512 tokens of
   // D 256 with 16 heads take 210 us, and 218 with the loads behind it. With fewer registers left, at D 128 with 16
