@@ -24,7 +24,7 @@
 // makes every 16-byte (D = 64: 8-byte) shared-memory read free of bank conflicts under the TMA's 128-byte
 // swizzle. P^T is S^T's accumulator layout transposed: one 8x8 transpose per 8 tokens. Computing S^T of the
 // next unit along with the softmax of this one (rings of three) was 1 to 5 % slower: two warps per scheduler are
-// short of issue slots, not of independent work (INT8, 16 heads: 874 instructions a unit, 350 of them conversions).
+// short of issue slots, not of independent work (INT8, 16 heads: some 860 instructions a unit, 350 of them conversions).
 //
 // Softmax. One running reference m per head. It moves only when a logit passes it by 2^8 (a vote instead
 // of a reduction per unit); P = 2^(z - m + 6) <= 2^14 is in FP16's normal range down to 2^-28 of the
@@ -33,12 +33,13 @@
 // back. That serves scales within 2^24 of the first. A segment with one further away is left for the worker's end, where
 // it is taken in a second form, in which l has exponentials of its own, relative to the largest logit, while m bounds
 // logit + k: what a page adds to l and what it adds to O^T may then be any powers of two apart, in any order. Every
-// finite scale is taken. (The second form in the usual loop took 47.7 us instead of 42.6 for 4,096 rows of 128 tokens of
-// D 128 with 16 heads; without it they take 42.0, and 4,096 rows of 512 tokens of D 256 201 instead of 210.)
+// finite scale is taken. (The second form in the usual loop took 47.7 us instead of 42.8 for 4,096 rows of 128 tokens of
+// D 128 with 16 heads. What is left of its cost, against a kernel without it: these 42.1, 16 x 4,096 tokens of D 256 with
+// 10 heads 33.9 instead of 34.4.)
 //
 // Measured on GB300, kernel time: 44 x 32,768 tokens (8 KV heads of 128, 64 query heads, E4M3) 429 us, 2.96 GB at
 // 6.9 TB/s, 103 % of the measured copy rate (DRAM busy 88 %, issue 33 %, tensor pipe 19 %); 1 x 1,048,576 (4
-// heads) 163 us; 64 ragged requests (4 KV heads, 16 query heads each, INT8) 79 us. What is short is bound by its
+// heads) 163 us; 64 ragged requests (4 KV heads, 16 query heads each, INT8) 80 us. What is short is bound by its
 // start and end: 2.5 to 3 us from the launch to the first unit (the worker's record, its page id and the page
 // are three reads in line, cold), 1 us a unit, 1 us for a partial to be written and counted, 1 to 3 us to join.
 #include <atomic>
@@ -60,7 +61,7 @@ constexpr int kH = kGqaPassHeads;
 constexpr int kHalf = 4096;              // bytes of K (and of V) in a unit
 constexpr int kUnit = 2 * kHalf;
 constexpr unsigned kFull = 0xffffffffu;
-// how far (log2) a logit may pass the reference; with 0 the 64 ragged INT8 requests take 83.2 us instead of 79.4
+// how far (log2) a logit may pass the reference; with 0 the 64 ragged INT8 requests take 83.1 us instead of 80.0
 constexpr float kSlack = 8.0f;
 constexpr float kLift = 6.0f;            // P is held as 2^(z - m + kLift)
 constexpr float kNone = -3e38f;          // reference before the first unit
@@ -69,6 +70,7 @@ constexpr float kNone = -3e38f;          // reference before the first unit
 // first: beside such a page weights down to 2^-80 of its own are normal numbers in FP16. And the least first scale: O^T's
 // last factor, weight / l 2^first, is not flushed for weights of a warp in its team of 2^-70 and more.
 constexpr int kReach = 24, kZeros = 60, kLowest = -30;
+constexpr int kFarApart = 1 << 20;       // in the place of the first scale's exponent
 
 // At D = 256 and 16 heads Q^T would take 64 of the 255 registers next to 128 of O^T: it is kept in shared memory (16 x
 // 4,096 tokens, 4 KV heads, 10 query heads each: 34 us, and 44 with it in registers, which spill).
@@ -383,12 +385,12 @@ __device__ __forceinline__ bool out_of_reach(float scale, int& first) {
 }
 
 // One unit: S^T, the running softmax, O^T. PARTIAL: some of its tokens may be not visible. first: the exponent of the
-// warp's first V scale of the segment that is not 0 (INT32_MIN: none yet). A unit whose scale is out of reach of it sets the
-// flag at `at` in shared memory; the state is worth nothing then. APART: no scale is; l is relative to the references at
-// `at` (for the lane's columns), and both references are renewed at every unit.
+// warp's first V scale of the segment that is not 0 (INT32_MIN: none yet). A unit whose scale is out of reach of it makes it
+// kFarApart; the state is worth nothing from there on. APART: no scale is; l is relative to the references at `ref` in
+// shared memory (for the lane's columns), and both references are renewed at every unit.
 template <int D, bool E4M3, int NT, int TEAM, bool PARTIAL, bool APART>
 __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& Q, uint32_t kbase, uint32_t scale_addr,
-                                          const Range& range, int& first, uint32_t at, int lane) {
+                                          const Range& range, int& first, uint32_t ref, int lane) {
   constexpr int MT = kHalf / D / 16;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t vbase = kbase + kHalf;
@@ -439,9 +441,9 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
   }
 
   // V's bytes are loaded ahead of the softmax, so that they wait for it and not it for them: 4,096 rows of 512 tokens of
-  // D 256 with 16 heads take 210 us, and 218 with the loads behind it. With fewer registers left, at D 128 with 16
-  // heads and at D 256 in a team, they come behind it: 4,096 rows of 512 tokens of D 128 99 us, 105 ahead of it;
-  // 16 x 4,096 tokens of D 256 34.0 us, 34.7. D 64 and up to 8 heads do not tell the two apart.
+  // D 256 with 16 heads take 195 us, and 204 with the loads behind it. With fewer registers left, at D 128 with 16
+  // heads and at D 256 in a team, they come behind it: 4,096 rows of 128 tokens of D 128 42.8 us, 46.8 ahead of it;
+  // 16 x 4,096 tokens of D 256 34.7 us, 34.9. D 64 and up to 8 heads do not tell the two apart.
   constexpr bool kEarlyV = NT == 1 || D == 64 || (D == 256 && TEAM == 1);
   const int ta = tok8<D>(2 * t), tb = tok8<D>(2 * t + 1);
   constexpr int kSides = (D + 127) / 128;              // 128-dim halves of a token
@@ -482,8 +484,8 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
 
   // V's scale f 2^vk, k relative to the first. A page of zeros adds to l alone.
   const bool out = out_of_reach(sc.y, first), zero = sc.y == 0.0f;
-  if (!APART && out) tc::sts_u32(at, 1);
   const int vk = exponent_of(sc.y), k = zero ? -kZeros : vk - first;
+  if (!APART && out) first = kFarApart;
   // (an f of 4 times a P of 2^14 would be past FP16's largest number)
   const float f = sc.y * __uint_as_float(static_cast<uint32_t>(127 - (APART ? min(vk, 126) : vk)) << 23) * (APART && vk == 127 ? 0.5f : 1.0f);
   const float kz = APART && zero ? -INFINITY : static_cast<float>(k);
@@ -524,10 +526,10 @@ __device__ __forceinline__ void take_unit(State<D, NT>& st, const Query<D, NT>& 
         x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
         if constexpr (APART) {
           // the lanes of a column write one value, once all have read the last
-          const uint32_t ref = at + 32 * n + 4 * e;
-          const float was = lds_f1(ref), y = fmaxf(fminf(x, 3e38f), was);
+          const uint32_t at = ref + 32 * n + 4 * e;
+          const float was = lds_f1(at), y = fmaxf(fminf(x, 3e38f), was);
           __syncwarp();
-          tc::sts_u32(ref, __float_as_uint(y));
+          tc::sts_u32(at, __float_as_uint(y));
           float l = st.l[n][e] * dev::fast_exp2(was - y);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
@@ -699,7 +701,7 @@ __device__ __forceinline__ void write_out(const GqaDecodeArgs& a, const GqaSegme
 }
 
 // The end of a segment: the warp's sums become outputs, or a partial that the last of its group joins. first: the exponent
-// that O^T is relative to. Where one of the warps met scales far apart its flag is cleared, nothing done, and false returned.
+// that O^T is relative to. Where one of the warps met scales far apart nothing is done, and false returned.
 template <int D, int NT, int TEAM>
 __device__ __forceinline__ bool finish_segment(const GqaDecodeArgs& a, const GqaSegment& s, State<D, NT>& st, int first, uint8_t* smem, int warp,
                                                int lane) {
@@ -708,13 +710,7 @@ __device__ __forceinline__ bool finish_segment(const GqaDecodeArgs& a, const Gqa
   float4* join = reinterpret_cast<float4*>(smem + P::kJoin);
   float* wl = reinterpret_cast<float*>(smem + P::kLse);          // [kWarps][kH] lse of each warp
   int* flag = reinterpret_cast<int*>(smem + P::kFlags);
-  volatile int* far = reinterpret_cast<volatile int*>(smem + P::kFar);
-  if (TEAM == 1 && __builtin_expect(far[warp] != 0, 0)) {
-    __syncwarp();
-    if (lane == 0) far[warp] = 0;
-    __syncwarp();
-    return false;
-  }
+  if (TEAM == 1 && __builtin_expect(first == kFarApart, 0)) return false;
   // this warp's l over its lanes, and its lse
   const float vref = first == INT32_MIN ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + first) << 23);
   float L[NT][2], weight[NT][2];
@@ -732,12 +728,12 @@ __device__ __forceinline__ bool finish_segment(const GqaDecodeArgs& a, const Gqa
       if (TEAM > 1 && g == 0) wl[warp * kH + 8 * n + 2 * t + e] = L[n][e];
     }
   if constexpr (TEAM > 1) {
+    int* far = reinterpret_cast<int*>(smem + P::kFar);
+    if (lane == 0) far[warp] = first == kFarApart;
     __syncthreads();
-    const int4 x = *reinterpret_cast<const int4*>(smem + P::kFar);
+    const int4 x = *reinterpret_cast<const int4*>(far);
     if (__builtin_expect((x.x | x.y | x.z | x.w) != 0, 0)) {
-      __syncthreads();                     // all have read the flags before they change
-      if (lane == 0) far[warp] = 0;
-      __syncwarp();
+      __syncthreads();                     // all have read it before the next segment writes it
       return false;
     }
 #pragma unroll
@@ -891,9 +887,11 @@ __device__ bool was_left(const GqaDecodeArgs& a, const GqaSegment& s, int member
 // whose barrier's parity is given. O^T is normalised here, so that the segment's end finds an l of 1 and values relative
 // to 2^0. Returns whether a wait ran out.
 template <int D, bool E4M3, int NT, int TEAM>
-__device__ __forceinline__ bool take_apart(const GqaDecodeArgs& a, const PoolMaps& maps, int begin, int end, unsigned parity, bool dead) {
+__device__ __forceinline__ bool take_apart(const GqaDecodeArgs& a, const PoolMaps& maps, unsigned parity, bool dead) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const GqaWorker* w = a.workers + (TEAM == 1 ? blockIdx.x * kWarps + warp : blockIdx.x);
+  const int begin = w->begin, end = w->end;          // read again, not kept
   using P = Shape<D, NT, TEAM>;
   const int member = TEAM == 1 ? 0 : warp;
   volatile int* far = reinterpret_cast<volatile int*>(smem + P::kFar);
@@ -910,8 +908,7 @@ __device__ __forceinline__ bool take_apart(const GqaDecodeArgs& a, const PoolMap
       if (lane == 0) far[warp] = mine;
       __syncthreads();
       mine = (far[0] | far[1] | far[2] | far[3]) != 0;
-      __syncthreads();
-      if (lane == 0) far[warp] = 0;
+      __syncthreads();                     // all have read it before it is written again
     }
     if (!mine) continue;
     RawQuery<D, NT, TEAM> raw;
@@ -975,10 +972,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
   const uint32_t ring = base + warp * P::kStages * kUnit;
   const uint32_t scales = base + P::kScale + warp * P::kStages * 8;
   const uint32_t bars = base + P::kBars + warp * P::kStages * 8;
-  const uint32_t far = base + P::kFar + warp * 4;
   float* wl = reinterpret_cast<float*>(smem + P::kLse);
   if (lane < P::kStages) tc::mbar_init(bars + 8 * lane, 2);
-  if (lane == 0) tc::sts_u32(far, 0);
   tc::fence_mbar_init();
   __syncwarp();
 
@@ -1024,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
         dead = __any_sync(kFull, dead);
         parity ^= 1u << stage;
         const Range range(s, page_of(s, s.page_begin + u / P::kUnits) * kPage + u % P::kUnits * P::kTokens);
-        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, far, lane);
-        else take_unit<D, E4M3, NT, TEAM, true, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, far, lane);
+        if (range.all(P::kTokens)) take_unit<D, E4M3, NT, TEAM, false, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, 0, lane);
+        else take_unit<D, E4M3, NT, TEAM, true, false>(st, Q, ring + stage * kUnit, scales + 8 * stage, range, vfirst, 0, lane);
         __syncwarp();
       }
       fill(stage);
@@ -1039,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, TEAM>::kCtas) gqa_decod
     if (!finish_segment<D, NT, TEAM>(a, s, st, vfirst, smem, warp, lane)) left = true;
     s = next;
   }
-  if (__builtin_expect(left, 0)) dead = take_apart<D, E4M3, NT, TEAM>(a, maps, w.begin, w.end, parity & 1u, dead);
+  if (__builtin_expect(left, 0)) dead = take_apart<D, E4M3, NT, TEAM>(a, maps, parity & 1u, dead);
   if (dead) {
     // copies may still be on their way into this CTA's shared memory: let them land before it is given up
     const long long c0 = clock64();
