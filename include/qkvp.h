@@ -485,7 +485,8 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
  * page id out of the pool) gives out 0 and lse -inf. One kernel launch: requests that are split are
  * joined by the last of their CTAs to finish, in a fixed order, so equal inputs give equal bits.
  * Codes of tokens that are not visible take no part, whatever they hold (NaN too).
- *  q            device bf16 [batch][num_heads][head_dim]. Held as FP16 times a power of two per head.
+ *  q            device bf16 [batch][num_heads][head_dim]. Held as FP16 times a power of two per head. The softmax's weights
+ *               enter the product with V as FP16 (off by up to 2^-11); its sum and lse are taken from FP32 weights.
  *  kv_data, kv_scale, num_pages: the head pool; kv_data 128-byte aligned (TMA reads it), scales finite
  *               and not negative. Page ids outside [0, num_pages) read as tokens that are not visible.
  *               V scales and logits may be any powers of two apart, in any order; a token's weight below 2^-70

@@ -21,15 +21,16 @@ constexpr int kMaxKvHeads = 256;
 constexpr int kMaxHeads = 4096;
 // The split, from decode times on one GB300 over 256 to 4,096 rows (a row: the visible pages of one request and
 // KV head, or of 16 of its query heads) of 128 to 2,048 tokens, D 64 to 256, 4 to 16 query heads per KV head:
-// - Rows per SM from which a worker is a warp: 512 rows of 512 tokens (D 64) 8.9 us against 11.4 with CTAs, 1,024 of
-//   2,048 (D 128) 81 against 87; below it CTAs: 352 of 32,768 428 against 436, 256 ragged ones (16 heads, INT8) 80
-//   against 88. From one row per SM already where a row has no more than 8 units: 256 of 128 tokens (D 256) 10.0 / 12.0.
-// - Pages below which a CTA is not worth its start: 8 rows of 4 pages 4.5 us whole, 6.4 as pairs of pages, 7.4 when
-//   workers span two rows.
+// - Rows per SM from which a worker is a warp: 512 rows of 512 tokens (D 64) 9.8 us against 11.4 with CTAs (ragged ones of 128
+//   to 1,024 tokens 9.0 against 8.8), 1,024 of 2,048 (D 128) 81 against 88; below it CTAs: 352 of 32,768 429 against 444, 256
+//   ragged ones (16 heads, INT8) 80 against 88. From one row per SM already where a row has no more than 8 units: 256
+//   ragged ones of 32 to 256 tokens 11.3 against 12.3 (D 256), 7.4 against 8.7 (D 128); equal ones of 128 (D 256) 11.2 / 10.1.
+// - Pages below which a CTA is not worth its start: 8 rows of 16 pages (D 128) 6.9 us with 1, 5.8 with 2, 6.4 with 4; a
+//   sweep of 15 other shapes does not tell 2 and 4 apart (8 rows of 4 pages stay whole, 4.3 us).
 // - Pages of work that starting a row counts as, some 128 KB for a CTA and 32 to 48 KB for a warp. Warps, 2 against 4
-//   against 8 pages: 24.7 / 23.0 / 22.3 us in the window case of D 64 (128 requests), 28.5 / 30.0 / 34.4 at 1,280 rows of
-//   512 tokens of D 128, 53.7 / 58.1 / 66.5 of D 256. CTAs, 4 against 8: 14.0 / 13.7 at 256 rows of 2,048 tokens of D 64,
-//   23.7 / 23.0 at 32 requests of 512 to 4,096 tokens of D 128, 24.6 / 27.7 at 40 of 100 to 1,000 of D 256.
+//   against 8 pages: 24.8 / 23.4 / 22.5 us in the window case of D 64 (128 requests), 28.9 / 30.5 / 35.1 at 1,280 rows of
+//   128 to 1,024 tokens of D 128, 55.2 / 59.7 / 69.6 of D 256 (52.6 with 1). CTAs, 4 against 8: 15.2 / 14.1 at 256 rows of 512
+//   to 4,096 tokens of D 64, 23.8 / 23.3 at 32 requests of 512 to 4,096 tokens of D 128, 24.8 / 27.7 at 40 of 100 to 1,000 of D 256.
 constexpr double kWarpRowsPerSm = 2.5;
 constexpr int kMinCtaPages = 4;
 int row_cost(int dim, int team) { return team > 1 ? 1024 / dim : dim == 64 ? 6 : 256 / dim; }
@@ -63,8 +64,8 @@ Visible visible_pages(int32_t len, int32_t window, int32_t sinks) {
 }
 
 // Subgroups that the join of m segments is cut into (1: none). A CTA joins a slot in about 0.1 us, a second level
-// costs about 2 us: one request of 65,536 tokens and one KV head (D 128, 256 segments) took 21.8 us with one
-// level and 11.8 with two; 8 x 8,192 tokens (32 segments each) 9.9 with one and 11.0 with two.
+// costs up to 2 us: one request of 65,536 tokens and one KV head (D 128, 256 segments) took 24.7 us with one
+// level and 11.0 with two; 8 x 8,192 tokens (32 segments each) 9.7 with one and 9.85 with two, of 4 KV heads 17.3 and 18.7.
 int join_subgroups(int m) {
   if (m <= kJoinFan) return 1;
   int size = 1;
@@ -291,7 +292,7 @@ int gqa_decode_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, i
     return QKVP_E_INVALID;
   // Whole rows instead, where that does not take longer: the bandwidth is shared, so a worker with less than the
   // others costs nothing while the others keep the memory busy, and partials do cost. (128 x 2,048 tokens of 8 KV
-  // heads, D 128: 81 us whole, 89 split evenly.)
+  // heads, D 128: 81 us whole, 88 split evenly.)
   if (min_splits == 0 && info.partials > 0) {
     const Times times = worker_times(head_dim, group, team);
     double split_us = 0.0;
