@@ -501,6 +501,77 @@ int gqa_decode_run(const gqa_plan* plan, const void* q, const void* kv_data, con
                    int64_t num_pages, const int32_t* kv_indices, float sm_scale, void* out, float* lse,
                    void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream);
 
+/* Host-side plan produced by gqa_tree_plan and consumed by gqa_tree_run; plain data, used as a qkvp_plan is. */
+typedef struct {
+  int32_t batch, num_heads, num_kv_heads, head_dim, page_size, cache_dtype;
+  int32_t window, sinks;       /* as given; window 0: every cached token is visible */
+  int32_t num_tokens;          /* drafted tokens of the batch */
+  int32_t max_drafted;         /* most drafted tokens of a request */
+  int32_t row_tiles;           /* tiles of 128 rows that share a pass over the pages: 1 or 2 */
+  int32_t num_workers;         /* CTAs of the attention kernel */
+  int32_t num_segments;        /* (request, KV head, row block, page range) pieces */
+  int32_t num_joins;           /* row blocks cut into more than one segment */
+  int32_t max_join_segments;   /* most segments of one row block */
+  int32_t num_partials;        /* FP32 split partials held in the workspace */
+  int32_t max_worker_pages, min_worker_pages;
+  int32_t table_entries;       /* entries of kv_indices that the plan may address: kv_indptr[batch] */
+  int32_t reserved;
+  int64_t total_pages;         /* pages read, summed over requests (of one KV head and row block) */
+  uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;
+  uint64_t status_offset;      /* int32 status word, as in qkvp_plan */
+  uint64_t magic;
+} qkvp_tree_plan;
+
+#define QKVP_TREE_MAX_DRAFTED 256
+
+/*
+ * gqa_tree_plan - split the work of gqa_tree_run: attention of a batch's drafted tokens over its head pool.
+ *  kv_indptr_host, kv_len_host, batch, page_size, num_sms, min_splits, workspace, workspace_bytes, stream:
+ *               as for mla_decode_plan (also its return values, the size query with workspace NULL, and the refusal
+ *               under stream capture). kv_len counts the drafted tokens: request r's last T_r tokens are drafted ones,
+ *               appended (by gqa_append_rope, say, with the positions of their depth) behind kv_len[r] - T_r cached ones.
+ *  tok_indptr_host  host int32 [batch + 1], from 0, non-decreasing: request r drafted the tokens tok_indptr[r] ..
+ *               tok_indptr[r+1] - 1 of the call, T_r of them: 0 to QKVP_TREE_MAX_DRAFTED and at most kv_len[r].
+ *  num_heads, num_kv_heads, head_dim, cache_dtype: as for gqa_decode_plan.
+ *  window       cached and drafted tokens that a drafted token sees back, itself included; 0: all of them. Not below
+ *               the most drafted tokens of a request.
+ *  sinks        with a window, the first cached tokens that stay visible as well; without one it must be 0.
+ * Host memory that runs out is reported as QKVP_E_WORKSPACE, too.
+ */
+int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, const int32_t* tok_indptr_host,
+                  int32_t batch, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                  int32_t page_size, int32_t cache_dtype, int32_t window, int32_t sinks, int32_t num_sms,
+                  int32_t min_splits, void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream,
+                  qkvp_tree_plan* plan);
+
+/*
+ * gqa_tree_run - attention of one layer's drafted tokens over a head pool. Per drafted token i of request r and
+ * query head a with KV head h = a / G (G = num_heads / num_kv_heads), over the tokens t that i sees,
+ *   z_t = sm_scale * sum_d q[i,a,d] * sk * kcode_t[d],  out[i,a,d] = sum_t softmax(z)_t * sv * vcode_t[d],
+ *   lse[i,a] = log sum_t exp z_t,
+ * sk, sv the scales of the token's K and V block. i, the j-th drafted token of r, sees
+ *   - the drafted tokens of r whose bit is set in its mask row (bit k % 32 of word k / 32 for the k-th; bits from T_r on
+ *     count as 0), or, where tree_mask is NULL, the first j + 1 (a chain);
+ *   - with n of these, the cached tokens t >= c + n - window (c of them are cached) or t < sinks; all where window is 0.
+ * The window so counts the tokens of i's own path. A token that sees nothing, or only tokens whose page id lies outside
+ * the pool, gives out 0 and lse -inf. Codes of tokens that i does not see take no part in its row, whatever they
+ * hold (NaN too). One or two kernel launches; equal inputs give equal bits.
+ *  q            device bf16 [num_tokens][num_heads][head_dim]. Held as FP16 times a power of two per head. The softmax's
+ *               weights enter the product with V as FP16 (off by up to 2^-11); its sum and lse are taken from FP32 weights.
+ *  kv_data, kv_scale, num_pages: the head pool; kv_data 16-byte aligned, scales finite and not negative. V scales may be
+ *               any powers of two apart; a token's weight below 2^-70 of its row's largest may count as zero.
+ *  kv_indices   device int32 page ids addressed by the plan's kv_indptr.
+ *  tree_mask    device uint32 [num_tokens][mask_words], mask_words at least (the most drafted tokens of a request + 31) / 32;
+ *               or NULL with mask_words 0.
+ *  out          device bf16 [num_tokens][num_heads][head_dim], 16-byte aligned; lse float [num_tokens][num_heads] or NULL.
+ *  workspace    the buffer given to gqa_tree_plan. It holds partials during the run: two runs that use one workspace must
+ *               not overlap (nor two graphs that captured them).
+ */
+int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data, const float* kv_scale,
+                 int64_t num_pages, const int32_t* kv_indices, const uint32_t* tree_mask, int32_t mask_words,
+                 float sm_scale, void* out, float* lse, void* workspace, uint64_t workspace_bytes,
+                 qkvp_stream_t stream);
+
 /*
  * qkvp_encode_f32 - the device rounding routines of kv_append_quant applied to raw FP32 values:
  * fmt 1 -> E4M3 (nearest even, saturating at +-448, NaN -> 0x7F); fmt 2 -> E2M1 (nearest even,

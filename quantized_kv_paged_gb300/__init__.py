@@ -28,7 +28,7 @@ LATENT_DIM, V_DIM, PAGE_SIZE = 576, 512, 64
 EXPORTS = ["kv_append_quant", "mla_decode_plan", "mla_decode_run", "mla_decode_attend",
            "mla_decode_combine", "mla_decode_noalloc", "kv_pool_cast_bf16", "kv_gather_fp8",
            "kv_gather_pages_bf16", "mla_append_rope", "gqa_append_rope", "gqa_decode_plan", "gqa_decode_run",
-           "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
+           "gqa_tree_plan", "gqa_tree_run", "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
 
 
 class qkvp_plan(ctypes.Structure):
@@ -55,6 +55,17 @@ class gqa_plan(ctypes.Structure):
         ("workspace_bytes", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64),
         ("partial_o_offset", ctypes.c_uint64), ("partial_lse_offset", ctypes.c_uint64),
         ("status_offset", ctypes.c_uint64), ("magic", ctypes.c_uint64)]
+
+    as_dict = qkvp_plan.as_dict
+
+
+class qkvp_tree_plan(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_heads", "num_kv_heads", "head_dim", "page_size", "cache_dtype", "window", "sinks", "num_tokens",
+        "max_drafted", "row_tiles", "num_workers", "num_segments", "num_joins", "max_join_segments", "num_partials",
+        "max_worker_pages", "min_worker_pages", "table_entries", "reserved")] + [
+        ("total_pages", ctypes.c_int64)] + [(n, ctypes.c_uint64) for n in (
+            "workspace_bytes", "table_bytes", "partial_o_offset", "partial_lse_offset", "status_offset", "magic")]
 
     as_dict = qkvp_plan.as_dict
 
@@ -100,13 +111,14 @@ def load(path: str | None = None):
         L.gqa_decode_plan.argtypes = [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, u64,
                                       vp, c.POINTER(gqa_plan)]
         L.gqa_decode_run.argtypes = [c.POINTER(gqa_plan), vp, vp, vp, i64, vp, f32, vp, vp, vp, u64, vp]
+        L.gqa_tree_plan.argtypes = [vp, vp, vp] + [i32] * 10 + [vp, u64, vp, c.POINTER(qkvp_tree_plan)]
+        L.gqa_tree_run.argtypes = [c.POINTER(qkvp_tree_plan), vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, u64, vp]
         L.qkvp_encode_f32.argtypes = [vp, i64, i32, vp, vp]
         L.qkvp_status_string.restype = c.c_char_p
         L.qkvp_status_string.argtypes = [c.c_int]
-        for fn in ("kv_append_quant", "mla_decode_plan", "mla_decode_run", "mla_decode_attend",
-                   "mla_decode_combine", "mla_decode_noalloc", "kv_pool_cast_bf16", "kv_gather_fp8",
-                   "kv_gather_pages_bf16", "mla_append_rope", "gqa_append_rope", "gqa_decode_plan",
-                   "gqa_decode_run", "qkvp_encode_f32", "qkvp_version"):
+        for fn in EXPORTS:
+            if fn == "qkvp_status_string":
+                continue
             getattr(L, fn).restype = c.c_int
         _lib = L
         return L
@@ -267,6 +279,7 @@ class _Torch:
             import torch
             cls.torch = torch
             cls.bf16, cls.f32, cls.i32, cls.i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+            cls.u32 = torch.uint32
             cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
             # the current stream's handle without a Stream object around it, where this torch has the call
             cls.handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -474,6 +487,67 @@ def gqa_decode_run(plan: gqa_plan, q, kv_data, kv_scale, kv_indices, sm_scale: f
                                          kv_indices.data_ptr(), sm_scale, out.data_ptr(), lse_at, workspace.data_ptr(),
                                          workspace.nbytes, on)
     return st if st == QKVP_OK else _check("gqa_decode_run", st, raise_on_error)
+
+
+def gqa_tree_plan(kv_indptr, kv_len, tok_indptr, num_heads: int, num_kv_heads: int, head_dim: int, cache_dtype: int,
+                  window: int = 0, sinks: int = 0, num_sms: int = 0, min_splits: int = 0, workspace=None,
+                  page_size: int = PAGE_SIZE, stream=None, raise_on_error: bool = True):
+    """Plan the attention of drafted tokens on the host: request r's last tok_indptr[r + 1] - tok_indptr[r] of kv_len[r]
+    tokens are drafted. With workspace=None only sizes are computed. Returns a qkvp_tree_plan."""
+    indptr, lens = _table(kv_indptr, kv_len)
+    tok, _ = _table(tok_indptr, lens)
+    plan = qkvp_tree_plan()
+    ws, nbytes, on = None, 0, None
+    if workspace is not None:
+        _Torch.get()
+        here = workspace.get_device()
+        _workspace(workspace, here)
+        on = _launch_on(stream, here)
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
+    st = load().gqa_tree_plan(indptr.ctypes.data, lens.ctypes.data, tok.ctypes.data, int(lens.shape[0]), num_heads,
+                              num_kv_heads, head_dim, page_size, cache_dtype, window, sinks, num_sms, min_splits, ws,
+                              nbytes, on, ctypes.byref(plan))
+    _check("gqa_tree_plan", st, raise_on_error)
+    plan.status = st
+    return plan
+
+
+def gqa_tree_run(plan: qkvp_tree_plan, q, kv_data, kv_scale, kv_indices, tree_mask, sm_scale: float, out, lse,
+                 workspace, stream=None, raise_on_error: bool = True) -> int:
+    """Attention of one layer's drafted tokens over a head pool: q, out bf16 [n, H, D], lse float32 [n, H] or None;
+    tree_mask int32 [n, words], bit k of a row set for the k-th drafted token that it sees, or None for chains."""
+    T = _Torch.get()
+    n, heads, dim = plan.num_tokens, plan.num_heads, plan.head_dim
+    here = q.get_device()
+    _dense("q", q, (n, heads, dim), T.bf16, here)
+    _dense("out", out, (n, heads, dim), T.bf16, here)
+    pages, heads_kv, kv_dim = _head_pool(kv_data, kv_scale, T, here)
+    if heads_kv != plan.num_kv_heads or kv_dim != dim:
+        raise ValueError(f"kv_data has {heads_kv} heads of {kv_dim}, the plan {plan.num_kv_heads} of {dim}")
+    entries = kv_indices.shape[0]
+    _dense("kv_indices", kv_indices, (entries,), T.i32, here)
+    if entries < plan.table_entries:
+        raise ValueError(f"kv_indices has {entries} entries, the plan's page table {plan.table_entries}")
+    mask_at, words = None, 0
+    if tree_mask is not None:
+        words = tree_mask.shape[-1]
+        if tree_mask.dtype is not T.i32 and tree_mask.dtype is not T.u32 or tree_mask.shape != (n, words) or not tree_mask.is_contiguous() or tree_mask.get_device() != here:
+            _refuse("tree_mask", tree_mask, (n, "words"), T.i32, "a contiguous layout", here)
+        mask_at = tree_mask.data_ptr()
+        if words * 32 < plan.max_drafted:
+            raise ValueError(f"tree_mask has {words} words a token, the plan's trees have up to {plan.max_drafted} tokens")
+        if n == 0:
+            mask_at, words = None, 0
+    lse_at = None
+    if lse is not None:
+        _dense("lse", lse, (n, heads), T.f32, here)
+        lse_at = lse.data_ptr()
+    _workspace(workspace, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).gqa_tree_run(ctypes.byref(plan), q.data_ptr(), kv_data.data_ptr(), kv_scale.data_ptr(), pages,
+                                       kv_indices.data_ptr(), mask_at, words, sm_scale, out.data_ptr(), lse_at,
+                                       workspace.data_ptr(), workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("gqa_tree_run", st, raise_on_error)
 
 
 def qkvp_encode_f32(x, fmt: int, codes, stream=None, raise_on_error: bool = True) -> int:

@@ -17,8 +17,6 @@ using namespace qkvp;
 
 namespace {
 
-constexpr int kMaxKvHeads = 256;
-constexpr int kMaxHeads = 4096;
 // The split, from decode times on one GB300 over 256 to 4,096 rows (a row: the visible pages of one request and
 // KV head, or of 16 of its query heads) of 128 to 2,048 tokens, D 64 to 256, 4 to 16 query heads per KV head:
 // - Rows per SM from which a worker is a warp: 512 rows of 512 tokens (D 64) 9.8 us against 11.4 with CTAs (ragged ones of 128
@@ -38,30 +36,6 @@ constexpr int kJoinFan = 40;
 
 // Row strides in elements: multiples of 8 (16-byte vectors), at least one row wide.
 bool stride_ok(int64_t s, int64_t width) { return s >= width && s % 8 == 0; }
-
-// The visible pages of one request: its sink pages, then the pages of its window.
-struct Visible {
-  int32_t sink_pages = 0, win_page = 0, win_begin = 0, sink_end = 0;
-  int32_t pages = 0;
-  int64_t tokens = 0;
-};
-Visible visible_pages(int32_t len, int32_t window, int32_t sinks) {
-  Visible v;
-  const int32_t pages = static_cast<int32_t>((static_cast<int64_t>(len) + kPage - 1) / kPage);
-  if (window == 0 || len <= window) {
-    v.pages = pages;
-    v.tokens = len;
-    return v;
-  }
-  v.win_begin = len - window;
-  v.sink_end = std::min(sinks, v.win_begin);
-  v.win_page = v.win_begin / kPage;
-  // a page that holds both sinks and window is counted once
-  v.sink_pages = std::min(static_cast<int32_t>((static_cast<int64_t>(v.sink_end) + kPage - 1) / kPage), v.win_page);
-  v.pages = v.sink_pages + pages - v.win_page;
-  v.tokens = static_cast<int64_t>(window) + v.sink_end;
-  return v;
-}
 
 // Subgroups that the join of m segments is cut into (1: none). A CTA joins a slot in about 0.1 us, a second level
 // costs up to 2 us: one request of 65,536 tokens and one KV head (D 128, 256 segments) took 24.7 us with one
@@ -111,9 +85,6 @@ double whole_rows(const std::vector<int32_t>& pages, int workers, const Times& t
   fill(hi, wptr.data());
   return hi;
 }
-
-bool dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
-bool cache_ok(int32_t c) { return c == QKVP_CACHE_E4M3 || c == QKVP_CACHE_INT8; }
 
 }  // namespace
 

@@ -1,0 +1,230 @@
+// C entry points of speculative decoding over a head pool: attention of drafted tokens (plan and run).
+//
+// The plan reuses the split-KV planner: each (request, KV head, block of 128 or 256 query rows) is a row of pages to it,
+// the visible ones only.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "../../include/qkvp.h"
+#include "qkvp_internal.h"
+
+using namespace qkvp;
+
+namespace {
+
+// Pages of work that starting a segment counts as, and pages below which a worker is not worth its start.
+constexpr int kStartPages = 4;
+constexpr int kMinPages = 2;
+
+}  // namespace
+
+extern "C" {
+
+int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, const int32_t* tok_indptr_host, int32_t batch,
+                  int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int32_t cache_dtype, int32_t window,
+                  int32_t sinks, int32_t num_sms, int32_t min_splits, void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream,
+                  qkvp_tree_plan* plan) try {
+  if (!plan) return QKVP_E_INVALID;
+  std::memset(plan, 0, sizeof(*plan));
+  if (page_size != QKVP_PAGE_SIZE || !dim_ok(head_dim) || !cache_ok(cache_dtype)) return QKVP_E_UNSUPPORTED;
+  if (num_kv_heads < 1 || num_kv_heads > kMaxKvHeads) return QKVP_E_UNSUPPORTED;
+  if (num_heads < 1 || num_heads > kMaxHeads || num_heads % num_kv_heads) return QKVP_E_UNSUPPORTED;
+  if (window < 0 || sinks < 0 || (window == 0 && sinks != 0)) return QKVP_E_INVALID;
+  // the page table's checks, with a head count that they accept
+  const int st = check_plan_args(kv_indptr_host, kv_len_host, batch, 16, page_size, QKVP_KV_FP8_E4M3, min_splits);
+  if (st != QKVP_OK) return st;
+  if (batch > 0 && (!tok_indptr_host || tok_indptr_host[0] != 0)) return QKVP_E_INVALID;
+  int max_drafted = 0;
+  for (int r = 0; r < batch; ++r) {
+    const int64_t t = static_cast<int64_t>(tok_indptr_host[r + 1]) - tok_indptr_host[r];
+    if (t < 0 || t > kv_len_host[r]) return QKVP_E_INVALID;
+    if (t > kTreeMaxDrafted) return QKVP_E_UNSUPPORTED;
+    max_drafted = std::max(max_drafted, static_cast<int>(t));
+  }
+  if (window > 0 && window < max_drafted) return QKVP_E_UNSUPPORTED;
+  if (num_sms <= 0) {
+    num_sms = query_sms();
+    if (num_sms <= 0) return QKVP_E_CUDA;
+  }
+  if (num_sms > 65536) return QKVP_E_INVALID;
+  const int group = num_heads / num_kv_heads;
+  const int tiles = head_dim == 256 || max_drafted * group <= kTreeTile ? 1 : 2, block = tiles * kTreeTile;
+
+  // one row of visible pages per (request, KV head, block of query rows)
+  std::vector<Visible> vis(batch);
+  std::vector<int32_t> blocks(batch);
+  int64_t rows = 0, row_pages = 0, pages = 0;
+  for (int r = 0; r < batch; ++r) {
+    const int drafted = tok_indptr_host[r + 1] - tok_indptr_host[r];
+    // a drafted token's window begins at the earliest `window` before the drafted ones
+    const int64_t reach = static_cast<int64_t>(window) + drafted;
+    vis[r] = visible_pages(kv_len_host[r], window == 0 || reach > INT32_MAX ? 0 : static_cast<int32_t>(reach), sinks);
+    blocks[r] = (drafted * group + block - 1) / block;
+    if (blocks[r] == 0) continue;
+    rows += static_cast<int64_t>(num_kv_heads) * blocks[r];
+    row_pages += static_cast<int64_t>(num_kv_heads) * blocks[r] * vis[r].pages;
+    pages += vis[r].pages;
+    if (static_cast<int64_t>(vis[r].pages) * kPage > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  }
+  if (rows > (1 << 24) || row_pages > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  std::vector<int32_t> len(rows), indptr(rows + 1), req(rows);
+  int64_t i = 0;
+  int32_t at = 0;
+  for (int r = 0; r < batch; ++r)
+    for (int k = 0; k < num_kv_heads * blocks[r]; ++k, ++i) {
+      req[i] = r;
+      indptr[i] = at;
+      len[i] = vis[r].pages * kPage;
+      at += vis[r].pages;
+    }
+  indptr[rows] = at;
+
+  const int64_t useful = std::max<int64_t>(1, (row_pages + kMinPages - 1) / kMinPages);
+  const int workers = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms) * tree_ctas_per_sm(head_dim, tiles), useful));
+  SplitInfo info;
+  info.num_segments = rows + workers;      // each worker's end cuts one row at most; asked-for splits are counted first
+  if (min_splits > 0) split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, kStartPages);
+  std::vector<Segment> cut(static_cast<size_t>(std::max<int64_t>(1, info.num_segments)));
+  std::vector<int32_t> wptr(workers + 1), rptr(rows + 1), wide(std::max<int64_t>(1, rows));
+  SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
+  if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, kStartPages)) return QKVP_E_INVALID;
+  if (info.num_segments > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  const TreeTable t = tree_table(info.num_segments, workers, info.split_reqs);
+
+  plan->batch = batch;
+  plan->num_heads = num_heads;
+  plan->num_kv_heads = num_kv_heads;
+  plan->head_dim = head_dim;
+  plan->page_size = page_size;
+  plan->cache_dtype = cache_dtype;
+  plan->window = window;
+  plan->sinks = sinks;
+  plan->num_tokens = batch > 0 ? tok_indptr_host[batch] : 0;
+  plan->max_drafted = max_drafted;
+  plan->row_tiles = tiles;
+  plan->num_workers = workers;
+  plan->num_segments = static_cast<int32_t>(info.num_segments);
+  plan->num_joins = info.split_reqs;
+  plan->max_join_segments = info.max_req_segs;
+  plan->num_partials = info.partials;
+  plan->max_worker_pages = info.max_pages;
+  plan->min_worker_pages = info.min_pages;
+  plan->table_entries = batch > 0 ? kv_indptr_host[batch] : 0;
+  plan->total_pages = pages;
+  plan->table_bytes = t.bytes;
+  plan->status_offset = t.status;
+  plan->partial_o_offset = t.bytes;
+  plan->partial_lse_offset = t.bytes + align_up(static_cast<uint64_t>(info.partials) * block * head_dim * 4);
+  plan->workspace_bytes = plan->partial_lse_offset + align_up(static_cast<uint64_t>(info.partials) * block * 4);
+  if (workspace == nullptr) return QKVP_OK;
+  if (workspace_bytes < plan->workspace_bytes || !aligned(workspace, kTableAlign)) {
+    const uint64_t need = plan->workspace_bytes;
+    std::memset(plan, 0, sizeof(*plan));
+    plan->workspace_bytes = need;
+    return QKVP_E_WORKSPACE;
+  }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(stream), &cap) != cudaSuccess) return QKVP_E_CUDA;
+  if (cap != cudaStreamCaptureStatusNone) {
+    std::memset(plan, 0, sizeof(*plan));
+    return QKVP_E_UNSUPPORTED;
+  }
+
+  std::vector<uint8_t> blob(t.bytes);
+  TreeSegment* segs = reinterpret_cast<TreeSegment*>(blob.data() + t.segs);
+  TreeJoin* joins = reinterpret_cast<TreeJoin*>(blob.data() + t.joins);
+  std::memcpy(blob.data() + t.wptr, wptr.data(), (workers + 1) * sizeof(int32_t));
+  int64_t first = 0;      // the request's first row
+  int num_joins = 0;
+  for (int64_t row = 0; row < rows; ++row) {
+    const int r = req[row];
+    if (row > 0 && req[row - 1] != r) first = row;
+    const int64_t k = row - first;
+    const int drafted = tok_indptr_host[r + 1] - tok_indptr_host[r], head = static_cast<int>(k / blocks[r]);
+    const int row0 = static_cast<int>(k % blocks[r]) * block, n = std::min(block, drafted * group - row0);
+    const int m = rptr[row + 1] - rptr[row];
+    for (int x = rptr[row]; x < rptr[row + 1]; ++x) {
+      TreeSegment& g = segs[x];
+      g.kv_head = head;
+      g.row0 = row0;
+      g.rows = n;
+      g.tok0 = tok_indptr_host[r];
+      g.page0 = kv_indptr_host[r];
+      g.len = kv_len_host[r];
+      g.cached = g.len - drafted;
+      g.sink_pages = vis[r].sink_pages;
+      g.win_page = vis[r].win_page;
+      g.page_begin = cut[x].page_begin - indptr[row];
+      g.num_pages = cut[x].num_pages;
+      g.partial = cut[x].partial;
+    }
+    if (m > 1) {
+      TreeJoin& j = joins[num_joins++];
+      j.first = cut[rptr[row]].partial;
+      j.count = m;
+      j.kv_head = head;
+      j.row0 = row0;
+      j.rows = n;
+      j.tok0 = tok_indptr_host[r];
+    }
+  }
+  if (upload_table(workspace, blob.data(), blob.size(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QKVP_E_CUDA;
+  plan->magic = kTreeMagic;
+  return QKVP_OK;
+} catch (const std::bad_alloc&) {
+  return QKVP_E_WORKSPACE;
+} catch (...) {
+  return QKVP_E_INVALID;
+}
+
+int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data, const float* kv_scale, int64_t num_pages,
+                 const int32_t* kv_indices, const uint32_t* tree_mask, int32_t mask_words, float sm_scale, void* out, float* lse,
+                 void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream) {
+  if (!plan || plan->magic != kTreeMagic) return QKVP_E_INVALID;
+  if (!workspace || workspace_bytes < plan->workspace_bytes || !aligned(workspace, kTableAlign)) return QKVP_E_WORKSPACE;
+  if (num_pages < 0 || !std::isfinite(sm_scale)) return QKVP_E_INVALID;
+  if (tree_mask ? mask_words < (plan->max_drafted + 31) / 32 : mask_words != 0) return QKVP_E_INVALID;
+  if (plan->num_tokens == 0) return QKVP_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || !aligned(tree_mask, 4)) return QKVP_E_INVALID;
+  if (!kv_data || !kv_scale || !kv_indices) return QKVP_E_INVALID;
+  if (!aligned(kv_data, 16) || !aligned(kv_scale, 4) || !aligned(kv_indices, 4)) return QKVP_E_INVALID;
+  if (num_pages > INT64_MAX / (2ll * plan->num_kv_heads * kPage * plan->head_dim)) return QKVP_E_INVALID;
+  const TreeTable t = tree_table(plan->num_segments, plan->num_workers, plan->num_joins);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  TreeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.kv = static_cast<const uint8_t*>(kv_data);
+  a.kv_scale = kv_scale;
+  a.num_pages = num_pages;
+  a.kv_indices = kv_indices;
+  a.mask = tree_mask;
+  a.segs = reinterpret_cast<const TreeSegment*>(ws + t.segs);
+  a.worker_ptr = reinterpret_cast<const int32_t*>(ws + t.wptr);
+  a.joins = reinterpret_cast<const TreeJoin*>(ws + t.joins);
+  a.status = reinterpret_cast<int*>(ws + t.status);
+  a.part_o = reinterpret_cast<float*>(ws + plan->partial_o_offset);
+  a.part_lse = reinterpret_cast<float*>(ws + plan->partial_lse_offset);
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.heads = plan->num_heads;
+  a.kv_heads = plan->num_kv_heads;
+  a.dim = plan->head_dim;
+  a.cache_dtype = plan->cache_dtype;
+  a.words = mask_words;
+  a.window = plan->window;
+  a.sinks = plan->sinks;
+  a.tiles = plan->row_tiles;
+  a.num_workers = plan->num_workers;
+  a.num_joins = plan->num_joins;
+  a.max_join = plan->max_join_segments;
+  a.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
+  a.flip = std::signbit(sm_scale) ? 0x80008000u : 0u;
+  return launch_tree(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QKVP_OK : QKVP_E_CUDA;
+}
+
+}  // extern "C"

@@ -1,6 +1,7 @@
 // Internal declarations shared by the translation units of libqkvp (not part of the ABI).
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
 
@@ -233,6 +234,99 @@ inline GqaTable gqa_table(int64_t segments, int64_t workers, int64_t counters) {
   return t;
 }
 
+// One piece of the pages that one block of query rows of a tree attention sees. Row i of a (request, KV head) is drafted
+// token i / G, query head kv_head * G + i % G; a block holds up to 128 or 256 consecutive rows. Page v of the request's
+// visible ones is page v of its list below sink_pages, and page win_page + (v - sink_pages) from there on.
+struct TreeSegment {
+  int32_t kv_head, row0, rows;    // rows [row0, row0 + rows) of the KV head
+  int32_t tok0;                   // the request's first drafted token among the call's
+  int32_t page0;                  // index into kv_indices of the request's first page
+  int32_t cached, len;            // tokens before the drafted ones, and with them
+  int32_t sink_pages, win_page;
+  int32_t page_begin, num_pages;  // visible pages [page_begin, page_begin + num_pages)
+  int32_t partial;                // partial slot, or -1 for a direct write
+};
+static_assert(sizeof(TreeSegment) == 48, "segment layout");
+
+// A block that was cut into segments: its partials are slots [first, first + count).
+struct TreeJoin {
+  int32_t first, count, kv_head, row0, rows, tok0;
+  int32_t pad[2];
+};
+static_assert(sizeof(TreeJoin) == 32, "join layout");
+
+constexpr uint64_t kTreeMagic = 0x716b76702d747265ull;
+constexpr int kTreeTile = 128;         // rows of a matrix product: the lanes of tensor memory
+constexpr int kTreeMaxDrafted = 256;   // drafted tokens of a request
+// CTAs of the tree attention that one SM holds: what tensor memory allows (512 columns).
+constexpr int tree_ctas_per_sm(int dim, int tiles) { return dim == 256 || tiles == 2 ? 1 : 2; }
+
+struct TreeArgs {
+  const uint16_t* q;          // bf16 [n][H][D]
+  const uint8_t* kv;
+  const float* kv_scale;
+  int64_t num_pages;
+  const int32_t* kv_indices;
+  const uint32_t* mask;       // [n][words], or null: a chain
+  const TreeSegment* segs;
+  const int32_t* worker_ptr;  // [num_workers + 1]
+  const TreeJoin* joins;
+  int* status;
+  float* part_o;              // [num_partials][128 tiles][D], normalised
+  float* part_lse;            // [num_partials][128 tiles], log2 domain
+  uint16_t* out;              // bf16 [n][H][D]
+  float* lse;                 // [n][H] or null
+  int heads, kv_heads, dim, cache_dtype, words, window, sinks;
+  int tiles;                  // row tiles of a block: 1 or 2
+  int num_workers, num_joins, max_join;
+  float scale_log2;           // |sm_scale| log2(e)
+  uint32_t flip;              // 0x80008000 where sm_scale is negative: turns Q's signs
+};
+
+// Work table of a tree plan.
+struct TreeTable {
+  uint64_t segs, wptr, joins, status, bytes;
+};
+inline TreeTable tree_table(int64_t segments, int64_t workers, int64_t joins) {
+  TreeTable t;
+  t.segs = 0;
+  t.wptr = align_up(static_cast<uint64_t>(segments) * sizeof(TreeSegment));
+  t.joins = t.wptr + align_up(static_cast<uint64_t>(workers + 1) * 4);
+  t.status = t.joins + align_up(static_cast<uint64_t>(joins) * sizeof(TreeJoin));
+  t.bytes = t.status + kTableAlign;
+  return t;
+}
+
+// Limits of the head pool's entry points.
+constexpr int kMaxKvHeads = 256;
+constexpr int kMaxHeads = 4096;
+inline bool dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
+inline bool cache_ok(int32_t c) { return c == QKVP_CACHE_E4M3 || c == QKVP_CACHE_INT8; }
+
+// The visible pages of one request: its sink pages, then the pages of its window.
+struct Visible {
+  int32_t sink_pages = 0, win_page = 0, win_begin = 0, sink_end = 0;
+  int32_t pages = 0;
+  int64_t tokens = 0;
+};
+inline Visible visible_pages(int32_t len, int32_t window, int32_t sinks) {
+  Visible v;
+  const int32_t pages = static_cast<int32_t>((static_cast<int64_t>(len) + kPage - 1) / kPage);
+  if (window == 0 || len <= window) {
+    v.pages = pages;
+    v.tokens = len;
+    return v;
+  }
+  v.win_begin = len - window;
+  v.sink_end = std::min(sinks, v.win_begin);
+  v.win_page = v.win_begin / kPage;
+  // a page that holds both sinks and window is counted once
+  v.sink_pages = std::min(static_cast<int32_t>((static_cast<int64_t>(v.sink_end) + kPage - 1) / kPage), v.win_page);
+  v.pages = v.sink_pages + pages - v.win_page;
+  v.tokens = static_cast<int64_t>(window) + v.sink_end;
+  return v;
+}
+
 // Copies a work table to the device in stream order, through pinned staging where it can (capi.cu).
 cudaError_t upload_table(void* dst, const void* src, size_t n, cudaStream_t st);
 int query_sms();
@@ -258,6 +352,7 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, unsigned
 cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t s);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 cudaError_t launch_gather_fp8(const GatherArgs& a, cudaStream_t s);
 cudaError_t launch_gather_pages_bf16(const uint8_t* pool, int64_t num_pages, const int32_t* ids, int64_t n,
                                      void* out, cudaStream_t s);
