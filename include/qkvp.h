@@ -573,6 +573,92 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
                  qkvp_stream_t stream);
 
 /*
+ * gqa_tree_commit - the end of a verified step: the accepted drafted tokens of each request become the tokens right behind
+ * its cached ones, in every layer of a head pool. Every array below is on the device but the two lists of layers, so a
+ * captured call replays with new paths. What follows (the next step's kv_len) is the caller's: kv_len[r] + path_len[r].
+ *   Token kv_len[r] + path[r][k] of request r moves to position kv_len[r] + k, k < path_len[r]; positions are looked up in the
+ *   page table as by gqa_append_rope. What other positions hold stays as it is.
+ *   Per block (page, K or V, head) that takes tokens: those that come from the block itself keep its scale. Of the
+ *   others, x = their block's scale * value(code) in FP32, need = amax / m over their finite |x|, m = 448 (E4M3) or 127
+ *   (INT8). The block's scale becomes need if it was 0, else scale * 2^j with the smallest j >= 0 for which that is at least
+ *   need; if j > 0, the codes of the block's tokens before the first one that the call puts there, and of the tokens
+ *   that move within the block, become round(code * 2^-j). Codes of the others are round(x / scale), or round(x) where scale
+ *   is 0; rounding as for gqa_append_rope. FP32 arithmetic with one rounding per operation.
+ *  kv_data, kv_scale  host arrays [num_layers] of the layers' device pools (kv_data 16-byte aligned); up to 128 layers of one
+ *               shape. Read before the call returns.
+ *  kv_len       device int32 [batch], the tokens before the drafted ones (gqa_append_rope's kv_len).
+ *  kv_indptr, kv_indices, nnz: page table on the device, as for gqa_append_rope.
+ *  path         device int32 [batch][max_path], strictly ascending from 0 on; path_len device int32 [batch], 0 to max_path.
+ *               max_path 0 to QKVP_TREE_MAX_DRAFTED.
+ * A request whose path does not ascend, whose path_len is out of range, or one of whose tokens lies outside its pages, the
+ * table or the pool, is left as it is. A page that one request's tokens move into must not be another's too.
+ */
+int gqa_tree_commit(void* const* kv_data, float* const* kv_scale, int32_t num_layers, const int32_t* kv_len,
+                    int32_t batch, const int32_t* kv_indptr, const int32_t* kv_indices, int64_t nnz,
+                    const int32_t* path, const int32_t* path_len, int32_t max_path, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t cache_dtype, int32_t page_size, int64_t num_pages,
+                    qkvp_stream_t stream);
+
+/* One buffer of a cache whose pages are copied: page p is the page_bytes (a multiple of 4) from data + p * page_bytes on. A
+ * cache is a list of them, up to 256: every layer's kv_data, and its kv_scale where the pool has one. */
+typedef struct {
+  void* data;          /* device, 4-byte aligned; 16-byte aligned with a multiple of 16 bytes a page is faster */
+  int64_t page_bytes;
+} qkvp_pool;
+
+/* Which request has which pages, on the device: a table row per request, reference counts and a free list. The table is the
+ * kv_indices of the other calls, with kv_indptr[r] = r * row_pages. */
+typedef struct {
+  int32_t* table;      /* [rows][row_pages] page ids; the first held[r] of row r count */
+  int32_t* held;       /* [rows] pages of the request, written or reserved */
+  int32_t* lens;       /* [rows] tokens of the request */
+  int32_t* refs;       /* [num_pages] table entries that hold the page; 0: free */
+  int32_t* free_list;  /* [num_pages]; the first *free_count entries are the free pages, taken from the end */
+  int32_t* free_count;
+  int32_t rows, row_pages;
+  int64_t num_pages;   /* up to 2^31 - 1 */
+} qkvp_page_state;
+
+/*
+ * kv_pages_* - the pages of a cache: copied, shared between requests, reserved, given back and moved together. All arrays are on
+ * the device and the calls only launch kernels, so they may be captured and replayed. Equal states give equal states:
+ * pages are taken in the order of the list and given back the highest first.
+ *  workspace    the *bytes of kv_pages_workspace for this num_pages and rows and lists of up to n, 256-byte aligned, zero before its first use; a call leaves
+ *               it ready for the next (with other lists and another n that it is large enough for). Calls that use one
+ *               workspace or one state must not overlap.
+ *  status       [n]: 1 for an entry that was carried out, 0 for one that was refused, which changes nothing.
+ * Ids outside the pool in a table or list are passed over; they never cause an out-of-bounds access. A state that does not
+ * add up (a page held more often than refs says, a free page in a table) stays so.
+ *
+ * kv_pages_copy     page src[i] to page dst[i] of every pool, i < n. Pairs with an id outside [0, num_pages) are passed over.
+ *                   A page that is written must not be read or written by another pair; otherwise it may hold a mix.
+ * kv_pages_fork     row children[i], which holds nothing, becomes a copy of row parents[i] with its tokens: full pages are shared
+ *                   (refs + 1), a started one is copied into a page from the free list. Reserved pages stay the parent's.
+ *                   Parents are taken as they are before the call. Refused: rows out of range, a child that is its parent, that
+ *                   holds pages or that an earlier entry names, a parent with fewer pages than its tokens need, and an entry
+ *                   that needs a page when the free list does not have one for it and all entries before it.
+ * kv_pages_grow     row list[i] gets the pages that tokens[i] tokens need (lens stays). Refused: rows out of range or named by an
+ *                   earlier entry, more tokens than row_pages hold, and an entry that needs pages when the free list does
+ *                   not have enough for it and all entries before it (those that were refused for that included).
+ * kv_pages_free     rows list[i] hold nothing any more (held and lens 0): refs - 1 for each page, and what nobody holds joins the free
+ *                   list. A row that is named twice is freed once; rows out of range are passed over.
+ * kv_pages_compact  the L pages with references move to the ids below L: the k-th lowest free id there takes the k-th
+ *                   lowest page from L on. Tables and counts follow, and the free list becomes num_pages - 1 down to L.
+ */
+int kv_pages_workspace(int64_t num_pages, int32_t rows, int32_t n, uint64_t* bytes);
+int kv_pages_copy(const qkvp_pool* pools, int32_t num_pools, const int32_t* src, const int32_t* dst, int64_t n,
+                  int64_t num_pages, qkvp_stream_t stream);
+int kv_pages_fork(const qkvp_pool* pools, int32_t num_pools, const qkvp_page_state* state,
+                  const int32_t* parents, const int32_t* children, int32_t n, int32_t* status, void* workspace,
+                  uint64_t workspace_bytes, qkvp_stream_t stream);
+int kv_pages_grow(const qkvp_page_state* state, const int32_t* list, const int32_t* tokens, int32_t n,
+                  int32_t* status, void* workspace, uint64_t workspace_bytes, qkvp_stream_t stream);
+int kv_pages_free(const qkvp_page_state* state, const int32_t* list, int32_t n, void* workspace,
+                  uint64_t workspace_bytes, qkvp_stream_t stream);
+int kv_pages_compact(const qkvp_pool* pools, int32_t num_pools, const qkvp_page_state* state, void* workspace,
+                     uint64_t workspace_bytes, qkvp_stream_t stream);
+
+/*
  * qkvp_encode_f32 - the device rounding routines of kv_append_quant applied to raw FP32 values:
  * fmt 1 -> E4M3 (nearest even, saturating at +-448, NaN -> 0x7F); fmt 2 -> E2M1 (nearest even,
  * saturating at +-6, NaN -> 0x0). One code byte per input. Exposed so the rounding can be checked

@@ -28,7 +28,8 @@ LATENT_DIM, V_DIM, PAGE_SIZE = 576, 512, 64
 EXPORTS = ["kv_append_quant", "mla_decode_plan", "mla_decode_run", "mla_decode_attend",
            "mla_decode_combine", "mla_decode_noalloc", "kv_pool_cast_bf16", "kv_gather_fp8",
            "kv_gather_pages_bf16", "mla_append_rope", "gqa_append_rope", "gqa_decode_plan", "gqa_decode_run",
-           "gqa_tree_plan", "gqa_tree_run", "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
+           "gqa_tree_plan", "gqa_tree_run", "gqa_tree_commit", "kv_pages_workspace", "kv_pages_copy", "kv_pages_fork",
+           "kv_pages_grow", "kv_pages_free", "kv_pages_compact", "qkvp_encode_f32", "qkvp_status_string", "qkvp_version"]
 
 
 class qkvp_plan(ctypes.Structure):
@@ -68,6 +69,15 @@ class qkvp_tree_plan(ctypes.Structure):
             "workspace_bytes", "table_bytes", "partial_o_offset", "partial_lse_offset", "status_offset", "magic")]
 
     as_dict = qkvp_plan.as_dict
+
+
+class qkvp_pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+class qkvp_page_state(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "held", "lens", "refs", "free_list", "free_count")] + [
+        ("rows", ctypes.c_int32), ("row_pages", ctypes.c_int32), ("num_pages", ctypes.c_int64)]
 
 
 class QkvpError(RuntimeError):
@@ -113,13 +123,20 @@ def load(path: str | None = None):
         L.gqa_decode_run.argtypes = [c.POINTER(gqa_plan), vp, vp, vp, i64, vp, f32, vp, vp, vp, u64, vp]
         L.gqa_tree_plan.argtypes = [vp, vp, vp] + [i32] * 10 + [vp, u64, vp, c.POINTER(qkvp_tree_plan)]
         L.gqa_tree_run.argtypes = [c.POINTER(qkvp_tree_plan), vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, u64, vp]
+        L.gqa_tree_commit.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i64, vp]
+        L.kv_pages_workspace.argtypes = [i64, i32, i32, c.POINTER(u64)]
+        pool, state = c.POINTER(qkvp_pool), c.POINTER(qkvp_page_state)
+        L.kv_pages_copy.argtypes = [pool, i32, vp, vp, i64, i64, vp]
+        L.kv_pages_fork.argtypes = [pool, i32, state, vp, vp, i32, vp, vp, u64, vp]
+        L.kv_pages_grow.argtypes = [state, vp, vp, i32, vp, vp, u64, vp]
+        L.kv_pages_free.argtypes = [state, vp, i32, vp, u64, vp]
+        L.kv_pages_compact.argtypes = [pool, i32, state, vp, u64, vp]
         L.qkvp_encode_f32.argtypes = [vp, i64, i32, vp, vp]
         L.qkvp_status_string.restype = c.c_char_p
         L.qkvp_status_string.argtypes = [c.c_int]
         for fn in EXPORTS:
-            if fn == "qkvp_status_string":
-                continue
-            getattr(L, fn).restype = c.c_int
+            if fn != "qkvp_status_string":
+                getattr(L, fn).restype = c.c_int
         _lib = L
         return L
 
@@ -548,6 +565,143 @@ def gqa_tree_run(plan: qkvp_tree_plan, q, kv_data, kv_scale, kv_indices, tree_ma
                                        kv_indices.data_ptr(), mask_at, words, sm_scale, out.data_ptr(), lse_at,
                                        workspace.data_ptr(), workspace.nbytes, on)
     return st if st == QKVP_OK else _check("gqa_tree_run", st, raise_on_error)
+
+
+def gqa_tree_commit(kv_data, kv_scale, cache_dtype: int, kv_len, kv_indptr, kv_indices, path, path_len, stream=None,
+                    raise_on_error: bool = True) -> int:
+    """Move the accepted drafted tokens right behind the cached ones in every layer: kv_data and kv_scale are lists of the
+    layers' head pools, path int32 [batch, max_path] ascending indices of drafted tokens, path_len int32 [batch],
+    kv_len int32 [batch] the tokens before the drafted ones (see qkvp.h)."""
+    T = _Torch.get()
+    layers = len(kv_data)
+    if layers != len(kv_scale):
+        raise ValueError(f"{layers} layers of kv_data and {len(kv_scale)} of kv_scale")
+    here = kv_len.get_device()
+    pages = heads = 0
+    dim = 64
+    for i, (data, scale) in enumerate(zip(kv_data, kv_scale)):
+        shape = _head_pool(data, scale, T, here)
+        if i and shape != (pages, heads, dim):
+            raise ValueError(f"layer {i} has (pages, KV heads, head dim) {shape}, the ones before it {(pages, heads, dim)}")
+        pages, heads, dim = shape
+    batch, nnz, i32 = kv_len.shape[0], kv_indices.shape[0], T.i32
+    max_path = path.shape[-1]
+    _dense("kv_len", kv_len, (batch,), i32, here)
+    _dense("kv_indptr", kv_indptr, (batch + 1,), i32, here)
+    _dense("kv_indices", kv_indices, (nnz,), i32, here)
+    _dense("path", path, (batch, max_path), i32, here)
+    _dense("path_len", path_len, (batch,), i32, here)
+    on = _launch_on(stream, here)
+    data = (ctypes.c_void_p * max(1, layers))(*[t.data_ptr() for t in kv_data])
+    scales = (ctypes.c_void_p * max(1, layers))(*[t.data_ptr() for t in kv_scale])
+    st = (_lib or load()).gqa_tree_commit(data, scales, layers, kv_len.data_ptr(), batch, kv_indptr.data_ptr(),
+                                          kv_indices.data_ptr(), nnz, path.data_ptr(), path_len.data_ptr(), max_path,
+                                          max(1, heads), dim, cache_dtype, PAGE_SIZE, pages, on)
+    return st if st == QKVP_OK else _check("gqa_tree_commit", st, raise_on_error)
+
+
+def kv_pages_workspace(num_pages: int, rows: int, n: int) -> int:
+    """Bytes of the workspace of the kv_pages_* calls, for lists of up to n entries. It has to be zero before its first use."""
+    size = ctypes.c_uint64()
+    _check("kv_pages_workspace", load().kv_pages_workspace(num_pages, rows, n, ctypes.byref(size)), True)
+    return size.value
+
+
+def _pools(pools, num_pages: int, here: int):
+    """The pools as the C array; every one a contiguous tensor with a page for each first index."""
+    arr = (qkvp_pool * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        if t.get_device() != here:
+            raise ValueError(f"tensors need to be on one device, the current CUDA device: pool {i} is on {t.device}")
+        if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
+            raise ValueError(f"pool {i} needs a contiguous layout and {num_pages} pages; got {tuple(t.shape)}, strides {t.stride()}")
+        arr[i].data = t.data_ptr()
+        arr[i].page_bytes = t.nbytes // num_pages if num_pages else 4
+    return arr
+
+
+def _page_state(table, held, lens, refs, free_list, free_count, T, here: int):
+    i32 = T.i32
+    if table.dim() != 2:
+        _refuse("table", table, ("rows", "pages"), i32, "a contiguous layout", here)
+    rows, row_pages = shape = table.shape
+    pages = refs.shape[0]
+    for name, t, want in (("table", table, shape), ("held", held, (rows,)), ("lens", lens, (rows,)), ("refs", refs, (pages,)),
+                          ("free_list", free_list, (pages,)), ("free_count", free_count, (1,))):
+        _dense(name, t, want, i32, here)
+    return qkvp_page_state(table.data_ptr(), held.data_ptr(), lens.data_ptr(), refs.data_ptr(), free_list.data_ptr(),
+                           free_count.data_ptr(), rows, row_pages, pages)
+
+
+def kv_pages_copy(pools, src, dst, stream=None, raise_on_error: bool = True) -> int:
+    """Copy page src[i] to page dst[i] (int32 device tensors) in every tensor of the list pools, each [num_pages, ...]."""
+    T = _Torch.get()
+    here, n = src.get_device(), src.shape[0]
+    _dense("src", src, (n,), T.i32, here)
+    _dense("dst", dst, (n,), T.i32, here)
+    pages = pools[0].shape[0] if len(pools) else 0
+    arr = _pools(pools, pages, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).kv_pages_copy(arr, len(pools), src.data_ptr(), dst.data_ptr(), n, pages, on)
+    return st if st == QKVP_OK else _check("kv_pages_copy", st, raise_on_error)
+
+
+def kv_pages_fork(pools, table, held, lens, refs, free_list, free_count, parents, children, status, workspace, stream=None,
+                  raise_on_error: bool = True) -> int:
+    """Rows children[i] become copies of rows parents[i]: full pages are shared, a started one is copied in every tensor of
+    pools. status[i] is 1 where that was done (see qkvp.h)."""
+    T = _Torch.get()
+    here, n = table.get_device(), parents.shape[0]
+    state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
+    for name, t in (("parents", parents), ("children", children), ("status", status)):
+        _dense(name, t, (n,), T.i32, here)
+    arr = _pools(pools, refs.shape[0], here)
+    _workspace(workspace, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).kv_pages_fork(arr, len(pools), ctypes.byref(state), parents.data_ptr(), children.data_ptr(), n,
+                                        status.data_ptr(), workspace.data_ptr(), workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("kv_pages_fork", st, raise_on_error)
+
+
+def kv_pages_grow(table, held, lens, refs, free_list, free_count, rows, tokens, status, workspace, stream=None,
+                  raise_on_error: bool = True) -> int:
+    """Rows rows[i] get the pages that tokens[i] tokens need. status[i] is 1 where that was done (see qkvp.h)."""
+    T = _Torch.get()
+    here, n = table.get_device(), rows.shape[0]
+    state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
+    for name, t in (("rows", rows), ("tokens", tokens), ("status", status)):
+        _dense(name, t, (n,), T.i32, here)
+    _workspace(workspace, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).kv_pages_grow(ctypes.byref(state), rows.data_ptr(), tokens.data_ptr(), n, status.data_ptr(),
+                                        workspace.data_ptr(), workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("kv_pages_grow", st, raise_on_error)
+
+
+def kv_pages_free(table, held, lens, refs, free_list, free_count, rows, workspace, stream=None,
+                  raise_on_error: bool = True) -> int:
+    """Rows rows[i] give their pages back; what nobody holds any more joins the free list (see qkvp.h)."""
+    T = _Torch.get()
+    here, n = table.get_device(), rows.shape[0]
+    state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
+    _dense("rows", rows, (n,), T.i32, here)
+    _workspace(workspace, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).kv_pages_free(ctypes.byref(state), rows.data_ptr(), n, workspace.data_ptr(), workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("kv_pages_free", st, raise_on_error)
+
+
+def kv_pages_compact(pools, table, held, lens, refs, free_list, free_count, workspace, stream=None,
+                     raise_on_error: bool = True) -> int:
+    """Move the pages with references to the lowest ids, in every tensor of pools, tables and counts with them (see qkvp.h)."""
+    T = _Torch.get()
+    here = table.get_device()
+    state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
+    arr = _pools(pools, refs.shape[0], here)
+    _workspace(workspace, here)
+    on = _launch_on(stream, here)
+    st = (_lib or load()).kv_pages_compact(arr, len(pools), ctypes.byref(state), workspace.data_ptr(), workspace.nbytes, on)
+    return st if st == QKVP_OK else _check("kv_pages_compact", st, raise_on_error)
 
 
 def qkvp_encode_f32(x, fmt: int, codes, stream=None, raise_on_error: bool = True) -> int:

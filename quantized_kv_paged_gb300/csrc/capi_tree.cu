@@ -1,4 +1,5 @@
-// C entry points of speculative decoding over a head pool: attention of drafted tokens (plan and run).
+// C entry points of speculative decoding over a head pool: attention of drafted tokens (plan and run), and the commit of the
+// accepted ones.
 //
 // The plan reuses the split-KV planner: each (request, KV head, block of 128 or 256 query rows) is a row of pages to it,
 // the visible ones only.
@@ -225,6 +226,40 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
   a.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
   a.flip = std::signbit(sm_scale) ? 0x80008000u : 0u;
   return launch_tree(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QKVP_OK : QKVP_E_CUDA;
+}
+
+int gqa_tree_commit(void* const* kv_data, float* const* kv_scale, int32_t num_layers, const int32_t* kv_len, int32_t batch,
+                    const int32_t* kv_indptr, const int32_t* kv_indices, int64_t nnz, const int32_t* path, const int32_t* path_len,
+                    int32_t max_path, int32_t num_kv_heads, int32_t head_dim, int32_t cache_dtype, int32_t page_size, int64_t num_pages,
+                    qkvp_stream_t stream) {
+  if (num_layers < 0 || batch < 0 || nnz < 0 || max_path < 0 || num_pages < 0) return QKVP_E_INVALID;
+  if (page_size != QKVP_PAGE_SIZE || !dim_ok(head_dim) || !cache_ok(cache_dtype)) return QKVP_E_UNSUPPORTED;
+  if (num_kv_heads < 1 || num_kv_heads > kMaxKvHeads || num_layers > kMaxLayers || max_path > kTreeMaxDrafted) return QKVP_E_UNSUPPORTED;
+  if (num_layers == 0 || batch == 0 || max_path == 0) return QKVP_OK;
+  if (!kv_data || !kv_scale || !kv_len || !kv_indptr || (!kv_indices && nnz > 0) || !path || !path_len) return QKVP_E_INVALID;
+  if (!aligned(kv_len, 4) || !aligned(kv_indptr, 4) || !aligned(kv_indices, 4) || !aligned(path, 4) || !aligned(path_len, 4)) return QKVP_E_INVALID;
+  if (num_pages > INT64_MAX / (2ll * num_kv_heads * kPage * head_dim)) return QKVP_E_INVALID;
+  TreeCommitArgs a{};
+  for (int i = 0; i < num_layers; ++i) {
+    if (!kv_data[i] || !kv_scale[i] || !aligned(kv_data[i], 16) || !aligned(kv_scale[i], 4)) return QKVP_E_INVALID;
+    a.kv[i] = static_cast<uint8_t*>(kv_data[i]);
+    a.scale[i] = kv_scale[i];
+  }
+  a.kv_len = kv_len;
+  a.kv_indptr = kv_indptr;
+  a.kv_indices = kv_indices;
+  a.path = path;
+  a.path_len = path_len;
+  a.nnz = nnz;
+  a.num_pages = num_pages;
+  a.layers = num_layers;
+  a.batch = batch;
+  a.max_path = max_path;
+  a.kv_heads = num_kv_heads;
+  a.dim = head_dim;
+  a.cache_dtype = cache_dtype;
+  const cudaError_t e = launch_tree_commit(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QKVP_OK : e == cudaErrorInvalidValue ? QKVP_E_UNSUPPORTED : QKVP_E_CUDA;
 }
 
 }  // extern "C"

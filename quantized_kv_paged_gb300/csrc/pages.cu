@@ -1,0 +1,403 @@
+// Pages of a cache: copies, and the bookkeeping of page tables, reference counts and a free list that live on the device.
+//
+// Copies. A page of every pool (all layers, codes and scales) is cut into units of 4 KB; a warp takes a unit with eight 16-byte
+// loads a lane in flight. Reading and writing each byte once is the floor.
+//
+// Bookkeeping. What depends on the order of a list (who gets which page) is a prefix sum in one CTA; what does not (table rows,
+// counts, copies) is shared out over the card. Every result is a function of the arguments alone: counts are
+// integers, pages are taken from the free list in the order of the list of requests and given back in descending order.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "qkvp_device.cuh"
+#include "qkvp_internal.h"
+
+namespace qkvp {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBook = 1024;             // threads of a bookkeeping CTA
+constexpr int kCopyThreads = 256;
+constexpr int kCopyWarps = kCopyThreads / 32;
+
+__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage ? 1 : 0); }
+__device__ __forceinline__ int free_pages(const PageState& t) {
+  return static_cast<int>(min(static_cast<int64_t>(max(*t.free_count, 0)), t.num_pages));
+}
+__device__ __forceinline__ bool in_pool(const PageState& t, int32_t page) { return page >= 0 && page < t.num_pages; }
+
+// Exclusive prefix sum over the CTA's threads; `total` the sum of all.
+__device__ __forceinline__ int64_t exclusive_sum(int64_t x, int64_t* total, int64_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int64_t sum = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) warp_sums[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = lane < warps ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  const int64_t before = warp > 0 ? warp_sums[warp - 1] : 0;
+  *total = warp_sums[warps - 1];
+  __syncthreads();
+  return before + sum - x;
+}
+
+// One unit of a page's copy by a warp.
+__device__ __forceinline__ void copy_unit(const PagePools& p, int64_t src, int64_t dst, uint32_t unit, int lane) {
+  int lo = 0, hi = p.count;               // the last pool whose first unit is not behind `unit`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.first_unit[mid] <= unit) lo = mid; else hi = mid;
+  }
+  const uint32_t bytes = p.bytes[lo], at = (unit - p.first_unit[lo]) * kCopyUnit, n = min(bytes - at, static_cast<uint32_t>(kCopyUnit));
+  const uint8_t* from = p.base[lo] + src * bytes + at;
+  uint8_t* to = p.base[lo] + dst * bytes + at;
+  if ((reinterpret_cast<uintptr_t>(p.base[lo]) | bytes) % 16 == 0) {
+    uint4 v[kCopyUnit / 512];
+#pragma unroll
+    for (int i = 0; i < kCopyUnit / 512; ++i) {
+      const uint32_t o = 512 * i + 16 * lane;
+      if (o < n) v[i] = *reinterpret_cast<const uint4*>(from + o);
+    }
+#pragma unroll
+    for (int i = 0; i < kCopyUnit / 512; ++i) {
+      const uint32_t o = 512 * i + 16 * lane;
+      if (o < n) *reinterpret_cast<uint4*>(to + o) = v[i];
+    }
+  } else {
+    for (uint32_t o = 4 * lane; o < n; o += 128) *reinterpret_cast<uint32_t*>(to + o) = *reinterpret_cast<const uint32_t*>(from + o);
+  }
+}
+
+// All units of n pairs, shared out over the warps of the grid. Pairs with a page outside the pool are passed over.
+__device__ __forceinline__ void copy_pairs(const PagePools& p, const int32_t* src, const int32_t* dst, int64_t n, int64_t num_pages) {
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps, units = n * p.units;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const int64_t pair = u / p.units;
+    const int64_t s = src[pair], d = dst[pair];
+    if (s < 0 || d < 0 || s >= num_pages || d >= num_pages || s == d) continue;
+    copy_unit(p, s, d, static_cast<uint32_t>(u - pair * p.units), lane);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PagePools p, const int32_t* src, const int32_t* dst,
+                                                                  int64_t n, int64_t num_pages) {
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  copy_pairs(p, src, dst, n, num_pages);
+}
+
+// ---- fork: who gets which page ------------------------------------------------------------------------
+// ws.claim[row] = n - (the first entry that names the row as its child), 0 between calls.
+__global__ void __launch_bounds__(kBook) pages_fork_plan_kernel(const PageState t, const int32_t* parents, const int32_t* children, int n,
+                                                                int32_t* status, const PageWork ws) {
+  __shared__ int64_t warp_sums[32];
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  const int avail = free_pages(t);
+  auto row_ok = [&](int r) { return r >= 0 && r < t.rows; };
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (row_ok(children[i])) atomicMax(&ws.claim[children[i]], n - i);
+  __syncthreads();
+  int64_t taken = 0;
+  for (int base = 0; base < n; base += kBook) {
+    const int i = base + threadIdx.x;
+    bool ok = false;
+    int need = 0, len = 0;
+    if (i < n) {
+      const int p = parents[i], c = children[i];
+      if (row_ok(p) && row_ok(c) && p != c && ws.claim[c] == n - i && t.held[c] == 0) {
+        len = t.lens[p];
+        ok = len >= 0 && pages_of(len) <= t.held[p] && pages_of(len) <= t.row_pages;
+        need = ok && len % kPage ? 1 : 0;
+      }
+    }
+    int64_t total;
+    const int64_t before = taken + exclusive_sum(need, &total, warp_sums);
+    if (i < n) {
+      ok = ok && before + need <= avail;
+      int32_t page = ok ? -1 : -2;       // -1: nothing to copy, -2: not forked
+      if (ok && need) page = t.free_list[avail - 1 - before];
+      ws.src[i] = len;                   // read here: the row may be another pair's child, which is written later
+      ws.dst[i] = page;
+      status[i] = ok ? 1 : 0;
+    }
+    taken += total;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (row_ok(children[i])) ws.claim[children[i]] = 0;
+  if (threadIdx.x == 0) *t.free_count = avail - static_cast<int>(min(taken, static_cast<int64_t>(avail)));
+}
+
+// ---- fork: table rows, counts and copies ----------------------------------------------------------------
+__global__ void __launch_bounds__(kCopyThreads) pages_fork_kernel(const __grid_constant__ PagePools p, const PageState t, const int32_t* parents,
+                                                                  const int32_t* children, int n, const PageWork ws) {
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int32_t fresh = ws.dst[i];
+    if (fresh == -2) continue;
+    const int from = parents[i], to = children[i], len = ws.src[i], pages = pages_of(len);
+    const int32_t* src = t.table + static_cast<int64_t>(from) * t.row_pages;
+    int32_t* dst = t.table + static_cast<int64_t>(to) * t.row_pages;
+    for (int j = threadIdx.x; j < pages; j += kCopyThreads) {
+      const bool started = fresh >= 0 && j == pages - 1;
+      const int32_t page = started ? fresh : src[j];
+      dst[j] = page;
+      if (in_pool(t, page)) {
+        if (started) t.refs[page] = 1; else atomicAdd(&t.refs[page], 1);
+      }
+    }
+    // a row that is a parent and a child held nothing as a parent, so nobody reads what is written here
+    if (threadIdx.x == 0) {
+      t.held[to] = pages;
+      t.lens[to] = len;
+    }
+  }
+  // the started pages: the parent's last entry, the new page
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps, units = static_cast<int64_t>(n) * p.units;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); u < units; u += step) {
+    const int i = static_cast<int>(u / p.units);
+    const int32_t d = ws.dst[i];
+    if (d < 0 || d >= t.num_pages) continue;
+    const int32_t s = t.table[static_cast<int64_t>(parents[i]) * t.row_pages + ws.src[i] / kPage];
+    if (in_pool(t, s) && s != d) copy_unit(p, s, d, static_cast<uint32_t>(u - static_cast<int64_t>(i) * p.units), lane);
+  }
+}
+
+// ---- grow -------------------------------------------------------------------------------------------------
+__global__ void __launch_bounds__(kBook) pages_grow_kernel(const PageState t, const int32_t* list, const int32_t* tokens, int n, int32_t* status,
+                                                           const PageWork ws) {
+  __shared__ int64_t warp_sums[32];
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  const int avail = free_pages(t);
+  auto row_ok = [&](int r) { return r >= 0 && r < t.rows; };
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (row_ok(list[i])) atomicMax(&ws.claim[list[i]], n - i);
+  __syncthreads();
+  int64_t taken = 0, given = 0;
+  for (int base = 0; base < n; base += kBook) {
+    const int i = base + threadIdx.x;
+    bool ok = false;
+    int need = 0;
+    if (i < n) {
+      const int r = list[i], want = tokens[i];
+      if (row_ok(r) && ws.claim[r] == n - i && want >= 0 && pages_of(want) <= t.row_pages && t.held[r] >= 0) {
+        ok = true;
+        need = max(0, pages_of(want) - t.held[r]);
+      }
+    }
+    int64_t total;
+    const int64_t before = taken + exclusive_sum(need, &total, warp_sums);
+    ok = ok && (need == 0 || before + need <= avail);
+    if (i < n) {
+      status[i] = ok ? 1 : 0;
+      ws.src[i] = ok ? need : 0;
+      ws.dst[i] = static_cast<int32_t>(min(before, static_cast<int64_t>(INT32_MAX)));
+    }
+    // what is refused counts in the sum all the same: every entry behind it that needs a page is refused, too
+    taken += total;
+    exclusive_sum(ok ? need : 0, &total, warp_sums);
+    given += total;
+  }
+  // a warp an entry
+  for (int i = threadIdx.x >> 5; i < n; i += kBook / 32) {
+    const int need = ws.src[i];
+    if (need == 0) continue;
+    const int r = list[i], have = t.held[r], lane = threadIdx.x & 31;
+    const int64_t at = avail - 1 - static_cast<int64_t>(ws.dst[i]);
+    int32_t* row = t.table + static_cast<int64_t>(r) * t.row_pages + have;
+    __syncwarp();
+    for (int j = lane; j < need; j += 32) {
+      const int32_t page = t.free_list[at - j];
+      row[j] = page;
+      if (in_pool(t, page)) t.refs[page] = 1;
+    }
+    if (lane == 0) t.held[r] = have + need;
+  }
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (row_ok(list[i])) ws.claim[list[i]] = 0;
+  if (threadIdx.x == 0) *t.free_count = avail - static_cast<int>(given);
+}
+
+// ---- free ---------------------------------------------------------------------------------------------------
+// A CTA a request takes its counts down and marks what nobody holds any more; the last one puts the marked pages on the free
+// list, the highest first.
+constexpr int kFreeThreads = 512;
+__global__ void __launch_bounds__(kFreeThreads) pages_free_kernel(const PageState t, const int32_t* list, int n, const PageWork ws) {
+  __shared__ int64_t warp_sums[32];
+  __shared__ int held, last;
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  const int r = list[blockIdx.x];
+  if (r >= 0 && r < t.rows) {
+    if (threadIdx.x == 0) {
+      held = atomicExch(&t.held[r], 0);      // a row that is named twice is freed once
+      t.lens[r] = 0;
+    }
+    __syncthreads();
+    const int pages = min(held, t.row_pages);
+    const int32_t* row = t.table + static_cast<int64_t>(r) * t.row_pages;
+    for (int j = threadIdx.x; j < pages; j += kFreeThreads) {
+      const int32_t page = row[j];
+      if (!in_pool(t, page)) continue;
+      const int before = atomicSub(&t.refs[page], 1);
+      if (before == 1) atomicOr(&ws.marks[page >> 5], 1u << (page & 31));
+      else if (before <= 0) atomicAdd(&t.refs[page], 1);
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(ws.arrived, 1) == n - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const int64_t words = (t.num_pages + 31) / 32, per = (words + kFreeThreads - 1) / kFreeThreads;
+  // thread 0 has the highest words
+  const int64_t hi = words - per * threadIdx.x, lo = max(static_cast<int64_t>(0), hi - per);
+  int count = 0;
+  for (int64_t w = hi - 1; w >= lo; --w) count += __popc(__ldcg(&ws.marks[w]));
+  int64_t total;
+  int64_t at = free_pages(t) + exclusive_sum(count, &total, warp_sums);
+  for (int64_t w = hi - 1; w >= lo && count; --w) {
+    uint32_t m = __ldcg(&ws.marks[w]);
+    if (!m) continue;
+    ws.marks[w] = 0;
+    for (; m; ++at) {
+      const int b = 31 - __clz(m);
+      m &= ~(1u << b);
+      if (at < t.num_pages) t.free_list[at] = static_cast<int32_t>(32 * w + b);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    *t.free_count = static_cast<int>(min(free_pages(t) + total, t.num_pages));
+    *ws.arrived = 0;
+  }
+}
+
+// ---- compact: which pages move where ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(kBook) pages_compact_plan_kernel(const PageState t, const PageWork ws) {
+  __shared__ int64_t warp_sums[32];
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t words = (t.num_pages + 31) / 32;
+  int count = 0;
+  for (int64_t w = warp; w < words; w += kBook / 32) {
+    const int64_t page = 32 * w + lane;
+    const uint32_t used = __ballot_sync(kFull, page < t.num_pages && t.refs[page] > 0);
+    if (lane == 0) {
+      ws.marks[w] = used;
+      count += __popc(used);
+    }
+  }
+  int64_t live;
+  exclusive_sum(count, &live, warp_sums);
+  // ranks: thread i has the words [i per, (i + 1) per); the k-th hole below `live` takes the k-th page from there on
+  const int64_t per = (words + kBook - 1) / kBook, lo = per * threadIdx.x, hi = min(words, lo + per);
+  auto part = [&](int64_t w, bool holes) -> uint32_t {
+    const uint32_t used = ws.marks[w];
+    const int64_t below = live - 32 * w;
+    const uint32_t low = below >= 32 ? kFull : below <= 0 ? 0u : (1u << below) - 1;
+    return holes ? ~used & low : used & ~low;
+  };
+  int holes = 0, movers = 0;
+  for (int64_t w = lo; w < hi; ++w) {
+    holes += __popc(part(w, true));
+    movers += __popc(part(w, false));
+  }
+  int64_t num_holes, num_movers;
+  int64_t h = exclusive_sum(holes, &num_holes, warp_sums), m = exclusive_sum(movers, &num_movers, warp_sums);
+  for (int64_t w = lo; w < hi; ++w) {
+    for (uint32_t x = part(w, true); x; x &= x - 1) ws.dst[h++] = static_cast<int32_t>(32 * w + __ffs(x) - 1);
+    for (uint32_t x = part(w, false); x; x &= x - 1) {
+      const int32_t page = static_cast<int32_t>(32 * w + __ffs(x) - 1);
+      ws.rank[page] = static_cast<int32_t>(m);
+      ws.src[m++] = page;
+    }
+  }
+  __syncthreads();
+  for (int64_t w = threadIdx.x; w < words; w += kBook) ws.marks[w] = 0;
+  if (threadIdx.x == 0) {
+    *ws.moves = static_cast<int32_t>(num_movers);
+    *t.free_count = static_cast<int32_t>(t.num_pages - live);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_compact_kernel(const __grid_constant__ PagePools p, const PageState t, const PageWork ws) {
+  dev::wait_for_previous();
+  dev::allow_dependents();
+  const int64_t moves = *ws.moves, live = t.num_pages - *t.free_count;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, step = static_cast<int64_t>(gridDim.x) * kCopyThreads;
+  for (int64_t i = first; i < t.num_pages - live; i += step) t.free_list[i] = static_cast<int32_t>(t.num_pages - 1 - i);
+  for (int64_t i = first; i < moves; i += step) {
+    t.refs[ws.dst[i]] = t.refs[ws.src[i]];
+    t.refs[ws.src[i]] = 0;
+  }
+  for (int64_t i = first; i < static_cast<int64_t>(t.rows) * t.row_pages; i += step) {
+    const int64_t r = i / t.row_pages;
+    if (i - r * t.row_pages >= t.held[r]) continue;
+    const int32_t page = t.table[i];
+    // pages that the table names without a reference stay as they are named
+    if (page >= live && page < t.num_pages) {
+      const int32_t k = ws.rank[page];
+      if (k >= 0 && k < moves && ws.src[k] == page) t.table[i] = ws.dst[k];
+    }
+  }
+  copy_pairs(p, ws.src, ws.dst, moves, t.num_pages);
+}
+
+// CTAs of a copy: as many as are resident at once, or as there is work for.
+unsigned copy_grid(int64_t units, int sms) {
+  const int64_t ctas = (units + kCopyWarps - 1) / kCopyWarps;
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ctas, static_cast<int64_t>(sms) * 8)));
+}
+
+}  // namespace
+
+cudaError_t launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst, int64_t n, int64_t num_pages, int sms, cudaStream_t s) {
+  return launch_overlapped(pages_copy_kernel, copy_grid(n * p.units, sms), kCopyThreads, 0, s, p, src, dst, n, num_pages);
+}
+
+cudaError_t launch_pages_fork(const PagePools& p, const PageState& t, const int32_t* parents, const int32_t* children, int n, int32_t* status,
+                              const PageWork& ws, int sms, cudaStream_t s) {
+  const cudaError_t e = launch_overlapped(pages_fork_plan_kernel, 1, kBook, 0, s, t, parents, children, n, status, ws);
+  if (e != cudaSuccess) return e;
+  const int64_t work = std::max<int64_t>(static_cast<int64_t>(n) * p.units, static_cast<int64_t>(n) * kCopyWarps);
+  return launch_overlapped(pages_fork_kernel, copy_grid(work, sms), kCopyThreads, 0, s, p, t, parents, children, n, ws);
+}
+
+cudaError_t launch_pages_grow(const PageState& t, const int32_t* list, const int32_t* tokens, int n, int32_t* status, const PageWork& ws,
+                              cudaStream_t s) {
+  return launch_overlapped(pages_grow_kernel, 1, kBook, 0, s, t, list, tokens, n, status, ws);
+}
+
+cudaError_t launch_pages_free(const PageState& t, const int32_t* list, int n, const PageWork& ws, cudaStream_t s) {
+  return launch_overlapped(pages_free_kernel, static_cast<unsigned>(n), kFreeThreads, 0, s, t, list, n, ws);
+}
+
+cudaError_t launch_pages_compact(const PagePools& p, const PageState& t, const PageWork& ws, int sms, cudaStream_t s) {
+  const cudaError_t e = launch_overlapped(pages_compact_plan_kernel, 1, kBook, 0, s, t, ws);
+  if (e != cudaSuccess) return e;
+  const int64_t most = t.num_pages / 2 * p.units + static_cast<int64_t>(t.rows) * t.row_pages / 32;
+  return launch_overlapped(pages_compact_kernel, copy_grid(most, sms), kCopyThreads, 0, s, p, t, ws);
+}
+
+}  // namespace qkvp

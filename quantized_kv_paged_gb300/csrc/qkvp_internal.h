@@ -297,6 +297,47 @@ inline TreeTable tree_table(int64_t segments, int64_t workers, int64_t joins) {
   return t;
 }
 
+// Arguments of gqa_tree_commit.
+constexpr int kMaxLayers = 128;
+struct TreeCommitArgs {
+  uint8_t* kv[kMaxLayers];    // [num_pages][2][kv_heads][64][dim] of each layer
+  float* scale[kMaxLayers];   // [num_pages][2][kv_heads]
+  const int32_t* kv_len;      // [batch] tokens before the drafted ones
+  const int32_t* kv_indptr;   // [batch + 1]
+  const int32_t* kv_indices;  // [nnz]
+  const int32_t* path;        // [batch][max_path]
+  const int32_t* path_len;    // [batch]
+  int64_t nnz, num_pages;
+  int layers, batch, max_path, kv_heads, dim, cache_dtype;
+};
+
+// The pools that a page is copied in, cut into units of kCopyUnit bytes.
+constexpr int kMaxPools = 256;
+constexpr int kCopyUnit = 4096;
+struct PagePools {
+  uint8_t* base[kMaxPools];
+  uint32_t bytes[kMaxPools];       // of a page
+  uint32_t first_unit[kMaxPools];  // of the pool's units within a page's
+  uint32_t units;                  // of a page, all pools
+  int count;
+};
+
+// Page tables, counts and the free list (qkvp_page_state).
+struct PageState {
+  int32_t *table, *held, *lens, *refs, *free_list, *free_count;
+  int rows, row_pages;
+  int64_t num_pages;
+};
+
+// A page call's workspace. arrived, claim and marks are zero between calls; the rest is scratch.
+struct PageWork {
+  int32_t *arrived, *moves;
+  int32_t* claim;      // [rows]
+  uint32_t* marks;     // [num_pages / 32]
+  int32_t *src, *dst;  // [max(n, num_pages)]
+  int32_t* rank;       // [num_pages]
+};
+
 // Limits of the head pool's entry points.
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxHeads = 4096;
@@ -353,6 +394,14 @@ cudaError_t launch_mla_append_rope(const MlaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_append_rope(const GqaAppendArgs& a, cudaStream_t s);
 cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t s);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t s);
+cudaError_t launch_pages_copy(const PagePools& p, const int32_t* src, const int32_t* dst, int64_t n, int64_t num_pages, int sms, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagePools& p, const PageState& t, const int32_t* parents, const int32_t* children, int n, int32_t* status,
+                              const PageWork& ws, int sms, cudaStream_t s);
+cudaError_t launch_pages_grow(const PageState& t, const int32_t* list, const int32_t* tokens, int n, int32_t* status, const PageWork& ws,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const PageState& t, const int32_t* list, int n, const PageWork& ws, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagePools& p, const PageState& t, const PageWork& ws, int sms, cudaStream_t s);
 cudaError_t launch_gather_fp8(const GatherArgs& a, cudaStream_t s);
 cudaError_t launch_gather_pages_bf16(const uint8_t* pool, int64_t num_pages, const int32_t* ids, int64_t n,
                                      void* out, cudaStream_t s);
