@@ -86,7 +86,7 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   indptr[rows] = at;
 
   const int64_t useful = std::max<int64_t>(1, (row_pages + kMinPages - 1) / kMinPages);
-  const int workers = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(num_sms) * tree_ctas_per_sm(head_dim, tiles), useful));
+  const int workers = static_cast<int>(std::min<int64_t>(num_sms, useful));
   SplitInfo info;
   info.num_segments = rows + workers;      // each worker's end cuts one row at most; asked-for splits are counted first
   if (min_splits > 0) split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, kStartPages);
@@ -139,7 +139,12 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   std::vector<uint8_t> blob(t.bytes);
   TreeSegment* segs = reinterpret_cast<TreeSegment*>(blob.data() + t.segs);
   TreeJoin* joins = reinterpret_cast<TreeJoin*>(blob.data() + t.joins);
-  std::memcpy(blob.data() + t.wptr, wptr.data(), (workers + 1) * sizeof(int32_t));
+  TreeWorker* work = reinterpret_cast<TreeWorker*>(blob.data() + t.workers);
+  for (int w = 0; w < workers; ++w) {
+    work[w].begin = wptr[w];
+    work[w].end = wptr[w + 1];
+    for (int x = wptr[w]; x < wptr[w + 1]; ++x) work[w].pages += cut[x].num_pages;
+  }
   int64_t first = 0;      // the request's first row
   int num_joins = 0;
   for (int64_t row = 0; row < rows; ++row) {
@@ -205,7 +210,7 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
   a.kv_indices = kv_indices;
   a.mask = tree_mask;
   a.segs = reinterpret_cast<const TreeSegment*>(ws + t.segs);
-  a.worker_ptr = reinterpret_cast<const int32_t*>(ws + t.wptr);
+  a.workers = reinterpret_cast<const TreeWorker*>(ws + t.workers);
   a.joins = reinterpret_cast<const TreeJoin*>(ws + t.joins);
   a.status = reinterpret_cast<int*>(ws + t.status);
   a.part_o = reinterpret_cast<float*>(ws + plan->partial_o_offset);

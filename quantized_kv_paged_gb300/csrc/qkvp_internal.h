@@ -258,8 +258,11 @@ static_assert(sizeof(TreeJoin) == 32, "join layout");
 constexpr uint64_t kTreeMagic = 0x716b76702d747265ull;
 constexpr int kTreeTile = 128;         // rows of a matrix product: the lanes of tensor memory
 constexpr int kTreeMaxDrafted = 256;   // drafted tokens of a request
-// CTAs of the tree attention that one SM holds: what tensor memory allows (512 columns).
-constexpr int tree_ctas_per_sm(int dim, int tiles) { return dim == 256 || tiles == 2 ? 1 : 2; }
+struct TreeWorker {
+  int32_t begin, end;             // its segments
+  int32_t pages;                  // of all of them
+  int32_t pad;
+};
 
 struct TreeArgs {
   const uint16_t* q;          // bf16 [n][H][D]
@@ -269,7 +272,7 @@ struct TreeArgs {
   const int32_t* kv_indices;
   const uint32_t* mask;       // [n][words], or null: a chain
   const TreeSegment* segs;
-  const int32_t* worker_ptr;  // [num_workers + 1]
+  const TreeWorker* workers;  // [num_workers]
   const TreeJoin* joins;
   int* status;
   float* part_o;              // [num_partials][128 tiles][D], normalised
@@ -285,13 +288,13 @@ struct TreeArgs {
 
 // Work table of a tree plan.
 struct TreeTable {
-  uint64_t segs, wptr, joins, status, bytes;
+  uint64_t segs, workers, joins, status, bytes;
 };
 inline TreeTable tree_table(int64_t segments, int64_t workers, int64_t joins) {
   TreeTable t;
   t.segs = 0;
-  t.wptr = align_up(static_cast<uint64_t>(segments) * sizeof(TreeSegment));
-  t.joins = t.wptr + align_up(static_cast<uint64_t>(workers + 1) * 4);
+  t.workers = align_up(static_cast<uint64_t>(segments) * sizeof(TreeSegment));
+  t.joins = t.workers + align_up(static_cast<uint64_t>(workers) * sizeof(TreeWorker));
   t.status = t.joins + align_up(static_cast<uint64_t>(joins) * sizeof(TreeJoin));
   t.bytes = t.status + kTableAlign;
   return t;

@@ -7,29 +7,37 @@
 // A page's 64 tokens of one KV head are 128 D bytes and 256 D T G operations (T drafted tokens, G query heads a KV head):
 // reading bounds it up to T G ~ 140 rows, the matrix products above.
 //
-// Work. A (request, KV head) has T G rows, cut into blocks of 128 (one tile) or 256 (two tiles), and a worker (a CTA) walks
-// segments, each a run of the pages that a block sees. Two CTAs of one tile share an SM, so that one's start and end
-// hide behind the other; two tiles share a page's conversion and take turns on the tensor cores.
+// Work. A (request, KV head) has T G rows, cut into blocks of up to 128 or (where there are more) 256, two tiles of 128 lanes of
+// tensor memory. A worker (a CTA, one per SM) walks segments, each a run of the pages that a block sees, page by page.
+// Two softmax warpgroups work at a time:
+//   - a block of two tiles: one for each tile, every page (unsplit);
+//   - a block of one tile: in turns, one page each, into one O (split).
+// A page is a chain (S = Q K^T, softmax, O += P V) of some 2,000 cycles at D 128; each warpgroup has two buffers of logits, so
+// that the products of its next page and of its last one run beside its softmax.
 //
-// Roles, per CTA:
-//   softmax warps (4 a tile, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
-//     memory; per page the row's 64 logits from there, running maximum, P back into their place as FP16; at the
-//     segment's end O / l.
-//   dequant warps: one thread keeps a ring of raw K and V blocks (64 D bytes each, contiguous in the pool) filled by bulk
-//     copies; all turn the codes into FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
-//   one thread a tile issues S = Q K^T (M 128, N 64; Q from tensor memory), another O += P V (M 128, N D; P from tensor
-//     memory). The same tile layout is K^T's K-major operand and V's MN-major one.
-// Q and P from tensor memory leave shared memory the raw bytes, the tiles and one operand's reads.
+// Roles, per CTA (20 warps):
+//   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
+//     memory (two tiles at D 128: shared memory, tensor memory is full); per page the row's 64 logits from there, the
+//     softmax, P back into their place as FP16; at the segment's end O / l.
+//   K and V conversion (a warpgroup each): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
+//   a loader thread: bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into a ring, and the blocks'
+//     scales into another. (Read by the softmax a page ahead, the scales came 1,500 cycles late.)
+//   a thread issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor memory). The same tile
+//     layout is K^T's K-major operand and V's MN-major one.
 //
-// Softmax. m is the row's largest logit so far, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv code, and
-// V's scales may be far apart, so O has a reference r of its own: P = p F, F = sv 2^(m - r + 6), r renewed (and O
-// rescaled) only when the largest z + log2 sv of a page passes it by 2^8. P <= 2^14 stays in FP16's normal range down to
-// 2^-28 of the largest contribution.
+// Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
+// code, and V's scales may be far apart, so O has a reference r of its own (common to the warpgroups that share O, handed
+// on from step to step): P = 2^(z - m) F, F = sv 2^(m - r + 6), r renewed (and O rescaled) only when the largest z + log2 sv
+// of a page passes it by 2^8. P <= 2^14 stays in FP16's normal range down to 2^-28 of the largest contribution. A page is
+// taken against the r at hand in one pass, F in the exponent, which l takes back from the sum of P; where its largest
+// logit shows that r has to move, where tokens are masked or F is extreme, it is taken in two passes.
 //
 // Masks. Only pages that hold drafted tokens or an edge of a row's window are masked by row: 64 bits from the row's mask
 // words. V codes that are NaN there count as zero in the product (0 times NaN would reach rows that do not see the token),
 // and the rows that do see one are found at the segment's end.
 #include <cstdint>
+
+#include <cuda_fp16.h>
 
 #include "decode_common.cuh"
 #include "qkvp_device.cuh"
@@ -39,7 +47,6 @@
 namespace qkvp {
 namespace {
 
-using kern::Sync;
 using kern::sts128_relaxed;
 
 constexpr float kSlack = 8.0f;     // how far (log2) a contribution may pass the reference
@@ -48,32 +55,39 @@ constexpr float kNoRef = -1e30f;   // reference before the first page that contr
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kCtas = tree_ctas_per_sm(D, NT);
-  static constexpr int kDqWarps = D == 256 ? 8 : 4;
-  static constexpr int kDQ = 32 * kDqWarps;
-  static constexpr int kSmWarps = 4 * NT;
-  static constexpr int kQkWarp = kSmWarps + kDqWarps, kPvWarp = kQkWarp + NT;
-  static constexpr int kThreads = 32 * (kPvWarp + NT);
+  // warps: two softmax warpgroups, K's and V's conversion, then Q.K^T, P.V of each tile, the loader
+  static constexpr int kKWarp = 8, kVWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 19, kThreads = 640;
   static constexpr int kAtoms = D / 64;
-  static constexpr uint32_t kRaw = kPage * D;            // bytes of a raw K or V block
-  static constexpr uint32_t kAtom = kPage * 128;         // 64 tokens x 64 FP16
-  static constexpr uint32_t kTile = kAtoms * kAtom;      // a converted block
-  static constexpr int kKS = D == 256 ? 2 : D == 128 && NT == 1 ? 2 : 3, kVS = kKS;
-  static constexpr int kRS = D == 256 || (D == 128 && NT == 1) ? 5 : 8;   // raw blocks in the ring
-  static constexpr int kSB = D == 128 ? 1 : 2;           // logit buffers of a tile
-  // tensor memory columns
-  static constexpr uint32_t TM_S = NT * D, TM_Q = TM_S + NT * kSB * 64, kCols = TM_Q + NT * D / 2 <= 256 ? 256 : 512;
-  static_assert(TM_Q + NT * D / 2 <= 512 && kCols * kCtas <= 512, "tensor memory");
+  static constexpr uint32_t kRaw = kPage * D;              // bytes of a raw K or V block
+  static constexpr uint32_t kAtom = kPage * 128;           // 64 tokens x 64 FP16
+  static constexpr uint32_t kTile = kAtoms * kAtom;        // a converted block
+  static constexpr bool kQSmem = D == 128 && NT == 2;
+  static constexpr uint32_t kQAtom = kTreeTile * 128, kQTile = kAtoms * kQAtom;
+  static constexpr int kSlots = D == 256 ? 2 : 4;          // pages of the K and V tiles
+  static constexpr int kRS = D == 64 ? 16 : D == 256 ? 6 : NT == 1 ? 10 : 4;   // raw blocks in the ring, an even number
+  // pages of the ring of scales: the loader is ahead of the softmax by the raw ring, the tiles and the logits, 15 at most
+  static constexpr int kInfo = 32;
+  static_assert(kRS / 2 + kSlots + 4 + 2 < kInfo, "an entry is read before it is written again");
+  // tensor memory columns: O, two buffers of logits for each warpgroup (D 256: one, there is no room), Q
+  static constexpr int kSB = D == 256 ? 1 : 2;
+  static constexpr uint32_t TM_S = NT * D, TM_Q = TM_S + 2 * kSB * kPage;
+  // of the k-th page of a warpgroup: its buffer, and the parity of the buffer's phases
+  __device__ static int buf(int w, int k) { return kSB * w + (k & (kSB - 1)); }
+  __device__ static uint32_t phase(int k) { return (k >> (kSB - 1)) & 1; }
+  static_assert(TM_Q + (kQSmem ? 0 : NT * D / 2) <= 512, "tensor memory");
   // shared memory
-  static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kKS * kTile, OFF_RAW = OFF_V + kVS * kTile, OFF_BAR = OFF_RAW + kRS * kRaw;
-  // barriers
-  static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_K_EMPTY = B_K_FULL + kKS,
-                            B_V_FULL = B_K_EMPTY + kKS, B_V_EMPTY = B_V_FULL + kVS, B_S_FULL = B_V_EMPTY + kVS,
-                            B_P_FULL = B_S_FULL + NT * kSB, B_O_DONE = B_P_FULL + NT * kSB, B_Q_FULL = B_O_DONE + NT * kSB,
-                            B_FINAL = B_Q_FULL + NT, kBars = B_FINAL + 1;
+  static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kSlots * kTile, OFF_Q = OFF_V + kSlots * kTile,
+                            OFF_RAW = OFF_Q + (kQSmem ? NT * kQTile : 0), OFF_REF = OFF_RAW + kRS * kRaw;
+  static constexpr uint32_t OFF_INFO = OFF_REF + 4 * kTreeTile;     // of a page: scale of K, of V, tokens and flags
+  static constexpr uint32_t OFF_BAR = OFF_INFO + 16 * kInfo;
+  static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_K_EMPTY = B_K_FULL + kSlots,
+                            B_V_FULL = B_K_EMPTY + kSlots, B_V_EMPTY = B_V_FULL + kSlots, B_S_FULL = B_V_EMPTY + kSlots, B_P_FULL = B_S_FULL + 4,
+                            B_O_DONE = B_P_FULL + 4, B_REF = B_O_DONE + 4, B_Q_FULL = B_REF + 4, B_O_FREE = B_Q_FULL + 1, B_SEG = B_O_FREE + 1,
+                            B_FINAL = B_SEG + 1, kBars = B_FINAL + 1;
   static constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * kBars, OFF_ABORT = OFF_TSLOT + 4, OFF_NAN = OFF_ABORT + 4;
-  static constexpr uint32_t kSmem = OFF_NAN + 8 + 1024;  // slack to align the base to 1024 bytes
-  static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory of an SM");
+  static constexpr uint32_t kSmem = OFF_NAN + 8 + 1024;    // slack to align the base to 1024 bytes
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kRS % 2 == 0, "K blocks have the even places of the ring");
 };
 
 __device__ __forceinline__ TreeSegment load_segment(const TreeSegment* p) {
@@ -85,25 +99,49 @@ __device__ __forceinline__ TreeSegment load_segment(const TreeSegment* p) {
   return s;
 }
 
-// Walks a worker's pages, segment by segment; every segment has a page at least.
-struct Walk {
-  int si, se, j;
-  TreeSegment s;
-  __device__ Walk(const TreeArgs& a, int b, int e) : si(b), se(e), j(0) {
-    if (si < se) s = load_segment(a.segs + si);
+// The CTA's mbarriers, its abort flag and the plan's status word. Waits are bounded (about a second): one that gives up sets
+// `code` in the status word and the abort flag, which ends every other wait of the CTA. The wait proper is a call: five
+// roles run side by side, and copies of it would crowd the instruction cache.
+struct Sync {
+  uint32_t bars;
+  volatile int* abort;
+  int* status;
+  __device__ uint32_t bar(uint32_t i) const { return bars + 8 * i; }
+  __device__ __forceinline__ bool wait(uint32_t i, uint32_t parity, int code) const {
+    return tc::mbar_try_wait(bar(i), parity) || patient(bar(i), parity, code, abort, status);
   }
-  __device__ bool done() const { return si >= se; }
-  __device__ void next(const TreeArgs& a) {
-    if (++j < s.num_pages) return;
-    j = 0;
-    if (++si < se) s = load_segment(a.segs + si);
+  __device__ static __noinline__ bool patient(uint32_t bar, uint32_t parity, int code, volatile int* abort, int* status) {
+    const long long t0 = clock64();
+    for (int n = 0;; ++n) {
+      if (tc::mbar_try_wait(bar, parity)) return true;
+      if ((n & 255) == 0) {
+        if (*abort) return false;
+        if (clock64() - t0 > (1ll << 31)) {
+          *abort = 1;
+          atomicOr(status, code);
+          return false;
+        }
+      }
+    }
   }
-  __device__ int local() const {
-    const int v = s.page_begin + j;
-    return v < s.sink_pages ? v : s.win_page + (v - s.sink_pages);
-  }
-  __device__ int32_t page(const TreeArgs& a) const { return a.kv_indices[s.page0 + local()]; }
 };
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// Page v of a segment's visible ones in the request's list.
+__device__ __forceinline__ int local_page(const TreeSegment& s, int j) {
+  const int v = s.page_begin + j;
+  return v < s.sink_pages ? v : s.win_page + (v - s.sink_pages);
+}
+
+// Whether a block is one tile, whose pages the two softmax warpgroups take in turns.
+template <int NT>
+__device__ __forceinline__ bool is_split(const TreeSegment& s) { return NT == 1 || s.rows <= kTreeTile; }
 
 __device__ __forceinline__ bool in_pool(const TreeArgs& a, int32_t page) { return page >= 0 && page < a.num_pages; }
 
@@ -184,178 +222,214 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// Raw blocks in, FP16 tiles out. Block e of a worker is page e / 2's K (e even) or V.
-template <int D, int NT, bool E4M3>
-__device__ void role_dequant(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int t, uint32_t base, volatile int* nan_seen) {
+// What is known of a page beside its scales: its tokens, and whether it is masked by row.
+constexpr uint32_t kMasked = 1u << 16;
+
+// One thread: raw K and V blocks of the worker's pages into the ring, K in the even places, and the page's entry. A block of K
+// is there when its copy and the scales' are.
+template <int D, int NT>
+__device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, uint32_t base, uint8_t* sbase) {
   using C = Cfg<D, NT>;
-  constexpr int kItems = C::kRaw / 16 / C::kDQ;            // 16 codes each
-  static_assert(kItems * C::kDQ * 16 == C::kRaw, "every thread the same number of items");
-  constexpr int kBlockRow = kPage * D;
-  Walk cur(a, seg_b, seg_e);
-  if (cur.done()) return;
-  // thread 0 loads kRS - 1 blocks ahead of the conversion; its page id is read a page before it is needed
-  Walk ld = cur;
-  int32_t ld_page = t == 0 ? ld.page(a) : 0;
-  int loaded = 0;                                          // blocks issued (thread 0)
   const uint32_t raw = base + C::OFF_RAW;
-  auto issue = [&]() {
-    if (ld.done()) return true;
-    const int slot = loaded % C::kRS;
-    if (loaded >= C::kRS && !sy.wait(C::B_RAW_EMPTY + slot, (loaded / C::kRS - 1) & 1, false, 1)) return false;
-    const bool v = loaded & 1;
-    // of a request's last page only the tokens that it has
-    const int p0 = ld.local() * kPage;
-    const uint32_t bytes = in_pool(a, ld_page) ? min(kPage, ld.s.len - p0) * D : 0;
-    const uint32_t bar = sy.bar(C::B_RAW_FULL + slot);
-    if (bytes) {
-      tc::mbar_arrive_expect_tx(bar, bytes);
-      const int64_t block = (static_cast<int64_t>(ld_page) * 2 + (v ? 1 : 0)) * a.kv_heads + ld.s.kv_head;
-      tc::bulk_load(raw + slot * C::kRaw, a.kv + block * kBlockRow, bytes, bar);
-    } else {
-      tc::mbar_arrive(bar);
-    }
-    if (v) {
-      ld.next(a);
-      if (!ld.done()) ld_page = ld.page(a);
-    }
-    ++loaded;
-    return true;
-  };
+  int n = 0, slot = 0, round = 0;
   bool ok = true;
-  if (t == 0)
-    for (int i = 0; i < C::kRS - 1 && ok; ++i) ok = issue();
-  int32_t page = cur.page(a);
-  int e = 0;
-  for (int g = 0; !cur.done() && ok; ++g) {
-    Walk nx = cur;
-    nx.next(a);
-    const int32_t npage = nx.done() ? 0 : nx.page(a);
-    const int p0 = cur.local() * kPage;
-    const int valid = in_pool(a, page) ? min(kPage, cur.s.len - p0) : 0;
-    const bool masked = E4M3 && by_row(a, cur.s, p0);
+  for (int si = seg_b; si < seg_e && ok; ++si) {
+    const TreeSegment s = load_segment(a.segs + si);
+    int32_t page = a.kv_indices[s.page0 + local_page(s, 0)];
+    for (int j = 0; j < s.num_pages && ok; ++j, ++n) {
+      const int32_t next = j + 1 < s.num_pages ? a.kv_indices[s.page0 + local_page(s, j + 1)] : -1;
+      const int p0 = local_page(s, j) * kPage;
+      // of a request's last page only the tokens that it has
+      const int valid = in_pool(a, page) ? min(kPage, s.len - p0) : 0;
+      const int64_t block = static_cast<int64_t>(page) * 2 * a.kv_heads + s.kv_head;
 #pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind, ++e) {
-      if (t == 0 && !issue()) { ok = false; break; }
-      const int slot = e % C::kRS;
-      if (!sy.wait(C::B_RAW_FULL + slot, (e / C::kRS) & 1, false, 1)) { ok = false; break; }
-      uint4 w[kItems];
+      for (int v = 0; v < 2; ++v) {
+        if (round > 0 && !sy.wait(C::B_RAW_EMPTY + slot, (round - 1) & 1, 1)) { ok = false; break; }
+        const uint32_t bar = sy.bar(C::B_RAW_FULL + slot);
+        if (v == 0) {
+          const uint32_t info = C::OFF_INFO + 16 * (n % C::kInfo);
+          *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = valid | (by_row(a, s, p0) || !valid ? kMasked : 0);
+          if (valid) {
+            cp_async4(base + info, a.kv_scale + block);
+            cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
+          } else {
+            *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
+            *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
+          }
+          cp_async_arrive(bar);
+        }
+        if (valid) {
+          tc::mbar_arrive_expect_tx(bar, valid * D);
+          tc::bulk_load(raw + slot * C::kRaw, a.kv + (block + (v ? a.kv_heads : 0)) * C::kRaw, valid * D, bar);
+        } else {
+          tc::mbar_arrive(bar);
+        }
+        if (++slot == C::kRS) { slot = 0; ++round; }
+      }
+      page = next;
+    }
+  }
+  // after a timeout: the copies in flight land before the CTA may end
+  if (*sy.abort) {
+    dev::cp_async_wait_all();
+    for (int k = 0; k < C::kRS; ++k)
+      if (k < slot || round > 0) tc::mbar_wait(sy.bar(C::B_RAW_FULL + k), (k < slot ? round : round - 1) & 1);
+  }
+}
+
+// A warpgroup: raw blocks of K (kind 0) or V (kind 1) to the FP16 tiles of a step. An item is 16 codes. Eight lanes take rows 2 p
+// and 2 p + 1, 64 dims each, of atoms that differ: their reads and their writes fall into distinct banks. K rows past a page's
+// tokens keep what is there (their logits are masked); V rows become zeros.
+template <int D, int NT, bool E4M3>
+__device__ void role_convert(const Sync& sy, int kind, int pages, int t, uint32_t base, volatile uint32_t* info, volatile int* nan_seen) {
+  using C = Cfg<D, NT>;
+  constexpr int kItems = C::kRaw / 16 / 128;
+  const int warp = t >> 5, lane = t & 31, c = lane & 3;
+  const int row0 = D == 64 ? t >> 2 : 16 * warp + 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
+  constexpr int kRowStep = D == 64 ? 32 : 8, kRowItems = D == 64 ? 1 : C::kAtoms;       // items of a row, rows from one to the next
+  const uint32_t raw = base + C::OFF_RAW, tiles = base + (kind == 0 ? C::OFF_K : C::OFF_V);
+  const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, empty = kind == 0 ? C::B_K_EMPTY : C::B_V_EMPTY;
+  const uint32_t read0 = raw + row0 * D + 16 * c;
+  const uint32_t write0 = (row0 >> 3) * 1024 + (row0 & 7) * 128 + (((2 * c) ^ (row0 & 7)) << 4), write1 = write0 ^ 16;
+  int slot = kind, parity = 0;
+  for (int n = 0; n < pages; ++n) {
+    const int ts = n % C::kSlots;
+    if (!sy.wait(C::B_RAW_FULL + slot, parity, 2)) return;
+    const uint32_t entry = info[4 * (n % C::kInfo) + 2];
+    const int valid = static_cast<int>(entry & 0xFFFF);
+    uint4 w[kItems];
+    if (valid) {
+      const uint32_t from = read0 + slot * C::kRaw;
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const int q = t + C::kDQ * i;
-        w[i] = q / (D / 16) < valid ? lds128(raw + slot * C::kRaw + 16 * q) : make_uint4(0, 0, 0, 0);
+        const int r = i / kRowItems * kRowStep, atom = i % kRowItems;
+        w[i] = lds128(from + r * D + ((atom ^ odd) << 6));
       }
-      tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
-      if (kind == 1 && masked) {
+    }
+    tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
+    slot += 2;
+    if (slot >= C::kRS) { slot = kind; parity ^= 1; }
+    if (kind == 1 && valid < kPage) {
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
+      for (int i = 0; i < kItems; ++i)
+        if (row0 + i / kRowItems * kRowStep >= valid) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (E4M3 && kind == 1 && (entry & kMasked)) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bad = nan_bytes(x[k]);
-            if (bad) {
-              x[k] &= ~(bad * 0xFFu);
-              *nan_seen = 1;
-            }
+      for (int i = 0; i < kItems; ++i) {
+        uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t bad = nan_bytes(x[k]);
+          if (bad) {
+            x[k] &= ~(bad * 0xFFu);
+            *nan_seen = 1;
           }
         }
       }
-      const int slots = kind == 0 ? C::kKS : C::kVS, s = g % slots;
-      const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, empty = kind == 0 ? C::B_K_EMPTY : C::B_V_EMPTY;
-      if (g >= slots && !sy.wait(empty + s, (g / slots - 1) & 1, false, 1)) { ok = false; break; }
-      const uint32_t tile = base + (kind == 0 ? C::OFF_K : C::OFF_V) + s * C::kTile;
-#pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int q = t + C::kDQ * i, row = q / (D / 16), col = q % (D / 16), atom = col / 4, chunk = 2 * (col % 4);
-        uint32_t o[8];
-        codes_to_f16<E4M3>(w[i].x, o[0], o[1]);
-        codes_to_f16<E4M3>(w[i].y, o[2], o[3]);
-        codes_to_f16<E4M3>(w[i].z, o[4], o[5]);
-        codes_to_f16<E4M3>(w[i].w, o[6], o[7]);
-        // the lanes of an odd atom write their second half first: eight lanes, eight bank groups
-        const int odd = D > 64 ? atom & 1 : 0;
-        const uint32_t at = tile + atom * C::kAtom;
-        const uint4 h0 = make_uint4(o[0], o[1], o[2], o[3]), h1 = make_uint4(o[4], o[5], o[6], o[7]);
-        sts128_relaxed(at + tc::sw128_offset(row, chunk + odd), odd ? h1 : h0);
-        sts128_relaxed(at + tc::sw128_offset(row, chunk + 1 - odd), odd ? h0 : h1);
-      }
-      tc::fence_proxy_async_smem();
-      tc::mbar_arrive(sy.bar(full + s));
     }
-    cur = nx;
-    page = npage;
+    if (n >= C::kSlots && !sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2)) return;
+    const uint32_t to = tiles + ts * C::kTile;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const uint32_t at = to + i / kRowItems * kRowStep * 128 + ((i % kRowItems) ^ odd) * C::kAtom;
+      uint32_t o[8];
+      codes_to_f16<E4M3>(w[i].x, o[0], o[1]);
+      codes_to_f16<E4M3>(w[i].y, o[2], o[3]);
+      codes_to_f16<E4M3>(w[i].z, o[4], o[5]);
+      codes_to_f16<E4M3>(w[i].w, o[6], o[7]);
+      sts128_relaxed(at + write0, make_uint4(o[0], o[1], o[2], o[3]));
+      sts128_relaxed(at + write1, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive(sy.bar(full + ts));
   }
-  // after a timeout: the copies in flight land before the CTA may end
-  if (t == 0 && !ok)
-    for (; e < loaded; ++e) tc::mbar_wait(sy.bar(C::B_RAW_FULL + e % C::kRS), (e / C::kRS) & 1);
 }
 
+// One thread: S = Q K^T of every page, for both tiles of an unsplit block. cnt[w]: pages of softmax warpgroup w so far.
 template <int D, int NT>
-__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int tile, uint32_t base, uint32_t tbase) {
+__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, uint32_t base, uint32_t tbase) {
   using C = Cfg<D, NT>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
-  const uint32_t q = tbase + C::TM_Q + tile * (D / 2);
-  int n = 0, segs = 0;                          // pages of this tile, segments of this tile
-  Walk w(a, seg_b, seg_e);
-  for (int g = 0; !w.done(); ++g) {
-    const int slot = g % C::kKS;
-    const bool first = w.j == 0, mine = w.s.rows > tile * kTreeTile;
-    if (!sy.wait(C::B_K_FULL + slot, (g / C::kKS) & 1, false, 2)) break;
-    if (mine) {
-      const int b = n % C::kSB;
-      // the buffer's last P has been read
-      if (n >= C::kSB && !sy.wait(C::B_O_DONE + tile * C::kSB + b, (n / C::kSB - 1) & 1, false, 2)) break;
-      if (first && !sy.wait(C::B_Q_FULL + tile, segs++ & 1, false, 2)) break;
-      tc::tc_fence_after();
-      const uint32_t s = tbase + C::TM_S + (tile * C::kSB + b) * kPage;
+  const tc::Desc2 qd = tc::split_desc(tc::smem_desc(base + C::OFF_Q, 16, 1024, tc::kSwizzle128));
+  int n = 0, cnt[2] = {0, 0};
+  for (int si = seg_b; si < seg_e; ++si) {
+    const TreeSegment s = load_segment(a.segs + si);
+    const bool split = is_split<NT>(s);
+    if (!sy.wait(C::B_Q_FULL, (si - seg_b) & 1, 4)) goto out;
+    for (int j = 0; j < s.num_pages; ++j, ++n) {
+      const int slot = n % C::kSlots;
+      if (!sy.wait(C::B_K_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t bd = kd.at(slot * C::kTile + (k >> 2) * C::kAtom + 32 * (k & 3));
-        if (k == 0) tc::mma_ts_k<false>(s, q, bd, kIdesc);
-        else tc::mma_ts_k<true>(s, q + 8 * k, bd, kIdesc);
+      for (int w = 0; w < 2; ++w) {
+        if (split && (j & 1) != w) continue;
+        // the buffer's last P has been read
+        const int b = C::buf(w, cnt[w]);
+        if (cnt[w] >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(cnt[w]) ^ 1, 4)) goto out;
+        tc::tc_fence_after();
+        const int tile = split ? 0 : w;
+        const uint32_t d = tbase + C::TM_S + b * kPage;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t bd = kd.at(slot * C::kTile + (k >> 2) * C::kAtom + 32 * (k & 3));
+          if constexpr (C::kQSmem) {
+            const uint64_t ad = qd.at(tile * C::kQTile + (k >> 2) * C::kQAtom + 32 * (k & 3));
+            if (k == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
+            else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
+          } else {
+            const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * k;
+            if (k == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+            else tc::mma_ts_k<true>(d, q, bd, kIdesc);
+          }
+        }
+        tc::mma_commit(sy.bar(C::B_S_FULL + b));
+        ++cnt[w];
       }
-      tc::mma_commit(sy.bar(C::B_S_FULL + tile * C::kSB + b));
       tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
-      ++n;
-    } else {
-      tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
     }
-    w.next(a);
   }
+out:
   tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
+// One thread a tile: O += P V. That of tile 0 takes the pages of split blocks, in order.
 template <int D, int NT>
 __device__ void role_pv(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int tile, uint32_t base, uint32_t tbase) {
   using C = Cfg<D, NT>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, D, 0, 1);
   const tc::Desc2 vd = tc::split_desc(tc::smem_desc(base + C::OFF_V, C::kAtom, 1024, tc::kSwizzle128));
   const uint32_t o = tbase + tile * D;
-  int n = 0;
-  Walk w(a, seg_b, seg_e);
-  for (int g = 0; !w.done(); ++g) {
-    const int slot = g % C::kVS;
-    const bool first = w.j == 0, mine = w.s.rows > tile * kTreeTile;
-    if (!sy.wait(C::B_V_FULL + slot, (g / C::kVS) & 1, false, 4)) break;
-    if (mine) {
-      const int b = n % C::kSB;
-      if (!sy.wait(C::B_P_FULL + tile * C::kSB + b, (n / C::kSB) & 1, false, 4)) break;
-      tc::tc_fence_after();
-      const uint32_t p = tbase + C::TM_S + (tile * C::kSB + b) * kPage;
+  int n = 0, cnt[2] = {0, 0};
+  for (int si = seg_b; si < seg_e; ++si) {
+    const TreeSegment s = load_segment(a.segs + si);
+    const bool split = is_split<NT>(s);
+    // O of the segment before has been read
+    if (si > seg_b && !sy.wait(C::B_O_FREE, (si - seg_b - 1) & 1, 4)) goto out;
+    for (int j = 0; j < s.num_pages; ++j, ++n) {
+      const int slot = n % C::kSlots;
+      if (!sy.wait(C::B_V_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
+      const int w = split ? j & 1 : tile, b = C::buf(w, cnt[w]);
+      if (split && tile == 1) {
+        tc::mbar_arrive(sy.bar(C::B_V_EMPTY + slot));
+      } else {
+        if (!sy.wait(C::B_P_FULL + b, C::phase(cnt[w]), 4)) goto out;
+        tc::tc_fence_after();
+        const uint32_t p = tbase + C::TM_S + b * kPage;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {              // 16 tokens each
-        const uint64_t bd = vd.at(slot * C::kTile + 2048 * k);
-        if (k == 0 && first) tc::mma_ts_k<false>(o, p, bd, kIdesc);
-        else tc::mma_ts_k<true>(o, p + 8 * k, bd, kIdesc);
+        for (int k = 0; k < kPage / 16; ++k) {
+          const uint64_t bd = vd.at(slot * C::kTile + 2048 * k);
+          if (k == 0 && j == 0) tc::mma_ts_k<false>(o, p, bd, kIdesc);
+          else tc::mma_ts_k<true>(o, p + 8 * k, bd, kIdesc);
+        }
+        tc::mma_commit(sy.bar(C::B_O_DONE + b));
+        tc::mma_commit(sy.bar(C::B_V_EMPTY + slot));
       }
-      tc::mma_commit(sy.bar(C::B_O_DONE + tile * C::kSB + b));
-      tc::mma_commit(sy.bar(C::B_V_EMPTY + slot));
-      ++n;
-    } else {
-      tc::mbar_arrive(sy.bar(C::B_V_EMPTY + slot));
+      ++cnt[w];
+      if (!split) ++cnt[1 - w];
     }
-    w.next(a);
   }
+out:
   tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
@@ -365,11 +439,11 @@ __device__ __forceinline__ float lg2(float x) {
   return r;
 }
 
-// Dims of V whose code is NaN at a token that the row sees, in the pages that are masked by row: the output is NaN there.
+// Whether the row sees a token whose V code is NaN in this dim, in the pages that are masked by row: the output is NaN there.
 template <int D>
 __device__ __noinline__ bool sees_nan(const TreeArgs& a, const TreeSegment& s, const RowMask& mask, int dim) {
   for (int j = 0; j < s.num_pages; ++j) {
-    const int v = s.page_begin + j, local = v < s.sink_pages ? v : s.win_page + (v - s.sink_pages), p0 = local * kPage;
+    const int local = local_page(s, j), p0 = local * kPage;
     if (!by_row(a, s, p0)) continue;
     const int32_t page = a.kv_indices[s.page0 + local];
     if (!in_pool(a, page)) continue;
@@ -380,190 +454,318 @@ __device__ __noinline__ bool sees_nan(const TreeArgs& a, const TreeSegment& s, c
   return false;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (a, b) of a pair of FP32 in a 64-bit register
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int D, int NT, bool E4M3>
-__device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int tile, int row, uint32_t tbase, volatile int* nan_seen) {
+__device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, int row, uint32_t base, uint8_t* sbase, uint32_t tbase,
+                             volatile int* nan_seen) {
   using C = Cfg<D, NT>;
   const uint32_t tl = tbase + (static_cast<uint32_t>(row & ~31) << 16);   // the warp's quarter of the lanes
   const int group = a.heads / a.kv_heads;
-  auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, sy.wait(bar, parity, false, 8)); };
-  int n = 0;                                     // pages of this tile so far
+  volatile float* refs = reinterpret_cast<volatile float*>(sbase + C::OFF_REF);
+  auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, sy.wait(bar, parity, 8))); };
+  int mine = 0, others = 0, n0 = 0;              // pages of this and the other warpgroup, and of all, in the segments before
   for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
-    const int at = tile * kTreeTile + row;       // row of the block
-    if (s.rows <= tile * kTreeTile) continue;
-    const bool live = at < s.rows;
+    const bool split = is_split<NT>(s);
+    const int tile = split ? 0 : w, at = tile * kTreeTile + row;
+    const bool live = at < s.rows, idle = (at & ~31) >= s.rows;   // a warp without a row has no logits to turn
     const int t = (s.row0 + at) / group;         // drafted token and query head
     const int64_t head = static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + at) % group;
-    auto local = [&](int j) {
-      const int v = s.page_begin + j;
-      return v < s.sink_pages ? v : s.win_page + (v - s.sink_pages);
-    };
-    float m = -INFINITY, l = 0.0f, r = kNoRef;
-    // the page ids and scales of the pages to come are read ahead of their use
-    auto page_id = [&](int j) { return j < s.num_pages ? a.kv_indices[s.page0 + local(j)] : -1; };
-    int32_t id = page_id(0), next_id = page_id(1);
-    const float* scales = a.kv_scale + s.kv_head;
-    auto k_scale = [&](int32_t p) { return in_pool(a, p) ? scales[static_cast<int64_t>(p) * 2 * a.kv_heads] : 0.0f; };
-    auto v_scale = [&](int32_t p) { return in_pool(a, p) ? scales[static_cast<int64_t>(p) * 2 * a.kv_heads + a.kv_heads] : 0.0f; };
-    float sk = k_scale(id), sv = v_scale(id);
     RowMask mask;
     mask.init(a, s, live ? t : 0);
-    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it ----
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + head * D);
-    uint32_t top = 0;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. The two warpgroups
+    // of a split block convert half the dims each ----
+    float q_scale = 0.0f;
+    if (!idle) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + head * D);
+      uint32_t top = 0;
+#pragma unroll 8
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-    }
-    const int e = top == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(top >> 7));
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    const float q_scale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {         // 32 dims, 16 columns
-      uint32_t x[16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = live ? src[4 * c + i] : make_uint4(0, 0, 0, 0);
-        x[4 * i] = dev::bf16x2_to_f16x2(v.x ^ a.flip, up);
-        x[4 * i + 1] = dev::bf16x2_to_f16x2(v.y ^ a.flip, up);
-        x[4 * i + 2] = dev::bf16x2_to_f16x2(v.z ^ a.flip, up);
-        x[4 * i + 3] = dev::bf16x2_to_f16x2(v.w ^ a.flip, up);
+        for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
       }
-      __syncwarp();
-      tc::tmem_st16(tl + C::TM_Q + tile * (D / 2) + 16 * c, x);
+      const int e = top == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(top >> 7));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      q_scale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      const int c0 = split ? w * (D / 64) : 0, c1 = split ? c0 + D / 64 : D / 32;
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {            // 32 dims
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = live ? src[4 * c + i] : make_uint4(0, 0, 0, 0);
+          x[4 * i] = dev::bf16x2_to_f16x2(v.x ^ a.flip, up);
+          x[4 * i + 1] = dev::bf16x2_to_f16x2(v.y ^ a.flip, up);
+          x[4 * i + 2] = dev::bf16x2_to_f16x2(v.z ^ a.flip, up);
+          x[4 * i + 3] = dev::bf16x2_to_f16x2(v.w ^ a.flip, up);
+        }
+        __syncwarp();
+        if constexpr (C::kQSmem) {
+          const uint32_t to = base + C::OFF_Q + tile * C::kQTile + (c >> 1) * C::kQAtom;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            sts128_relaxed(to + tc::sw128_offset(row, 4 * (c & 1) + i), make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+        } else {
+          tc::tmem_st16(tl + C::TM_Q + tile * (D / 2) + 16 * c, x);
+        }
+      }
+      if constexpr (C::kQSmem) tc::fence_proxy_async_smem();
+      else tc::tmem_wait_st();
     }
-    tc::tmem_wait_st();
     tc::tc_fence_before();
-    tc::mbar_arrive(sy.bar(C::B_Q_FULL + tile));
+    tc::mbar_arrive(sy.bar(C::B_Q_FULL));
 
-    for (int j = 0; j < s.num_pages; ++j, ++n) {
-      const int p0 = local(j) * kPage, b = n % C::kSB;
-      const bool masked = by_row(a, s, p0) || !in_pool(a, id);
-      const float zs = sk * q_scale, vs = sv;
-      uint64_t seen = ~0ull;
-      if (masked) seen = in_pool(a, id) ? mask.page(a, s, p0) : 0;
-      id = next_id;
-      next_id = page_id(j + 2);
-      sk = k_scale(id);
-      sv = v_scale(id);
-      if (!wait(C::B_S_FULL + tile * C::kSB + b, (n / C::kSB) & 1)) return;
+    float m = -INFINITY, l = 0.0f, r = kNoRef;
+    for (int j = split ? w : 0; j < s.num_pages; j += split ? 2 : 1) {
+      const int k = mine + (split ? j >> 1 : j), b = C::buf(w, k);     // the page among the warpgroup's, its buffer
+      const int before = split ? others + ((j + w) >> 1) - 1 : k - 1;  // the page before among those of its warpgroup
+      if (!wait(C::B_S_FULL + b, C::phase(k))) return;
       tc::tc_fence_after();
-      const uint32_t ts = tl + C::TM_S + (tile * C::kSB + b) * kPage;
-      uint32_t x0[32], x1[32];
-      tc::tmem_ld32(ts, x0);
-      tc::tmem_ld32(ts + 32, x1);
-      tc::tmem_wait_ld();
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (masked) {
-        const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (!(s0 >> i & 1)) x0[i] = 0xff800000u;
-          if (!(s1 >> i & 1)) x1[i] = 0xff800000u;
+      if (!idle) {
+        const uint32_t ts = tl + C::TM_S + b * kPage;
+        const volatile float* info = reinterpret_cast<const volatile float*>(sbase + C::OFF_INFO + 16 * ((n0 + j) % C::kInfo));
+        const float zs = info[0] * q_scale, vs = info[1], lsv = lg2(vs);
+        const bool masked = __float_as_uint(info[2]) & kMasked;
+        // Without a reference yet that of the page before is waited for. Later pages take the one at hand, and make up for it
+        // below where that page renewed it in the meantime.
+        bool fetched = !split || j == 0;
+        if (!fetched && j < 2) {
+          if (!wait(C::B_REF + C::buf(1 - w, before), C::phase(before))) return;
+          r = refs[row];
+          fetched = true;
         }
-      }
+        float ro = r;                            // O's reference, as far as it is known
+        // against the reference at hand, in one pass, unless that proves to be too far below
+        bool plain = masked;
+        if (!plain) {
+          const float shift = r - kLift - lsv;
+          const uint64_t scale2 = pair(zs, zs), shift2 = pair(-shift, -shift);
+          uint64_t sum0 = 0, sum1 = 0;
+          float top0 = -INFINITY, top1 = -INFINITY;
+          uint32_t pk[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], fmaxf(__uint_as_float(x0[i]), __uint_as_float(x1[i])));
-      const float top_s = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // a scale of 0 makes every visible logit 0, not -inf * 0
-      const float z = top_s == -INFINITY ? -INFINITY : top_s * zs;
-      const float m_new = fmaxf(m, z);
-      const float back = m_new == -INFINITY ? 0.0f : m_new;
-      l *= dev::fast_exp2(m - back);
-      m = m_new;
-      const float c = z + lg2(vs);             // -inf where the page adds nothing to O
-      const bool renew = c > r + kSlack;
-      if (__any_sync(0xffffffffu, renew && j > 0)) {
-        // O of the pages before, once they are all in
-        if (!wait(C::B_O_DONE + tile * C::kSB + (n - 1) % C::kSB, ((n - 1) / C::kSB) & 1)) return;
-        tc::tc_fence_after();
-        const float f = renew ? dev::fast_exp2(r - c) : 1.0f;
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t o[16];
-          tc::tmem_ld16(tl + tile * D + 16 * k, o);
-          tc::tmem_wait_ld();
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[32];
+            tc::tmem_ld32(ts + 32 * h, x);
+            tc::tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tc::tmem_st16(tl + tile * D + 16 * k, o);
-        }
-      }
-      if (renew) r = c;
-      // held below 2^126: where that cuts, a weight is below 2^-70 of the largest
-      const float F = fminf(vs * dev::fast_exp2(fminf(back - r + kLift, 126.0f)), 0x1p126f);
-      float l0 = 0.0f, l1 = 0.0f;
-      uint32_t pk[16];
-      // masked places hold -inf: with a scale of 0 their product is NaN, so they are cleared by the mask
-      const float neg = zs > 0.0f ? zs : 0.0f;
-      auto half = [&](const uint32_t (&x)[32], uint32_t bits, uint32_t dst) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float p0v = dev::fast_exp2(fmaf(__uint_as_float(x[2 * i]), neg, -back));
-          float p1v = dev::fast_exp2(fmaf(__uint_as_float(x[2 * i + 1]), neg, -back));
-          if (masked) {
-            p0v = bits >> (2 * i) & 1 ? p0v : 0.0f;
-            p1v = bits >> (2 * i + 1) & 1 ? p1v : 0.0f;
+            for (int k = 0; k < 16; ++k) {
+              const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
+              if (k & 1) top1 = max3(top1, x0, x1);
+              else top0 = max3(top0, x0, x1);
+              float z0, z1;
+              unpair(fma2(pair(x0, x1), scale2, shift2), z0, z1);
+              z0 = dev::fast_exp2(z0);
+              z1 = dev::fast_exp2(z1);
+              if (k & 1) sum1 = add2(sum1, pair(z0, z1));
+              else sum0 = add2(sum0, pair(z0, z1));
+              pk[16 * h + k] = dev::pack_f16x2(z0, z1);
+            }
           }
-          l0 += p0v;
-          l1 += p1v;
-          pk[i] = dev::pack_f16x2(p0v * F, p1v * F);
+          const float z = fmaxf(top0, top1) * zs, m_new = fmaxf(m, z);
+          // log2 of what P has on 2^(z - m): moderate, and so is l's part of it
+          plain = !__all_sync(0xffffffffu, fabsf(m_new - shift) < 60.0f && r != kNoRef && !(z + lsv > r + kSlack));
+          if (!plain) {
+            float a0, a1;
+            unpair(add2(sum0, sum1), a0, a1);
+            l = fmaf(a0 + a1, dev::fast_exp2(shift - m_new), l * dev::fast_exp2(m - m_new));
+            m = m_new;
+            tc::tmem_st32<false>(ts, pk);
+          }
         }
-        tc::tmem_st16(dst, pk);
-      };
-      half(x0, static_cast<uint32_t>(seen), ts);
-      half(x1, static_cast<uint32_t>(seen >> 32), ts + 16);
-      l += l0 + l1;
+        if (plain) {
+          // the largest visible logit first
+          uint64_t bits = ~0ull;
+          if (masked) bits = __float_as_uint(info[2]) & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[16];
+            tc::tmem_ld16(ts + 16 * k, x);
+            tc::tmem_wait_ld();
+            const uint32_t v = static_cast<uint32_t>(bits >> (16 * k));
+#pragma unroll
+            for (int u = 0; u < 16; ++u) top = fmaxf(top, v >> u & 1 ? __uint_as_float(x[u]) : -INFINITY);
+          }
+          // a scale of 0 makes every visible logit 0, not -inf * 0
+          const float z = top == -INFINITY ? -INFINITY : top * zs;
+          const float m_new = fmaxf(m, z), back = m_new == -INFINITY ? 0.0f : m_new;
+          l *= dev::fast_exp2(m - back);
+          m = m_new;
+          const float c = z + lsv;                           // -inf where the page adds nothing to O
+          if (c > r + kSlack) r = c;
+          // F is held below 2^126: where that cuts, a weight is below 2^-70 of the largest
+          const float F = fminf(vs * dev::fast_exp2(fminf(back - r + kLift, 126.0f)), 0x1p126f);
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[16], pk[8];
+            tc::tmem_ld16(ts + 16 * k, x);
+            tc::tmem_wait_ld();
+            const uint32_t v = static_cast<uint32_t>(bits >> (16 * k));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              float z0 = dev::fast_exp2(fmaf(__uint_as_float(x[2 * u]), zs, -back));
+              float z1 = dev::fast_exp2(fmaf(__uint_as_float(x[2 * u + 1]), zs, -back));
+              z0 = v >> (2 * u) & 1 ? z0 : 0.0f;
+              z1 = v >> (2 * u + 1) & 1 ? z1 : 0.0f;
+              sum += z0 + z1;
+              pk[u] = dev::pack_f16x2(z0 * F, z1 * F);
+            }
+            tc::tmem_st8(ts + 8 * k, pk);
+          }
+          l += sum;
+        }
+        const float held = r;                    // P's reference
+        if (!fetched) {
+          if (!wait(C::B_REF + C::buf(1 - w, before), C::phase(before))) return;
+          ro = refs[row];
+          r = fmaxf(r, ro);
+        }
+        if (__any_sync(0xffffffffu, r != held || r != ro)) {
+          if (__any_sync(0xffffffffu, r != held)) {          // P to the reference that the page before left
+            const float f = dev::fast_exp2(held - r);
+            tc::tmem_wait_st();
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+              uint32_t x[16];
+              tc::tmem_ld16(ts + 16 * k, x);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+                x[i] = dev::pack_f16x2(y.x * f, y.y * f);
+              }
+              tc::tmem_st16(ts + 16 * k, x);
+            }
+          }
+          if (j > 0) {                                       // O to this page's, once the pages before are all in
+            if (!wait(C::B_O_DONE + C::buf(split ? 1 - w : w, before), C::phase(before))) return;
+            tc::tc_fence_after();
+            const float f = dev::fast_exp2(ro - r);
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              tc::tmem_ld16(tl + tile * D + 16 * k, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::tmem_st16(tl + tile * D + 16 * k, o);
+            }
+          }
+        }
+        if (split) refs[row] = r;
+      }
+      tc::mbar_arrive(sy.bar(C::B_REF + b));         // in unsplit blocks, too: its phases count the warpgroup's pages
+      if (!idle) tc::tmem_wait_st();
+      tc::tc_fence_before();
+      tc::mbar_arrive(sy.bar(C::B_P_FULL + b));
+    }
+    n0 += s.num_pages;
+    mine += split ? (s.num_pages + 1 - w) >> 1 : s.num_pages;
+    others += split ? (s.num_pages + w) >> 1 : s.num_pages;
+    // ---- the segment's end: O 2^(r - 6 - m) / l; nothing visible: 0 and -inf ----
+    const int last = split ? (s.num_pages - 1) & 1 : w, end = (last == w ? mine : others) - 1;
+    // the warpgroup's own last page first: after it the barrier of the other's is in its last page's phase or past it (a wait
+    // tells two phases apart, not three)
+    if (last != w && s.num_pages > 1 && !wait(C::B_O_DONE + C::buf(w, mine - 1), C::phase(mine - 1))) return;
+    if (!wait(C::B_O_DONE + C::buf(last, end), C::phase(end))) return;
+    tc::tc_fence_after();
+    const uint32_t ts = tl + C::TM_S + C::kSB * w * kPage;
+    if (split) {
+      // m and l change hands in the logits' place
+      __syncwarp();
+      tc::tmem_st2(ts, __float_as_uint(m), __float_as_uint(l));
       tc::tmem_wait_st();
       tc::tc_fence_before();
-      tc::mbar_arrive(sy.bar(C::B_P_FULL + tile * C::kSB + b));
     }
-    if (!wait(C::B_O_DONE + tile * C::kSB + (n - 1) % C::kSB, ((n - 1) / C::kSB) & 1)) return;
-    tc::tc_fence_after();
-    // ---- the segment's end: O 2^(r - 6 - m) / l; nothing visible: 0 and -inf ----
-    const bool none = m == -INFINITY && l == 0.0f;      // (l is NaN where every logit is)
-    const float lse2 = none ? -INFINITY : m + log2f(l);
-    const float f = none || r == kNoRef ? 0.0f : dev::fast_exp2(r - kLift - m) / l;
-    const bool nans = E4M3 && *nan_seen != 0 && live;
-    const int64_t slot = static_cast<int64_t>(s.partial) * (NT * kTreeTile) + at;
-#pragma unroll 1
-    for (int k = 0; k < D / 16; ++k) {
-      uint32_t o[16];
-      tc::tmem_ld16(tl + tile * D + 16 * k, o);
+    // past this every product of the segment is in: Q may be written again
+    tc::mbar_arrive(sy.bar(C::B_SEG));
+    if (!wait(C::B_SEG, (si - seg_b) & 1)) return;
+    int k0 = 0, k1 = D / 16;                     // 16 columns each
+    if (split) {
+      tc::tc_fence_after();
+      uint32_t om, ol;
+      tc::tmem_ld2(tl + C::TM_S + C::kSB * (1 - w) * kPage, om, ol);
       tc::tmem_wait_ld();
-      float y[16];
+      r = refs[row];
+      const float m0 = w == 0 ? m : __uint_as_float(om), m1 = w == 0 ? __uint_as_float(om) : m;
+      const float l0 = w == 0 ? l : __uint_as_float(ol), l1 = w == 0 ? __uint_as_float(ol) : l;
+      m = fmaxf(m0, m1);
+      const float back = m == -INFINITY ? 0.0f : m;
+      l = l0 * dev::fast_exp2(m0 - back) + l1 * dev::fast_exp2(m1 - back);
+      k0 = w * (D / 32);
+      k1 = k0 + D / 32;
+    }
+    if (!idle) {
+      const bool none = m == -INFINITY && l == 0.0f;      // (l is NaN where every logit is)
+      const float lse2 = none ? -INFINITY : m + log2f(l);
+      const float f = none || r == kNoRef ? 0.0f : dev::fast_exp2(r - kLift - m) / l;
+      const bool nans = E4M3 && *nan_seen != 0 && live;
+      const int64_t slot = static_cast<int64_t>(s.partial) * (NT * kTreeTile) + at;
+#pragma unroll 1
+      for (int k = k0; k < k1; ++k) {
+        uint32_t o[16];
+        tc::tmem_ld16(tl + tile * D + 16 * k, o);
+        tc::tmem_wait_ld();
+        float y[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = none ? 0.0f : __uint_as_float(o[i]) * f;
-      if (nans)
-        for (int i = 0; i < 16; ++i)
-          if (sees_nan<D>(a, s, mask, 16 * k + i)) y[i] = __uint_as_float(0x7FC00000u);
-      if (live) {
-        if (s.partial < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + head * D + 16 * k);
+        for (int i = 0; i < 16; ++i) y[i] = none ? 0.0f : __uint_as_float(o[i]) * f;
+        if (nans)
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-            dst[u] = make_uint4(dev::pack_bf16x2(y[8 * u], y[8 * u + 1]), dev::pack_bf16x2(y[8 * u + 2], y[8 * u + 3]),
-                                dev::pack_bf16x2(y[8 * u + 4], y[8 * u + 5]), dev::pack_bf16x2(y[8 * u + 6], y[8 * u + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 16 * k);
+          for (int i = 0; i < 16; ++i)
+            if (sees_nan<D>(a, s, mask, 16 * k + i)) y[i] = __uint_as_float(0x7FC00000u);
+        if (live) {
+          if (s.partial < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + head * D + 16 * k);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) dst[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+            for (int u = 0; u < 2; ++u)
+              dst[u] = make_uint4(dev::pack_bf16x2(y[8 * u], y[8 * u + 1]), dev::pack_bf16x2(y[8 * u + 2], y[8 * u + 3]),
+                                  dev::pack_bf16x2(y[8 * u + 4], y[8 * u + 5]), dev::pack_bf16x2(y[8 * u + 6], y[8 * u + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 16 * k);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dst[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+          }
         }
+        __syncwarp();
       }
-      __syncwarp();
+      if (live && (!split || w == 0)) {
+        if (s.partial >= 0) a.part_lse[slot] = lse2;
+        else if (a.lse) a.lse[head] = none ? -INFINITY : lse2 * 0.69314718055994531f;
+      }
     }
     tc::tc_fence_before();
-    if (live) {
-      if (s.partial >= 0) a.part_lse[slot] = lse2;
-      else if (a.lse) a.lse[head] = none ? -INFINITY : lse2 * 0.69314718055994531f;
-    }
+    tc::mbar_arrive(sy.bar(C::B_O_FREE));
   }
 }
 
 template <int D, int NT, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas) tree_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const TreeArgs a) {
   using C = Cfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
@@ -575,23 +777,34 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas) tree_
   sy.abort = reinterpret_cast<volatile int*>(sbase + C::OFF_ABORT);
   sy.status = a.status;
   volatile int* nan_seen = reinterpret_cast<volatile int*>(sbase + C::OFF_NAN);
+  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_INFO);
   if (tid == 0) {
-    for (int i = 0; i < C::kRS; ++i) { tc::mbar_init(sy.bar(C::B_RAW_FULL + i), 1); tc::mbar_init(sy.bar(C::B_RAW_EMPTY + i), C::kDQ); }
-    for (int i = 0; i < C::kKS; ++i) { tc::mbar_init(sy.bar(C::B_K_FULL + i), C::kDQ); tc::mbar_init(sy.bar(C::B_K_EMPTY + i), NT); }
-    for (int i = 0; i < C::kVS; ++i) { tc::mbar_init(sy.bar(C::B_V_FULL + i), C::kDQ); tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT); }
-    for (int i = 0; i < NT * C::kSB; ++i) {
-      tc::mbar_init(sy.bar(C::B_S_FULL + i), 1);
-      tc::mbar_init(sy.bar(C::B_P_FULL + i), kTreeTile);
-      tc::mbar_init(sy.bar(C::B_O_DONE + i), 1);
+    for (int i = 0; i < C::kRS; ++i) {
+      tc::mbar_init(sy.bar(C::B_RAW_FULL + i), i & 1 ? 1 : 2);       // K: the scales', too
+      tc::mbar_init(sy.bar(C::B_RAW_EMPTY + i), 128);
     }
-    for (int i = 0; i < NT; ++i) tc::mbar_init(sy.bar(C::B_Q_FULL + i), kTreeTile);
-    tc::mbar_init(sy.bar(C::B_FINAL), 2 * NT);      // one commit per issuing thread
+    for (int i = 0; i < C::kSlots; ++i) {
+      tc::mbar_init(sy.bar(C::B_K_FULL + i), 128);
+      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 1);
+      tc::mbar_init(sy.bar(C::B_V_FULL + i), 128);
+      tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(sy.bar(C::B_S_FULL + i), 1);
+      tc::mbar_init(sy.bar(C::B_P_FULL + i), 128);
+      tc::mbar_init(sy.bar(C::B_O_DONE + i), 1);
+      tc::mbar_init(sy.bar(C::B_REF + i), 128);
+    }
+    tc::mbar_init(sy.bar(C::B_Q_FULL), 256);
+    tc::mbar_init(sy.bar(C::B_O_FREE), 256);
+    tc::mbar_init(sy.bar(C::B_SEG), 256);
+    tc::mbar_init(sy.bar(C::B_FINAL), 1 + NT);       // one commit per issuing thread
     *sy.abort = 0;
     *nan_seen = 0;
     tc::fence_mbar_init();
   }
   if (warp == C::kQkWarp) {
-    tc::tmem_alloc(base + C::OFF_TSLOT, C::kCols);
+    tc::tmem_alloc(base + C::OFF_TSLOT, 512);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
@@ -600,23 +813,27 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, Cfg<D, NT>::kCtas) tree_
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_TSLOT);
   dev::wait_for_previous();
   dev::allow_dependents();
-  const int seg_b = a.worker_ptr[blockIdx.x], seg_e = a.worker_ptr[blockIdx.x + 1];
+  const TreeWorker work = a.workers[blockIdx.x];
 
-  if (warp < C::kSmWarps) {
-    role_softmax<D, NT, E4M3>(a, sy, seg_b, seg_e, warp / 4, tid & 127, tbase, nan_seen);
+  if (warp < C::kKWarp) {
+    role_softmax<D, NT, E4M3>(a, sy, work.begin, work.end, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
-    role_dequant<D, NT, E4M3>(a, sy, seg_b, seg_e, tid - 32 * C::kSmWarps, base, nan_seen);
+    role_convert<D, NT, E4M3>(sy, warp >= C::kVWarp, work.pages, tid & 127, base, info, nan_seen);
   } else if ((tid & 31) == 0) {
-    if (warp < C::kPvWarp) role_qk<D, NT>(a, sy, seg_b, seg_e, warp - C::kQkWarp, base, tbase);
-    else role_pv<D, NT>(a, sy, seg_b, seg_e, warp - C::kPvWarp, base, tbase);
-    sy.wait(C::B_FINAL, 0, false, 16);              // every product has completed before tensor memory is released
+    if (warp == C::kLoadWarp) {
+      role_load<D, NT>(a, sy, work.begin, work.end, base, sbase);
+    } else if (warp < C::kPvWarp + NT) {
+      if (warp == C::kQkWarp) role_qk<D, NT>(a, sy, work.begin, work.end, base, tbase);
+      else role_pv<D, NT>(a, sy, work.begin, work.end, warp - C::kPvWarp, base, tbase);
+      sy.wait(C::B_FINAL, 0, 16);             // every product has completed before tensor memory is released
+    }
   }
   __syncwarp();
   tc::tc_fence_before();
   __syncthreads();
   if (warp == C::kQkWarp) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(tbase, C::kCols);
+    tc::tmem_dealloc(tbase, 512);
   }
 }
 
