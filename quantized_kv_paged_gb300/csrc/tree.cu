@@ -15,15 +15,15 @@
 // A page is a chain (S = Q K^T, softmax, O += P V) of some 2,000 cycles at D 128; each warpgroup has two buffers of logits, so
 // that the products of its next page and of its last one run beside its softmax.
 //
-// Roles, per CTA (20 warps):
+// Roles, per CTA (20 or 21 warps):
 //   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
 //     memory (two tiles at D 128: shared memory, tensor memory is full); per page the row's 64 logits from there, the
 //     softmax, P back into their place as FP16; at the segment's end O / l.
 //   K and V conversion (a warpgroup each): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
-//   a loader thread: bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into a ring, and the blocks'
+//   a loader warp: bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into a ring, and the blocks'
 //     scales into another. (Read by the softmax a page ahead, the scales came 1,500 cycles late.)
-//   a thread issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor memory). The same tile
-//     layout is K^T's K-major operand and V's MN-major one.
+//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
+//     memory). The same tile layout is K^T's K-major operand and V's MN-major one.
 //
 // Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
 // code, and V's scales may be far apart, so O has a reference r of its own (common to the warpgroups that share O, handed
@@ -55,8 +55,8 @@ constexpr float kNoRef = -1e30f;   // reference before the first page that contr
 
 template <int D, int NT>
 struct Cfg {
-  // warps: two softmax warpgroups, K's and V's conversion, then Q.K^T, P.V of each tile, the loader
-  static constexpr int kKWarp = 8, kVWarp = 12, kQkWarp = 16, kPvWarp = 17, kLoadWarp = 19, kThreads = 640;
+  // warps: two softmax warpgroups, K's and V's conversion, then Q.K^T of each warpgroup, P.V of each tile, the loader
+  static constexpr int kKWarp = 8, kVWarp = 12, kQkWarp = 16, kPvWarp = 18, kLoadWarp = 18 + NT, kThreads = 32 * (19 + NT);
   static constexpr int kAtoms = D / 64;
   static constexpr uint32_t kRaw = kPage * D;              // bytes of a raw K or V block
   static constexpr uint32_t kAtom = kPage * 128;           // 64 tokens x 64 FP16
@@ -225,55 +225,67 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // What is known of a page beside its scales: its tokens, and whether it is masked by row.
 constexpr uint32_t kMasked = 1u << 16;
 
-// One thread: raw K and V blocks of the worker's pages into the ring, K in the even places, and the page's entry. A block of K
-// is there when its copy and the scales' are.
+// A warp: raw K and V blocks of the worker's pages into the ring, K in the even places, and the page's entry. A block of K is
+// there when its copy and the scales' are. The page ids are read 32 at a time, a batch ahead: one at a time, each cost the
+// loader its latency (44 x 32,768 tokens, 4 drafted: 804 us).
 template <int D, int NT>
-__device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, uint32_t base, uint8_t* sbase) {
+__device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int lane, uint32_t base, uint8_t* sbase) {
   using C = Cfg<D, NT>;
   const uint32_t raw = base + C::OFF_RAW;
-  int n = 0, slot = 0, round = 0;
-  bool ok = true;
-  for (int si = seg_b; si < seg_e && ok; ++si) {
+  int n = 0, slot = 0, round = 0, issued = 0;    // issued: by this lane
+  for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
-    int32_t page = a.kv_indices[s.page0 + local_page(s, 0)];
-    for (int j = 0; j < s.num_pages && ok; ++j, ++n) {
-      const int32_t next = j + 1 < s.num_pages ? a.kv_indices[s.page0 + local_page(s, j + 1)] : -1;
+    auto ids_from = [&](int j) { return j + lane < s.num_pages ? a.kv_indices[s.page0 + local_page(s, j + lane)] : -1; };
+    int32_t ids = ids_from(0), next_ids = ids_from(32);
+    for (int j = 0; j < s.num_pages; ++j, ++n) {
+      if (j > 0 && (j & 31) == 0) {
+        ids = next_ids;
+        next_ids = ids_from(j + 32);
+      }
+      const int32_t page = __shfl_sync(0xffffffffu, ids, j & 31);
       const int p0 = local_page(s, j) * kPage;
       // of a request's last page only the tokens that it has
       const int valid = in_pool(a, page) ? min(kPage, s.len - p0) : 0;
-      const int64_t block = static_cast<int64_t>(page) * 2 * a.kv_heads + s.kv_head;
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        if (round > 0 && !sy.wait(C::B_RAW_EMPTY + slot, (round - 1) & 1, 1)) { ok = false; break; }
-        const uint32_t bar = sy.bar(C::B_RAW_FULL + slot);
-        if (v == 0) {
-          const uint32_t info = C::OFF_INFO + 16 * (n % C::kInfo);
-          *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = valid | (by_row(a, s, p0) || !valid ? kMasked : 0);
+      const uint32_t info = C::OFF_INFO + 16 * (n % C::kInfo);
+      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = valid | (by_row(a, s, p0) || !valid ? kMasked : 0);
+      __syncwarp();                              // written before either lane's blocks can be seen
+      bool ok = true;
+      if (lane < 2) {                            // lane 0: K, lane 1: V
+        const int64_t block = (static_cast<int64_t>(page) * 2 + lane) * a.kv_heads + s.kv_head;
+        const uint32_t bar = sy.bar(C::B_RAW_FULL + slot + lane);
+        ok = round == 0 || sy.wait(C::B_RAW_EMPTY + slot + lane, (round - 1) & 1, 1);
+        if (ok) {
+          ++issued;
           if (valid) {
-            cp_async4(base + info, a.kv_scale + block);
-            cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
+            tc::mbar_arrive_expect_tx(bar, valid * D);
+            tc::bulk_load(raw + (slot + lane) * C::kRaw, a.kv + block * C::kRaw, valid * D, bar);
           } else {
-            *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
-            *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
+            tc::mbar_arrive(bar);
           }
-          cp_async_arrive(bar);
+          // both scales by K's lane: V's may be a block ahead, when K's barrier is still in the phase before
+          if (lane == 0) {
+            if (valid) {
+              cp_async4(base + info, a.kv_scale + block);
+              cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
+            } else {
+              *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
+              *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
+            }
+            cp_async_arrive(bar);
+          }
         }
-        if (valid) {
-          tc::mbar_arrive_expect_tx(bar, valid * D);
-          tc::bulk_load(raw + slot * C::kRaw, a.kv + (block + (v ? a.kv_heads : 0)) * C::kRaw, valid * D, bar);
-        } else {
-          tc::mbar_arrive(bar);
-        }
-        if (++slot == C::kRS) { slot = 0; ++round; }
       }
-      page = next;
+      if (!__all_sync(0xffffffffu, ok)) goto out;
+      slot += 2;
+      if (slot == C::kRS) { slot = 0; ++round; }
     }
   }
+out:
   // after a timeout: the copies in flight land before the CTA may end
   if (*sy.abort) {
     dev::cp_async_wait_all();
-    for (int k = 0; k < C::kRS; ++k)
-      if (k < slot || round > 0) tc::mbar_wait(sy.bar(C::B_RAW_FULL + k), (k < slot ? round : round - 1) & 1);
+    constexpr int kOwn = C::kRS / 2;
+    for (int k = max(0, issued - kOwn); k < issued; ++k) tc::mbar_wait(sy.bar(C::B_RAW_FULL + 2 * (k % kOwn) + lane), (k / kOwn) & 1);
   }
 }
 
@@ -346,47 +358,48 @@ __device__ void role_convert(const Sync& sy, int kind, int pages, int t, uint32_
   }
 }
 
-// One thread: S = Q K^T of every page, for both tiles of an unsplit block. cnt[w]: pages of softmax warpgroup w so far.
+// One thread a softmax warpgroup: S = Q K^T of its pages. (A thread has some 45 cycles from one product of 32 to the next; two of
+// them fill the tensor cores.)
 template <int D, int NT>
-__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, uint32_t base, uint32_t tbase) {
+__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, uint32_t base, uint32_t tbase) {
   using C = Cfg<D, NT>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
   const tc::Desc2 qd = tc::split_desc(tc::smem_desc(base + C::OFF_Q, 16, 1024, tc::kSwizzle128));
-  int n = 0, cnt[2] = {0, 0};
+  int n = 0, k = 0;                              // pages, and those of the warpgroup
   for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
     const bool split = is_split<NT>(s);
+    const int tile = split ? 0 : w;
     if (!sy.wait(C::B_Q_FULL, (si - seg_b) & 1, 4)) goto out;
     for (int j = 0; j < s.num_pages; ++j, ++n) {
       const int slot = n % C::kSlots;
       if (!sy.wait(C::B_K_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (split && (j & 1) != w) continue;
-        // the buffer's last P has been read
-        const int b = C::buf(w, cnt[w]);
-        if (cnt[w] >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(cnt[w]) ^ 1, 4)) goto out;
-        tc::tc_fence_after();
-        const int tile = split ? 0 : w;
-        const uint32_t d = tbase + C::TM_S + b * kPage;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t bd = kd.at(slot * C::kTile + (k >> 2) * C::kAtom + 32 * (k & 3));
-          if constexpr (C::kQSmem) {
-            const uint64_t ad = qd.at(tile * C::kQTile + (k >> 2) * C::kQAtom + 32 * (k & 3));
-            if (k == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
-            else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
-          } else {
-            const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * k;
-            if (k == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
-            else tc::mma_ts_k<true>(d, q, bd, kIdesc);
-          }
-        }
-        tc::mma_commit(sy.bar(C::B_S_FULL + b));
-        ++cnt[w];
+      if (split && (j & 1) != w) {
+        tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
+        continue;
       }
+      // the buffer's last P has been read
+      const int b = C::buf(w, k);
+      if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
+      tc::tc_fence_after();
+      const uint32_t d = tbase + C::TM_S + b * kPage;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
+        if constexpr (C::kQSmem) {
+          const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
+          if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
+          else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
+        } else {
+          const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
+          if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+          else tc::mma_ts_k<true>(d, q, bd, kIdesc);
+        }
+      }
+      tc::mma_commit(sy.bar(C::B_S_FULL + b));
       tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
+      ++k;
     }
   }
 out:
@@ -785,7 +798,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
     }
     for (int i = 0; i < C::kSlots; ++i) {
       tc::mbar_init(sy.bar(C::B_K_FULL + i), 128);
-      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 1);
+      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 2);
       tc::mbar_init(sy.bar(C::B_V_FULL + i), 128);
       tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT);
     }
@@ -798,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
     tc::mbar_init(sy.bar(C::B_Q_FULL), 256);
     tc::mbar_init(sy.bar(C::B_O_FREE), 256);
     tc::mbar_init(sy.bar(C::B_SEG), 256);
-    tc::mbar_init(sy.bar(C::B_FINAL), 1 + NT);       // one commit per issuing thread
+    tc::mbar_init(sy.bar(C::B_FINAL), 2 + NT);       // one commit per issuing thread
     *sy.abort = 0;
     *nan_seen = 0;
     tc::fence_mbar_init();
@@ -819,14 +832,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
     role_softmax<D, NT, E4M3>(a, sy, work.begin, work.end, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
     role_convert<D, NT, E4M3>(sy, warp >= C::kVWarp, work.pages, tid & 127, base, info, nan_seen);
+  } else if (warp == C::kLoadWarp) {
+    role_load<D, NT>(a, sy, work.begin, work.end, tid & 31, base, sbase);
   } else if ((tid & 31) == 0) {
-    if (warp == C::kLoadWarp) {
-      role_load<D, NT>(a, sy, work.begin, work.end, base, sbase);
-    } else if (warp < C::kPvWarp + NT) {
-      if (warp == C::kQkWarp) role_qk<D, NT>(a, sy, work.begin, work.end, base, tbase);
-      else role_pv<D, NT>(a, sy, work.begin, work.end, warp - C::kPvWarp, base, tbase);
-      sy.wait(C::B_FINAL, 0, 16);             // every product has completed before tensor memory is released
-    }
+    if (warp < C::kPvWarp) role_qk<D, NT>(a, sy, work.begin, work.end, warp - C::kQkWarp, base, tbase);
+    else role_pv<D, NT>(a, sy, work.begin, work.end, warp - C::kPvWarp, base, tbase);
+    sy.wait(C::B_FINAL, 0, 16);                      // every product has completed before tensor memory is released
   }
   __syncwarp();
   tc::tc_fence_before();
