@@ -15,14 +15,14 @@
 // A page is a chain (S = Q K^T, softmax, O += P V) of some 2,000 cycles at D 128; each warpgroup has two buffers of logits, so
 // that the products of its next page and of its last one run beside its softmax.
 //
-// Roles, per CTA (20 or 21 warps):
+// Roles, per CTA (20 warps):
 //   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
 //     memory (two tiles at D 128: shared memory, tensor memory is full); per page the row's 64 logits from there, the
 //     softmax, P back into their place as FP16; at the segment's end O / l.
-//   K and V conversion (a warpgroup each): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
+//   conversion (8 warps, one to four a block): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
 //   a loader warp: bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into a ring, and the blocks'
 //     scales into another. (Read by the softmax a page ahead, the scales came 1,500 cycles late.)
-//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
+//   a thread or two issue S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
 //     memory). The same tile layout is K^T's K-major operand and V's MN-major one.
 //
 // Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
@@ -52,11 +52,12 @@ using kern::sts128_relaxed;
 constexpr float kSlack = 8.0f;     // how far (log2) a contribution may pass the reference
 constexpr float kLift = 6.0f;      // P is held as 2^(... + kLift)
 constexpr float kNoRef = -1e30f;   // reference before the first page that contributes
+constexpr unsigned kFull = 0xffffffffu;
 
 template <int D, int NT>
 struct Cfg {
-  // warps: two softmax warpgroups, K's and V's conversion, then Q.K^T of each warpgroup, P.V of each tile, the loader
-  static constexpr int kKWarp = 8, kVWarp = 12, kQkWarp = 16, kPvWarp = 18, kLoadWarp = 18 + NT, kThreads = 32 * (19 + NT);
+  // warps: two softmax warpgroups, the conversion, then Q.K^T (of each warpgroup, or of both), P.V of each tile, the loader
+  static constexpr int kConvertWarp = 8, kQkWarp = 16, kQkThreads = 3 - NT, kPvWarp = kQkWarp + kQkThreads, kLoadWarp = 19, kThreads = 640;
   static constexpr int kAtoms = D / 64;
   static constexpr uint32_t kRaw = kPage * D;              // bytes of a raw K or V block
   static constexpr uint32_t kAtom = kPage * 128;           // 64 tokens x 64 FP16
@@ -64,7 +65,10 @@ struct Cfg {
   static constexpr bool kQSmem = D == 128 && NT == 2;
   static constexpr uint32_t kQAtom = kTreeTile * 128, kQTile = kAtoms * kQAtom;
   static constexpr int kSlots = D == 256 ? 2 : 4;          // pages of the K and V tiles
-  static constexpr int kRS = D == 64 ? 16 : D == 256 ? 6 : NT == 1 ? 10 : 4;   // raw blocks in the ring, an even number
+  static constexpr int kRS = D == 64 ? 16 : D == 256 ? 6 : NT == 1 ? 12 : 4;   // raw blocks in the ring
+  static constexpr int kBlockWarps = D / 64, kGroups = 8 / kBlockWarps;        // warps that convert a block, blocks at a time
+  // K blocks have the even places of the ring; a slot and a tile are always the same group's (a wait tells two phases apart)
+  static_assert(kRS % kGroups == 0 && kSlots % ((kGroups + 1) / 2) == 0 && kGroups % 2 == 0, "groups");
   // pages of the ring of scales: the loader is ahead of the softmax by the raw ring, the tiles and the logits, 15 at most
   static constexpr int kInfo = 32;
   static_assert(kRS / 2 + kSlots + 4 + 2 < kInfo, "an entry is read before it is written again");
@@ -78,7 +82,7 @@ struct Cfg {
   // shared memory
   static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kSlots * kTile, OFF_Q = OFF_V + kSlots * kTile,
                             OFF_RAW = OFF_Q + (kQSmem ? NT * kQTile : 0), OFF_REF = OFF_RAW + kRS * kRaw;
-  static constexpr uint32_t OFF_INFO = OFF_REF + 4 * kTreeTile;     // of a page: scale of K, of V, tokens and flags
+  static constexpr uint32_t OFF_QS = OFF_REF + 4 * kTreeTile, OFF_INFO = OFF_QS + 2 * kTreeTile;     // of a page: scale of K, of V, tokens and flags
   static constexpr uint32_t OFF_BAR = OFF_INFO + 16 * kInfo;
   static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_K_EMPTY = B_K_FULL + kSlots,
                             B_V_FULL = B_K_EMPTY + kSlots, B_V_EMPTY = B_V_FULL + kSlots, B_S_FULL = B_V_EMPTY + kSlots, B_P_FULL = B_S_FULL + 4,
@@ -87,7 +91,6 @@ struct Cfg {
   static constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * kBars, OFF_ABORT = OFF_TSLOT + 4, OFF_NAN = OFF_ABORT + 4;
   static constexpr uint32_t kSmem = OFF_NAN + 8 + 1024;    // slack to align the base to 1024 bytes
   static_assert(kSmem <= 232448, "shared memory");
-  static_assert(kRS % 2 == 0, "K blocks have the even places of the ring");
 };
 
 __device__ __forceinline__ TreeSegment load_segment(const TreeSegment* p) {
@@ -242,7 +245,7 @@ __device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_
         ids = next_ids;
         next_ids = ids_from(j + 32);
       }
-      const int32_t page = __shfl_sync(0xffffffffu, ids, j & 31);
+      const int32_t page = __shfl_sync(kFull, ids, j & 31);
       const int p0 = local_page(s, j) * kPage;
       // of a request's last page only the tokens that it has
       const int valid = in_pool(a, page) ? min(kPage, s.len - p0) : 0;
@@ -275,7 +278,7 @@ __device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_
           }
         }
       }
-      if (!__all_sync(0xffffffffu, ok)) goto out;
+      if (!__all_sync(kFull, ok)) goto out;
       slot += 2;
       if (slot == C::kRS) { slot = 0; ++round; }
     }
@@ -289,117 +292,122 @@ out:
   }
 }
 
-// A warpgroup: raw blocks of K (kind 0) or V (kind 1) to the FP16 tiles of a step. An item is 16 codes. Eight lanes take rows 2 p
-// and 2 p + 1, 64 dims each, of atoms that differ: their reads and their writes fall into distinct banks. K rows past a page's
-// tokens keep what is there (their logits are masked); V rows become zeros.
+// kBlockWarps warps: raw blocks to the FP16 tiles, every kGroups-th block, so that the latencies of one block (wait, read,
+// convert, write, fence) hide behind the others'. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms
+// that differ: their reads and their writes fall into distinct banks. K rows past a page's tokens keep what is there (their
+// logits are masked); V rows become zeros.
 template <int D, int NT, bool E4M3>
-__device__ void role_convert(const Sync& sy, int kind, int pages, int t, uint32_t base, volatile uint32_t* info, volatile int* nan_seen) {
+__device__ void role_convert(const Sync& sy, int warp, int pages, int lane, uint32_t base, volatile uint32_t* info, volatile int* nan_seen) {
   using C = Cfg<D, NT>;
-  constexpr int kItems = C::kRaw / 16 / 128;
-  const int warp = t >> 5, lane = t & 31, c = lane & 3;
-  const int row0 = D == 64 ? t >> 2 : 16 * warp + 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
-  constexpr int kRowStep = D == 64 ? 32 : 8, kRowItems = D == 64 ? 1 : C::kAtoms;       // items of a row, rows from one to the next
-  const uint32_t raw = base + C::OFF_RAW, tiles = base + (kind == 0 ? C::OFF_K : C::OFF_V);
+  constexpr int kGroups = C::kGroups, kSets = 8 / C::kBlockWarps;        // sets of 8 rows that a warp has of a block
+  constexpr int kSetItems = D == 64 ? 1 : C::kAtoms, kBatchSets = 4 / kSetItems, kItems = kBatchSets * kSetItems;
+  const int group = warp / C::kBlockWarps, kind = group & 1, c = lane & 3;
+  const int sub = D == 64 ? lane >> 2 : 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
+  const int row0 = warp % C::kBlockWarps * 8 * kSets + sub;
   const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, empty = kind == 0 ? C::B_K_EMPTY : C::B_V_EMPTY;
-  const uint32_t read0 = raw + row0 * D + 16 * c;
-  const uint32_t write0 = (row0 >> 3) * 1024 + (row0 & 7) * 128 + (((2 * c) ^ (row0 & 7)) << 4), write1 = write0 ^ 16;
-  int slot = kind, parity = 0;
-  for (int n = 0; n < pages; ++n) {
+  const uint32_t read0 = base + C::OFF_RAW + row0 * D + 16 * c;
+  const uint32_t write0 = base + (kind == 0 ? C::OFF_K : C::OFF_V) + (row0 >> 3) * 1024 + sub * 128 + (((2 * c) ^ sub) << 4), write1 = write0 ^ 16;
+  int slot = group, parity = 0;
+  for (int n = group >> 1; n < pages; n += kGroups / 2) {
     const int ts = n % C::kSlots;
-    if (!sy.wait(C::B_RAW_FULL + slot, parity, 2)) return;
-    const uint32_t entry = info[4 * (n % C::kInfo) + 2];
+    if (!__all_sync(kFull, sy.wait(C::B_RAW_FULL + slot, parity, 2))) return;
+    const uint32_t entry = info[4 * (n % C::kInfo) + 2], from = read0 + slot * C::kRaw, to = ts * C::kTile;
     const int valid = static_cast<int>(entry & 0xFFFF);
-    uint4 w[kItems];
-    if (valid) {
-      const uint32_t from = read0 + slot * C::kRaw;
+    const bool waited = n < C::kSlots || sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2);
+    if (!__all_sync(kFull, waited)) return;
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        const int r = i / kRowItems * kRowStep, atom = i % kRowItems;
-        w[i] = lds128(from + r * D + ((atom ^ odd) << 6));
+    for (int b = 0; b < kSets; b += kBatchSets) {
+      uint4 w[kItems];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) w[i] = lds128(from + (b + i / kSetItems) * 8 * D + (((i % kSetItems) ^ odd) << 6));
+      if (b + kBatchSets >= kSets) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
       }
-    }
-    tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
-    slot += 2;
-    if (slot >= C::kRS) { slot = kind; parity ^= 1; }
-    if (kind == 1 && valid < kPage) {
+      if (kind == 1 && valid < kPage) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i)
-        if (row0 + i / kRowItems * kRowStep >= valid) w[i] = make_uint4(0, 0, 0, 0);
-    }
-    if (E4M3 && kind == 1 && (entry & kMasked)) {
+        for (int i = 0; i < kItems; ++i)
+          if (row0 + 8 * (b + i / kSetItems) >= valid) w[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (E4M3 && kind == 1 && (entry & kMasked)) {
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
+        for (int i = 0; i < kItems; ++i) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(&w[i]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t bad = nan_bytes(x[k]);
-          if (bad) {
-            x[k] &= ~(bad * 0xFFu);
-            *nan_seen = 1;
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = nan_bytes(x[k]);
+            if (bad) {
+              x[k] &= ~(bad * 0xFFu);
+              *nan_seen = 1;
+            }
           }
         }
       }
-    }
-    if (n >= C::kSlots && !sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2)) return;
-    const uint32_t to = tiles + ts * C::kTile;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const uint32_t at = to + i / kRowItems * kRowStep * 128 + ((i % kRowItems) ^ odd) * C::kAtom;
-      uint32_t o[8];
-      codes_to_f16<E4M3>(w[i].x, o[0], o[1]);
-      codes_to_f16<E4M3>(w[i].y, o[2], o[3]);
-      codes_to_f16<E4M3>(w[i].z, o[4], o[5]);
-      codes_to_f16<E4M3>(w[i].w, o[6], o[7]);
-      sts128_relaxed(at + write0, make_uint4(o[0], o[1], o[2], o[3]));
-      sts128_relaxed(at + write1, make_uint4(o[4], o[5], o[6], o[7]));
+      for (int i = 0; i < kItems; ++i) {
+        const uint32_t at = to + (b + i / kSetItems) * 1024 + ((i % kSetItems) ^ odd) * C::kAtom;
+        uint32_t o[8];
+        codes_to_f16<E4M3>(w[i].x, o[0], o[1]);
+        codes_to_f16<E4M3>(w[i].y, o[2], o[3]);
+        codes_to_f16<E4M3>(w[i].z, o[4], o[5]);
+        codes_to_f16<E4M3>(w[i].w, o[6], o[7]);
+        sts128_relaxed(write0 + at, make_uint4(o[0], o[1], o[2], o[3]));
+        sts128_relaxed(write1 + at, make_uint4(o[4], o[5], o[6], o[7]));
+      }
     }
     tc::fence_proxy_async_smem();
-    tc::mbar_arrive(sy.bar(full + ts));
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(sy.bar(full + ts));
+    for (slot += kGroups; slot >= C::kRS; slot -= C::kRS) parity ^= 1;
   }
 }
 
-// One thread a softmax warpgroup: S = Q K^T of its pages. (A thread has some 45 cycles from one product of 32 to the next; two of
-// them fill the tensor cores.)
+// S = Q K^T, by one thread or (blocks of one tile only) by two, one for each softmax warpgroup. A thread has some 45 cycles from one
+// product of 32 to the next, so two of them fill the tensor cores; with Q in shared memory a product takes 48 anyway, and a
+// 21st warp would cost every thread 16 registers.
 template <int D, int NT>
-__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, uint32_t base, uint32_t tbase) {
+__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int thread, uint32_t base, uint32_t tbase) {
   using C = Cfg<D, NT>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
   const tc::Desc2 qd = tc::split_desc(tc::smem_desc(base + C::OFF_Q, 16, 1024, tc::kSwizzle128));
-  int n = 0, k = 0;                              // pages, and those of the warpgroup
+  int n = 0, cnt0 = 0, cnt1 = 0;                 // pages, and those of either warpgroup
   for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
     const bool split = is_split<NT>(s);
-    const int tile = split ? 0 : w;
     if (!sy.wait(C::B_Q_FULL, (si - seg_b) & 1, 4)) goto out;
     for (int j = 0; j < s.num_pages; ++j, ++n) {
       const int slot = n % C::kSlots;
       if (!sy.wait(C::B_K_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
-      if (split && (j & 1) != w) {
-        tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
-        continue;
-      }
-      // the buffer's last P has been read
-      const int b = C::buf(w, k);
-      if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
-      tc::tc_fence_after();
-      const uint32_t d = tbase + C::TM_S + b * kPage;
+      bool any = false;
+#pragma unroll 1
+      for (int w = split ? j & 1 : 0; w < (split ? (j & 1) + 1 : 2); ++w) {
+        if (C::kQkThreads == 2 && w != thread) continue;
+        // the buffer's last P has been read
+        const int k = w == 0 ? cnt0 : cnt1, b = C::buf(w, k);
+        if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
+        tc::tc_fence_after();
+        const int tile = split ? 0 : w;
+        const uint32_t d = tbase + C::TM_S + b * kPage;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
-        if constexpr (C::kQSmem) {
-          const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
-          if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
-          else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
-        } else {
-          const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
-          if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
-          else tc::mma_ts_k<true>(d, q, bd, kIdesc);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
+          if constexpr (C::kQSmem) {
+            const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
+            if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
+            else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
+          } else {
+            const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
+            if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+            else tc::mma_ts_k<true>(d, q, bd, kIdesc);
+          }
         }
+        tc::mma_commit(sy.bar(C::B_S_FULL + b));
+        if (w == 0) ++cnt0; else ++cnt1;
+        any = true;
       }
-      tc::mma_commit(sy.bar(C::B_S_FULL + b));
-      tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
-      ++k;
+      if (any) tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
+      else tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
     }
   }
 out:
@@ -467,6 +475,10 @@ __device__ __noinline__ bool sees_nan(const TreeArgs& a, const TreeSegment& s, c
   return false;
 }
 
+__device__ __forceinline__ int64_t shfl64(int64_t x, int from) {
+  return __shfl_sync(kFull, static_cast<long long>(x), from);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -495,9 +507,14 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
                              volatile int* nan_seen) {
   using C = Cfg<D, NT>;
   const uint32_t tl = tbase + (static_cast<uint32_t>(row & ~31) << 16);   // the warp's quarter of the lanes
-  const int group = a.heads / a.kv_heads;
+  const int group = a.heads / a.kv_heads, lane = row & 31;
   volatile float* refs = reinterpret_cast<volatile float*>(sbase + C::OFF_REF);
-  auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xffffffffu, sy.wait(bar, parity, 8))); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, sy.wait(bar, parity, 8))); };
+  // a warp's arrival, after what all its lanes did
+  auto arrive = [&](uint32_t bar) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(sy.bar(bar));
+  };
   int mine = 0, others = 0, n0 = 0;              // pages of this and the other warpgroup, and of all, in the segments before
   for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
@@ -505,53 +522,81 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
     const int tile = split ? 0 : w, at = tile * kTreeTile + row;
     const bool live = at < s.rows, idle = (at & ~31) >= s.rows;   // a warp without a row has no logits to turn
     const int t = (s.row0 + at) / group;         // drafted token and query head
-    const int64_t head = static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + at) % group;
+    // the row among those of q, out and lse; -1: none
+    const int64_t head = live ? static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + at) % group : -1;
+    volatile int8_t* lifts = reinterpret_cast<volatile int8_t*>(sbase + C::OFF_QS) + tile * kTreeTile;   // e of the rows
     RowMask mask;
     mask.init(a, s, live ? t : 0);
-    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. The two warpgroups
-    // of a split block convert half the dims each ----
-    float q_scale = 0.0f;
+    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. A warp takes 16 rows
+    // at a time, four lanes a row, so that its loads are of whole sectors (a row a thread, Q and the output took 12 of a
+    // segment's 15 us); the two warpgroups of a split block take 16 rows of each 32 ----
     if (!idle) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + head * D);
-      uint32_t top = 0;
-#pragma unroll 8
-      for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
-      }
-      const int e = top == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(top >> 7));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      q_scale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      const int c0 = split ? w * (D / 64) : 0, c1 = split ? c0 + D / 64 : D / 32;
 #pragma unroll 1
-      for (int c = c0; c < c1; ++c) {            // 32 dims
-        uint32_t x[16];
+      for (int h = split ? w : 0; h < (split ? w + 1 : 2); ++h) {
+        const int64_t top_head = shfl64(head, 16 * h + (lane >> 2)), low_head = shfl64(head, 16 * h + 8 + (lane >> 2));
+        const uint2* top = reinterpret_cast<const uint2*>(a.q + top_head * D) + (lane & 3);
+        const uint2* low = reinterpret_cast<const uint2*>(a.q + low_head * D) + (lane & 3);
+        uint2 x[2][D / 16];
+        uint32_t amax[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = live ? src[4 * c + i] : make_uint4(0, 0, 0, 0);
-          x[4 * i] = dev::bf16x2_to_f16x2(v.x ^ a.flip, up);
-          x[4 * i + 1] = dev::bf16x2_to_f16x2(v.y ^ a.flip, up);
-          x[4 * i + 2] = dev::bf16x2_to_f16x2(v.z ^ a.flip, up);
-          x[4 * i + 3] = dev::bf16x2_to_f16x2(v.w ^ a.flip, up);
+        for (int i = 0; i < D / 16; ++i) {
+          x[0][i] = top_head >= 0 ? top[4 * i] : make_uint2(0, 0);
+          x[1][i] = low_head >= 0 ? low[4 * i] : make_uint2(0, 0);
         }
-        __syncwarp();
-        if constexpr (C::kQSmem) {
-          const uint32_t to = base + C::OFF_Q + tile * C::kQTile + (c >> 1) * C::kQAtom;
+        float up[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sts128_relaxed(to + tc::sw128_offset(row, 4 * (c & 1) + i), make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
-        } else {
-          tc::tmem_st16(tl + C::TM_Q + tile * (D / 2) + 16 * c, x);
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) amax[k] = __vmaxu2(amax[k], __vmaxu2(x[k][i].x & 0x7FFF7FFFu, x[k][i].y & 0x7FFF7FFFu));
+          amax[k] = max(amax[k] & 0xFFFFu, amax[k] >> 16);
+          amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 1));
+          amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 2));
+          const int e = amax[k] == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(amax[k] >> 7));
+          up[k] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          if ((lane & 3) == 0) lifts[(row & ~31) + 16 * h + 8 * k + (lane >> 2)] = static_cast<int8_t>(e);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {       // 64 dims
+          uint32_t y[16];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              y[4 * u + 2 * k] = dev::bf16x2_to_f16x2(x[k][4 * i + u].x ^ a.flip, up[k]);
+              y[4 * u + 2 * k + 1] = dev::bf16x2_to_f16x2(x[k][4 * i + u].y ^ a.flip, up[k]);
+            }
+          if constexpr (C::kQSmem) {
+            const uint32_t to = base + C::OFF_Q + tile * C::kQTile + i * C::kQAtom;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t at8 = to + tc::sw128_offset((row & ~31) + 16 * h + 8 * k + (lane >> 2), 2 * u + ((lane & 3) >> 1)) + 8 * (lane & 1);
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(at8), "r"(y[4 * u + 2 * k]), "r"(y[4 * u + 2 * k + 1]));
+              }
+          } else {
+            tc::tmem_st_rows16(tl + ((16 * h) << 16) + C::TM_Q + tile * (D / 2) + 32 * i, y);
+          }
         }
       }
       if constexpr (C::kQSmem) tc::fence_proxy_async_smem();
       else tc::tmem_wait_st();
     }
     tc::tc_fence_before();
-    tc::mbar_arrive(sy.bar(C::B_Q_FULL));
-
+    arrive(C::B_Q_FULL);
+    // the next segment's Q on its way into L2
+    if (si + 1 < seg_e) {
+      const TreeSegment* nx = a.segs + si + 1;
+      const int to = (is_split<NT>(*nx) ? 0 : tile * kTreeTile) + row, rows = nx->rows, first = nx->row0 + to;
+      if (to < rows) {
+        const uint16_t* p = a.q + (static_cast<int64_t>(nx->tok0 + first / group) * a.heads + nx->kv_head * group + first % group) * D;
+#pragma unroll
+        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+      }
+    }
+    // the rows' factors are there when all of Q is
+    if (!wait(C::B_Q_FULL, (si - seg_b) & 1)) return;
+    const float q_scale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - lifts[row]) << 23);
     float m = -INFINITY, l = 0.0f, r = kNoRef;
     for (int j = split ? w : 0; j < s.num_pages; j += split ? 2 : 1) {
       const int k = mine + (split ? j >> 1 : j), b = C::buf(w, k);     // the page among the warpgroup's, its buffer
@@ -601,7 +646,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
           }
           const float z = fmaxf(top0, top1) * zs, m_new = fmaxf(m, z);
           // log2 of what P has on 2^(z - m): moderate, and so is l's part of it
-          plain = !__all_sync(0xffffffffu, fabsf(m_new - shift) < 60.0f && r != kNoRef && !(z + lsv > r + kSlack));
+          plain = !__all_sync(kFull, fabsf(m_new - shift) < 60.0f && r != kNoRef && !(z + lsv > r + kSlack));
           if (!plain) {
             float a0, a1;
             unpair(add2(sum0, sum1), a0, a1);
@@ -659,8 +704,8 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
           ro = refs[row];
           r = fmaxf(r, ro);
         }
-        if (__any_sync(0xffffffffu, r != held || r != ro)) {
-          if (__any_sync(0xffffffffu, r != held)) {          // P to the reference that the page before left
+        if (__any_sync(kFull, r != held || r != ro)) {
+          if (__any_sync(kFull, r != held)) {          // P to the reference that the page before left
             const float f = dev::fast_exp2(held - r);
             tc::tmem_wait_st();
 #pragma unroll 1
@@ -693,10 +738,10 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
         }
         if (split) refs[row] = r;
       }
-      tc::mbar_arrive(sy.bar(C::B_REF + b));         // in unsplit blocks, too: its phases count the warpgroup's pages
+      arrive(C::B_REF + b);         // in unsplit blocks, too: its phases count the warpgroup's pages
       if (!idle) tc::tmem_wait_st();
       tc::tc_fence_before();
-      tc::mbar_arrive(sy.bar(C::B_P_FULL + b));
+      arrive(C::B_P_FULL + b);
     }
     n0 += s.num_pages;
     mine += split ? (s.num_pages + 1 - w) >> 1 : s.num_pages;
@@ -717,7 +762,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
       tc::tc_fence_before();
     }
     // past this every product of the segment is in: Q may be written again
-    tc::mbar_arrive(sy.bar(C::B_SEG));
+    arrive(C::B_SEG);
     if (!wait(C::B_SEG, (si - seg_b) & 1)) return;
     int k0 = 0, k1 = D / 16;                     // 16 columns each
     if (split) {
@@ -738,42 +783,81 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
       const bool none = m == -INFINITY && l == 0.0f;      // (l is NaN where every logit is)
       const float lse2 = none ? -INFINITY : m + log2f(l);
       const float f = none || r == kNoRef ? 0.0f : dev::fast_exp2(r - kLift - m) / l;
-      const bool nans = E4M3 && *nan_seen != 0 && live;
-      const int64_t slot = static_cast<int64_t>(s.partial) * (NT * kTreeTile) + at;
+      const bool nans = E4M3 && *nan_seen != 0;
+      const int64_t slot = s.partial;
+      if (s.partial >= 0 || nans) {
+        // a row a thread; partials lie as [slot][4 columns][row], so that a warp writes 512 bytes in a row
 #pragma unroll 1
-      for (int k = k0; k < k1; ++k) {
-        uint32_t o[16];
-        tc::tmem_ld16(tl + tile * D + 16 * k, o);
-        tc::tmem_wait_ld();
-        float y[16];
+        for (int k = k0; k < k1; ++k) {
+          uint32_t o[16];
+          tc::tmem_ld16(tl + tile * D + 16 * k, o);
+          tc::tmem_wait_ld();
+          float y[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = none ? 0.0f : __uint_as_float(o[i]) * f;
-        if (nans)
+          for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(o[i]) * f;
+          if (nans && live)
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+              if (sees_nan<D>(a, s, mask, 16 * k + i))
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (sees_nan<D>(a, s, mask, 16 * k + i)) y[i] = __uint_as_float(0x7FC00000u);
-        if (live) {
-          if (s.partial < 0) {
+                for (int u = 0; u < 16; ++u)
+                  if (u == i) y[u] = __uint_as_float(0x7FC00000u);
+          if (s.partial >= 0) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + 4 * k) * (NT * kTreeTile) + at;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dst[u * (NT * kTreeTile)] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+          } else if (live) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + head * D + 16 * k);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
               dst[u] = make_uint4(dev::pack_bf16x2(y[8 * u], y[8 * u + 1]), dev::pack_bf16x2(y[8 * u + 2], y[8 * u + 3]),
                                   dev::pack_bf16x2(y[8 * u + 4], y[8 * u + 5]), dev::pack_bf16x2(y[8 * u + 6], y[8 * u + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + 16 * k);
+          }
+          __syncwarp();
+        }
+      } else {
+        // 16 rows at a time, four lanes a row, 8 columns a lane after a 4 x 4 transpose
+#pragma unroll 1
+        for (int h = split ? w : 0; h < (split ? w + 1 : 2); ++h) {
+          const int64_t top_head = shfl64(head, 16 * h + (lane >> 2)), low_head = shfl64(head, 16 * h + 8 + (lane >> 2));
+          const float ft = __shfl_sync(kFull, f, 16 * h + (lane >> 2)), fl = __shfl_sync(kFull, f, 16 * h + 8 + (lane >> 2));
+#pragma unroll 1
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t o[16];
+            tc::tmem_ld_rows16(tl + ((16 * h) << 16) + tile * D + 32 * k, o);
+            tc::tmem_wait_ld();
+            uint32_t y[2][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) dst[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+            for (int u = 0; u < 4; ++u) {
+              y[0][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u]) * ft, __uint_as_float(o[4 * u + 1]) * ft);
+              y[1][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u + 2]) * fl, __uint_as_float(o[4 * u + 3]) * fl);
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              uint32_t* x = y[v];
+#pragma unroll
+              for (int u = 0; u < 4; u += 2) {
+                const uint32_t z = __shfl_xor_sync(kFull, lane & 1 ? x[u] : x[u + 1], 1);
+                if (lane & 1) x[u] = z; else x[u + 1] = z;
+              }
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t z = __shfl_xor_sync(kFull, lane & 2 ? x[u] : x[u + 2], 2);
+                if (lane & 2) x[u] = z; else x[u + 2] = z;
+              }
+              const int64_t to = v == 0 ? top_head : low_head;
+              if (to >= 0) *reinterpret_cast<uint4*>(a.out + to * D + 32 * k + 8 * (lane & 3)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
           }
         }
-        __syncwarp();
       }
       if (live && (!split || w == 0)) {
-        if (s.partial >= 0) a.part_lse[slot] = lse2;
+        if (s.partial >= 0) a.part_lse[slot * (NT * kTreeTile) + at] = lse2;
         else if (a.lse) a.lse[head] = none ? -INFINITY : lse2 * 0.69314718055994531f;
       }
     }
     tc::tc_fence_before();
-    tc::mbar_arrive(sy.bar(C::B_O_FREE));
+    arrive(C::B_O_FREE);
   }
 }
 
@@ -794,24 +878,24 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   if (tid == 0) {
     for (int i = 0; i < C::kRS; ++i) {
       tc::mbar_init(sy.bar(C::B_RAW_FULL + i), i & 1 ? 1 : 2);       // K: the scales', too
-      tc::mbar_init(sy.bar(C::B_RAW_EMPTY + i), 128);
+      tc::mbar_init(sy.bar(C::B_RAW_EMPTY + i), C::kBlockWarps);
     }
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(sy.bar(C::B_K_FULL + i), 128);
-      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 2);
-      tc::mbar_init(sy.bar(C::B_V_FULL + i), 128);
+      tc::mbar_init(sy.bar(C::B_K_FULL + i), C::kBlockWarps);
+      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), C::kQkThreads);
+      tc::mbar_init(sy.bar(C::B_V_FULL + i), C::kBlockWarps);
       tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT);
     }
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(sy.bar(C::B_S_FULL + i), 1);
-      tc::mbar_init(sy.bar(C::B_P_FULL + i), 128);
+      tc::mbar_init(sy.bar(C::B_P_FULL + i), 4);        // one arrival a warp
       tc::mbar_init(sy.bar(C::B_O_DONE + i), 1);
-      tc::mbar_init(sy.bar(C::B_REF + i), 128);
+      tc::mbar_init(sy.bar(C::B_REF + i), 4);
     }
-    tc::mbar_init(sy.bar(C::B_Q_FULL), 256);
-    tc::mbar_init(sy.bar(C::B_O_FREE), 256);
-    tc::mbar_init(sy.bar(C::B_SEG), 256);
-    tc::mbar_init(sy.bar(C::B_FINAL), 2 + NT);       // one commit per issuing thread
+    tc::mbar_init(sy.bar(C::B_Q_FULL), 8);
+    tc::mbar_init(sy.bar(C::B_O_FREE), 8);
+    tc::mbar_init(sy.bar(C::B_SEG), 8);
+    tc::mbar_init(sy.bar(C::B_FINAL), C::kQkThreads + NT);       // one commit per issuing thread
     *sy.abort = 0;
     *nan_seen = 0;
     tc::fence_mbar_init();
@@ -828,10 +912,10 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   dev::allow_dependents();
   const TreeWorker work = a.workers[blockIdx.x];
 
-  if (warp < C::kKWarp) {
+  if (warp < C::kConvertWarp) {
     role_softmax<D, NT, E4M3>(a, sy, work.begin, work.end, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
-    role_convert<D, NT, E4M3>(sy, warp >= C::kVWarp, work.pages, tid & 127, base, info, nan_seen);
+    role_convert<D, NT, E4M3>(sy, warp - C::kConvertWarp, work.pages, tid & 31, base, info, nan_seen);
   } else if (warp == C::kLoadWarp) {
     role_load<D, NT>(a, sy, work.begin, work.end, tid & 31, base, sbase);
   } else if ((tid & 31) == 0) {
@@ -848,70 +932,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   }
 }
 
-// Joins the partials of blocks that were cut: WARPS warps of a CTA share a row's partials, each takes every WARPS-th one, and
-// their sums are added in order. Grid: (rows of a block / rows of a CTA, joins).
+// Joins the partials of blocks that were cut. A lane has a row, a warp 8 columns of 32 rows, so that all reads are of whole
+// lines; the slots are summed in order. Grid: (32 rows of a block, 64 columns, joins).
 constexpr int kJoinThreads = 256;
-template <int D, int WARPS>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs a) {
-  constexpr int kRows = kJoinThreads / 32 / WARPS, V = D / 32;
-  __shared__ float sums[kJoinThreads / 32][D + 1];
   dev::wait_for_previous();
   dev::allow_dependents();
-  const TreeJoin* jp = a.joins + blockIdx.y;
-  const int first = jp->first, count = jp->count, rows = jp->rows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, member = warp % WARPS;
-  const int row = blockIdx.x * kRows + warp / WARPS;
-  const int pitch = a.tiles * kTreeTile;
-  if (static_cast<int>(blockIdx.x) * kRows >= rows) return;
-  const bool live = row < rows;
+  const TreeJoin* jp = a.joins + blockIdx.z;
+  const int first = jp->first, count = jp->count, rows = jp->rows, pitch = a.tiles * kTreeTile;
+  const int row = blockIdx.x * 32 + (threadIdx.x & 31), c8 = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
   const float* lse = a.part_lse + static_cast<int64_t>(first) * pitch + row;
-  float m = -INFINITY, total = 0.0f, acc[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  if (live) {
-    for (int i = lane; i < count; i += 32) m = fmaxf(m, lse[static_cast<int64_t>(i) * pitch]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float back = m == -INFINITY ? 0.0f : m;
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < count; ++i) m = fmaxf(m, lse[static_cast<int64_t>(i) * pitch]);
+  const float back = m == -INFINITY ? 0.0f : m;
+  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (static_cast<int64_t>(first) * (D / 4) + 2 * c8) * pitch + row;
+  float total = 0.0f, acc[8] = {};
 #pragma unroll 4
-    for (int i = member; i < count; i += WARPS) {
-      const float w = dev::fast_exp2(lse[static_cast<int64_t>(i) * pitch] - back);
-      const float* src = a.part_o + (static_cast<int64_t>(first + i) * pitch + row) * D + lane * V;
-      float x[V];
-      if constexpr (V == 2) *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
-      else
+  for (int i = 0; i < count; ++i) {
+    const float w = dev::fast_exp2(lse[static_cast<int64_t>(i) * pitch] - back);
+    const float4 x = src[static_cast<int64_t>(i) * (D / 4) * pitch], y = src[static_cast<int64_t>(i) * (D / 4) * pitch + pitch];
+    total += w;
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(x + v) = *reinterpret_cast<const float4*>(src + v);
-      total += w;
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] = fmaf(w, x[v], acc[v]);
-    }
+    for (int u = 0; u < 8; ++u) acc[u] = fmaf(w, v[u], acc[u]);
   }
-  if constexpr (WARPS > 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) sums[warp][lane * V + v] = acc[v];
-    if (lane == 0) sums[warp][D] = total;
-    __syncthreads();
-    if (member != 0) return;
-#pragma unroll 1
-    for (int w = 1; w < WARPS; ++w) {
-      total += sums[warp + w][D];
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += sums[warp + w][lane * V + v];
-    }
-  }
-  if (!live) return;
   const int group = a.heads / a.kv_heads, at = jp->row0 + row;
   const int64_t head = static_cast<int64_t>(jp->tok0 + at / group) * a.heads + jp->kv_head * group + at % group;
-  const float inv = m == -INFINITY ? 0.0f : 1.0f / total;
-  uint32_t o[V / 2];
-#pragma unroll
-  for (int v = 0; v < V; v += 2) o[v / 2] = dev::pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
-  uint16_t* dst = a.out + head * D + lane * V;
-  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(dst) = o[0];
-  else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-  else *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-  if (lane == 0 && a.lse) a.lse[head] = m == -INFINITY ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
+  // l is NaN where every logit was; no visible token: 0 and -inf
+  const bool none = m == -INFINITY && total == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / total;
+  *reinterpret_cast<uint4*>(a.out + head * D + 8 * c8) =
+      make_uint4(dev::pack_bf16x2(acc[0] * inv, acc[1] * inv), dev::pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                 dev::pack_bf16x2(acc[4] * inv, acc[5] * inv), dev::pack_bf16x2(acc[6] * inv, acc[7] * inv));
+  if (c8 == 0 && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
 template <int D, int NT, bool E4M3>
@@ -933,11 +989,8 @@ cudaError_t launch_dim(const TreeArgs& a, cudaStream_t s) {
     else e = e4m3 ? launch_attend<D, 2, true>(a, s) : launch_attend<D, 2, false>(a, s);
   }
   if (e != cudaSuccess || a.num_joins == 0) return e;
-  const int rows = a.tiles * kTreeTile;
-  const bool wide = a.max_join > 16;
-  const int per = kJoinThreads / 32 / (wide ? 8 : 1);
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), static_cast<unsigned>(a.num_joins));
+  c.gridDim = dim3(static_cast<unsigned>(a.tiles * kTreeTile / 32), D / 64, static_cast<unsigned>(a.num_joins));
   c.blockDim = dim3(kJoinThreads);
   c.stream = s;
   cudaLaunchAttribute attr{};
@@ -945,7 +998,7 @@ cudaError_t launch_dim(const TreeArgs& a, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &attr;
   c.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&c, tree_join_kernel<D, 8>, a) : cudaLaunchKernelEx(&c, tree_join_kernel<D, 1>, a);
+  return cudaLaunchKernelEx(&c, tree_join_kernel<D>, a);
 }
 
 }  // namespace
