@@ -19,10 +19,10 @@
 //   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
 //     memory (two tiles at D 128: shared memory, tensor memory is full); per page the row's 64 logits from there, the
 //     softmax, P back into their place as FP16; at the segment's end O / l.
-//   conversion (8 warps, one to four a block): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
-//   a loader warp: bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into a ring, and the blocks'
-//     scales into another. (Read by the softmax a page ahead, the scales came 1,500 cycles late.)
-//   a thread or two issue S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
+//   conversion (8 warps, one to four a block): bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into
+//     a ring, and the pages' scales into another (read by the softmax a page ahead, they came 1,500 cycles late); raw blocks
+//     to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
+//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
 //     memory). The same tile layout is K^T's K-major operand and V's MN-major one.
 //
 // Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
@@ -56,8 +56,8 @@ constexpr unsigned kFull = 0xffffffffu;
 
 template <int D, int NT>
 struct Cfg {
-  // warps: two softmax warpgroups, the conversion, then Q.K^T (of each warpgroup, or of both), P.V of each tile, the loader
-  static constexpr int kConvertWarp = 8, kQkWarp = 16, kQkThreads = 3 - NT, kPvWarp = kQkWarp + kQkThreads, kLoadWarp = 19, kThreads = 640;
+  // warps: two softmax warpgroups, the conversion, then Q.K^T of each softmax warpgroup and P.V of each tile
+  static constexpr int kConvertWarp = 8, kQkWarp = 16, kPvWarp = 18, kThreads = 640;
   static constexpr int kAtoms = D / 64;
   static constexpr uint32_t kRaw = kPage * D;              // bytes of a raw K or V block
   static constexpr uint32_t kAtom = kPage * 128;           // 64 tokens x 64 FP16
@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int kBlockWarps = D / 64, kGroups = 8 / kBlockWarps;        // warps that convert a block, blocks at a time
   // K blocks have the even places of the ring; a slot and a tile are always the same group's (a wait tells two phases apart)
   static_assert(kRS % kGroups == 0 && kSlots % ((kGroups + 1) / 2) == 0 && kGroups % 2 == 0, "groups");
-  // pages of the ring of scales: the loader is ahead of the softmax by the raw ring, the tiles and the logits, 15 at most
+  // pages of the ring of scales: the copies are ahead of the softmax by the raw ring, the tiles and the logits, 15 at most
   static constexpr int kInfo = 32;
   static_assert(kRS / 2 + kSlots + 4 + 2 < kInfo, "an entry is read before it is written again");
   // tensor memory columns: O, two buffers of logits for each warpgroup (D 256: one, there is no room), Q
@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kSlots * kTile, OFF_Q = OFF_V + kSlots * kTile,
                             OFF_RAW = OFF_Q + (kQSmem ? NT * kQTile : 0), OFF_REF = OFF_RAW + kRS * kRaw;
   static constexpr uint32_t OFF_QS = OFF_REF + 4 * kTreeTile, OFF_INFO = OFF_QS + 2 * kTreeTile;     // of a page: scale of K, of V, tokens and flags
-  static constexpr uint32_t OFF_BAR = OFF_INFO + 16 * kInfo;
+  static constexpr uint32_t OFF_META = OFF_INFO + 16 * kInfo, OFF_BAR = (OFF_META + 4 * kRS + 7) / 8 * 8;
   static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_K_EMPTY = B_K_FULL + kSlots,
                             B_V_FULL = B_K_EMPTY + kSlots, B_V_EMPTY = B_V_FULL + kSlots, B_S_FULL = B_V_EMPTY + kSlots, B_P_FULL = B_S_FULL + 4,
                             B_O_DONE = B_P_FULL + 4, B_REF = B_O_DONE + 4, B_Q_FULL = B_REF + 4, B_O_FREE = B_Q_FULL + 1, B_SEG = B_O_FREE + 1,
@@ -228,93 +228,97 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // What is known of a page beside its scales: its tokens, and whether it is masked by row.
 constexpr uint32_t kMasked = 1u << 16;
 
-// A warp: raw K and V blocks of the worker's pages into the ring, K in the even places, and the page's entry. A block of K is
-// there when its copy and the scales' are. The page ids are read 32 at a time, a batch ahead: one at a time, each cost the
-// loader its latency (44 x 32,768 tokens, 4 drafted: 804 us).
-template <int D, int NT>
-__device__ void role_load(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int lane, uint32_t base, uint8_t* sbase) {
-  using C = Cfg<D, NT>;
-  const uint32_t raw = base + C::OFF_RAW;
-  int n = 0, slot = 0, round = 0, issued = 0;    // issued: by this lane
-  for (int si = seg_b; si < seg_e; ++si) {
-    const TreeSegment s = load_segment(a.segs + si);
-    auto ids_from = [&](int j) { return j + lane < s.num_pages ? a.kv_indices[s.page0 + local_page(s, j + lane)] : -1; };
-    int32_t ids = ids_from(0), next_ids = ids_from(32);
-    for (int j = 0; j < s.num_pages; ++j, ++n) {
-      if (j > 0 && (j & 31) == 0) {
-        ids = next_ids;
-        next_ids = ids_from(j + 32);
-      }
-      const int32_t page = __shfl_sync(kFull, ids, j & 31);
-      const int p0 = local_page(s, j) * kPage;
-      // of a request's last page only the tokens that it has
-      const int valid = in_pool(a, page) ? min(kPage, s.len - p0) : 0;
-      const uint32_t info = C::OFF_INFO + 16 * (n % C::kInfo);
-      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = valid | (by_row(a, s, p0) || !valid ? kMasked : 0);
-      __syncwarp();                              // written before either lane's blocks can be seen
-      bool ok = true;
-      if (lane < 2) {                            // lane 0: K, lane 1: V
-        const int64_t block = (static_cast<int64_t>(page) * 2 + lane) * a.kv_heads + s.kv_head;
-        const uint32_t bar = sy.bar(C::B_RAW_FULL + slot + lane);
-        ok = round == 0 || sy.wait(C::B_RAW_EMPTY + slot + lane, (round - 1) & 1, 1);
-        if (ok) {
-          ++issued;
-          if (valid) {
-            tc::mbar_arrive_expect_tx(bar, valid * D);
-            tc::bulk_load(raw + (slot + lane) * C::kRaw, a.kv + block * C::kRaw, valid * D, bar);
-          } else {
-            tc::mbar_arrive(bar);
-          }
-          // both scales by K's lane: V's may be a block ahead, when K's barrier is still in the phase before
-          if (lane == 0) {
-            if (valid) {
-              cp_async4(base + info, a.kv_scale + block);
-              cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
-            } else {
-              *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
-              *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
-            }
-            cp_async_arrive(bar);
-          }
-        }
-      }
-      if (!__all_sync(kFull, ok)) goto out;
-      slot += 2;
-      if (slot == C::kRS) { slot = 0; ++round; }
+// Walks the pages of a worker that one group converts, ahead of their use; the id of the page it stands on is read when it gets
+// there, one block before it is needed.
+struct Feed {
+  const TreeArgs& a;
+  int si, se, j, n;                              // n: the page among the worker's
+  int32_t page;
+  TreeSegment s;
+  __device__ Feed(const TreeArgs& args, int b, int e, int first) : a(args), si(b), se(e), j(first), n(first), page(-1) {
+    if (si < se) s = load_segment(a.segs + si);
+    settle();
+  }
+  __device__ bool done() const { return si >= se; }
+  __device__ void settle() {
+    while (si < se && j >= s.num_pages) {
+      j -= s.num_pages;
+      if (++si < se) s = load_segment(a.segs + si);
     }
+    if (si < se) page = a.kv_indices[s.page0 + local_page(s, j)];
   }
-out:
-  // after a timeout: the copies in flight land before the CTA may end
-  if (*sy.abort) {
-    dev::cp_async_wait_all();
-    constexpr int kOwn = C::kRS / 2;
-    for (int k = max(0, issued - kOwn); k < issued; ++k) tc::mbar_wait(sy.bar(C::B_RAW_FULL + 2 * (k % kOwn) + lane), (k / kOwn) & 1);
+  __device__ void next(int by) {
+    j += by;
+    n += by;
+    settle();
   }
-}
+};
 
 // kBlockWarps warps: raw blocks to the FP16 tiles, every kGroups-th block, so that the latencies of one block (wait, read,
-// convert, write, fence) hide behind the others'. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms
-// that differ: their reads and their writes fall into distinct banks. K rows past a page's tokens keep what is there (their
-// logits are masked); V rows become zeros.
+// convert, write, fence) hide behind the others'. A group also fills its own slots of the ring again, by bulk copies: a loader of
+// its own, be it a warp, took 1,200 cycles a page (44 x 32,768 tokens, 4 drafted: 663 us). K's groups bring the page's scales
+// along. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms that differ: their reads and their writes
+// fall into distinct banks. K rows past a page's tokens keep what is there (their logits are masked); V rows become zeros.
 template <int D, int NT, bool E4M3>
-__device__ void role_convert(const Sync& sy, int warp, int pages, int lane, uint32_t base, volatile uint32_t* info, volatile int* nan_seen) {
+__device__ void role_convert(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int warp, int lane, uint32_t base, uint8_t* sbase,
+                             volatile int* nan_seen) {
   using C = Cfg<D, NT>;
   constexpr int kGroups = C::kGroups, kSets = 8 / C::kBlockWarps;        // sets of 8 rows that a warp has of a block
   constexpr int kSetItems = D == 64 ? 1 : C::kAtoms, kBatchSets = 4 / kSetItems, kItems = kBatchSets * kSetItems;
+  constexpr int kOwn = C::kRS / kGroups;                                 // the group's slots of the ring
   const int group = warp / C::kBlockWarps, kind = group & 1, c = lane & 3;
+  const bool lead = warp % C::kBlockWarps == 0;
   const int sub = D == 64 ? lane >> 2 : 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
   const int row0 = warp % C::kBlockWarps * 8 * kSets + sub;
   const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, empty = kind == 0 ? C::B_K_EMPTY : C::B_V_EMPTY;
   const uint32_t read0 = base + C::OFF_RAW + row0 * D + 16 * c;
   const uint32_t write0 = base + (kind == 0 ? C::OFF_K : C::OFF_V) + (row0 >> 3) * 1024 + sub * 128 + (((2 * c) ^ sub) << 4), write1 = write0 ^ 16;
-  int slot = group, parity = 0;
-  for (int n = group >> 1; n < pages; n += kGroups / 2) {
-    const int ts = n % C::kSlots;
-    if (!__all_sync(kFull, sy.wait(C::B_RAW_FULL + slot, parity, 2))) return;
-    const uint32_t entry = info[4 * (n % C::kInfo) + 2], from = read0 + slot * C::kRaw, to = ts * C::kTile;
+  volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_META);
+  Feed feed(a, work.begin, work.end, group >> 1);
+  int issued = 0;
+  // lead, one lane: the block that the feed stands on into the group's next slot, whose last block has been read
+  auto issue = [&]() {
+    const int slot = group + kGroups * (issued % kOwn), p0 = local_page(feed.s, feed.j) * kPage;
+    // of a request's last page only the tokens that it has
+    const int valid = in_pool(a, feed.page) ? min(kPage, feed.s.len - p0) : 0;
+    const uint32_t entry = valid | (by_row(a, feed.s, p0) || !valid ? kMasked : 0), bar = sy.bar(C::B_RAW_FULL + slot);
+    const int64_t block = (static_cast<int64_t>(feed.page) * 2 + kind) * a.kv_heads + feed.s.kv_head;
+    meta[slot] = entry;
+    if (valid) {
+      tc::mbar_arrive_expect_tx(bar, valid * D);
+      tc::bulk_load(base + C::OFF_RAW + slot * C::kRaw, a.kv + block * C::kRaw, valid * D, bar);
+    } else {
+      tc::mbar_arrive(bar);
+    }
+    if (kind == 0) {
+      const uint32_t info = C::OFF_INFO + 16 * (feed.n % C::kInfo);
+      *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = entry;
+      if (valid) {
+        cp_async4(base + info, a.kv_scale + block);
+        cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
+      } else {
+        *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
+        *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
+      }
+      cp_async_arrive(bar);
+    }
+  };
+  if (lead) {
+#pragma unroll 1
+    for (; issued < kOwn && !feed.done(); ++issued) {
+      if (lane == 0) issue();
+      feed.next(kGroups / 2);
+    }
+  }
+  int own = 0, parity = 0;                       // the slot among the group's
+  for (int n = group >> 1; n < work.pages; n += kGroups / 2) {
+    const int ts = n % C::kSlots, slot = group + kGroups * own;
+    bool ok = sy.wait(C::B_RAW_FULL + slot, parity, 2);
+    if (!__all_sync(kFull, ok)) break;
+    const uint32_t entry = meta[slot], from = read0 + slot * C::kRaw, to = ts * C::kTile;
     const int valid = static_cast<int>(entry & 0xFFFF);
-    const bool waited = n < C::kSlots || sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2);
-    if (!__all_sync(kFull, waited)) return;
+    ok = n < C::kSlots || sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2);
+    if (!__all_sync(kFull, ok)) break;
 #pragma unroll
     for (int b = 0; b < kSets; b += kBatchSets) {
       uint4 w[kItems];
@@ -322,7 +326,7 @@ __device__ void role_convert(const Sync& sy, int warp, int pages, int lane, uint
       for (int i = 0; i < kItems; ++i) w[i] = lds128(from + (b + i / kSetItems) * 8 * D + (((i % kSetItems) ^ odd) << 6));
       if (b + kBatchSets >= kSets) {
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
+        if (C::kBlockWarps > 1 && lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
       }
       if (kind == 1 && valid < kPage) {
 #pragma unroll
@@ -358,56 +362,66 @@ __device__ void role_convert(const Sync& sy, int warp, int pages, int lane, uint
     tc::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(sy.bar(full + ts));
-    for (slot += kGroups; slot >= C::kRS; slot -= C::kRS) parity ^= 1;
+    if (lead && !feed.done()) {
+      if (lane == 0) {
+        ok = C::kBlockWarps == 1 || sy.wait(C::B_RAW_EMPTY + slot, parity, 1);
+        if (ok) issue();
+      }
+      if (!__all_sync(kFull, ok)) break;
+      ++issued;
+      feed.next(kGroups / 2);
+    }
+    if (++own == kOwn) { own = 0; parity ^= 1; }
+  }
+  // after a timeout: the copies in flight land before the CTA may end
+  if (*sy.abort && lead && lane == 0) {
+    dev::cp_async_wait_all();
+    for (int k = max(0, issued - kOwn); k < issued; ++k) tc::mbar_wait(sy.bar(C::B_RAW_FULL + group + kGroups * (k % kOwn)), (k / kOwn) & 1);
   }
 }
 
-// S = Q K^T, by one thread or (blocks of one tile only) by two, one for each softmax warpgroup. A thread has some 45 cycles from one
-// product of 32 to the next, so two of them fill the tensor cores; with Q in shared memory a product takes 48 anyway, and a
-// 21st warp would cost every thread 16 registers.
+// One thread a softmax warpgroup: S = Q K^T of its pages. (A thread has some 45 cycles from one product of 32 to the next; two of
+// them fill the tensor cores.)
 template <int D, int NT>
-__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int thread, uint32_t base, uint32_t tbase) {
+__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, uint32_t base, uint32_t tbase) {
   using C = Cfg<D, NT>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
   const tc::Desc2 qd = tc::split_desc(tc::smem_desc(base + C::OFF_Q, 16, 1024, tc::kSwizzle128));
-  int n = 0, cnt0 = 0, cnt1 = 0;                 // pages, and those of either warpgroup
+  int n = 0, k = 0;                              // pages, and those of the warpgroup
   for (int si = seg_b; si < seg_e; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
     const bool split = is_split<NT>(s);
+    const int tile = split ? 0 : w;
     if (!sy.wait(C::B_Q_FULL, (si - seg_b) & 1, 4)) goto out;
     for (int j = 0; j < s.num_pages; ++j, ++n) {
       const int slot = n % C::kSlots;
       if (!sy.wait(C::B_K_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
-      bool any = false;
-#pragma unroll 1
-      for (int w = split ? j & 1 : 0; w < (split ? (j & 1) + 1 : 2); ++w) {
-        if (C::kQkThreads == 2 && w != thread) continue;
-        // the buffer's last P has been read
-        const int k = w == 0 ? cnt0 : cnt1, b = C::buf(w, k);
-        if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
-        tc::tc_fence_after();
-        const int tile = split ? 0 : w;
-        const uint32_t d = tbase + C::TM_S + b * kPage;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
-          if constexpr (C::kQSmem) {
-            const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
-            if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
-            else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
-          } else {
-            const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
-            if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
-            else tc::mma_ts_k<true>(d, q, bd, kIdesc);
-          }
-        }
-        tc::mma_commit(sy.bar(C::B_S_FULL + b));
-        if (w == 0) ++cnt0; else ++cnt1;
-        any = true;
+      if (split && (j & 1) != w) {
+        tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
+        continue;
       }
-      if (any) tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
-      else tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
+      // the buffer's last P has been read
+      const int b = C::buf(w, k);
+      if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
+      tc::tc_fence_after();
+      const uint32_t d = tbase + C::TM_S + b * kPage;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
+        if constexpr (C::kQSmem) {
+          const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
+          if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
+          else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
+        } else {
+          const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
+          if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+          else tc::mma_ts_k<true>(d, q, bd, kIdesc);
+        }
+      }
+      tc::mma_commit(sy.bar(C::B_S_FULL + b));
+      tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
+      ++k;
     }
   }
 out:
@@ -874,7 +888,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   sy.abort = reinterpret_cast<volatile int*>(sbase + C::OFF_ABORT);
   sy.status = a.status;
   volatile int* nan_seen = reinterpret_cast<volatile int*>(sbase + C::OFF_NAN);
-  volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_INFO);
   if (tid == 0) {
     for (int i = 0; i < C::kRS; ++i) {
       tc::mbar_init(sy.bar(C::B_RAW_FULL + i), i & 1 ? 1 : 2);       // K: the scales', too
@@ -882,7 +895,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
     }
     for (int i = 0; i < C::kSlots; ++i) {
       tc::mbar_init(sy.bar(C::B_K_FULL + i), C::kBlockWarps);
-      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), C::kQkThreads);
+      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 2);
       tc::mbar_init(sy.bar(C::B_V_FULL + i), C::kBlockWarps);
       tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT);
     }
@@ -895,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
     tc::mbar_init(sy.bar(C::B_Q_FULL), 8);
     tc::mbar_init(sy.bar(C::B_O_FREE), 8);
     tc::mbar_init(sy.bar(C::B_SEG), 8);
-    tc::mbar_init(sy.bar(C::B_FINAL), C::kQkThreads + NT);       // one commit per issuing thread
+    tc::mbar_init(sy.bar(C::B_FINAL), 2 + NT);       // one commit per issuing thread
     *sy.abort = 0;
     *nan_seen = 0;
     tc::fence_mbar_init();
@@ -915,10 +928,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   if (warp < C::kConvertWarp) {
     role_softmax<D, NT, E4M3>(a, sy, work.begin, work.end, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
-    role_convert<D, NT, E4M3>(sy, warp - C::kConvertWarp, work.pages, tid & 31, base, info, nan_seen);
-  } else if (warp == C::kLoadWarp) {
-    role_load<D, NT>(a, sy, work.begin, work.end, tid & 31, base, sbase);
-  } else if ((tid & 31) == 0) {
+    role_convert<D, NT, E4M3>(a, sy, work, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
+  } else if ((tid & 31) == 0 && warp < C::kPvWarp + NT) {
     if (warp < C::kPvWarp) role_qk<D, NT>(a, sy, work.begin, work.end, warp - C::kQkWarp, base, tbase);
     else role_pv<D, NT>(a, sy, work.begin, work.end, warp - C::kPvWarp, base, tbase);
     sy.wait(C::B_FINAL, 0, 16);                      // every product has completed before tensor memory is released
