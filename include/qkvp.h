@@ -507,15 +507,13 @@ typedef struct {
   int32_t window, sinks;       /* as given; window 0: every cached token is visible */
   int32_t num_tokens;          /* drafted tokens of the batch */
   int32_t max_drafted;         /* most drafted tokens of a request */
-  int32_t row_tiles;           /* tiles of 128 rows that share a pass over the pages: 1 or 2 */
   int32_t num_workers;         /* CTAs of the attention kernel */
-  int32_t num_segments;        /* (request, KV head, row block, page range) pieces */
+  int32_t num_segments;        /* (request, KV head, block of 128 query rows, page range) pieces */
   int32_t num_joins;           /* row blocks cut into more than one segment */
   int32_t max_join_segments;   /* most segments of one row block */
   int32_t num_partials;        /* FP32 split partials held in the workspace */
   int32_t max_worker_pages, min_worker_pages;
   int32_t table_entries;       /* entries of kv_indices that the plan may address: kv_indptr[batch] */
-  int32_t reserved;
   int64_t total_pages;         /* pages read, summed over requests (of one KV head and row block) */
   uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;
   uint64_t status_offset;      /* int32 status word, as in qkvp_plan */

@@ -1,7 +1,7 @@
 // C entry points of speculative decoding over a head pool: attention of drafted tokens (plan and run), and the commit of the
 // accepted ones.
 //
-// The plan reuses the split-KV planner: each (request, KV head, block of 128 or 256 query rows) is a row of pages to it,
+// The plan reuses the split-KV planner: each (request, KV head, block of 128 query rows) is a row of pages to it,
 // the visible ones only.
 #include <algorithm>
 #include <climits>
@@ -54,7 +54,7 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   }
   if (num_sms > 65536) return QKVP_E_INVALID;
   const int group = num_heads / num_kv_heads;
-  const int tiles = head_dim == 256 || max_drafted * group <= kTreeTile ? 1 : 2, block = tiles * kTreeTile;
+  constexpr int block = kTreeTile;
 
   // one row of visible pages per (request, KV head, block of query rows)
   std::vector<Visible> vis(batch);
@@ -107,7 +107,6 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   plan->sinks = sinks;
   plan->num_tokens = batch > 0 ? tok_indptr_host[batch] : 0;
   plan->max_drafted = max_drafted;
-  plan->row_tiles = tiles;
   plan->num_workers = workers;
   plan->num_segments = static_cast<int32_t>(info.num_segments);
   plan->num_joins = info.split_reqs;
@@ -224,7 +223,6 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
   a.words = mask_words;
   a.window = plan->window;
   a.sinks = plan->sinks;
-  a.tiles = plan->row_tiles;
   a.num_workers = plan->num_workers;
   a.num_joins = plan->num_joins;
   a.max_join = plan->max_join_segments;

@@ -235,7 +235,7 @@ inline GqaTable gqa_table(int64_t segments, int64_t workers, int64_t counters) {
 }
 
 // One piece of the pages that one block of query rows of a tree attention sees. Row i of a (request, KV head) is drafted
-// token i / G, query head kv_head * G + i % G; a block holds up to 128 or 256 consecutive rows. Page v of the request's
+// token i / G, query head kv_head * G + i % G; a block holds up to 128 consecutive rows. Page v of the request's
 // visible ones is page v of its list below sink_pages, and page win_page + (v - sink_pages) from there on.
 struct TreeSegment {
   int32_t kv_head, row0, rows;    // rows [row0, row0 + rows) of the KV head
@@ -256,7 +256,7 @@ struct TreeJoin {
 static_assert(sizeof(TreeJoin) == 32, "join layout");
 
 constexpr uint64_t kTreeMagic = 0x716b76702d747265ull;
-constexpr int kTreeTile = 128;         // rows of a matrix product: the lanes of tensor memory
+constexpr int kTreeTile = 128;         // rows of a block: the lanes of tensor memory
 constexpr int kTreeMaxDrafted = 256;   // drafted tokens of a request
 struct TreeWorker {
   int32_t begin, end;             // its segments
@@ -275,12 +275,11 @@ struct TreeArgs {
   const TreeWorker* workers;  // [num_workers]
   const TreeJoin* joins;
   int* status;
-  float* part_o;              // [num_partials][128 tiles][D], normalised
-  float* part_lse;            // [num_partials][128 tiles], log2 domain
+  float* part_o;              // [num_partials][D / 4][128][4], normalised
+  float* part_lse;            // [num_partials][128], log2 domain
   uint16_t* out;              // bf16 [n][H][D]
   float* lse;                 // [n][H] or null
   int heads, kv_heads, dim, cache_dtype, words, window, sinks;
-  int tiles;                  // row tiles of a block: 1 or 2
   int num_workers, num_joins, max_join;
   float scale_log2;           // |sm_scale| log2(e)
   uint32_t flip;              // 0x80008000 where sm_scale is negative: turns Q's signs

@@ -7,23 +7,23 @@
 // A page's 64 tokens of one KV head are 128 D bytes and 256 D T G operations (T drafted tokens, G query heads a KV head):
 // reading bounds it up to T G ~ 140 rows, the matrix products above.
 //
-// Work. A (request, KV head) has T G rows, cut into blocks of up to 128 or (where there are more) 256, two tiles of 128 lanes of
-// tensor memory. A worker (a CTA, one per SM) walks segments, each a run of the pages that a block sees, page by page.
-// Two softmax warpgroups work at a time:
-//   - a block of two tiles: one for each tile, every page (unsplit);
-//   - a block of one tile: in turns, one page each, into one O (split).
-// A page is a chain (S = Q K^T, softmax, O += P V) of some 2,000 cycles at D 128; each warpgroup has two buffers of logits, so
-// that the products of its next page and of its last one run beside its softmax.
+// Work. A (request, KV head) has T G rows, cut into blocks of up to 128, the lanes of tensor memory. A worker (a CTA, one per SM)
+// walks segments, each a run of the pages that a block sees, page by page: S = Q K^T, softmax, O += P V, a chain of some 2,500
+// cycles at D 128. Two softmax warpgroups take the pages in turns, with two buffers of logits each (D 256: one), so four
+// pages are on their way at a time. (Blocks of 256 rows, a warpgroup for each half and the pages converted once for both, took
+// 2,100 cycles a page: Q of the second half does not fit in tensor memory, and from shared memory its products wait on
+// operand reads.)
 //
-// Roles, per CTA (20 warps):
+// Roles, per CTA (20 warps); page n of the worker has buffer, K tile and V tile n % kBufs:
 //   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
-//     memory (two tiles at D 128: shared memory, tensor memory is full); per page the row's 64 logits from there, the
-//     softmax, P back into their place as FP16; at the segment's end O / l.
-//   conversion (8 warps, one to four a block): bulk copies of raw K and V blocks (64 D bytes each, contiguous in the pool) into
-//     a ring, and the pages' scales into another (read by the softmax a page ahead, they came 1,500 cycles late); raw blocks
-//     to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
-//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64), one for each tile O += P V (M 128, N D; P from tensor
-//     memory). The same tile layout is K^T's K-major operand and V's MN-major one.
+//     memory; per page the row's 64 logits from there, the softmax, P back into their place as FP16; at the segment's end O / l.
+//   loader (a warp, one lane for each slot of the ring): bulk copies of raw K and V blocks (64 D bytes each, contiguous in the
+//     pool), and the pages' scales into another ring (read by the softmax a page ahead, they came 1,500 cycles late).
+//   conversion (8 warps, one to four a block): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
+//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64; Q from tensor memory), one O += P V (M 128, N D; P from
+//     tensor memory). The same tile layout is K^T's K-major operand and V's MN-major one.
+// A commit of Q K^T says that the logits are there and that the K tile is free, one of P V that O is and the V tile and the
+// buffer are free.
 //
 // Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
 // code, and V's scales may be far apart, so O has a reference r of its own (common to the warpgroups that share O, handed
@@ -54,43 +54,36 @@ constexpr float kLift = 6.0f;      // P is held as 2^(... + kLift)
 constexpr float kNoRef = -1e30f;   // reference before the first page that contributes
 constexpr unsigned kFull = 0xffffffffu;
 
-template <int D, int NT>
+template <int D>
 struct Cfg {
-  // warps: two softmax warpgroups, the conversion, then Q.K^T of each softmax warpgroup and P.V of each tile
-  static constexpr int kConvertWarp = 8, kQkWarp = 16, kPvWarp = 18, kThreads = 640;
+  static constexpr int kConvertWarp = 8, kQkWarp = 16, kPvWarp = 18, kLoadWarp = 19, kThreads = 640;
   static constexpr int kAtoms = D / 64;
   static constexpr uint32_t kRaw = kPage * D;              // bytes of a raw K or V block
   static constexpr uint32_t kAtom = kPage * 128;           // 64 tokens x 64 FP16
   static constexpr uint32_t kTile = kAtoms * kAtom;        // a converted block
-  static constexpr bool kQSmem = D == 128 && NT == 2;
-  static constexpr uint32_t kQAtom = kTreeTile * 128, kQTile = kAtoms * kQAtom;
-  static constexpr int kSlots = D == 256 ? 2 : 4;          // pages of the K and V tiles
-  static constexpr int kRS = D == 64 ? 16 : D == 256 ? 6 : NT == 1 ? 12 : 4;   // raw blocks in the ring
+  static constexpr int kBufs = D == 256 ? 2 : 4;           // pages on their way: K tiles, V tiles, buffers of logits
+  static constexpr int kRS = D == 64 ? 16 : D == 128 ? 12 : 6;                 // raw blocks in the ring, K in the even places
   static constexpr int kBlockWarps = D / 64, kGroups = 8 / kBlockWarps;        // warps that convert a block, blocks at a time
-  // K blocks have the even places of the ring; a slot and a tile are always the same group's (a wait tells two phases apart)
-  static_assert(kRS % kGroups == 0 && kSlots % ((kGroups + 1) / 2) == 0 && kGroups % 2 == 0, "groups");
-  // pages of the ring of scales: the copies are ahead of the softmax by the raw ring, the tiles and the logits, 15 at most
+  // a slot and a tile are always the same group's (a wait tells two phases apart, not three)
+  static_assert(kRS % kGroups == 0 && kBufs % ((kGroups + 1) / 2) == 0 && kGroups % 2 == 0 && kRS <= 32, "groups");
+  // pages of the ring of scales: the copies are ahead of the softmax by the raw ring and the tiles
   static constexpr int kInfo = 32;
-  static_assert(kRS / 2 + kSlots + 4 + 2 < kInfo, "an entry is read before it is written again");
-  // tensor memory columns: O, two buffers of logits for each warpgroup (D 256: one, there is no room), Q
-  static constexpr int kSB = D == 256 ? 1 : 2;
-  static constexpr uint32_t TM_S = NT * D, TM_Q = TM_S + 2 * kSB * kPage;
-  // of the k-th page of a warpgroup: its buffer, and the parity of the buffer's phases
-  __device__ static int buf(int w, int k) { return kSB * w + (k & (kSB - 1)); }
-  __device__ static uint32_t phase(int k) { return (k >> (kSB - 1)) & 1; }
-  static_assert(TM_Q + (kQSmem ? 0 : NT * D / 2) <= 512, "tensor memory");
+  static_assert(kRS / 2 + 2 * kBufs + 2 < kInfo, "an entry is read before it is written again");
+  // tensor memory columns: O, logits, Q
+  static constexpr uint32_t TM_S = D, TM_Q = TM_S + kBufs * kPage;
+  static_assert(TM_Q + D / 2 <= 512, "tensor memory");
   // shared memory
-  static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kSlots * kTile, OFF_Q = OFF_V + kSlots * kTile,
-                            OFF_RAW = OFF_Q + (kQSmem ? NT * kQTile : 0), OFF_REF = OFF_RAW + kRS * kRaw;
-  static constexpr uint32_t OFF_QS = OFF_REF + 4 * kTreeTile, OFF_INFO = OFF_QS + 2 * kTreeTile;     // of a page: scale of K, of V, tokens and flags
+  static constexpr uint32_t OFF_K = 0, OFF_V = OFF_K + kBufs * kTile, OFF_RAW = OFF_V + kBufs * kTile, OFF_REF = OFF_RAW + kRS * kRaw;
+  static constexpr uint32_t OFF_QS = OFF_REF + 4 * kTreeTile, OFF_INFO = OFF_QS + kTreeTile;     // of a page: scale of K, of V, tokens and flags
   static constexpr uint32_t OFF_META = OFF_INFO + 16 * kInfo, OFF_BAR = (OFF_META + 4 * kRS + 7) / 8 * 8;
-  static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_K_EMPTY = B_K_FULL + kSlots,
-                            B_V_FULL = B_K_EMPTY + kSlots, B_V_EMPTY = B_V_FULL + kSlots, B_S_FULL = B_V_EMPTY + kSlots, B_P_FULL = B_S_FULL + 4,
-                            B_O_DONE = B_P_FULL + 4, B_REF = B_O_DONE + 4, B_Q_FULL = B_REF + 4, B_O_FREE = B_Q_FULL + 1, B_SEG = B_O_FREE + 1,
-                            B_FINAL = B_SEG + 1, kBars = B_FINAL + 1;
+  static constexpr uint32_t B_RAW_FULL = 0, B_RAW_EMPTY = B_RAW_FULL + kRS, B_K_FULL = B_RAW_EMPTY + kRS, B_V_FULL = B_K_FULL + kBufs,
+                            B_S_FULL = B_V_FULL + kBufs, B_P_FULL = B_S_FULL + kBufs, B_O_DONE = B_P_FULL + kBufs, B_REF = B_O_DONE + kBufs,
+                            B_Q_FULL = B_REF + kBufs, B_O_FREE = B_Q_FULL + 1, B_SEG = B_O_FREE + 1, B_FINAL = B_SEG + 1, kBars = B_FINAL + 1;
   static constexpr uint32_t OFF_TSLOT = OFF_BAR + 8 * kBars, OFF_ABORT = OFF_TSLOT + 4, OFF_NAN = OFF_ABORT + 4;
   static constexpr uint32_t kSmem = OFF_NAN + 8 + 1024;    // slack to align the base to 1024 bytes
   static_assert(kSmem <= 232448, "shared memory");
+  __device__ static int buf(int n) { return n & (kBufs - 1); }
+  __device__ static uint32_t phase(int n) { return (n / kBufs) & 1; }
 };
 
 __device__ __forceinline__ TreeSegment load_segment(const TreeSegment* p) {
@@ -141,10 +134,6 @@ __device__ __forceinline__ int local_page(const TreeSegment& s, int j) {
   const int v = s.page_begin + j;
   return v < s.sink_pages ? v : s.win_page + (v - s.sink_pages);
 }
-
-// Whether a block is one tile, whose pages the two softmax warpgroups take in turns.
-template <int NT>
-__device__ __forceinline__ bool is_split(const TreeSegment& s) { return NT == 1 || s.rows <= kTreeTile; }
 
 __device__ __forceinline__ bool in_pool(const TreeArgs& a, int32_t page) { return page >= 0 && page < a.num_pages; }
 
@@ -228,110 +217,133 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // What is known of a page beside its scales: its tokens, and whether it is masked by row.
 constexpr uint32_t kMasked = 1u << 16;
 
-// Walks the pages of a worker that one group converts, ahead of their use; the id of the page it stands on is read when it gets
-// there, one block before it is needed.
-struct Feed {
-  const TreeArgs& a;
-  int si, se, j, n;                              // n: the page among the worker's
-  int32_t page;
-  TreeSegment s;
-  __device__ Feed(const TreeArgs& args, int b, int e, int first) : a(args), si(b), se(e), j(first), n(first), page(-1) {
-    if (si < se) s = load_segment(a.segs + si);
-    settle();
-  }
-  __device__ bool done() const { return si >= se; }
-  __device__ void settle() {
-    while (si < se && j >= s.num_pages) {
+// Not blocking: whether the phase of `parity` has completed.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+// A warp: raw blocks into the ring. Lane i has slot i and so every kRS-th block: it looks whether the last one has been read, and
+// copies the next; lanes that are ready go together. (Block after block by one thread took 1,000 cycles a page, 612 us at 44 x
+// 32,768 tokens with nothing else done.) The id of a lane's next page is read when it has issued the one before. K's lanes
+// bring the page's scales along: a block of K is there when its copy and the scales' are.
+template <int D>
+__device__ void role_load(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int lane, uint32_t base, uint8_t* sbase) {
+  using C = Cfg<D>;
+  constexpr int kStride = C::kRS / 2;            // pages from a lane's block to its next
+  volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_META);
+  const int kind = lane & 1;
+  const uint32_t full = sy.bar(C::B_RAW_FULL + lane), empty = sy.bar(C::B_RAW_EMPTY + lane);
+  int si = work.begin, j = lane >> 1, n = j, count = 0;
+  int32_t page = -1;
+  TreeSegment s{};
+  auto settle = [&]() {
+    while (si < work.end && j >= s.num_pages) {
       j -= s.num_pages;
-      if (++si < se) s = load_segment(a.segs + si);
+      if (++si < work.end) s = load_segment(a.segs + si);
     }
-    if (si < se) page = a.kv_indices[s.page0 + local_page(s, j)];
+    if (si < work.end) page = a.kv_indices[s.page0 + local_page(s, j)];
+  };
+  if (si < work.end) s = load_segment(a.segs + si);
+  settle();
+  bool busy = lane < C::kRS && n < work.pages;
+  long long t0 = clock64();
+  for (int idle = 0; __any_sync(kFull, busy); ++idle) {
+    const bool ready = busy && (count == 0 || mbar_test(empty, (count - 1) & 1));
+    if (ready) {
+      const int p0 = local_page(s, j) * kPage;
+      // of a request's last page only the tokens that it has
+      const int valid = in_pool(a, page) ? min(kPage, s.len - p0) : 0;
+      const uint32_t entry = valid | (by_row(a, s, p0) || !valid ? kMasked : 0);
+      const int64_t block = (static_cast<int64_t>(page) * 2 + kind) * a.kv_heads + s.kv_head;
+      meta[lane] = entry;
+      if (valid) {
+        tc::mbar_arrive_expect_tx(full, valid * D);
+        tc::bulk_load(base + C::OFF_RAW + lane * C::kRaw, a.kv + block * C::kRaw, valid * D, full);
+      } else {
+        tc::mbar_arrive(full);
+      }
+      if (kind == 0) {
+        const uint32_t info = C::OFF_INFO + 16 * (n % C::kInfo);
+        *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = entry;
+        if (valid) {
+          cp_async4(base + info, a.kv_scale + block);
+          cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
+        } else {
+          *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
+          *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
+        }
+        cp_async_arrive(full);
+      }
+      ++count;
+      j += kStride;
+      n += kStride;
+      settle();
+      busy = n < work.pages;
+    }
+    // bounded: a second without a block to load ends it
+    if (__any_sync(kFull, ready)) {
+      idle = 0;
+      t0 = clock64();
+    } else if ((idle & 255) == 255) {
+      const bool late = clock64() - t0 > (1ll << 31);
+      if (late && lane == 0) {
+        *sy.abort = 1;
+        atomicOr(sy.status, 1);
+      }
+      if (__any_sync(kFull, late || *sy.abort)) break;
+    }
   }
-  __device__ void next(int by) {
-    j += by;
-    n += by;
-    settle();
+  // after a timeout: the copies in flight land before the CTA may end
+  if (*sy.abort) {
+    dev::cp_async_wait_all();
+    if (count > 0) tc::mbar_wait(full, (count - 1) & 1);
   }
-};
+}
 
 // kBlockWarps warps: raw blocks to the FP16 tiles, every kGroups-th block, so that the latencies of one block (wait, read,
-// convert, write, fence) hide behind the others'. A group also fills its own slots of the ring again, by bulk copies: a loader of
-// its own, be it a warp, took 1,200 cycles a page (44 x 32,768 tokens, 4 drafted: 663 us). K's groups bring the page's scales
-// along. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms that differ: their reads and their writes
-// fall into distinct banks. K rows past a page's tokens keep what is there (their logits are masked); V rows become zeros.
-template <int D, int NT, bool E4M3>
-__device__ void role_convert(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int warp, int lane, uint32_t base, uint8_t* sbase,
-                             volatile int* nan_seen) {
-  using C = Cfg<D, NT>;
+// convert, write, fence) hide behind the others'. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms
+// that differ: their reads and their writes fall into distinct banks. K rows past a page's tokens keep what is there (their
+// logits are masked); V rows become zeros.
+template <int D, bool E4M3>
+__device__ void role_convert(const Sync& sy, int pages, int warp, int lane, uint32_t base, const uint8_t* sbase, volatile int* nan_seen) {
+  using C = Cfg<D>;
   constexpr int kGroups = C::kGroups, kSets = 8 / C::kBlockWarps;        // sets of 8 rows that a warp has of a block
   constexpr int kSetItems = D == 64 ? 1 : C::kAtoms, kBatchSets = 4 / kSetItems, kItems = kBatchSets * kSetItems;
-  constexpr int kOwn = C::kRS / kGroups;                                 // the group's slots of the ring
   const int group = warp / C::kBlockWarps, kind = group & 1, c = lane & 3;
-  const bool lead = warp % C::kBlockWarps == 0;
   const int sub = D == 64 ? lane >> 2 : 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
   const int row0 = warp % C::kBlockWarps * 8 * kSets + sub;
-  const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, empty = kind == 0 ? C::B_K_EMPTY : C::B_V_EMPTY;
+  const uint32_t full = kind == 0 ? C::B_K_FULL : C::B_V_FULL, freed = kind == 0 ? C::B_S_FULL : C::B_O_DONE;
   const uint32_t read0 = base + C::OFF_RAW + row0 * D + 16 * c;
   const uint32_t write0 = base + (kind == 0 ? C::OFF_K : C::OFF_V) + (row0 >> 3) * 1024 + sub * 128 + (((2 * c) ^ sub) << 4), write1 = write0 ^ 16;
-  volatile uint32_t* meta = reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_META);
-  Feed feed(a, work.begin, work.end, group >> 1);
-  int issued = 0;
-  // lead, one lane: the block that the feed stands on into the group's next slot, whose last block has been read
-  auto issue = [&]() {
-    const int slot = group + kGroups * (issued % kOwn), p0 = local_page(feed.s, feed.j) * kPage;
-    // of a request's last page only the tokens that it has
-    const int valid = in_pool(a, feed.page) ? min(kPage, feed.s.len - p0) : 0;
-    const uint32_t entry = valid | (by_row(a, feed.s, p0) || !valid ? kMasked : 0), bar = sy.bar(C::B_RAW_FULL + slot);
-    const int64_t block = (static_cast<int64_t>(feed.page) * 2 + kind) * a.kv_heads + feed.s.kv_head;
-    meta[slot] = entry;
-    if (valid) {
-      tc::mbar_arrive_expect_tx(bar, valid * D);
-      tc::bulk_load(base + C::OFF_RAW + slot * C::kRaw, a.kv + block * C::kRaw, valid * D, bar);
-    } else {
-      tc::mbar_arrive(bar);
-    }
-    if (kind == 0) {
-      const uint32_t info = C::OFF_INFO + 16 * (feed.n % C::kInfo);
-      *reinterpret_cast<volatile uint32_t*>(sbase + info + 8) = entry;
-      if (valid) {
-        cp_async4(base + info, a.kv_scale + block);
-        cp_async4(base + info + 4, a.kv_scale + block + a.kv_heads);
-      } else {
-        *reinterpret_cast<volatile uint32_t*>(sbase + info) = 0;
-        *reinterpret_cast<volatile uint32_t*>(sbase + info + 4) = 0;
-      }
-      cp_async_arrive(bar);
-    }
-  };
-  if (lead) {
-#pragma unroll 1
-    for (; issued < kOwn && !feed.done(); ++issued) {
-      if (lane == 0) issue();
-      feed.next(kGroups / 2);
-    }
-  }
-  int own = 0, parity = 0;                       // the slot among the group's
-  for (int n = group >> 1; n < work.pages; n += kGroups / 2) {
-    const int ts = n % C::kSlots, slot = group + kGroups * own;
+  const volatile uint32_t* meta = reinterpret_cast<const volatile uint32_t*>(sbase + C::OFF_META);
+  int slot = group, parity = 0;
+  for (int n = group >> 1; n < pages; n += kGroups / 2) {
+    const int b = C::buf(n);
     bool ok = sy.wait(C::B_RAW_FULL + slot, parity, 2);
-    if (!__all_sync(kFull, ok)) break;
-    const uint32_t entry = meta[slot], from = read0 + slot * C::kRaw, to = ts * C::kTile;
+    if (!__all_sync(kFull, ok)) return;
+    const uint32_t entry = meta[slot], from = read0 + slot * C::kRaw, to = b * C::kTile;
     const int valid = static_cast<int>(entry & 0xFFFF);
-    ok = n < C::kSlots || sy.wait(empty + ts, (n / C::kSlots - 1) & 1, 2);
-    if (!__all_sync(kFull, ok)) break;
+    // the product that read the tile's last block is done
+    ok = n < C::kBufs || sy.wait(freed + b, C::phase(n) ^ 1, 2);
+    if (!__all_sync(kFull, ok)) return;
 #pragma unroll
-    for (int b = 0; b < kSets; b += kBatchSets) {
+    for (int x0 = 0; x0 < kSets; x0 += kBatchSets) {
       uint4 w[kItems];
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) w[i] = lds128(from + (b + i / kSetItems) * 8 * D + (((i % kSetItems) ^ odd) << 6));
-      if (b + kBatchSets >= kSets) {
+      for (int i = 0; i < kItems; ++i) w[i] = lds128(from + (x0 + i / kSetItems) * 8 * D + (((i % kSetItems) ^ odd) << 6));
+      if (x0 + kBatchSets >= kSets) {
         __syncwarp();
-        if (C::kBlockWarps > 1 && lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
+        if (lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
       }
       if (kind == 1 && valid < kPage) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
-          if (row0 + 8 * (b + i / kSetItems) >= valid) w[i] = make_uint4(0, 0, 0, 0);
+          if (row0 + 8 * (x0 + i / kSetItems) >= valid) w[i] = make_uint4(0, 0, 0, 0);
       }
       if (E4M3 && kind == 1 && (entry & kMasked)) {
 #pragma unroll
@@ -349,7 +361,7 @@ __device__ void role_convert(const TreeArgs& a, const Sync& sy, const TreeWorker
       }
 #pragma unroll
       for (int i = 0; i < kItems; ++i) {
-        const uint32_t at = to + (b + i / kSetItems) * 1024 + ((i % kSetItems) ^ odd) * C::kAtom;
+        const uint32_t at = to + (x0 + i / kSetItems) * 1024 + ((i % kSetItems) ^ odd) * C::kAtom;
         uint32_t o[8];
         codes_to_f16<E4M3>(w[i].x, o[0], o[1]);
         codes_to_f16<E4M3>(w[i].y, o[2], o[3]);
@@ -361,107 +373,68 @@ __device__ void role_convert(const TreeArgs& a, const Sync& sy, const TreeWorker
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) tc::mbar_arrive(sy.bar(full + ts));
-    if (lead && !feed.done()) {
-      if (lane == 0) {
-        ok = C::kBlockWarps == 1 || sy.wait(C::B_RAW_EMPTY + slot, parity, 1);
-        if (ok) issue();
-      }
-      if (!__all_sync(kFull, ok)) break;
-      ++issued;
-      feed.next(kGroups / 2);
-    }
-    if (++own == kOwn) { own = 0; parity ^= 1; }
-  }
-  // after a timeout: the copies in flight land before the CTA may end
-  if (*sy.abort && lead && lane == 0) {
-    dev::cp_async_wait_all();
-    for (int k = max(0, issued - kOwn); k < issued; ++k) tc::mbar_wait(sy.bar(C::B_RAW_FULL + group + kGroups * (k % kOwn)), (k / kOwn) & 1);
+    if (lane == 0) tc::mbar_arrive(sy.bar(full + b));
+    for (slot += kGroups; slot >= C::kRS; slot -= C::kRS) parity ^= 1;
   }
 }
 
 // One thread a softmax warpgroup: S = Q K^T of its pages. (A thread has some 45 cycles from one product of 32 to the next; two of
 // them fill the tensor cores.)
-template <int D, int NT>
-__device__ void role_qk(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, uint32_t base, uint32_t tbase) {
-  using C = Cfg<D, NT>;
+template <int D>
+__device__ void role_qk(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, uint32_t base, uint32_t tbase) {
+  using C = Cfg<D>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
-  const tc::Desc2 qd = tc::split_desc(tc::smem_desc(base + C::OFF_Q, 16, 1024, tc::kSwizzle128));
-  int n = 0, k = 0;                              // pages, and those of the warpgroup
-  for (int si = seg_b; si < seg_e; ++si) {
-    const TreeSegment s = load_segment(a.segs + si);
-    const bool split = is_split<NT>(s);
-    const int tile = split ? 0 : w;
-    if (!sy.wait(C::B_Q_FULL, (si - seg_b) & 1, 4)) goto out;
-    for (int j = 0; j < s.num_pages; ++j, ++n) {
-      const int slot = n % C::kSlots;
-      if (!sy.wait(C::B_K_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
-      if (split && (j & 1) != w) {
-        tc::mbar_arrive(sy.bar(C::B_K_EMPTY + slot));
-        continue;
-      }
+  const uint32_t q = tbase + C::TM_Q;
+  int n = w, end = 0;                            // pages, and those up to the segment's end
+  for (int si = work.begin; si < work.end; ++si) {
+    end += a.segs[si].num_pages;
+    if (!sy.wait(C::B_Q_FULL, (si - work.begin) & 1, 4)) goto out;
+    for (; n < end; n += 2) {
+      const int b = C::buf(n);
+      if (!sy.wait(C::B_K_FULL + b, C::phase(n), 4)) goto out;
       // the buffer's last P has been read
-      const int b = C::buf(w, k);
-      if (k >= C::kSB && !sy.wait(C::B_O_DONE + b, C::phase(k) ^ 1, 4)) goto out;
+      if (n >= C::kBufs && !sy.wait(C::B_O_DONE + b, C::phase(n) ^ 1, 4)) goto out;
       tc::tc_fence_after();
       const uint32_t d = tbase + C::TM_S + b * kPage;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const uint64_t bd = kd.at(slot * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
-        if constexpr (C::kQSmem) {
-          const uint64_t ad = qd.at(tile * C::kQTile + (i >> 2) * C::kQAtom + 32 * (i & 3));
-          if (i == 0) tc::mma_ss_k<false>(d, ad, bd, kIdesc);
-          else tc::mma_ss_k<true>(d, ad, bd, kIdesc);
-        } else {
-          const uint32_t q = tbase + C::TM_Q + tile * (D / 2) + 8 * i;
-          if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
-          else tc::mma_ts_k<true>(d, q, bd, kIdesc);
-        }
+        const uint64_t bd = kd.at(b * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
+        if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+        else tc::mma_ts_k<true>(d, q + 8 * i, bd, kIdesc);
       }
       tc::mma_commit(sy.bar(C::B_S_FULL + b));
-      tc::mma_commit(sy.bar(C::B_K_EMPTY + slot));
-      ++k;
     }
   }
 out:
   tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
-// One thread a tile: O += P V. That of tile 0 takes the pages of split blocks, in order.
-template <int D, int NT>
-__device__ void role_pv(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int tile, uint32_t base, uint32_t tbase) {
-  using C = Cfg<D, NT>;
+// One thread: O += P V, page after page.
+template <int D>
+__device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& work, uint32_t base, uint32_t tbase) {
+  using C = Cfg<D>;
   constexpr uint32_t kIdesc = tc::idesc_f16(128, D, 0, 1);
   const tc::Desc2 vd = tc::split_desc(tc::smem_desc(base + C::OFF_V, C::kAtom, 1024, tc::kSwizzle128));
-  const uint32_t o = tbase + tile * D;
-  int n = 0, cnt[2] = {0, 0};
-  for (int si = seg_b; si < seg_e; ++si) {
-    const TreeSegment s = load_segment(a.segs + si);
-    const bool split = is_split<NT>(s);
+  int n = 0, end = 0;
+  for (int si = work.begin; si < work.end; ++si) {
+    const int first = end;
+    end += a.segs[si].num_pages;
     // O of the segment before has been read
-    if (si > seg_b && !sy.wait(C::B_O_FREE, (si - seg_b - 1) & 1, 4)) goto out;
-    for (int j = 0; j < s.num_pages; ++j, ++n) {
-      const int slot = n % C::kSlots;
-      if (!sy.wait(C::B_V_FULL + slot, (n / C::kSlots) & 1, 4)) goto out;
-      const int w = split ? j & 1 : tile, b = C::buf(w, cnt[w]);
-      if (split && tile == 1) {
-        tc::mbar_arrive(sy.bar(C::B_V_EMPTY + slot));
-      } else {
-        if (!sy.wait(C::B_P_FULL + b, C::phase(cnt[w]), 4)) goto out;
-        tc::tc_fence_after();
-        const uint32_t p = tbase + C::TM_S + b * kPage;
+    if (si > work.begin && !sy.wait(C::B_O_FREE, (si - work.begin - 1) & 1, 4)) goto out;
+    for (; n < end; ++n) {
+      const int b = C::buf(n);
+      if (!sy.wait(C::B_V_FULL + b, C::phase(n), 4)) goto out;
+      if (!sy.wait(C::B_P_FULL + b, C::phase(n), 4)) goto out;
+      tc::tc_fence_after();
+      const uint32_t p = tbase + C::TM_S + b * kPage;
 #pragma unroll
-        for (int k = 0; k < kPage / 16; ++k) {
-          const uint64_t bd = vd.at(slot * C::kTile + 2048 * k);
-          if (k == 0 && j == 0) tc::mma_ts_k<false>(o, p, bd, kIdesc);
-          else tc::mma_ts_k<true>(o, p + 8 * k, bd, kIdesc);
-        }
-        tc::mma_commit(sy.bar(C::B_O_DONE + b));
-        tc::mma_commit(sy.bar(C::B_V_EMPTY + slot));
+      for (int k = 0; k < kPage / 16; ++k) {
+        const uint64_t bd = vd.at(b * C::kTile + 2048 * k);
+        if (k == 0 && n == first) tc::mma_ts_k<false>(tbase, p, bd, kIdesc);
+        else tc::mma_ts_k<true>(tbase, p + 8 * k, bd, kIdesc);
       }
-      ++cnt[w];
-      if (!split) ++cnt[1 - w];
+      tc::mma_commit(sy.bar(C::B_O_DONE + b));
     }
   }
 out:
@@ -516,117 +489,100 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int D, int NT, bool E4M3>
-__device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int seg_e, int w, int row, uint32_t base, uint8_t* sbase, uint32_t tbase,
+template <int D, bool E4M3>
+__device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, int row, uint8_t* sbase, uint32_t tbase,
                              volatile int* nan_seen) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   const uint32_t tl = tbase + (static_cast<uint32_t>(row & ~31) << 16);   // the warp's quarter of the lanes
   const int group = a.heads / a.kv_heads, lane = row & 31;
   volatile float* refs = reinterpret_cast<volatile float*>(sbase + C::OFF_REF);
+  volatile int8_t* lifts = reinterpret_cast<volatile int8_t*>(sbase + C::OFF_QS);
   auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, sy.wait(bar, parity, 8))); };
   // a warp's arrival, after what all its lanes did
   auto arrive = [&](uint32_t bar) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(sy.bar(bar));
   };
-  int mine = 0, others = 0, n0 = 0;              // pages of this and the other warpgroup, and of all, in the segments before
-  for (int si = seg_b; si < seg_e; ++si) {
+  int begin = 0;                                 // the segment's first page among the worker's
+  for (int si = work.begin; si < work.end; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
-    const bool split = is_split<NT>(s);
-    const int tile = split ? 0 : w, at = tile * kTreeTile + row;
-    const bool live = at < s.rows, idle = (at & ~31) >= s.rows;   // a warp without a row has no logits to turn
-    const int t = (s.row0 + at) / group;         // drafted token and query head
+    const bool live = row < s.rows, idle = (row & ~31) >= s.rows;   // a warp without a row has no logits to turn
+    const int t = (s.row0 + row) / group;        // drafted token and query head
     // the row among those of q, out and lse; -1: none
-    const int64_t head = live ? static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + at) % group : -1;
-    volatile int8_t* lifts = reinterpret_cast<volatile int8_t*>(sbase + C::OFF_QS) + tile * kTreeTile;   // e of the rows
+    const int64_t head = live ? static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + row) % group : -1;
     RowMask mask;
     mask.init(a, s, live ? t : 0);
-    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. A warp takes 16 rows
-    // at a time, four lanes a row, so that its loads are of whole sectors (a row a thread, Q and the output took 12 of a
-    // segment's 15 us); the two warpgroups of a split block take 16 rows of each 32 ----
+    // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. Each of the two warps
+    // of 32 rows takes 16, four lanes a row, so that its loads are of whole sectors (a row a thread, Q and the output took 12
+    // of a segment's 15 us) ----
     if (!idle) {
-#pragma unroll 1
-      for (int h = split ? w : 0; h < (split ? w + 1 : 2); ++h) {
-        const int64_t top_head = shfl64(head, 16 * h + (lane >> 2)), low_head = shfl64(head, 16 * h + 8 + (lane >> 2));
-        const uint2* top = reinterpret_cast<const uint2*>(a.q + top_head * D) + (lane & 3);
-        const uint2* low = reinterpret_cast<const uint2*>(a.q + low_head * D) + (lane & 3);
-        uint2 x[2][D / 16];
-        uint32_t amax[2] = {0, 0};
+      const int64_t top_head = shfl64(head, 16 * w + (lane >> 2)), low_head = shfl64(head, 16 * w + 8 + (lane >> 2));
+      const uint2* top = reinterpret_cast<const uint2*>(a.q + top_head * D) + (lane & 3);
+      const uint2* low = reinterpret_cast<const uint2*>(a.q + low_head * D) + (lane & 3);
+      uint2 x[2][D / 16];
+      uint32_t amax[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          x[0][i] = top_head >= 0 ? top[4 * i] : make_uint2(0, 0);
-          x[1][i] = low_head >= 0 ? low[4 * i] : make_uint2(0, 0);
-        }
-        float up[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) amax[k] = __vmaxu2(amax[k], __vmaxu2(x[k][i].x & 0x7FFF7FFFu, x[k][i].y & 0x7FFF7FFFu));
-          amax[k] = max(amax[k] & 0xFFFFu, amax[k] >> 16);
-          amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 1));
-          amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 2));
-          const int e = amax[k] == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(amax[k] >> 7));
-          up[k] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-          if ((lane & 3) == 0) lifts[(row & ~31) + 16 * h + 8 * k + (lane >> 2)] = static_cast<int8_t>(e);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {       // 64 dims
-          uint32_t y[16];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              y[4 * u + 2 * k] = dev::bf16x2_to_f16x2(x[k][4 * i + u].x ^ a.flip, up[k]);
-              y[4 * u + 2 * k + 1] = dev::bf16x2_to_f16x2(x[k][4 * i + u].y ^ a.flip, up[k]);
-            }
-          if constexpr (C::kQSmem) {
-            const uint32_t to = base + C::OFF_Q + tile * C::kQTile + i * C::kQAtom;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t at8 = to + tc::sw128_offset((row & ~31) + 16 * h + 8 * k + (lane >> 2), 2 * u + ((lane & 3) >> 1)) + 8 * (lane & 1);
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" :: "r"(at8), "r"(y[4 * u + 2 * k]), "r"(y[4 * u + 2 * k + 1]));
-              }
-          } else {
-            tc::tmem_st_rows16(tl + ((16 * h) << 16) + C::TM_Q + tile * (D / 2) + 32 * i, y);
-          }
-        }
+      for (int i = 0; i < D / 16; ++i) {
+        x[0][i] = top_head >= 0 ? top[4 * i] : make_uint2(0, 0);
+        x[1][i] = low_head >= 0 ? low[4 * i] : make_uint2(0, 0);
       }
-      if constexpr (C::kQSmem) tc::fence_proxy_async_smem();
-      else tc::tmem_wait_st();
+      float up[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) amax[k] = __vmaxu2(amax[k], __vmaxu2(x[k][i].x & 0x7FFF7FFFu, x[k][i].y & 0x7FFF7FFFu));
+        amax[k] = max(amax[k] & 0xFFFFu, amax[k] >> 16);
+        amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 1));
+        amax[k] = max(amax[k], __shfl_xor_sync(kFull, amax[k], 2));
+        const int e = amax[k] == 0 ? 0 : min(126, 14 + 127 - static_cast<int>(amax[k] >> 7));
+        up[k] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        if ((lane & 3) == 0) lifts[(row & ~31) + 16 * w + 8 * k + (lane >> 2)] = static_cast<int8_t>(e);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {         // 64 dims
+        uint32_t y[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            y[4 * u + 2 * k] = dev::bf16x2_to_f16x2(x[k][4 * i + u].x ^ a.flip, up[k]);
+            y[4 * u + 2 * k + 1] = dev::bf16x2_to_f16x2(x[k][4 * i + u].y ^ a.flip, up[k]);
+          }
+        tc::tmem_st_rows16(tl + ((16 * w) << 16) + C::TM_Q + 32 * i, y);
+      }
+      tc::tmem_wait_st();
     }
     tc::tc_fence_before();
     arrive(C::B_Q_FULL);
     // the next segment's Q on its way into L2
-    if (si + 1 < seg_e) {
+    if (si + 1 < work.end) {
       const TreeSegment* nx = a.segs + si + 1;
-      const int to = (is_split<NT>(*nx) ? 0 : tile * kTreeTile) + row, rows = nx->rows, first = nx->row0 + to;
-      if (to < rows) {
+      const int first = nx->row0 + row;
+      if (row < nx->rows) {
         const uint16_t* p = a.q + (static_cast<int64_t>(nx->tok0 + first / group) * a.heads + nx->kv_head * group + first % group) * D;
 #pragma unroll
         for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
       }
     }
     // the rows' factors are there when all of Q is
-    if (!wait(C::B_Q_FULL, (si - seg_b) & 1)) return;
+    if (!wait(C::B_Q_FULL, (si - work.begin) & 1)) return;
     const float q_scale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - lifts[row]) << 23);
     float m = -INFINITY, l = 0.0f, r = kNoRef;
-    for (int j = split ? w : 0; j < s.num_pages; j += split ? 2 : 1) {
-      const int k = mine + (split ? j >> 1 : j), b = C::buf(w, k);     // the page among the warpgroup's, its buffer
-      const int before = split ? others + ((j + w) >> 1) - 1 : k - 1;  // the page before among those of its warpgroup
-      if (!wait(C::B_S_FULL + b, C::phase(k))) return;
+    const int end = begin + s.num_pages;
+    for (int n = begin + ((begin ^ w) & 1); n < end; n += 2) {
+      const int b = C::buf(n), j = n - begin;
+      if (!wait(C::B_S_FULL + b, C::phase(n))) return;
       tc::tc_fence_after();
       if (!idle) {
         const uint32_t ts = tl + C::TM_S + b * kPage;
-        const volatile float* info = reinterpret_cast<const volatile float*>(sbase + C::OFF_INFO + 16 * ((n0 + j) % C::kInfo));
+        const volatile float* info = reinterpret_cast<const volatile float*>(sbase + C::OFF_INFO + 16 * (n % C::kInfo));
         const float zs = info[0] * q_scale, vs = info[1], lsv = lg2(vs);
         const bool masked = __float_as_uint(info[2]) & kMasked;
         // Without a reference yet that of the page before is waited for. Later pages take the one at hand, and make up for it
         // below where that page renewed it in the meantime.
-        bool fetched = !split || j == 0;
-        if (!fetched && j < 2) {
-          if (!wait(C::B_REF + C::buf(1 - w, before), C::phase(before))) return;
+        bool fetched = j == 0;
+        if (j == 1) {
+          if (!wait(C::B_REF + C::buf(n - 1), C::phase(n - 1))) return;
           r = refs[row];
           fetched = true;
         }
@@ -714,7 +670,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
         }
         const float held = r;                    // P's reference
         if (!fetched) {
-          if (!wait(C::B_REF + C::buf(1 - w, before), C::phase(before))) return;
+          if (!wait(C::B_REF + C::buf(n - 1), C::phase(n - 1))) return;
           ro = refs[row];
           r = fmaxf(r, ro);
         }
@@ -736,62 +692,53 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
             }
           }
           if (j > 0) {                                       // O to this page's, once the pages before are all in
-            if (!wait(C::B_O_DONE + C::buf(split ? 1 - w : w, before), C::phase(before))) return;
+            if (!wait(C::B_O_DONE + C::buf(n - 1), C::phase(n - 1))) return;
             tc::tc_fence_after();
             const float f = dev::fast_exp2(ro - r);
 #pragma unroll 1
             for (int k = 0; k < D / 16; ++k) {
               uint32_t o[16];
-              tc::tmem_ld16(tl + tile * D + 16 * k, o);
+              tc::tmem_ld16(tl + 16 * k, o);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tc::tmem_st16(tl + tile * D + 16 * k, o);
+              tc::tmem_st16(tl + 16 * k, o);
             }
           }
         }
-        if (split) refs[row] = r;
+        refs[row] = r;
       }
-      arrive(C::B_REF + b);         // in unsplit blocks, too: its phases count the warpgroup's pages
+      arrive(C::B_REF + b);
       if (!idle) tc::tmem_wait_st();
       tc::tc_fence_before();
       arrive(C::B_P_FULL + b);
     }
-    n0 += s.num_pages;
-    mine += split ? (s.num_pages + 1 - w) >> 1 : s.num_pages;
-    others += split ? (s.num_pages + w) >> 1 : s.num_pages;
-    // ---- the segment's end: O 2^(r - 6 - m) / l; nothing visible: 0 and -inf ----
-    const int last = split ? (s.num_pages - 1) & 1 : w, end = (last == w ? mine : others) - 1;
-    // the warpgroup's own last page first: after it the barrier of the other's is in its last page's phase or past it (a wait
-    // tells two phases apart, not three)
-    if (last != w && s.num_pages > 1 && !wait(C::B_O_DONE + C::buf(w, mine - 1), C::phase(mine - 1))) return;
-    if (!wait(C::B_O_DONE + C::buf(last, end), C::phase(end))) return;
+    // ---- the segment's end: O 2^(r - 6 - m) / l; nothing visible: 0 and -inf. The warpgroup's own last page first: after it the
+    // barrier of the last one is in that page's phase or past it ----
+    const int last = end - 1;
+    if (((last ^ w) & 1) && s.num_pages > 1 && !wait(C::B_O_DONE + C::buf(last - 1), C::phase(last - 1))) return;
+    if (!wait(C::B_O_DONE + C::buf(last), C::phase(last))) return;
     tc::tc_fence_after();
-    const uint32_t ts = tl + C::TM_S + C::kSB * w * kPage;
-    if (split) {
-      // m and l change hands in the logits' place
-      __syncwarp();
-      tc::tmem_st2(ts, __float_as_uint(m), __float_as_uint(l));
-      tc::tmem_wait_st();
-      tc::tc_fence_before();
-    }
+    begin = end;
+    // m and l change hands in the logits' place
+    __syncwarp();
+    tc::tmem_st2(tl + C::TM_S + w * kPage, __float_as_uint(m), __float_as_uint(l));
+    tc::tmem_wait_st();
+    tc::tc_fence_before();
     // past this every product of the segment is in: Q may be written again
     arrive(C::B_SEG);
-    if (!wait(C::B_SEG, (si - seg_b) & 1)) return;
-    int k0 = 0, k1 = D / 16;                     // 16 columns each
-    if (split) {
-      tc::tc_fence_after();
-      uint32_t om, ol;
-      tc::tmem_ld2(tl + C::TM_S + C::kSB * (1 - w) * kPage, om, ol);
-      tc::tmem_wait_ld();
-      r = refs[row];
+    if (!wait(C::B_SEG, (si - work.begin) & 1)) return;
+    tc::tc_fence_after();
+    uint32_t om, ol;
+    tc::tmem_ld2(tl + C::TM_S + (1 - w) * kPage, om, ol);
+    tc::tmem_wait_ld();
+    r = refs[row];
+    {
       const float m0 = w == 0 ? m : __uint_as_float(om), m1 = w == 0 ? __uint_as_float(om) : m;
       const float l0 = w == 0 ? l : __uint_as_float(ol), l1 = w == 0 ? __uint_as_float(ol) : l;
       m = fmaxf(m0, m1);
       const float back = m == -INFINITY ? 0.0f : m;
       l = l0 * dev::fast_exp2(m0 - back) + l1 * dev::fast_exp2(m1 - back);
-      k0 = w * (D / 32);
-      k1 = k0 + D / 32;
     }
     if (!idle) {
       const bool none = m == -INFINITY && l == 0.0f;      // (l is NaN where every logit is)
@@ -800,11 +747,11 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
       const bool nans = E4M3 && *nan_seen != 0;
       const int64_t slot = s.partial;
       if (s.partial >= 0 || nans) {
-        // a row a thread; partials lie as [slot][4 columns][row], so that a warp writes 512 bytes in a row
+        // a row a thread, half the columns a warpgroup; partials lie as [slot][4 columns][row], so that a warp writes 512 bytes in a row
 #pragma unroll 1
-        for (int k = k0; k < k1; ++k) {
+        for (int k = w * (D / 32); k < (w + 1) * (D / 32); ++k) {
           uint32_t o[16];
-          tc::tmem_ld16(tl + tile * D + 16 * k, o);
+          tc::tmem_ld16(tl + 16 * k, o);
           tc::tmem_wait_ld();
           float y[16];
 #pragma unroll
@@ -817,9 +764,9 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
                 for (int u = 0; u < 16; ++u)
                   if (u == i) y[u] = __uint_as_float(0x7FC00000u);
           if (s.partial >= 0) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + 4 * k) * (NT * kTreeTile) + at;
+            float4* dst = reinterpret_cast<float4*>(a.part_o) + (slot * (D / 4) + 4 * k) * kTreeTile + row;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) dst[u * (NT * kTreeTile)] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+            for (int u = 0; u < 4; ++u) dst[u * kTreeTile] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
           } else if (live) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + head * D + 16 * k);
 #pragma unroll
@@ -830,43 +777,40 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
           __syncwarp();
         }
       } else {
-        // 16 rows at a time, four lanes a row, 8 columns a lane after a 4 x 4 transpose
+        // 16 rows a warp, four lanes a row, 8 columns a lane after a 4 x 4 transpose
+        const int64_t top_head = shfl64(head, 16 * w + (lane >> 2)), low_head = shfl64(head, 16 * w + 8 + (lane >> 2));
+        const float ft = __shfl_sync(kFull, f, 16 * w + (lane >> 2)), fl = __shfl_sync(kFull, f, 16 * w + 8 + (lane >> 2));
 #pragma unroll 1
-        for (int h = split ? w : 0; h < (split ? w + 1 : 2); ++h) {
-          const int64_t top_head = shfl64(head, 16 * h + (lane >> 2)), low_head = shfl64(head, 16 * h + 8 + (lane >> 2));
-          const float ft = __shfl_sync(kFull, f, 16 * h + (lane >> 2)), fl = __shfl_sync(kFull, f, 16 * h + 8 + (lane >> 2));
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t o[16];
-            tc::tmem_ld_rows16(tl + ((16 * h) << 16) + tile * D + 32 * k, o);
-            tc::tmem_wait_ld();
-            uint32_t y[2][4];
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t o[16];
+          tc::tmem_ld_rows16(tl + ((16 * w) << 16) + 32 * k, o);
+          tc::tmem_wait_ld();
+          uint32_t y[2][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              y[0][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u]) * ft, __uint_as_float(o[4 * u + 1]) * ft);
-              y[1][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u + 2]) * fl, __uint_as_float(o[4 * u + 3]) * fl);
+          for (int u = 0; u < 4; ++u) {
+            y[0][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u]) * ft, __uint_as_float(o[4 * u + 1]) * ft);
+            y[1][u] = dev::pack_bf16x2(__uint_as_float(o[4 * u + 2]) * fl, __uint_as_float(o[4 * u + 3]) * fl);
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t* x = y[v];
+#pragma unroll
+            for (int u = 0; u < 4; u += 2) {
+              const uint32_t z = __shfl_xor_sync(kFull, lane & 1 ? x[u] : x[u + 1], 1);
+              if (lane & 1) x[u] = z; else x[u + 1] = z;
             }
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t* x = y[v];
-#pragma unroll
-              for (int u = 0; u < 4; u += 2) {
-                const uint32_t z = __shfl_xor_sync(kFull, lane & 1 ? x[u] : x[u + 1], 1);
-                if (lane & 1) x[u] = z; else x[u + 1] = z;
-              }
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const uint32_t z = __shfl_xor_sync(kFull, lane & 2 ? x[u] : x[u + 2], 2);
-                if (lane & 2) x[u] = z; else x[u + 2] = z;
-              }
-              const int64_t to = v == 0 ? top_head : low_head;
-              if (to >= 0) *reinterpret_cast<uint4*>(a.out + to * D + 32 * k + 8 * (lane & 3)) = make_uint4(x[0], x[1], x[2], x[3]);
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t z = __shfl_xor_sync(kFull, lane & 2 ? x[u] : x[u + 2], 2);
+              if (lane & 2) x[u] = z; else x[u + 2] = z;
             }
+            const int64_t to = v == 0 ? top_head : low_head;
+            if (to >= 0) *reinterpret_cast<uint4*>(a.out + to * D + 32 * k + 8 * (lane & 3)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
       }
-      if (live && (!split || w == 0)) {
-        if (s.partial >= 0) a.part_lse[slot * (NT * kTreeTile) + at] = lse2;
+      if (live && w == 0) {
+        if (s.partial >= 0) a.part_lse[slot * kTreeTile + row] = lse2;
         else if (a.lse) a.lse[head] = none ? -INFINITY : lse2 * 0.69314718055994531f;
       }
     }
@@ -875,9 +819,9 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, int seg_b, int s
   }
 }
 
-template <int D, int NT, bool E4M3>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const TreeArgs a) {
-  using C = Cfg<D, NT>;
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArgs a) {
+  using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -893,22 +837,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
       tc::mbar_init(sy.bar(C::B_RAW_FULL + i), i & 1 ? 1 : 2);       // K: the scales', too
       tc::mbar_init(sy.bar(C::B_RAW_EMPTY + i), C::kBlockWarps);
     }
-    for (int i = 0; i < C::kSlots; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       tc::mbar_init(sy.bar(C::B_K_FULL + i), C::kBlockWarps);
-      tc::mbar_init(sy.bar(C::B_K_EMPTY + i), 2);
       tc::mbar_init(sy.bar(C::B_V_FULL + i), C::kBlockWarps);
-      tc::mbar_init(sy.bar(C::B_V_EMPTY + i), NT);
-    }
-    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(sy.bar(C::B_S_FULL + i), 1);
-      tc::mbar_init(sy.bar(C::B_P_FULL + i), 4);        // one arrival a warp
+      tc::mbar_init(sy.bar(C::B_P_FULL + i), 4);     // one arrival a warp
       tc::mbar_init(sy.bar(C::B_O_DONE + i), 1);
       tc::mbar_init(sy.bar(C::B_REF + i), 4);
     }
     tc::mbar_init(sy.bar(C::B_Q_FULL), 8);
     tc::mbar_init(sy.bar(C::B_O_FREE), 8);
     tc::mbar_init(sy.bar(C::B_SEG), 8);
-    tc::mbar_init(sy.bar(C::B_FINAL), 2 + NT);       // one commit per issuing thread
+    tc::mbar_init(sy.bar(C::B_FINAL), 3);            // one commit per issuing thread
     *sy.abort = 0;
     *nan_seen = 0;
     tc::fence_mbar_init();
@@ -926,12 +866,14 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) tree_kernel(const Tre
   const TreeWorker work = a.workers[blockIdx.x];
 
   if (warp < C::kConvertWarp) {
-    role_softmax<D, NT, E4M3>(a, sy, work.begin, work.end, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
+    role_softmax<D, E4M3>(a, sy, work, warp / 4, tid & 127, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
-    role_convert<D, NT, E4M3>(a, sy, work, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
-  } else if ((tid & 31) == 0 && warp < C::kPvWarp + NT) {
-    if (warp < C::kPvWarp) role_qk<D, NT>(a, sy, work.begin, work.end, warp - C::kQkWarp, base, tbase);
-    else role_pv<D, NT>(a, sy, work.begin, work.end, warp - C::kPvWarp, base, tbase);
+    role_convert<D, E4M3>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
+  } else if (warp == C::kLoadWarp) {
+    role_load<D>(a, sy, work, tid & 31, base, sbase);
+  } else if ((tid & 31) == 0) {
+    if (warp == C::kPvWarp) role_pv<D>(a, sy, work, base, tbase);
+    else role_qk<D>(a, sy, work, warp - C::kQkWarp, base, tbase);
     sy.wait(C::B_FINAL, 0, 16);                      // every product has completed before tensor memory is released
   }
   __syncwarp();
@@ -951,7 +893,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   dev::wait_for_previous();
   dev::allow_dependents();
   const TreeJoin* jp = a.joins + blockIdx.z;
-  const int first = jp->first, count = jp->count, rows = jp->rows, pitch = a.tiles * kTreeTile;
+  const int first = jp->first, count = jp->count, rows = jp->rows, pitch = kTreeTile;
   const int row = blockIdx.x * 32 + (threadIdx.x & 31), c8 = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   const float* lse = a.part_lse + static_cast<int64_t>(first) * pitch + row;
@@ -981,27 +923,20 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   if (c8 == 0 && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
-template <int D, int NT, bool E4M3>
+template <int D, bool E4M3>
 cudaError_t launch_attend(const TreeArgs& a, cudaStream_t s) {
-  using C = Cfg<D, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, NT, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = Cfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(tree_kernel<D, NT, E4M3>, static_cast<unsigned>(a.num_workers), C::kThreads, C::kSmem, s, a);
+  return launch_overlapped(tree_kernel<D, E4M3>, static_cast<unsigned>(a.num_workers), C::kThreads, C::kSmem, s, a);
 }
 
 template <int D>
 cudaError_t launch_dim(const TreeArgs& a, cudaStream_t s) {
-  const bool e4m3 = a.cache_dtype == QKVP_CACHE_E4M3;
-  cudaError_t e;
-  if constexpr (D == 256) {
-    e = e4m3 ? launch_attend<D, 1, true>(a, s) : launch_attend<D, 1, false>(a, s);
-  } else {
-    if (a.tiles == 1) e = e4m3 ? launch_attend<D, 1, true>(a, s) : launch_attend<D, 1, false>(a, s);
-    else e = e4m3 ? launch_attend<D, 2, true>(a, s) : launch_attend<D, 2, false>(a, s);
-  }
+  const cudaError_t e = a.cache_dtype == QKVP_CACHE_E4M3 ? launch_attend<D, true>(a, s) : launch_attend<D, false>(a, s);
   if (e != cudaSuccess || a.num_joins == 0) return e;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(static_cast<unsigned>(a.tiles * kTreeTile / 32), D / 64, static_cast<unsigned>(a.num_joins));
+  c.gridDim = dim3(kTreeTile / 32, D / 64, static_cast<unsigned>(a.num_joins));
   c.blockDim = dim3(kJoinThreads);
   c.stream = s;
   cudaLaunchAttribute attr{};
