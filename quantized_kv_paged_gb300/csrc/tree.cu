@@ -26,18 +26,17 @@
 // buffer are free.
 //
 // Softmax. m is the largest logit that the thread has seen, l the sum of 2^(z - m) in FP32. What a page adds to O is p sv
-// code, and V's scales may be far apart, so O has a reference r of its own (common to the warpgroups that share O, handed
-// on from step to step): P = 2^(z - m) F, F = sv 2^(m - r + 6), r renewed (and O rescaled) only when the largest z + log2 sv
-// of a page passes it by 2^8. P <= 2^14 stays in FP16's normal range down to 2^-28 of the largest contribution. A page is
-// taken against the r at hand in one pass, F in the exponent, which l takes back from the sum of P; where its largest
-// logit shows that r has to move, where tokens are masked or F is extreme, it is taken in two passes.
+// code, and V's scales may be far apart, so O has a reference r of its own, handed on from page to page: P = 2^(z - m) F,
+// F = sv 2^(m - r + 6), r renewed (and O rescaled) only when the largest z + log2 sv of a page passes it by 2^8. P <= 2^14
+// stays in FP16's normal range down to 2^-28 of the largest contribution. A page is taken in one pass against the r that its
+// warpgroup knows, F in the exponent, which l takes back from the sum of P, and then looks whether the page before left that
+// r: where it did not, where the page's own largest logit shows that r has to move, where tokens are masked or F is
+// extreme, it is taken again, in two passes.
 //
 // Masks. Only pages that hold drafted tokens or an edge of a row's window are masked by row: 64 bits from the row's mask
 // words. V codes that are NaN there count as zero in the product (0 times NaN would reach rows that do not see the token),
 // and the rows that do see one are found at the segment's end.
 #include <cstdint>
-
-#include <cuda_fp16.h>
 
 #include "decode_common.cuh"
 #include "qkvp_device.cuh"
@@ -490,7 +489,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 template <int D, bool E4M3>
-__device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, int row, uint8_t* sbase, uint32_t tbase,
+__device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, int row, uint32_t base, uint8_t* sbase, uint32_t tbase,
                              volatile int* nan_seen) {
   using C = Cfg<D>;
   const uint32_t tl = tbase + (static_cast<uint32_t>(row & ~31) << 16);   // the warp's quarter of the lanes
@@ -570,39 +569,33 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
     float m = -INFINITY, l = 0.0f, r = kNoRef;
     const int end = begin + s.num_pages;
     for (int n = begin + ((begin ^ w) & 1); n < end; n += 2) {
-      const int b = C::buf(n), j = n - begin;
+      const int b = C::buf(n), before = C::buf(n - 1), j = n - begin;
+      const uint32_t before_phase = C::phase(n - 1);
       if (!wait(C::B_S_FULL + b, C::phase(n))) return;
       tc::tc_fence_after();
+      bool said = false;                         // the page's reference
       if (!idle) {
         const uint32_t ts = tl + C::TM_S + b * kPage;
-        const volatile float* info = reinterpret_cast<const volatile float*>(sbase + C::OFF_INFO + 16 * (n % C::kInfo));
-        const float zs = info[0] * q_scale, vs = info[1], lsv = lg2(vs);
-        const bool masked = __float_as_uint(info[2]) & kMasked;
-        // Without a reference yet that of the page before is waited for. Later pages take the one at hand, and make up for it
-        // below where that page renewed it in the meantime.
-        bool fetched = j == 0;
-        if (j == 1) {
-          if (!wait(C::B_REF + C::buf(n - 1), C::phase(n - 1))) return;
-          r = refs[row];
-          fetched = true;
-        }
-        float ro = r;                            // O's reference, as far as it is known
-        // against the reference at hand, in one pass, unless that proves to be too far below
-        bool plain = masked;
-        if (!plain) {
+        const uint4 info = lds128(base + C::OFF_INFO + 16 * (n % C::kInfo));
+        const float zs = __uint_as_float(info.x) * q_scale, vs = __uint_as_float(info.y), lsv = lg2(vs);
+        const bool masked = info.z & kMasked;
+        bool good = !masked && j > 1, ok = true;
+        float ro = r;                            // O's reference: the one that the page before left
+        if (good) {
+          // in one pass against the reference of the page before the last one, which is hardly ever another
           const float shift = r - kLift - lsv;
           const uint64_t scale2 = pair(zs, zs), shift2 = pair(-shift, -shift);
           uint64_t sum0 = 0, sum1 = 0;
           float top0 = -INFINITY, top1 = -INFINITY;
-          uint32_t pk[32];
+          uint32_t pk[32], x[2][32];
+          tc::tmem_ld32(ts, x[0]);
+          tc::tmem_ld32(ts + 32, x[1]);
+          tc::tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t x[32];
-            tc::tmem_ld32(ts + 32 * h, x);
-            tc::tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float x0 = __uint_as_float(x[2 * k]), x1 = __uint_as_float(x[2 * k + 1]);
+              const float x0 = __uint_as_float(x[h][2 * k]), x1 = __uint_as_float(x[h][2 * k + 1]);
               if (k & 1) top1 = max3(top1, x0, x1);
               else top0 = max3(top0, x0, x1);
               float z0, z1;
@@ -615,20 +608,29 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
             }
           }
           const float z = fmaxf(top0, top1) * zs, m_new = fmaxf(m, z);
-          // log2 of what P has on 2^(z - m): moderate, and so is l's part of it
-          plain = !__all_sync(kFull, fabsf(m_new - shift) < 60.0f && r != kNoRef && !(z + lsv > r + kSlack));
-          if (!plain) {
+          ok = sy.wait(C::B_REF + before, before_phase, 8);
+          ro = refs[row];
+          // m_new - shift: log2 of what P has on 2^(z - m); moderate, and so is l's part of it
+          good = __all_sync(kFull, ok && ro == r && fabsf(m_new - shift) < 60.0f && !(z + lsv > r + kSlack));
+          if (good) {
+            arrive(C::B_REF + b);                // refs[row] stays
+            said = true;
+            tc::tmem_st32<false>(ts, pk);
             float a0, a1;
             unpair(add2(sum0, sum1), a0, a1);
             l = fmaf(a0 + a1, dev::fast_exp2(shift - m_new), l * dev::fast_exp2(m - m_new));
             m = m_new;
-            tc::tmem_st32<false>(ts, pk);
           }
+        } else if (j > 0) {
+          ok = sy.wait(C::B_REF + before, before_phase, 8);
+          ro = refs[row];
         }
-        if (plain) {
+        if (!good) {
+          if (!__all_sync(kFull, ok)) return;
+          r = ro;
           // the largest visible logit first
           uint64_t bits = ~0ull;
-          if (masked) bits = __float_as_uint(info[2]) & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
+          if (masked) bits = info.z & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
           float top = -INFINITY;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
@@ -646,6 +648,24 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           m = m_new;
           const float c = z + lsv;                           // -inf where the page adds nothing to O
           if (c > r + kSlack) r = c;
+          if (j > 0 && __any_sync(kFull, r != ro)) {
+            // O to the page's reference, once the pages before are all in
+            if (!wait(C::B_O_DONE + before, before_phase)) return;
+            tc::tc_fence_after();
+            const float f = dev::fast_exp2(ro - r);
+#pragma unroll 1
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t o[16];
+              tc::tmem_ld16(tl + 16 * k, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc::tmem_st16(tl + 16 * k, o);
+            }
+          }
+          refs[row] = r;
+          arrive(C::B_REF + b);
+          said = true;
           // F is held below 2^126: where that cuts, a weight is below 2^-70 of the largest
           const float F = fminf(vs * dev::fast_exp2(fminf(back - r + kLift, 126.0f)), 0x1p126f);
           float sum = 0.0f;
@@ -668,48 +688,9 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           }
           l += sum;
         }
-        const float held = r;                    // P's reference
-        if (!fetched) {
-          if (!wait(C::B_REF + C::buf(n - 1), C::phase(n - 1))) return;
-          ro = refs[row];
-          r = fmaxf(r, ro);
-        }
-        if (__any_sync(kFull, r != held || r != ro)) {
-          if (__any_sync(kFull, r != held)) {          // P to the reference that the page before left
-            const float f = dev::fast_exp2(held - r);
-            tc::tmem_wait_st();
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-              uint32_t x[16];
-              tc::tmem_ld16(ts + 16 * k, x);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-                x[i] = dev::pack_f16x2(y.x * f, y.y * f);
-              }
-              tc::tmem_st16(ts + 16 * k, x);
-            }
-          }
-          if (j > 0) {                                       // O to this page's, once the pages before are all in
-            if (!wait(C::B_O_DONE + C::buf(n - 1), C::phase(n - 1))) return;
-            tc::tc_fence_after();
-            const float f = dev::fast_exp2(ro - r);
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t o[16];
-              tc::tmem_ld16(tl + 16 * k, o);
-              tc::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tc::tmem_st16(tl + 16 * k, o);
-            }
-          }
-        }
-        refs[row] = r;
+        tc::tmem_wait_st();
       }
-      arrive(C::B_REF + b);
-      if (!idle) tc::tmem_wait_st();
+      if (!said) arrive(C::B_REF + b);
       tc::tc_fence_before();
       arrive(C::B_P_FULL + b);
     }
@@ -866,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
   const TreeWorker work = a.workers[blockIdx.x];
 
   if (warp < C::kConvertWarp) {
-    role_softmax<D, E4M3>(a, sy, work, warp / 4, tid & 127, sbase, tbase, nan_seen);
+    role_softmax<D, E4M3>(a, sy, work, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
     role_convert<D, E4M3>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
   } else if (warp == C::kLoadWarp) {
