@@ -19,7 +19,7 @@ using namespace qkvp;
 namespace {
 
 // Pages of work that starting a segment counts as, and pages below which a worker is not worth its start.
-constexpr int kStartPages = 4;
+int start_pages(int dim) { return dim == 64 ? 5 : dim == 128 ? 12 : 8; }
 constexpr int kMinPages = 2;
 
 }  // namespace
@@ -89,11 +89,11 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   const int workers = static_cast<int>(std::min<int64_t>(num_sms, useful));
   SplitInfo info;
   info.num_segments = rows + workers;      // each worker's end cuts one row at most; asked-for splits are counted first
-  if (min_splits > 0) split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, kStartPages);
+  if (min_splits > 0) split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, SplitOut{}, info, start_pages(head_dim));
   std::vector<Segment> cut(static_cast<size_t>(std::max<int64_t>(1, info.num_segments)));
   std::vector<int32_t> wptr(workers + 1), rptr(rows + 1), wide(std::max<int64_t>(1, rows));
   SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
-  if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, kStartPages)) return QKVP_E_INVALID;
+  if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, start_pages(head_dim))) return QKVP_E_INVALID;
   if (info.num_segments > INT32_MAX) return QKVP_E_UNSUPPORTED;
   const TreeTable t = tree_table(info.num_segments, workers, info.split_reqs);
 

@@ -505,6 +505,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
   int begin = 0;                                 // the segment's first page among the worker's
   for (int si = work.begin; si < work.end; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
+    if (si + 1 < work.end) asm volatile("prefetch.global.L1 [%0];" :: "l"(a.segs + si + 1));
     const bool live = row < s.rows, idle = (row & ~31) >= s.rows;   // a warp without a row has no logits to turn
     const int t = (s.row0 + row) / group;        // drafted token and query head
     // the row among those of q, out and lse; -1: none
