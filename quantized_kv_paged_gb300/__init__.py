@@ -8,8 +8,10 @@ PyTorch is used for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
+from array import array
 
 import numpy as np
 
@@ -71,10 +73,6 @@ class qkvp_tree_plan(ctypes.Structure):
     as_dict = qkvp_plan.as_dict
 
 
-class qkvp_pool(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
-
-
 class qkvp_page_state(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("table", "held", "lens", "refs", "free_list", "free_count")] + [
         ("rows", ctypes.c_int32), ("row_pages", ctypes.c_int32), ("num_pages", ctypes.c_int64)]
@@ -125,7 +123,7 @@ def load(path: str | None = None):
         L.gqa_tree_run.argtypes = [c.POINTER(qkvp_tree_plan), vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, u64, vp]
         L.gqa_tree_commit.argtypes = [vp, vp, i32, vp, i32, vp, vp, i64, vp, vp, i32, i32, i32, i32, i32, i64, vp]
         L.kv_pages_workspace.argtypes = [i64, i32, i32, c.POINTER(u64)]
-        pool, state = c.POINTER(qkvp_pool), c.POINTER(qkvp_page_state)
+        pool, state = vp, c.POINTER(qkvp_page_state)      # pool: qkvp_pool array
         L.kv_pages_copy.argtypes = [pool, i32, vp, vp, i64, i64, vp]
         L.kv_pages_fork.argtypes = [pool, i32, state, vp, vp, i32, vp, vp, u64, vp]
         L.kv_pages_grow.argtypes = [state, vp, vp, i32, vp, vp, u64, vp]
@@ -297,11 +295,24 @@ class _Torch:
             cls.torch = torch
             cls.bf16, cls.f32, cls.i32, cls.i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
             cls.u32 = torch.uint32
+            # for looks over lists of tensors
+            cls.ptr, cls.stride, cls.numel, cls.device = torch.Tensor.data_ptr, torch.Tensor.stride, torch.Tensor.numel, torch.Tensor.get_device
+            cls.contiguous, cls.dtype, cls.itemsize = torch.Tensor.is_contiguous, operator.attrgetter("dtype"), torch.Tensor.element_size
             cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
             # the current stream's handle without a Stream object around it, where this torch has the call
             cls.handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
             cls.ready = True
         return cls
+
+
+def _alike(name: str, tensors, dtypes, T, here: int):
+    """Refuses tensors that do not lie in memory as the first one does, of another type or on another device. A call takes two
+    for each layer, so each look goes over the whole list."""
+    first = tensors[0]
+    if len(set(map(T.stride, tensors))) > 1 or len(set(map(T.numel, tensors))) > 1 or not set(map(T.dtype, tensors)) <= dtypes or set(map(T.device, tensors)) != {here}:
+        for i, t in enumerate(tensors):
+            if t.shape != first.shape or t.stride() != first.stride() or t.dtype not in dtypes or t.get_device() != here:
+                _refuse(f"{name}[{i}]", t, first.shape, dtypes, "a contiguous layout", here)
 
 
 def _refuse(name: str, t, shape, dtype, layout: str, here: int):
@@ -577,13 +588,11 @@ def gqa_tree_commit(kv_data, kv_scale, cache_dtype: int, kv_len, kv_indptr, kv_i
     if layers != len(kv_scale):
         raise ValueError(f"{layers} layers of kv_data and {len(kv_scale)} of kv_scale")
     here = kv_len.get_device()
-    pages = heads = 0
-    dim = 64
-    for i, (data, scale) in enumerate(zip(kv_data, kv_scale)):
-        shape = _head_pool(data, scale, T, here)
-        if i and shape != (pages, heads, dim):
-            raise ValueError(f"layer {i} has (pages, KV heads, head dim) {shape}, the ones before it {(pages, heads, dim)}")
-        pages, heads, dim = shape
+    pages, heads, dim = 0, 1, 64
+    if layers:
+        pages, heads, dim = _head_pool(kv_data[0], kv_scale[0], T, here)
+        _alike("kv_data", kv_data, set(T.codes), T, here)
+        _alike("kv_scale", kv_scale, {T.f32}, T, here)
     batch, nnz, i32 = kv_len.shape[0], kv_indices.shape[0], T.i32
     max_path = path.shape[-1]
     _dense("kv_len", kv_len, (batch,), i32, here)
@@ -592,11 +601,10 @@ def gqa_tree_commit(kv_data, kv_scale, cache_dtype: int, kv_len, kv_indptr, kv_i
     _dense("path", path, (batch, max_path), i32, here)
     _dense("path_len", path_len, (batch,), i32, here)
     on = _launch_on(stream, here)
-    data = (ctypes.c_void_p * max(1, layers))(*[t.data_ptr() for t in kv_data])
-    scales = (ctypes.c_void_p * max(1, layers))(*[t.data_ptr() for t in kv_scale])
-    st = (_lib or load()).gqa_tree_commit(data, scales, layers, kv_len.data_ptr(), batch, kv_indptr.data_ptr(),
+    data, scales = array("Q", map(T.ptr, kv_data)), array("Q", map(T.ptr, kv_scale))
+    st = (_lib or load()).gqa_tree_commit(data.buffer_info()[0], scales.buffer_info()[0], layers, kv_len.data_ptr(), batch, kv_indptr.data_ptr(),
                                           kv_indices.data_ptr(), nnz, path.data_ptr(), path_len.data_ptr(), max_path,
-                                          max(1, heads), dim, cache_dtype, PAGE_SIZE, pages, on)
+                                          heads, dim, cache_dtype, PAGE_SIZE, pages, on)
     return st if st == QKVP_OK else _check("gqa_tree_commit", st, raise_on_error)
 
 
@@ -607,16 +615,20 @@ def kv_pages_workspace(num_pages: int, rows: int, n: int) -> int:
     return size.value
 
 
-def _pools(pools, num_pages: int, here: int):
-    """The pools as the C array; every one a contiguous tensor with a page for each first index."""
-    arr = (qkvp_pool * max(1, len(pools)))()
-    for i, t in enumerate(pools):
-        if t.get_device() != here:
-            raise ValueError(f"tensors need to be on one device, the current CUDA device: pool {i} is on {t.device}")
-        if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous():
-            raise ValueError(f"pool {i} needs a contiguous layout and {num_pages} pages; got {tuple(t.shape)}, strides {t.stride()}")
-        arr[i].data = t.data_ptr()
-        arr[i].page_bytes = t.nbytes // num_pages if num_pages else 4
+def _pools(pools, num_pages: int, T, here: int):
+    """The pools as the C array (data, page_bytes); every one a contiguous tensor with a page for each first index. A call
+    takes one or two for each layer, so each look goes over the whole list."""
+    step = [s[0] if s else 0 for s in map(T.stride, pools)]      # elements of a page
+    if pools and (set(map(T.device, pools)) != {here} or not all(map(T.contiguous, pools)) or
+                  [n * num_pages for n in step] != list(map(T.numel, pools)) or 0 in step):
+        for i, t in enumerate(pools):
+            if t.get_device() != here:
+                raise ValueError(f"tensors need to be on one device, the current CUDA device: pool {i} is on {t.device}")
+            if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous() or t.stride(0) * num_pages != t.numel():
+                raise ValueError(f"pool {i} needs a contiguous layout and {num_pages} pages; got {tuple(t.shape)}, strides {t.stride()}")
+    arr = array("q", bytes(16 * len(pools)))
+    arr[::2] = array("q", map(T.ptr, pools))
+    arr[1::2] = array("q", map(operator.mul, step, map(T.itemsize, pools)))
     return arr
 
 
@@ -640,9 +652,9 @@ def kv_pages_copy(pools, src, dst, stream=None, raise_on_error: bool = True) -> 
     _dense("src", src, (n,), T.i32, here)
     _dense("dst", dst, (n,), T.i32, here)
     pages = pools[0].shape[0] if len(pools) else 0
-    arr = _pools(pools, pages, here)
+    arr = _pools(pools, pages, T, here)
     on = _launch_on(stream, here)
-    st = (_lib or load()).kv_pages_copy(arr, len(pools), src.data_ptr(), dst.data_ptr(), n, pages, on)
+    st = (_lib or load()).kv_pages_copy(arr.buffer_info()[0], len(pools), src.data_ptr(), dst.data_ptr(), n, pages, on)
     return st if st == QKVP_OK else _check("kv_pages_copy", st, raise_on_error)
 
 
@@ -655,10 +667,10 @@ def kv_pages_fork(pools, table, held, lens, refs, free_list, free_count, parents
     state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
     for name, t in (("parents", parents), ("children", children), ("status", status)):
         _dense(name, t, (n,), T.i32, here)
-    arr = _pools(pools, refs.shape[0], here)
+    arr = _pools(pools, refs.shape[0], T, here)
     _workspace(workspace, here)
     on = _launch_on(stream, here)
-    st = (_lib or load()).kv_pages_fork(arr, len(pools), ctypes.byref(state), parents.data_ptr(), children.data_ptr(), n,
+    st = (_lib or load()).kv_pages_fork(arr.buffer_info()[0], len(pools), ctypes.byref(state), parents.data_ptr(), children.data_ptr(), n,
                                         status.data_ptr(), workspace.data_ptr(), workspace.nbytes, on)
     return st if st == QKVP_OK else _check("kv_pages_fork", st, raise_on_error)
 
@@ -697,10 +709,10 @@ def kv_pages_compact(pools, table, held, lens, refs, free_list, free_count, work
     T = _Torch.get()
     here = table.get_device()
     state = _page_state(table, held, lens, refs, free_list, free_count, T, here)
-    arr = _pools(pools, refs.shape[0], here)
+    arr = _pools(pools, refs.shape[0], T, here)
     _workspace(workspace, here)
     on = _launch_on(stream, here)
-    st = (_lib or load()).kv_pages_compact(arr, len(pools), ctypes.byref(state), workspace.data_ptr(), workspace.nbytes, on)
+    st = (_lib or load()).kv_pages_compact(arr.buffer_info()[0], len(pools), ctypes.byref(state), workspace.data_ptr(), workspace.nbytes, on)
     return st if st == QKVP_OK else _check("kv_pages_compact", st, raise_on_error)
 
 
