@@ -309,9 +309,10 @@ def _alike(name: str, tensors, dtypes, T, here: int):
     """Refuses tensors that do not lie in memory as the first one does, of another type or on another device. A call takes two
     for each layer, so each look goes over the whole list."""
     first = tensors[0]
-    if len(set(map(T.stride, tensors))) > 1 or len(set(map(T.numel, tensors))) > 1 or not set(map(T.dtype, tensors)) <= dtypes or set(map(T.device, tensors)) != {here}:
+    if (len(set(map(T.stride, tensors))) > 1 or len(set(map(T.numel, tensors))) > 1 or not all(map(T.contiguous, tensors)) or
+            not set(map(T.dtype, tensors)) <= dtypes or set(map(T.device, tensors)) != {here}):
         for i, t in enumerate(tensors):
-            if t.shape != first.shape or t.stride() != first.stride() or t.dtype not in dtypes or t.get_device() != here:
+            if t.shape != first.shape or not t.is_contiguous() or t.dtype not in dtypes or t.get_device() != here:
                 _refuse(f"{name}[{i}]", t, first.shape, dtypes, "a contiguous layout", here)
 
 
@@ -651,7 +652,7 @@ def kv_pages_copy(pools, src, dst, stream=None, raise_on_error: bool = True) -> 
     here, n = src.get_device(), src.shape[0]
     _dense("src", src, (n,), T.i32, here)
     _dense("dst", dst, (n,), T.i32, here)
-    pages = pools[0].shape[0] if len(pools) else 0
+    pages = pools[0].shape[0] if len(pools) and pools[0].dim() else 0
     arr = _pools(pools, pages, T, here)
     on = _launch_on(stream, here)
     st = (_lib or load()).kv_pages_copy(arr.buffer_info()[0], len(pools), src.data_ptr(), dst.data_ptr(), n, pages, on)

@@ -175,3 +175,19 @@ def test_captured_and_replayed(qkvp):
         s.release([2, 3, 4, 5])
         s.compact()
         s.same(state, pools)
+
+
+def test_pages_of_latent_pools(qkvp):
+    """Every cache layout of the library has its page first, so its codes and scales are pools like any other."""
+    rng = np.random.default_rng(9)
+    shapes = [(12, 64, 576), (12, 64, 288), (12, 64, 36), (12, 64, 580), (12, 2, 3, 64, 128)]
+    host = [rng.integers(0, 256, s, dtype=np.uint8) for s in shapes] + [rng.standard_normal((12, 2, 3)).astype(np.float32)]
+    d = [torch.from_numpy(x).cuda() for x in host]
+    d.append(torch.randn((12, 64, 576), device="cuda").bfloat16())
+    last = d[-1].clone()
+    q.kv_pages_copy(d, dev([0, 3, 7]), dev([11, 2, 6]))
+    for x, got in zip(host, d):
+        x[[11, 2, 6]] = x[[0, 3, 7]]
+        assert np.array_equal(got.cpu().numpy(), x)
+    last[[11, 2, 6]] = last[[0, 3, 7]]
+    assert torch.equal(d[-1], last)

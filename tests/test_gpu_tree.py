@@ -204,3 +204,80 @@ def test_captured_and_replayed(qkvp):
         call()
         torch.cuda.synchronize()
         assert torch.equal(got[0].view(torch.int16), out.view(torch.int16)) and torch.equal(got[1], lse)
+
+
+@pytest.mark.parametrize("sms", [1, 2, 5])
+@pytest.mark.parametrize("heads,kv_heads,dim,window", [(8, 2, 128, 0), (8, 4, 64, 300), (3, 1, 256, 0)])
+def test_few_workers_with_many_segments(qkvp, sms, heads, kv_heads, dim, window):
+    """One worker goes through segments of every kind: 1 to 128 rows, one to many pages, split ones and whole ones."""
+    b = Batch(20 + sms, [700, 3, 0, 64, 129, 1500, 1, 63], [40, 1, 64, 33, 2, 7, 150, 65], heads, kv_heads, dim, q.CACHE_E4M3, empty=0.1)
+    for splits in (0, 30):
+        out, lse, plan = b.run(q, dim ** -0.5, window=window, sinks=5 if window else 0, num_sms=sms, min_splits=splits)
+        assert plan.num_workers == sms
+        check(b, out, lse, b.reference(dim ** -0.5, window, 5 if window else 0))
+
+
+def test_queries_that_hold_no_number_stay_in_their_rows(qkvp):
+    """The other rows are as near to 64 bits as ever. (Not the same bits: rows of a warp share the choice of when their
+    running maximum is renewed, which moves roundings.)"""
+    b = Batch(21, [200, 30], [20, 9], 8, 2, 128, q.CACHE_E4M3)
+    ref = b.reference(0.1)
+    b.q[3, 2, 5], b.q[7, 0, 0], b.q[28, 7, 127] = float("nan"), float("inf"), float("-inf")
+    out, lse, _ = b.run(q, 0.1)
+    bad = np.zeros(lse.shape, bool)
+    bad[3, 2] = bad[7, 0] = bad[28, 7] = True
+    assert not torch.isfinite(lse.cpu()[torch.from_numpy(bad)]).any()
+    keep = torch.from_numpy(~bad).cuda()
+    R.check_attend(out[keep], lse[keep], tuple(x[~bad] for x in ref), int(b.lens.max()) + 64, 128)
+
+
+def test_mask_bits_behind_the_last_drafted_token_do_not_count(qkvp):
+    b = Batch(22, [100, 64, 0], [5, 40, 33], 4, 2, 64, q.CACHE_INT8, extra_words=2)
+    want, lse, _ = b.run(q, 0.1)
+    for r, n in enumerate(b.drafted):
+        for i in range(b.tok[r], b.tok[r + 1]):
+            for k in range(n, 32 * b.words):
+                b.mask[i, k // 32] |= np.uint32(1 << (k % 32))
+    out, lse2, _ = b.run(q, 0.1)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse2, lse)
+
+
+def test_pages_past_32_bits(qkvp):
+    """A pool of 5 GB whose used pages begin behind 2^32 bytes, decoded, committed and copied."""
+    b = Batch(23, [300, 90], [20, 33], 16, 8, 128, q.CACHE_E4M3, spare=3)
+    pages, first = 40000, 40000 - b.pages
+    codes, scale = torch.zeros((pages, 2, 8, 64, 128), dtype=torch.uint8, device="cuda"), torch.zeros((pages, 2, 8), device="cuda")
+    codes[first:], scale[first:] = torch.from_numpy(b.codes), torch.from_numpy(b.scale)
+    assert first * codes[0].numel() > 2 ** 32
+    want, want_lse, _ = b.run(q, 0.1)
+    plan, ws = b.plan(q)
+    out, lse, ids = torch.zeros_like(want), torch.zeros_like(want_lse), torch.from_numpy(b.ids + first).to(torch.int32).cuda()
+    q.gqa_tree_run(plan, b.q.cuda(), codes, scale, ids, torch.from_numpy(b.mask.view(np.int32)).cuda(), 0.1, out, lse, ws)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse, want_lse)
+    from tests import tree_ref as T
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, np.int32)).cuda()          # noqa: E731
+    path, n = np.array([[0, 3, 5, 19], [1, 2, 30, 0]]), np.array([4, 3])
+    q.gqa_tree_commit([codes], [scale], b.cache, i32(b.cached), i32(b.indptr), ids, i32(path), i32(n))
+    T.commit(b.codes, b.scale, b.cache, b.cached, b.indptr, b.ids, path, n)
+    assert np.array_equal(codes[first:].cpu().numpy(), b.codes) and np.array_equal(scale[first:].cpu().numpy(), b.scale)
+    q.kv_pages_copy([codes, scale], i32([pages - 1, first]), i32([1, pages - 2]))
+    assert np.array_equal(codes[1].cpu().numpy(), b.codes[-1]) and np.array_equal(codes[pages - 2].cpu().numpy(), b.codes[0])
+    assert not codes[2:first].any()
+
+
+def test_two_streams_at_once(qkvp):
+    jobs = [Batch(24 + i, [900, 77, 1300], [33, 50, 64], 8, 2, 128, q.CACHE_E4M3) for i in range(2)]
+    want = [b.run(q, 0.1)[:2] for b in jobs]
+    streams, held = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for b in jobs:
+        plan, ws = b.plan(q)
+        held.append((plan, b.q.cuda(), torch.from_numpy(b.codes).cuda(), torch.from_numpy(b.scale).cuda(), torch.from_numpy(b.ids).cuda(),
+                     torch.from_numpy(b.mask.view(np.int32)).cuda(), ws))
+    outs = [(torch.zeros_like(o), torch.zeros_like(l)) for o, l in want]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, (plan, qq, codes, scale, ids, mask, ws), (o, l) in zip(streams, held, outs):
+            q.gqa_tree_run(plan, qq, codes, scale, ids, mask, 0.1, o, l, ws, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(outs, want):
+        assert torch.equal(o.view(torch.int16), wo.view(torch.int16)) and torch.equal(l, wl)

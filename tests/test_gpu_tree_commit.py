@@ -102,3 +102,42 @@ def test_captured_and_replayed(qkvp):
         c, s = c0.copy(), s0.copy()
         T.commit(c, s, q.CACHE_E4M3, kv_len.tolist(), indptr.tolist(), ids.tolist(), np.array(new), length)
         assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scale.cpu().numpy(), s)
+
+
+@pytest.mark.parametrize("cache", [q.CACHE_E4M3, q.CACHE_INT8])
+def test_scales_at_the_ends_of_the_range(qkvp, cache):
+    """Values past FP32's range do not count towards a block's amax; subnormal, negative, infinite and NaN scales of the pages
+    that tokens come from (a block that takes them has a scale that is not negative)."""
+    rng = np.random.default_rng(11)
+    big = [3e38, 3.4e38 / R.QMAX[cache], 2.7e36, 1e37, -3e36, 2e-45, np.inf, np.nan, -0.25, 1e-38]
+    batch, per = 2 * len(big), 2
+    layers = layers_of(rng, 2, batch * per, 2, 64, cache, 0)
+    codes, scale = layers[0]
+    codes[1::2, :, :, :3] = rng.integers(0, 256, codes[1::2, :, :, :3].shape, dtype=np.uint8)      # every code, -128 and NaN too
+    ids = np.arange(batch * per)
+    for r in range(batch):
+        scale[2 * r + 1] = np.float32(big[r % len(big)])
+        scale[2 * r] *= np.float32(1 if r < len(big) else 1e-38)
+    path = np.array([[3, 6, 8]] * batch)
+    run(layers, cache, [58 + r % 4 for r in range(batch)], np.arange(batch + 1) * per, ids, path, [3] * batch)
+
+
+def test_two_streams_at_once(qkvp):
+    """Two pools committed on two streams, more layers than one warp's share, with nothing between the calls."""
+    rng = np.random.default_rng(12)
+    batch, per, layers = 5, 4, 40
+    ids, indptr, kv_len = np.arange(batch * per), np.arange(batch + 1) * per, np.array([0, 63, 64, 100, 128])
+    path, n = np.array([[1, 2, 4, 8, 16, 40]] * batch), [6, 5, 4, 6, 0]
+    streams, jobs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for i in range(2):
+        host = layers_of(rng, layers, batch * per, 3, 128, q.CACHE_E4M3, 2)
+        jobs.append((host, [(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()) for c, s in host]))
+    args = [torch.from_numpy(np.asarray(x, np.int32)).cuda() for x in (kv_len, indptr, ids, path, n)]
+    torch.cuda.synchronize()
+    for s, (_, dev) in zip(streams, jobs):
+        q.gqa_tree_commit([c for c, _ in dev], [x for _, x in dev], q.CACHE_E4M3, *args, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for host, dev in jobs:
+        for (c, s), (gc, gs) in zip(host, dev):
+            T.commit(c, s, q.CACHE_E4M3, kv_len, indptr, ids, path, n)
+            assert np.array_equal(gc.cpu().numpy(), c) and np.array_equal(gs.cpu().numpy(), s)
