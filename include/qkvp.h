@@ -509,11 +509,13 @@ typedef struct {
   int32_t max_drafted;         /* most drafted tokens of a request */
   int32_t num_workers;         /* CTAs of the attention kernel */
   int32_t num_segments;        /* (request, KV head, block of 128 query rows, page range) pieces */
-  int32_t num_joins;           /* row blocks cut into more than one segment */
+  int32_t num_joins;           /* row blocks whose partials are joined: those cut into more than one segment (all with row_copies) */
   int32_t max_join_segments;   /* most segments of one row block */
   int32_t num_partials;        /* FP32 split partials held in the workspace */
   int32_t max_worker_pages, min_worker_pages;
   int32_t table_entries;       /* entries of kv_indices that the plan may address: kv_indptr[batch] */
+  int32_t row_copies;          /* 1; 2 or 4 where up to 64 or 32 rows lie that often in a block, each copy with its share of a page's tokens */
+  int32_t reserved;
   int64_t total_pages;         /* pages read, summed over requests (of one KV head and row block) */
   uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;
   uint64_t status_offset;      /* int32 status word, as in qkvp_plan */

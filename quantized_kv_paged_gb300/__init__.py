@@ -66,7 +66,7 @@ class qkvp_tree_plan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "batch", "num_heads", "num_kv_heads", "head_dim", "page_size", "cache_dtype", "window", "sinks", "num_tokens",
         "max_drafted", "num_workers", "num_segments", "num_joins", "max_join_segments", "num_partials",
-        "max_worker_pages", "min_worker_pages", "table_entries")] + [
+        "max_worker_pages", "min_worker_pages", "table_entries", "row_copies", "reserved")] + [
         ("total_pages", ctypes.c_int64)] + [(n, ctypes.c_uint64) for n in (
             "workspace_bytes", "table_bytes", "partial_o_offset", "partial_lse_offset", "status_offset", "magic")]
 

@@ -21,6 +21,8 @@ namespace {
 // Pages of work that starting a segment counts as, and pages below which a worker is not worth its start.
 int start_pages(int dim) { return dim == 64 ? 5 : dim == 128 ? 12 : 8; }
 constexpr int kMinPages = 2;
+// Pages of a block on average from which a block of few rows takes copies of them: every block's partials are joined then.
+constexpr int kCopyPages = 16;
 
 }  // namespace
 
@@ -95,6 +97,14 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
   if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, start_pages(head_dim))) return QKVP_E_INVALID;
   if (info.num_segments > INT32_MAX) return QKVP_E_UNSUPPORTED;
+  const int widest = std::min<int64_t>(block, static_cast<int64_t>(max_drafted) * group);
+  const int copies = row_pages < rows * kCopyPages ? 1 : widest <= block / 4 ? 4 : widest <= block / 2 ? 2 : 1;
+  if (copies > 1) {      // every block is joined, from its copies at the least
+    for (int64_t row = 0; row < rows; ++row)
+      if (rptr[row + 1] - rptr[row] == 1) cut[rptr[row]].partial = static_cast<int32_t>(info.partials++);
+    info.split_reqs = static_cast<int32_t>(rows);
+    info.max_req_segs = std::max(info.max_req_segs, 1);
+  }
   const TreeTable t = tree_table(info.num_segments, workers, info.split_reqs);
 
   plan->batch = batch;
@@ -115,6 +125,7 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   plan->max_worker_pages = info.max_pages;
   plan->min_worker_pages = info.min_pages;
   plan->table_entries = batch > 0 ? kv_indptr_host[batch] : 0;
+  plan->row_copies = copies;
   plan->total_pages = pages;
   plan->table_bytes = t.bytes;
   plan->status_offset = t.status;
@@ -168,7 +179,7 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
       g.num_pages = cut[x].num_pages;
       g.partial = cut[x].partial;
     }
-    if (m > 1) {
+    if (m > 1 || copies > 1) {
       TreeJoin& j = joins[num_joins++];
       j.first = cut[rptr[row]].partial;
       j.count = m;
@@ -225,7 +236,7 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
   a.sinks = plan->sinks;
   a.num_workers = plan->num_workers;
   a.num_joins = plan->num_joins;
-  a.max_join = plan->max_join_segments;
+  a.row_copies = plan->row_copies;
   a.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
   a.flip = std::signbit(sm_scale) ? 0x80008000u : 0u;
   return launch_tree(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QKVP_OK : QKVP_E_CUDA;

@@ -276,11 +276,11 @@ struct TreeArgs {
   const TreeJoin* joins;
   int* status;
   float* part_o;              // [num_partials][D / 4][128][4], normalised
-  float* part_lse;            // [num_partials][128], log2 domain
+  float* part_lse;            // [num_partials][128], log2 domain; with row_copies the lanes are [row_copies][128 / row_copies]
   uint16_t* out;              // bf16 [n][H][D]
   float* lse;                 // [n][H] or null
   int heads, kv_heads, dim, cache_dtype, words, window, sinks;
-  int num_workers, num_joins, max_join;
+  int num_workers, num_joins, row_copies;
   float scale_log2;           // |sm_scale| log2(e)
   uint32_t flip;              // 0x80008000 where sm_scale is negative: turns Q's signs
 };

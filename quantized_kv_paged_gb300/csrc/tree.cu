@@ -488,12 +488,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int D, bool E4M3>
+// kCopies: each row lies that often among the lanes, copy i with tokens [64 i / kCopies, 64 (i + 1) / kCopies) of a page; in
+// the other columns its P is zero. Each copy is a partial of its own.
+template <int D, bool E4M3, int kCopies>
 __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, int row, uint32_t base, uint8_t* sbase, uint32_t tbase,
                              volatile int* nan_seen) {
   using C = Cfg<D>;
   const uint32_t tl = tbase + (static_cast<uint32_t>(row & ~31) << 16);   // the warp's quarter of the lanes
-  const int group = a.heads / a.kv_heads, lane = row & 31;
+  constexpr int kCols = kPage / kCopies, kLd = kCols < 32 ? kCols : 32;       // logits of a page that the thread has
+  const int group = a.heads / a.kv_heads, lane = row & 31, part = row / (kTreeTile / kCopies), rest = row % (kTreeTile / kCopies);
   volatile float* refs = reinterpret_cast<volatile float*>(sbase + C::OFF_REF);
   volatile int8_t* lifts = reinterpret_cast<volatile int8_t*>(sbase + C::OFF_QS);
   auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, sy.wait(bar, parity, 8))); };
@@ -506,10 +509,10 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
   for (int si = work.begin; si < work.end; ++si) {
     const TreeSegment s = load_segment(a.segs + si);
     if (si + 1 < work.end) asm volatile("prefetch.global.L1 [%0];" :: "l"(a.segs + si + 1));
-    const bool live = row < s.rows, idle = (row & ~31) >= s.rows;   // a warp without a row has no logits to turn
-    const int t = (s.row0 + row) / group;        // drafted token and query head
+    const bool live = rest < s.rows, idle = (rest & ~31) >= s.rows;   // a warp without a row has no logits to turn
+    const int t = (s.row0 + rest) / group;       // drafted token and query head
     // the row among those of q, out and lse; -1: none
-    const int64_t head = live ? static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + row) % group : -1;
+    const int64_t head = live ? static_cast<int64_t>(s.tok0 + t) * a.heads + s.kv_head * group + (s.row0 + rest) % group : -1;
     RowMask mask;
     mask.init(a, s, live ? t : 0);
     // ---- Q: 2^e brings the row's largest |q| to [2^14, 2^15), where FP16 holds 8 bits down to 2^-29 of it. Each of the two warps
@@ -588,14 +591,17 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           const uint64_t scale2 = pair(zs, zs), shift2 = pair(-shift, -shift);
           uint64_t sum0 = 0, sum1 = 0;
           float top0 = -INFINITY, top1 = -INFINITY;
-          uint32_t pk[32], x[2][32];
-          tc::tmem_ld32(ts, x[0]);
-          tc::tmem_ld32(ts + 32, x[1]);
+          uint32_t pk[kCols / 2], x[kCols / kLd][kLd];
+#pragma unroll
+          for (int h = 0; h < kCols / kLd; ++h) {
+            if constexpr (kLd == 32) tc::tmem_ld32(ts + part * kCols + 32 * h, x[h]);
+            else tc::tmem_ld16(ts + part * kCols, x[h]);
+          }
           tc::tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kCols / kLd; ++h) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < kLd / 2; ++k) {
               const float x0 = __uint_as_float(x[h][2 * k]), x1 = __uint_as_float(x[h][2 * k + 1]);
               if (k & 1) top1 = max3(top1, x0, x1);
               else top0 = max3(top0, x0, x1);
@@ -605,7 +611,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
               z1 = dev::fast_exp2(z1);
               if (k & 1) sum1 = add2(sum1, pair(z0, z1));
               else sum0 = add2(sum0, pair(z0, z1));
-              pk[16 * h + k] = dev::pack_f16x2(z0, z1);
+              pk[kLd / 2 * h + k] = dev::pack_f16x2(z0, z1);
             }
           }
           const float z = fmaxf(top0, top1) * zs, m_new = fmaxf(m, z);
@@ -616,7 +622,18 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           if (good) {
             arrive(C::B_REF + b);                // refs[row] stays
             said = true;
-            tc::tmem_st32<false>(ts, pk);
+            if constexpr (kCopies == 1) {
+              tc::tmem_st32<false>(ts, pk);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kCopies; ++i) {
+                uint32_t y[kCols / 2];
+#pragma unroll
+                for (int u = 0; u < kCols / 2; ++u) y[u] = i == part ? pk[u] : 0;
+                if constexpr (kCopies == 2) tc::tmem_st16(ts + 16 * i, y);
+                else tc::tmem_st8(ts + 8 * i, y);
+              }
+            }
             float a0, a1;
             unpair(add2(sum0, sum1), a0, a1);
             l = fmaf(a0 + a1, dev::fast_exp2(shift - m_new), l * dev::fast_exp2(m - m_new));
@@ -634,7 +651,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           if (masked) bits = info.z & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
           float top = -INFINITY;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
+          for (int k = part * (4 / kCopies); k < (part + 1) * (4 / kCopies); ++k) {
             uint32_t x[16];
             tc::tmem_ld16(ts + 16 * k, x);
             tc::tmem_wait_ld();
@@ -675,7 +692,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
             uint32_t x[16], pk[8];
             tc::tmem_ld16(ts + 16 * k, x);
             tc::tmem_wait_ld();
-            const uint32_t v = static_cast<uint32_t>(bits >> (16 * k));
+            const uint32_t v = kCopies == 1 || k / (4 / kCopies) == part ? static_cast<uint32_t>(bits >> (16 * k)) : 0;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               float z0 = dev::fast_exp2(fmaf(__uint_as_float(x[2 * u]), zs, -back));
@@ -801,7 +818,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
   }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int kCopies>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArgs a) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -848,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
   const TreeWorker work = a.workers[blockIdx.x];
 
   if (warp < C::kConvertWarp) {
-    role_softmax<D, E4M3>(a, sy, work, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
+    role_softmax<D, E4M3, kCopies>(a, sy, work, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
     role_convert<D, E4M3>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
   } else if (warp == C::kLoadWarp) {
@@ -868,27 +885,29 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
 }
 
 // Joins the partials of blocks that were cut. A lane has a row, a warp 8 columns of 32 rows, so that all reads are of whole
-// lines; the slots are summed in order. Grid: (32 rows of a block, 64 columns, joins).
+// lines; the slots, and a slot's copies of the row, are summed in order. Grid: (joins, 32 rows of a block, 64 columns).
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs a) {
   dev::wait_for_previous();
   dev::allow_dependents();
-  const TreeJoin* jp = a.joins + blockIdx.z;
-  const int first = jp->first, count = jp->count, rows = jp->rows, pitch = kTreeTile;
-  const int row = blockIdx.x * 32 + (threadIdx.x & 31), c8 = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const TreeJoin* jp = a.joins + blockIdx.x;
+  const int first = jp->first, count = jp->count * a.row_copies, rows = jp->rows;
+  const int copy = kTreeTile / a.row_copies;     // lanes from one copy of a row to the next
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), c8 = blockIdx.z * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const float* lse = a.part_lse + static_cast<int64_t>(first) * pitch + row;
+  const float* lse = a.part_lse + static_cast<int64_t>(first) * kTreeTile + row;
   float m = -INFINITY;
 #pragma unroll 8
-  for (int i = 0; i < count; ++i) m = fmaxf(m, lse[static_cast<int64_t>(i) * pitch]);
+  for (int i = 0; i < count; ++i) m = fmaxf(m, lse[static_cast<int64_t>(i) * copy]);
   const float back = m == -INFINITY ? 0.0f : m;
-  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (static_cast<int64_t>(first) * (D / 4) + 2 * c8) * pitch + row;
+  const float4* src = reinterpret_cast<const float4*>(a.part_o) + (static_cast<int64_t>(first) * (D / 4) + 2 * c8) * kTreeTile + row;
   float total = 0.0f, acc[8] = {};
 #pragma unroll 4
   for (int i = 0; i < count; ++i) {
-    const float w = dev::fast_exp2(lse[static_cast<int64_t>(i) * pitch] - back);
-    const float4 x = src[static_cast<int64_t>(i) * (D / 4) * pitch], y = src[static_cast<int64_t>(i) * (D / 4) * pitch + pitch];
+    const float w = dev::fast_exp2(lse[static_cast<int64_t>(i) * copy] - back);
+    const int64_t at = static_cast<int64_t>(i / a.row_copies) * (D / 4) * kTreeTile + i % a.row_copies * copy;
+    const float4 x = src[at], y = src[at + kTreeTile];
     total += w;
     const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -905,20 +924,25 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs 
   if (c8 == 0 && a.lse) a.lse[head] = none ? -INFINITY : (m + log2f(total)) * 0.69314718055994531f;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int kCopies>
 cudaError_t launch_attend(const TreeArgs& a, cudaStream_t s) {
   using C = Cfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, E4M3, kCopies>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(tree_kernel<D, E4M3>, static_cast<unsigned>(a.num_workers), C::kThreads, C::kSmem, s, a);
+  return launch_overlapped(tree_kernel<D, E4M3, kCopies>, static_cast<unsigned>(a.num_workers), C::kThreads, C::kSmem, s, a);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_copies(const TreeArgs& a, cudaStream_t s) {
+  return a.row_copies == 4 ? launch_attend<D, E4M3, 4>(a, s) : a.row_copies == 2 ? launch_attend<D, E4M3, 2>(a, s) : launch_attend<D, E4M3, 1>(a, s);
 }
 
 template <int D>
 cudaError_t launch_dim(const TreeArgs& a, cudaStream_t s) {
-  const cudaError_t e = a.cache_dtype == QKVP_CACHE_E4M3 ? launch_attend<D, true>(a, s) : launch_attend<D, false>(a, s);
+  const cudaError_t e = a.cache_dtype == QKVP_CACHE_E4M3 ? launch_copies<D, true>(a, s) : launch_copies<D, false>(a, s);
   if (e != cudaSuccess || a.num_joins == 0) return e;
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(kTreeTile / 32, D / 64, static_cast<unsigned>(a.num_joins));
+  c.gridDim = dim3(static_cast<unsigned>(a.num_joins), kTreeTile / 32 / a.row_copies, D / 64);
   c.blockDim = dim3(kJoinThreads);
   c.stream = s;
   cudaLaunchAttribute attr{};
