@@ -377,8 +377,16 @@ __device__ void role_convert(const Sync& sy, int pages, int warp, int lane, uint
   }
 }
 
-// One thread a softmax warpgroup: S = Q K^T of its pages. (A thread has some 45 cycles from one product of 32 to the next; two of
-// them fill the tensor cores.)
+// The same lane of a whole warp every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+
+// One warp a softmax warpgroup: S = Q K^T of its pages. All lanes walk the pages, so that what a product names lies in uniform
+// registers, and an elected one issues. (Roles of a single thread, which moved every operand there, took some 110 cycles a
+// product: 574 against 523 us at 44 x 32,768 with 4 drafted, 291 against 265 at 16 mixed with 64.)
 template <int D>
 __device__ void role_qk(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, uint32_t base, uint32_t tbase) {
   using C = Cfg<D>;
@@ -396,20 +404,24 @@ __device__ void role_qk(const TreeArgs& a, const Sync& sy, const TreeWorker& wor
       if (n >= C::kBufs && !sy.wait(C::B_O_DONE + b, C::phase(n) ^ 1, 4)) goto out;
       tc::tc_fence_after();
       const uint32_t d = tbase + C::TM_S + b * kPage;
+      if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint64_t bd = kd.at(b * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
-        if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
-        else tc::mma_ts_k<true>(d, q + 8 * i, bd, kIdesc);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t bd = kd.at(b * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
+          if (i == 0) tc::mma_ts_k<false>(d, q, bd, kIdesc);
+          else tc::mma_ts_k<true>(d, q + 8 * i, bd, kIdesc);
+        }
+        tc::mma_commit(sy.bar(C::B_S_FULL + b));
       }
-      tc::mma_commit(sy.bar(C::B_S_FULL + b));
+      __syncwarp();
     }
   }
 out:
-  tc::mma_commit(sy.bar(C::B_FINAL));
+  __syncwarp();
+  if (elect_one()) tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
-// One thread: O += P V, page after page.
+// One warp: O += P V, page after page.
 template <int D>
 __device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& work, uint32_t base, uint32_t tbase) {
   using C = Cfg<D>;
@@ -427,17 +439,21 @@ __device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& wor
       if (!sy.wait(C::B_P_FULL + b, C::phase(n), 4)) goto out;
       tc::tc_fence_after();
       const uint32_t p = tbase + C::TM_S + b * kPage;
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kPage / 16; ++k) {
-        const uint64_t bd = vd.at(b * C::kTile + 2048 * k);
-        if (k == 0 && n == first) tc::mma_ts_k<false>(tbase, p, bd, kIdesc);
-        else tc::mma_ts_k<true>(tbase, p + 8 * k, bd, kIdesc);
+        for (int k = 0; k < kPage / 16; ++k) {
+          const uint64_t bd = vd.at(b * C::kTile + 2048 * k);
+          if (k == 0 && n == first) tc::mma_ts_k<false>(tbase, p, bd, kIdesc);
+          else tc::mma_ts_k<true>(tbase, p + 8 * k, bd, kIdesc);
+        }
+        tc::mma_commit(sy.bar(C::B_O_DONE + b));
       }
-      tc::mma_commit(sy.bar(C::B_O_DONE + b));
+      __syncwarp();
     }
   }
 out:
-  tc::mma_commit(sy.bar(C::B_FINAL));
+  __syncwarp();
+  if (elect_one()) tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -825,7 +841,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* sbase = smem_raw + (base - raw);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0);
   Sync sy;
   sy.bars = base + C::OFF_BAR;
   sy.abort = reinterpret_cast<volatile int*>(sbase + C::OFF_ABORT);
@@ -859,7 +875,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_TSLOT);
+  const uint32_t tbase = __shfl_sync(kFull, *reinterpret_cast<volatile uint32_t*>(sbase + C::OFF_TSLOT), 0);
   dev::wait_for_previous();
   dev::allow_dependents();
   const TreeWorker work = a.workers[blockIdx.x];
@@ -870,7 +886,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
     role_convert<D, E4M3>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
   } else if (warp == C::kLoadWarp) {
     role_load<D>(a, sy, work, tid & 31, base, sbase);
-  } else if ((tid & 31) == 0) {
+  } else {
     if (warp == C::kPvWarp) role_pv<D>(a, sy, work, base, tbase);
     else role_qk<D>(a, sy, work, warp - C::kQkWarp, base, tbase);
     sy.wait(C::B_FINAL, 0, 16);                      // every product has completed before tensor memory is released

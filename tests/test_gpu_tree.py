@@ -320,3 +320,19 @@ def test_copies_of_few_rows_with_nan_and_v_scales_far_apart(qkvp, drafted):
     few.ids[-2] = 0
     out, lse, _ = few.run(q, 0.1)
     check(few, out, lse, few.reference(0.1))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_pools_on_16_byte_boundaries(qkvp, dim):
+    """Codes need 16-byte alignment and no more; the bits are those of a pool on a larger boundary."""
+    b = Batch(60 + dim, [700, 5, 64], [20, 3, 40], 4, 2, dim, q.CACHE_E4M3)
+    want, lse, _ = b.run(q, 0.1)
+    plan, ws = b.plan(q)
+    flat = torch.zeros(b.codes.size + 64, dtype=torch.uint8, device="cuda")
+    codes = flat[16:16 + b.codes.size].view(b.codes.shape)
+    assert codes.data_ptr() % 32 == 16
+    codes.copy_(torch.from_numpy(b.codes))
+    out, lse2 = torch.zeros_like(want), torch.zeros_like(lse)
+    q.gqa_tree_run(plan, b.q.cuda(), codes, torch.from_numpy(b.scale).cuda(), torch.from_numpy(b.ids).cuda(), torch.from_numpy(b.mask.view(np.int32)).cuda(),
+                   0.1, out, lse2, ws)
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(lse2, lse)
