@@ -514,7 +514,7 @@ typedef struct {
   int32_t num_partials;        /* FP32 split partials held in the workspace */
   int32_t max_worker_pages, min_worker_pages;
   int32_t table_entries;       /* entries of kv_indices that the plan may address: kv_indptr[batch] */
-  int32_t row_copies;          /* 1; 2 or 4 where up to 64 or 32 rows lie that often in a block, each copy with its share of a page's tokens */
+  int32_t row_copies;          /* how often a block of few rows holds them, each copy with its share of a page's tokens: 1, 2, 4 */
   int32_t reserved;
   int64_t total_pages;         /* pages read, summed over requests (of one KV head and row block) */
   uint64_t workspace_bytes, table_bytes, partial_o_offset, partial_lse_offset;

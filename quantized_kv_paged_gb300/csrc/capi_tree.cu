@@ -21,8 +21,16 @@ namespace {
 // Pages of work that starting a segment counts as, and pages below which a worker is not worth its start.
 int start_pages(int dim) { return dim == 64 ? 5 : dim == 128 ? 12 : 8; }
 constexpr int kMinPages = 2;
-// Pages of a block on average from which a block of few rows takes copies of them: every block's partials are joined then.
-constexpr int kCopyPages = 16;
+// How often a row lies among the lanes: with 4 copies of up to 32 rows (2 of up to 64) the softmax of a page takes a quarter
+// (half) as long, but every segment leaves a partial, 512 D bytes, that is joined. 44 requests of 8 KV heads, us without and
+// with 4 copies: D 64 at 512 / 1,024 / 8,192 tokens 29 / 37 / 147 and 29 / 35 / 120; D 128 at 1,024 / 2,048 / 8,192 43 / 61 /
+// 163 and 45 / 60 / 154; D 256 at 2,048 / 4,096 / 8,192 105 / 175 / 314 and 107 / 167 / 287, but 77 and 81 where 24 blocks are
+// cut into segments of 60 pages. 2 copies: D 64 at 1,024 / 8,192 38 / 148 and 38 / 130; at D 128 and 256 within 2 % of none.
+int row_copies(int dim, int rows, int64_t pages, int64_t segments) {
+  const int few = dim == 64 ? 16 : dim == 128 ? 40 : 96;       // pages of a segment
+  if (rows <= kTreeTile / 4 && pages >= few * segments) return 4;
+  return dim == 64 && rows <= kTreeTile / 2 && pages >= 24 * segments ? 2 : 1;
+}
 
 }  // namespace
 
@@ -97,8 +105,8 @@ int gqa_tree_plan(const int32_t* kv_indptr_host, const int32_t* kv_len_host, con
   SplitOut out{cut.data(), info.num_segments, wptr.data(), rptr.data(), wide.data()};
   if (!split_pages(indptr.data(), len.data(), static_cast<int>(rows), workers, min_splits, out, info, start_pages(head_dim))) return QKVP_E_INVALID;
   if (info.num_segments > INT32_MAX) return QKVP_E_UNSUPPORTED;
-  const int widest = std::min<int64_t>(block, static_cast<int64_t>(max_drafted) * group);
-  const int copies = row_pages < rows * kCopyPages ? 1 : widest <= block / 4 ? 4 : widest <= block / 2 ? 2 : 1;
+  const int widest = static_cast<int>(std::min<int64_t>(block, static_cast<int64_t>(max_drafted) * group));
+  const int copies = row_pages == 0 ? 1 : row_copies(head_dim, widest, row_pages, info.num_segments);
   if (copies > 1) {      // every block is joined, from its copies at the least
     for (int64_t row = 0; row < rows; ++row)
       if (rptr[row + 1] - rptr[row] == 1) cut[rptr[row]].partial = static_cast<int32_t>(info.partials++);

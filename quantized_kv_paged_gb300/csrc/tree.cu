@@ -105,6 +105,8 @@ struct Sync {
   __device__ __forceinline__ bool wait(uint32_t i, uint32_t parity, int code) const {
     return tc::mbar_try_wait(bar(i), parity) || patient(bar(i), parity, code, abort, status);
   }
+  // by a whole warp: true for all lanes or for none
+  __device__ __forceinline__ bool warp_wait(uint32_t i, uint32_t parity, int code) const { return __all_sync(kFull, wait(i, parity, code)); }
   __device__ static __noinline__ bool patient(uint32_t bar, uint32_t parity, int code, volatile int* abort, int* status) {
     const long long t0 = clock64();
     for (int n = 0;; ++n) {
@@ -323,13 +325,11 @@ __device__ void role_convert(const Sync& sy, int pages, int warp, int lane, uint
   int slot = group, parity = 0;
   for (int n = group >> 1; n < pages; n += kGroups / 2) {
     const int b = C::buf(n);
-    bool ok = sy.wait(C::B_RAW_FULL + slot, parity, 2);
-    if (!__all_sync(kFull, ok)) return;
+    if (!sy.warp_wait(C::B_RAW_FULL + slot, parity, 2)) return;
     const uint32_t entry = meta[slot], from = read0 + slot * C::kRaw, to = b * C::kTile;
     const int valid = static_cast<int>(entry & 0xFFFF);
     // the product that read the tile's last block is done
-    ok = n < C::kBufs || sy.wait(freed + b, C::phase(n) ^ 1, 2);
-    if (!__all_sync(kFull, ok)) return;
+    if (n >= C::kBufs && !sy.warp_wait(freed + b, C::phase(n) ^ 1, 2)) return;
 #pragma unroll
     for (int x0 = 0; x0 < kSets; x0 += kBatchSets) {
       uint4 w[kItems];
@@ -390,21 +390,23 @@ __device__ __forceinline__ bool elect_one() {
 template <int D>
 __device__ void role_qk(const TreeArgs& a, const Sync& sy, const TreeWorker& work, int w, uint32_t base, uint32_t tbase) {
   using C = Cfg<D>;
+  const bool leader = elect_one();
   constexpr uint32_t kIdesc = tc::idesc_f16(128, kPage, 0, 0);
   const tc::Desc2 kd = tc::split_desc(tc::smem_desc(base + C::OFF_K, 16, 1024, tc::kSwizzle128));
   const uint32_t q = tbase + C::TM_Q;
   int n = w, end = 0;                            // pages, and those up to the segment's end
   for (int si = work.begin; si < work.end; ++si) {
     end += a.segs[si].num_pages;
-    if (!sy.wait(C::B_Q_FULL, (si - work.begin) & 1, 4)) goto out;
+    if (!sy.warp_wait(C::B_Q_FULL, (si - work.begin) & 1, 4)) goto out;
     for (; n < end; n += 2) {
       const int b = C::buf(n);
-      if (!sy.wait(C::B_K_FULL + b, C::phase(n), 4)) goto out;
+      bool ok = sy.wait(C::B_K_FULL + b, C::phase(n), 4);
       // the buffer's last P has been read
-      if (n >= C::kBufs && !sy.wait(C::B_O_DONE + b, C::phase(n) ^ 1, 4)) goto out;
+      if (n >= C::kBufs) ok = ok && sy.wait(C::B_O_DONE + b, C::phase(n) ^ 1, 4);
+      if (!__all_sync(kFull, ok)) goto out;
       tc::tc_fence_after();
       const uint32_t d = tbase + C::TM_S + b * kPage;
-      if (elect_one()) {
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint64_t bd = kd.at(b * C::kTile + (i >> 2) * C::kAtom + 32 * (i & 3));
@@ -413,18 +415,18 @@ __device__ void role_qk(const TreeArgs& a, const Sync& sy, const TreeWorker& wor
         }
         tc::mma_commit(sy.bar(C::B_S_FULL + b));
       }
-      __syncwarp();
     }
   }
 out:
   __syncwarp();
-  if (elect_one()) tc::mma_commit(sy.bar(C::B_FINAL));
+  if (leader) tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
 // One warp: O += P V, page after page.
 template <int D>
 __device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& work, uint32_t base, uint32_t tbase) {
   using C = Cfg<D>;
+  const bool leader = elect_one();
   constexpr uint32_t kIdesc = tc::idesc_f16(128, D, 0, 1);
   const tc::Desc2 vd = tc::split_desc(tc::smem_desc(base + C::OFF_V, C::kAtom, 1024, tc::kSwizzle128));
   int n = 0, end = 0;
@@ -432,14 +434,14 @@ __device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& wor
     const int first = end;
     end += a.segs[si].num_pages;
     // O of the segment before has been read
-    if (si > work.begin && !sy.wait(C::B_O_FREE, (si - work.begin - 1) & 1, 4)) goto out;
+    if (si > work.begin && !sy.warp_wait(C::B_O_FREE, (si - work.begin - 1) & 1, 4)) goto out;
     for (; n < end; ++n) {
       const int b = C::buf(n);
-      if (!sy.wait(C::B_V_FULL + b, C::phase(n), 4)) goto out;
-      if (!sy.wait(C::B_P_FULL + b, C::phase(n), 4)) goto out;
+      const bool ok = sy.wait(C::B_V_FULL + b, C::phase(n), 4) && sy.wait(C::B_P_FULL + b, C::phase(n), 4);
+      if (!__all_sync(kFull, ok)) goto out;
       tc::tc_fence_after();
       const uint32_t p = tbase + C::TM_S + b * kPage;
-      if (elect_one()) {
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < kPage / 16; ++k) {
           const uint64_t bd = vd.at(b * C::kTile + 2048 * k);
@@ -448,12 +450,11 @@ __device__ void role_pv(const TreeArgs& a, const Sync& sy, const TreeWorker& wor
         }
         tc::mma_commit(sy.bar(C::B_O_DONE + b));
       }
-      __syncwarp();
     }
   }
 out:
   __syncwarp();
-  if (elect_one()) tc::mma_commit(sy.bar(C::B_FINAL));
+  if (leader) tc::mma_commit(sy.bar(C::B_FINAL));
 }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -515,7 +516,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
   const int group = a.heads / a.kv_heads, lane = row & 31, part = row / (kTreeTile / kCopies), rest = row % (kTreeTile / kCopies);
   volatile float* refs = reinterpret_cast<volatile float*>(sbase + C::OFF_REF);
   volatile int8_t* lifts = reinterpret_cast<volatile int8_t*>(sbase + C::OFF_QS);
-  auto wait = [&](uint32_t bar, uint32_t parity) { return static_cast<bool>(__all_sync(kFull, sy.wait(bar, parity, 8))); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return sy.warp_wait(bar, parity, 8); };
   // a warp's arrival, after what all its lanes did
   auto arrive = [&](uint32_t bar) {
     __syncwarp();
@@ -950,7 +951,10 @@ cudaError_t launch_attend(const TreeArgs& a, cudaStream_t s) {
 
 template <int D, bool E4M3>
 cudaError_t launch_copies(const TreeArgs& a, cudaStream_t s) {
-  return a.row_copies == 4 ? launch_attend<D, E4M3, 4>(a, s) : a.row_copies == 2 ? launch_attend<D, E4M3, 2>(a, s) : launch_attend<D, E4M3, 1>(a, s);
+  if (a.row_copies == 4) return launch_attend<D, E4M3, 4>(a, s);
+  if constexpr (D == 64)
+    if (a.row_copies == 2) return launch_attend<D, E4M3, 2>(a, s);
+  return a.row_copies == 1 ? launch_attend<D, E4M3, 1>(a, s) : cudaErrorInvalidValue;
 }
 
 template <int D>

@@ -285,40 +285,43 @@ def test_two_streams_at_once(qkvp):
 
 @pytest.mark.parametrize("cache", [q.CACHE_E4M3, q.CACHE_INT8])
 @pytest.mark.parametrize("cached,drafted,heads,kv_heads,dim,copies", [
-    ([5000, 4097], [4, 1], 8, 1, 128, 4), ([7000], [1], 1, 1, 64, 4), ([6001, 4444, 5555], [9, 16, 0], 4, 2, 64, 4), ([4900], [32], 2, 2, 256, 4),
-    ([5000, 4097], [9, 3], 8, 2, 128, 2), ([5000, 6000], [8, 7], 8, 1, 128, 2), ([4500, 4600], [33, 2], 1, 1, 64, 2), ([4800], [12], 10, 2, 256, 2),
-    ([4800], [13], 10, 2, 256, 1)])
+    ([8000, 7001], [4, 1], 8, 1, 128, 4), ([4000], [1], 1, 1, 64, 4), ([4001, 3444, 2555], [9, 16, 0], 4, 2, 64, 4), ([14900], [32], 1, 1, 256, 4),
+    ([8000, 7097], [9, 3], 8, 2, 128, 1), ([5000, 4600], [33, 2], 1, 1, 64, 2), ([5000], [8], 16, 2, 64, 2), ([5000], [13], 10, 2, 64, 1),
+    ([14800], [12], 10, 2, 256, 1)])
 def test_copies_of_few_rows(qkvp, cached, drafted, heads, kv_heads, dim, copies, cache):
     b = Batch(30 + dim + copies, cached, drafted, heads, kv_heads, dim, cache, empty=0.1)
-    for kw in (dict(), dict(num_sms=3), dict(min_splits=40), dict(window=3500, sinks=70)):
-        splits = {k: kw.pop(k) for k in ("num_sms", "min_splits") if k in kw}
+    for kw, splits in ((dict(), dict(num_sms=1)), (dict(), dict(num_sms=2)), (dict(), dict(num_sms=1, min_splits=2)),
+                       (dict(window=max(cached) - 70, sinks=70), dict(num_sms=1))):
         out, lse, plan = b.run(q, dim ** -0.5, **kw, **splits)
+        assert plan.row_copies == copies, (plan.total_pages, plan.num_segments)
         check(b, out, lse, b.reference(dim ** -0.5, **kw))
-        assert plan.row_copies == copies
+    out, lse, plan = b.run(q, dim ** -0.5, min_splits=40)
+    assert plan.row_copies == 1                # short segments
+    check(b, out, lse, b.reference(dim ** -0.5))
 
 
-@pytest.mark.parametrize("drafted", [6, 12])
-def test_copies_of_few_rows_with_nan_and_v_scales_far_apart(qkvp, drafted):
+@pytest.mark.parametrize("drafted,dim", [(6, 128), (12, 64)])
+def test_copies_of_few_rows_with_nan_and_v_scales_far_apart(qkvp, drafted, dim):
     """A NaN V code reaches the rows that see it whichever copy has the token, V's scales differ within a copy's tokens, and
     rows that see nothing but a few tokens have copies that see none."""
-    b = Batch(40 + drafted, [4800], [drafted], 4, 1, 128, q.CACHE_E4M3, chain=True)
+    b = Batch(40 + drafted, [4800], [drafted], 4, 1, dim, q.CACHE_E4M3, chain=True)
     rng = np.random.default_rng(drafted)
     b.scale[b.ids, 1] *= np.exp2(rng.integers(-40, 41, len(b.ids))).astype(np.float32)[:, None]
     want = b.reference(0.1)
-    out, lse, plan = b.run(q, 0.1)
+    out, lse, plan = b.run(q, 0.1, num_sms=1)
     assert plan.row_copies > 1
     check(b, out, lse, want)
     page, off = int(b.ids[4802 // 64]), 4802 % 64
     b.codes[page, 1, 0, off, 5] = 0x7F
-    out, lse, _ = b.run(q, 0.1)
+    out, lse, _ = b.run(q, 0.1, num_sms=1)
     o = out.float().cpu()
     assert torch.isnan(o[2:, :, 5]).all() and not torch.isnan(o[:2]).any() and not torch.isnan(o[2:, :, :5]).any() and not torch.isnan(o[2:, :, 6:]).any()
     keep = torch.arange(2).cuda()
-    R.check_attend(out[keep], lse[keep], tuple(x[:2] for x in want), 4900, 128)
-    few = Batch(44, [4800], [drafted], 4, 1, 128, q.CACHE_INT8)
-    few.ids[:-1] = -1                          # pages outside the pool: the drafted tokens alone are left
-    few.ids[-2] = 0
-    out, lse, _ = few.run(q, 0.1)
+    R.check_attend(out[keep], lse[keep], tuple(x[:2] for x in want), 4900, dim)
+    few = Batch(44, [4800], [drafted], 4, 1, dim, q.CACHE_INT8)
+    few.ids[:75] = -1                          # pages outside the pool: the drafted tokens alone are left
+    out, lse, plan = few.run(q, 0.1, num_sms=1)
+    assert plan.row_copies > 1
     check(few, out, lse, few.reference(0.1))
 
 
