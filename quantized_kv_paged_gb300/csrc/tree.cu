@@ -602,6 +602,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
         const bool masked = info.z & kMasked;
         bool good = !masked && j > 1, ok = true;
         float ro = r;                            // O's reference: the one that the page before left
+        float seen = -INFINITY;                  // the largest visible logit, where the first pass found it
         if (good) {
           // in one pass against the reference of the page before the last one, which is hardly ever another
           const float shift = r - kLift - lsv;
@@ -631,7 +632,8 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
               pk[kLd / 2 * h + k] = dev::pack_f16x2(z0, z1);
             }
           }
-          const float z = fmaxf(top0, top1) * zs, m_new = fmaxf(m, z);
+          seen = fmaxf(top0, top1);
+          const float z = seen * zs, m_new = fmaxf(m, z);
           ok = sy.wait(C::B_REF + before, before_phase, 8);
           ro = refs[row];
           // m_new - shift: log2 of what P has on 2^(z - m); moderate, and so is l's part of it
@@ -663,18 +665,19 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
         if (!good) {
           if (!__all_sync(kFull, ok)) return;
           r = ro;
-          // the largest visible logit first
-          uint64_t bits = ~0ull;
-          if (masked) bits = info.z & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
-          float top = -INFINITY;
+          uint64_t bits = kCopies == 1 ? ~0ull : low_bits(kCols) << (part * kCols % kPage);
+          if (masked) bits &= info.z & 0xFFFF ? mask.page(a, s, local_page(s, j) * kPage) : 0;
+          float top = seen;
+          if (masked || j < 2) {
 #pragma unroll 1
-          for (int k = part * (4 / kCopies); k < (part + 1) * (4 / kCopies); ++k) {
-            uint32_t x[16];
-            tc::tmem_ld16(ts + 16 * k, x);
-            tc::tmem_wait_ld();
-            const uint32_t v = static_cast<uint32_t>(bits >> (16 * k));
+            for (int k = 0; k < 2; ++k) {
+              uint32_t x[32];
+              tc::tmem_ld32(ts + 32 * k, x);
+              tc::tmem_wait_ld();
+              const uint32_t v = static_cast<uint32_t>(bits >> (32 * k));
 #pragma unroll
-            for (int u = 0; u < 16; ++u) top = fmaxf(top, v >> u & 1 ? __uint_as_float(x[u]) : -INFINITY);
+              for (int u = 0; u < 32; ++u) top = fmaxf(top, v >> u & 1 ? __uint_as_float(x[u]) : -INFINITY);
+            }
           }
           // a scale of 0 makes every visible logit 0, not -inf * 0
           const float z = top == -INFINITY ? -INFINITY : top * zs;
@@ -705,13 +708,13 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
           const float F = fminf(vs * dev::fast_exp2(fminf(back - r + kLift, 126.0f)), 0x1p126f);
           float sum = 0.0f;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t x[16], pk[8];
-            tc::tmem_ld16(ts + 16 * k, x);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t x[32], pk[16];
+            tc::tmem_ld32(ts + 32 * k, x);
             tc::tmem_wait_ld();
-            const uint32_t v = kCopies == 1 || k / (4 / kCopies) == part ? static_cast<uint32_t>(bits >> (16 * k)) : 0;
+            const uint32_t v = static_cast<uint32_t>(bits >> (32 * k));
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 16; ++u) {
               float z0 = dev::fast_exp2(fmaf(__uint_as_float(x[2 * u]), zs, -back));
               float z1 = dev::fast_exp2(fmaf(__uint_as_float(x[2 * u + 1]), zs, -back));
               z0 = v >> (2 * u) & 1 ? z0 : 0.0f;
@@ -719,7 +722,7 @@ __device__ void role_softmax(const TreeArgs& a, const Sync& sy, const TreeWorker
               sum += z0 + z1;
               pk[u] = dev::pack_f16x2(z0 * F, z1 * F);
             }
-            tc::tmem_st8(ts + 8 * k, pk);
+            tc::tmem_st16(ts + 16 * k, pk);
           }
           l += sum;
         }
