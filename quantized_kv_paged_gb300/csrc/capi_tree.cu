@@ -18,9 +18,12 @@ using namespace qkvp;
 
 namespace {
 
-// Pages of work that starting a segment counts as, and pages below which a worker is not worth its start.
-int start_pages(int dim) { return dim == 64 ? 5 : dim == 128 ? 12 : 8; }
-constexpr int kMinPages = 2;
+// Pages of work that starting a segment counts as. D 128, 16 mixed with 64 drafted: 8 / 12 / 16 / 24 pages 294 / 269 / 263 / 271
+// us; D 64, windows of 1,024: 3 / 5 / 8 / 12 pages 88 / 78 / 79 / 82; D 256, 12 with 20 drafted: 5 / 8 / 12 / 18 pages 43.5 / 43.3
+// / 44.3 / 45.
+int start_pages(int dim) { return dim == 64 ? 5 : dim == 128 ? 16 : 8; }
+// Pages below which a worker is not worth its start and the join (1 x 300 tokens with 8 drafted: 2 pages 13.0 us, 4 pages 11.3).
+constexpr int kMinPages = 4;
 // How often a row lies among the lanes: with 4 copies of up to 32 rows (2 of up to 64) the softmax of a page takes a quarter
 // (half) as long, but every segment leaves a partial, 512 D bytes, that is joined. 44 requests of 8 KV heads, us without and
 // with 4 copies: D 64 at 512 / 1,024 / 8,192 tokens 29 / 37 / 147 and 29 / 35 / 120; D 128 at 1,024 / 2,048 / 8,192 43 / 61 /
