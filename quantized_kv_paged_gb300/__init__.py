@@ -8,6 +8,7 @@ PyTorch is used for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import operator
 import os
 import threading
@@ -296,8 +297,8 @@ class _Torch:
             cls.bf16, cls.f32, cls.i32, cls.i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
             cls.u32 = torch.uint32
             # for looks over lists of tensors
-            cls.ptr, cls.stride, cls.numel, cls.device = torch.Tensor.data_ptr, torch.Tensor.stride, torch.Tensor.numel, torch.Tensor.get_device
-            cls.contiguous, cls.dtype, cls.itemsize = torch.Tensor.is_contiguous, operator.attrgetter("dtype"), torch.Tensor.element_size
+            cls.ptr, cls.size, cls.same_size, cls.device = torch.Tensor.data_ptr, torch.Tensor.size, torch.Tensor.is_same_size, torch.Tensor.get_device
+            cls.contiguous, cls.dtype, cls.nbytes = torch.Tensor.is_contiguous, operator.attrgetter("dtype"), operator.attrgetter("nbytes")
             cls.codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
             # the current stream's handle without a Stream object around it, where this torch has the call
             cls.handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -309,7 +310,7 @@ def _alike(name: str, tensors, dtypes, T, here: int):
     """Refuses tensors that do not lie in memory as the first one does, of another type or on another device. A call takes two
     for each layer, so each look goes over the whole list."""
     first = tensors[0]
-    if (len(set(map(T.stride, tensors))) > 1 or len(set(map(T.numel, tensors))) > 1 or not all(map(T.contiguous, tensors)) or
+    if (not all(map(T.same_size, tensors, itertools.repeat(first))) or not all(map(T.contiguous, tensors)) or
             not set(map(T.dtype, tensors)) <= dtypes or set(map(T.device, tensors)) != {here}):
         for i, t in enumerate(tensors):
             if t.shape != first.shape or not t.is_contiguous() or t.dtype not in dtypes or t.get_device() != here:
@@ -619,17 +620,20 @@ def kv_pages_workspace(num_pages: int, rows: int, n: int) -> int:
 def _pools(pools, num_pages: int, T, here: int):
     """The pools as the C array (data, page_bytes); every one a contiguous tensor with a page for each first index. A call
     takes one or two for each layer, so each look goes over the whole list."""
-    step = [s[0] if s else 0 for s in map(T.stride, pools)]      # elements of a page
-    if pools and (set(map(T.device, pools)) != {here} or not all(map(T.contiguous, pools)) or
-                  [n * num_pages for n in step] != list(map(T.numel, pools)) or 0 in step):
+    try:
+        rows = set(map(T.size, pools, itertools.repeat(0)))
+    except IndexError:                         # a tensor without dimensions
+        rows = set()
+    sizes = list(map(T.nbytes, pools))
+    if pools and (rows != {num_pages} or set(map(T.device, pools)) != {here} or not all(map(T.contiguous, pools)) or 0 in sizes):
         for i, t in enumerate(pools):
             if t.get_device() != here:
                 raise ValueError(f"tensors need to be on one device, the current CUDA device: pool {i} is on {t.device}")
-            if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous() or t.stride(0) * num_pages != t.numel():
+            if t.dim() < 1 or t.shape[0] != num_pages or not t.is_contiguous() or t.nbytes == 0:
                 raise ValueError(f"pool {i} needs a contiguous layout and {num_pages} pages; got {tuple(t.shape)}, strides {t.stride()}")
     arr = array("q", bytes(16 * len(pools)))
     arr[::2] = array("q", map(T.ptr, pools))
-    arr[1::2] = array("q", map(operator.mul, step, map(T.itemsize, pools)))
+    arr[1::2] = array("q", [n // num_pages for n in sizes])
     return arr
 
 

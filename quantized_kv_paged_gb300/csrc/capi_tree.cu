@@ -28,11 +28,12 @@ constexpr int kMinPages = 4;
 // (half) as long, but every segment leaves a partial, 512 D bytes, that is joined. 44 requests of 8 KV heads, us without and
 // with 4 copies: D 64 at 512 / 1,024 / 8,192 tokens 29 / 37 / 147 and 29 / 35 / 120; D 128 at 1,024 / 2,048 / 8,192 43 / 61 /
 // 163 and 45 / 60 / 154; D 256 at 2,048 / 4,096 / 8,192 105 / 175 / 314 and 107 / 167 / 287, but 77 and 81 where 24 blocks are
-// cut into segments of 60 pages. 2 copies: D 64 at 1,024 / 8,192 38 / 148 and 38 / 130; at D 128 and 256 within 2 % of none.
+// cut into segments of 60 pages. 2 copies: D 64 at 1,024 / 8,192 38 / 148 and 38 / 130; D 128 at 2,048 / 4,096 / 8,192 / 32,768 62 / 97
+// / 165 / 566 and 66 / 97 / 160 / 534; at D 256 within 2 % of none.
 int row_copies(int dim, int rows, int64_t pages, int64_t segments) {
-  const int few = dim == 64 ? 16 : dim == 128 ? 40 : 96;       // pages of a segment
-  if (rows <= kTreeTile / 4 && pages >= few * segments) return 4;
-  return dim == 64 && rows <= kTreeTile / 2 && pages >= 24 * segments ? 2 : 1;
+  const int four = dim == 64 ? 16 : dim == 128 ? 40 : 96, two = dim == 64 ? 24 : 80;       // pages of a segment
+  if (rows <= kTreeTile / 4 && pages >= four * segments) return 4;
+  return dim <= 128 && rows <= kTreeTile / 2 && pages >= two * segments ? 2 : 1;
 }
 
 }  // namespace

@@ -8,11 +8,22 @@
 // reading bounds it up to T G ~ 140 rows, the matrix products above.
 //
 // Work. A (request, KV head) has T G rows, cut into blocks of up to 128, the lanes of tensor memory. A worker (a CTA, one per SM)
-// walks segments, each a run of the pages that a block sees, page by page: S = Q K^T, softmax, O += P V, a chain of some 2,500
-// cycles at D 128. Two softmax warpgroups take the pages in turns, with two buffers of logits each (D 256: one), so four
-// pages are on their way at a time. (Blocks of 256 rows, a warpgroup for each half and the pages converted once for both, took
-// 2,100 cycles a page: Q of the second half does not fit in tensor memory, and from shared memory its products wait on
-// operand reads.)
+// walks segments, each a run of the pages that a block sees, page by page: S = Q K^T, softmax, O += P V. Two softmax warpgroups
+// take the pages in turns, with two buffers of logits each (D 256: one), so four pages are on their way at a time. (Blocks of
+// 256 rows, a warpgroup for each half and the pages converted once for both, took 2,100 cycles a page: Q of the second half
+// does not fit in tensor memory, and from shared memory its products wait on operand reads.)
+//
+// Few rows. A warp's time for a page is that of its 64 logits however many of its lanes have rows. Where the plan says so, up to
+// 32 (64) rows lie four (two) times among the 128 lanes, and each copy takes a quarter (half) of a page's tokens, with a
+// reference, m, l and part of O of its own; the products stay as they are, a copy's P is zero in the others' columns. The
+// copies leave the segment as partials that the join adds up (D 128, 44 x 32,768 tokens: 32 rows 566 -> 506 us, 64 rows 566 -> 534).
+//
+// What bounds it (D 128, cycles a page and SM, of 1.94 GHz). 128 rows: 1,050, two warpgroups at 2,100 each, of which the 64
+// exponentials a row and what goes with them take 900, the wait for the logits, the look at the page before, the vote and
+// the stores the rest (264 us at 16 requests mixed with 64 drafted, 1.1 PFLOP/s). 32 rows: 800, the conversion's two groups at 1,600
+// a block, next to 770 that shared memory needs for the 96 KB of a page (raw in and out, FP16 in, operands out): 506 us at 44 x 32,768,
+// 5.9 TB/s. A segment costs some 7 us beside its pages: Q, first pages in two passes, the last products, O.
+// Tried: 16 conversion warps (523 -> 597 us), conversion straight from global memory without the ring (536; 128 rows 266 -> 280).
 //
 // Roles, per CTA (20 warps); page n of the worker has buffer, K tile and V tile n % kBufs:
 //   softmax (2 warpgroups, one row a thread): at a segment's start the row of Q, to FP16 times a power of two, into tensor
@@ -20,7 +31,7 @@
 //   loader (a warp, one lane for each slot of the ring): bulk copies of raw K and V blocks (64 D bytes each, contiguous in the
 //     pool), and the pages' scales into another ring (read by the softmax a page ahead, they came 1,500 cycles late).
 //   conversion (8 warps, one to four a block): raw blocks to FP16, exactly, in 128-byte-swizzled tiles of 64-dim atoms.
-//   a thread for each softmax warpgroup issues S = Q K^T (M 128, N 64; Q from tensor memory), one O += P V (M 128, N D; P from
+//   a warp for each softmax warpgroup issues S = Q K^T (M 128, N 64; Q from tensor memory), one O += P V (M 128, N D; P from
 //     tensor memory). The same tile layout is K^T's K-major operand and V's MN-major one.
 // A commit of Q K^T says that the logits are there and that the K tile is free, one of P V that O is and the V tile and the
 // buffer are free.
@@ -309,12 +320,13 @@ __device__ void role_load(const TreeArgs& a, const Sync& sy, const TreeWorker& w
 // kBlockWarps warps: raw blocks to the FP16 tiles, every kGroups-th block, so that the latencies of one block (wait, read,
 // convert, write, fence) hide behind the others'. An item is 16 codes. Eight lanes take rows 2 p and 2 p + 1, 64 dims each, of atoms
 // that differ: their reads and their writes fall into distinct banks. K rows past a page's tokens keep what is there (their
-// logits are masked); V rows become zeros.
-template <int D, bool E4M3>
+// logits are masked); V rows become zeros. kAhead: all of a warp's part is read before the wait for the tile, not half of it at a
+// time behind it (copies of rows 523 -> 510 us, as the conversion bounds them; 64 rows and no copies 566 -> 586).
+template <int D, bool E4M3, bool kAhead>
 __device__ void role_convert(const Sync& sy, int pages, int warp, int lane, uint32_t base, const uint8_t* sbase, volatile int* nan_seen) {
   using C = Cfg<D>;
   constexpr int kGroups = C::kGroups, kSets = 8 / C::kBlockWarps;        // sets of 8 rows that a warp has of a block
-  constexpr int kSetItems = D == 64 ? 1 : C::kAtoms, kBatchSets = 4 / kSetItems, kItems = kBatchSets * kSetItems;
+  constexpr int kSetItems = D == 64 ? 1 : C::kAtoms, kBatchSets = kAhead ? kSets : 4 / kSetItems, kItems = kBatchSets * kSetItems;
   const int group = warp / C::kBlockWarps, kind = group & 1, c = lane & 3;
   const int sub = D == 64 ? lane >> 2 : 2 * (lane >> 3) + ((lane >> 2) & 1), odd = D == 64 ? 0 : (lane >> 2) & 1;
   const int row0 = warp % C::kBlockWarps * 8 * kSets + sub;
@@ -325,20 +337,26 @@ __device__ void role_convert(const Sync& sy, int pages, int warp, int lane, uint
   int slot = group, parity = 0;
   for (int n = group >> 1; n < pages; n += kGroups / 2) {
     const int b = C::buf(n);
-    if (!sy.warp_wait(C::B_RAW_FULL + slot, parity, 2)) return;
+    bool ok = sy.wait(C::B_RAW_FULL + slot, parity, 2);
+    __syncwarp();
     const uint32_t entry = meta[slot], from = read0 + slot * C::kRaw, to = b * C::kTile;
     const int valid = static_cast<int>(entry & 0xFFFF);
-    // the product that read the tile's last block is done
-    if (n >= C::kBufs && !sy.warp_wait(freed + b, C::phase(n) ^ 1, 2)) return;
-#pragma unroll
-    for (int x0 = 0; x0 < kSets; x0 += kBatchSets) {
-      uint4 w[kItems];
+    uint4 w[kItems];
+    auto read = [&](int x0) {
 #pragma unroll
       for (int i = 0; i < kItems; ++i) w[i] = lds128(from + (x0 + i / kSetItems) * 8 * D + (((i % kSetItems) ^ odd) << 6));
       if (x0 + kBatchSets >= kSets) {
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
+        if (lane == 0 && ok) tc::mbar_arrive(sy.bar(C::B_RAW_EMPTY + slot));
       }
+    };
+    if (kAhead) read(0);
+    // the product that read the tile's last block is done
+    if (n >= C::kBufs) ok = ok && sy.wait(freed + b, C::phase(n) ^ 1, 2);
+    if (!__all_sync(kFull, ok)) return;
+#pragma unroll
+    for (int x0 = 0; x0 < kSets; x0 += kBatchSets) {
+      if (!kAhead) read(x0);
       if (kind == 1 && valid < kPage) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i)
@@ -887,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
   if (warp < C::kConvertWarp) {
     role_softmax<D, E4M3, kCopies>(a, sy, work, warp / 4, tid & 127, base, sbase, tbase, nan_seen);
   } else if (warp < C::kQkWarp) {
-    role_convert<D, E4M3>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
+    role_convert<D, E4M3, (kCopies > 1)>(sy, work.pages, warp - C::kConvertWarp, tid & 31, base, sbase, nan_seen);
   } else if (warp == C::kLoadWarp) {
     role_load<D>(a, sy, work, tid & 31, base, sbase);
   } else {
@@ -955,7 +973,7 @@ cudaError_t launch_attend(const TreeArgs& a, cudaStream_t s) {
 template <int D, bool E4M3>
 cudaError_t launch_copies(const TreeArgs& a, cudaStream_t s) {
   if (a.row_copies == 4) return launch_attend<D, E4M3, 4>(a, s);
-  if constexpr (D == 64)
+  if constexpr (D <= 128)
     if (a.row_copies == 2) return launch_attend<D, E4M3, 2>(a, s);
   return a.row_copies == 1 ? launch_attend<D, E4M3, 1>(a, s) : cudaErrorInvalidValue;
 }

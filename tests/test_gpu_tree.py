@@ -286,7 +286,7 @@ def test_two_streams_at_once(qkvp):
 @pytest.mark.parametrize("cache", [q.CACHE_E4M3, q.CACHE_INT8])
 @pytest.mark.parametrize("cached,drafted,heads,kv_heads,dim,copies", [
     ([8000, 7001], [4, 1], 8, 1, 128, 4), ([4000], [1], 1, 1, 64, 4), ([4001, 3444, 2555], [9, 16, 0], 4, 2, 64, 4), ([14900], [32], 1, 1, 256, 4),
-    ([8000, 7097], [9, 3], 8, 2, 128, 1), ([5000, 4600], [33, 2], 1, 1, 64, 2), ([5000], [8], 16, 2, 64, 2), ([5000], [13], 10, 2, 64, 1),
+    ([12000, 12097], [9, 3], 8, 2, 128, 2), ([5000, 4600], [33, 2], 1, 1, 64, 2), ([5000], [8], 16, 2, 64, 2), ([5000], [13], 10, 2, 64, 1),
     ([14800], [12], 10, 2, 256, 1)])
 def test_copies_of_few_rows(qkvp, cached, drafted, heads, kv_heads, dim, copies, cache):
     b = Batch(30 + dim + copies, cached, drafted, heads, kv_heads, dim, cache, empty=0.1)

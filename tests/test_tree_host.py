@@ -98,8 +98,9 @@ def test_plan_of_nothing_and_of_much(lib):
         assert p.status == OK and (p.num_tokens, p.num_segments, p.num_joins) == (0, 0, 0)
     few = plan([32768] * 44, [4] * 44, heads=64)
     assert (few.row_copies, few.num_joins) == (4, 352) and few.num_partials == few.num_segments
-    assert plan([32768] * 44, [5] * 44, heads=64).row_copies == 1 and plan([500] * 44, [4] * 44, heads=64).row_copies == 1
-    assert plan([32768] * 44, [8] * 44, heads=64, dim=64).row_copies == 2
+    assert plan([32768] * 44, [5] * 44, heads=64).row_copies == 2 and plan([500] * 44, [4] * 44, heads=64).row_copies == 1
+    assert plan([32768] * 44, [8] * 44, heads=64, dim=64).row_copies == 2 and plan([32768] * 44, [8] * 44, heads=64, dim=256).row_copies == 1
+    assert plan([32768] * 44, [9] * 44, heads=64).row_copies == 1
     assert plan([1 << 20], [8], heads=8, kv_heads=1, min_splits=100, ptr=[0, 16384]).max_join_segments >= 100
     assert plan([LONGEST], [1], ptr=[0, 1 << 25]).status == U
     assert plan([LONGEST], [1], ptr=[0, 1 << 25], window=1, heads=1, kv_heads=1).status in (OK, U)
