@@ -584,8 +584,8 @@ int gqa_tree_run(const qkvp_tree_plan* plan, const void* q, const void* kv_data,
  *   need; if j > 0, the codes of the block's tokens before the first one that the call puts there, and of the tokens
  *   that move within the block, become round(code * 2^-j). Codes of the others are round(x / scale), or round(x) where scale
  *   is 0; rounding as for gqa_append_rope. FP32 arithmetic with one rounding per operation.
- *  kv_data, kv_scale  host arrays [num_layers] of the layers' device pools (kv_data 16-byte aligned); up to 128 layers of one
- *               shape. Read before the call returns.
+ *  kv_data, kv_scale  host arrays [num_layers] of the layers' device pools (kv_data 16-byte aligned, scales not negative); up to
+ *               128 layers of one shape, each listed once. Read before the call returns.
  *  kv_len       device int32 [batch], the tokens before the drafted ones (gqa_append_rope's kv_len).
  *  kv_indptr, kv_indices, nnz: page table on the device, as for gqa_append_rope.
  *  path         device int32 [batch][max_path], strictly ascending from 0 on; path_len device int32 [batch], 0 to max_path.
@@ -623,9 +623,9 @@ typedef struct {
  * kv_pages_* - the pages of a cache: copied, shared between requests, reserved, given back and moved together. All arrays are on
  * the device and the calls only launch kernels, so they may be captured and replayed. Equal states give equal states:
  * pages are taken in the order of the list and given back the highest first.
- *  workspace    the *bytes of kv_pages_workspace for this num_pages and rows and lists of up to n, 256-byte aligned, zero before its first use; a call leaves
- *               it ready for the next (with other lists and another n that it is large enough for). Calls that use one
- *               workspace or one state must not overlap.
+ *  workspace    the *bytes of kv_pages_workspace for this num_pages and rows and lists of up to n, 256-byte aligned, zero
+ *               before its first use; a call leaves it ready for the next (with other lists and another n that it is large
+ *               enough for). Calls that use one workspace or one state must not overlap.
  *  status       [n]: 1 for an entry that was carried out, 0 for one that was refused, which changes nothing.
  * Ids outside the pool in a table or list are passed over; they never cause an out-of-bounds access. A state that does not
  * add up (a page held more often than refs says, a free page in a table) stays so.
