@@ -923,7 +923,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) tree_kernel(const TreeArg
 }
 
 // Joins the partials of blocks that were cut. A lane has a row, a warp 8 columns of 32 rows, so that all reads are of whole
-// lines; the slots, and a slot's copies of the row, are summed in order. Grid: (joins, 32 rows of a block, 64 columns).
+// lines; the slots, and a slot's copies of the row, are summed in order. Grid: (joins, 32 rows of a block, 64 columns). The latency
+// of dependent loads bounds it (record, lse, partials). Alone and cold: 44 x 32,768 with copies 13 us for 32 MB, 1 x 200,001 with 19
+// slots a block 16, 16 mixed with 64 drafted 9 (4 columns a warp: 12, 12 and 11).
 constexpr int kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeArgs a) {

@@ -2,8 +2,8 @@
 // tokens, in every layer of a head pool.
 //
 // A CTA looks a request's path up once (path, page ids: four dependent reads, some 3 us) and then serves many of its blocks
-// (layer, K or V, head), one a warp. (A warp that looked the path up for its one block: 64 requests, 48 layers of 4 heads, 28.9
-// us.) Nobody else touches the blocks of a (layer, K or V, head) that the request's tokens move into: they are walked in
+// (layer, K or V, head), one a warp: 64 requests, 48 layers of 4 heads of 128, INT8, paths of 9 take 22 us, one request of 28 layers
+// 3.1. (A warp that looked the path up for its one block and converted code by code: 28.9 and 3.6.) Nobody else touches the blocks of a (layer, K or V, head) that the request's tokens move into: they are walked in
 // order, so a block's scale changes only after the blocks before it have read from it, and within a block the tokens go in
 // order of the path, each no later than where it comes from, a batch of them in registers between the loads and
 // the stores. A token from another block is requantized; the amax of those decides how far the block's scale grows.
